@@ -376,6 +376,151 @@ class Buffer:
                          recv_x, recv_scales if use_fp8 else None, y, out, chunk_tokens)
         return out, handle
 
+    # -------------------------------------------------------- expert operators
+    def _weights(self, w: torch.Tensor, name: str) -> tuple[int, int]:
+        """The two channel counts of an [E, ., .] weight tensor."""
+        if w.dim() != 3 or w.shape[0] != self.num_experts:
+            raise ValueError(f"{name} must be [E={self.num_experts}, ., .], got {tuple(w.shape)}")
+        return w.shape[1], w.shape[2]
+
+    def _rows(self, t: torch.Tensor, width: int, name: str) -> None:
+        if t.dim() != 2 or t.shape[0] != self.rows or t.shape[1] != width:
+            raise ValueError(f"{name} must be [{self.rows}, {width}], got {tuple(t.shape)}")
+
+    def _new_rows(self, width: int, dtype: torch.dtype, like: torch.Tensor) -> torch.Tensor:
+        return torch.empty(self.rows, width, dtype=dtype, device=like.device)
+
+    def expert_gemm(self, x: torch.Tensor, w: torch.Tensor, handle: Handle, transpose_w: bool = False,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+        """y[r] = W[e] x[r] for the rows r that expert e received: x
+        [rows, k] bf16, w [E, n, k] bf16, y [rows, n] bf16.  transpose_w=True:
+        y[r] = W[e]^T x[r] ([rows, n] -> [rows, k]), the gradient of the
+        input.  Rows that received nothing are not written."""
+        a, b = self._weights(w, "w")
+        n, k = (b, a) if transpose_w else (a, b)
+        self._rows(x, k, "x")
+        if out is None:
+            out = self._new_rows(n, torch.bfloat16, x)
+        self._rows(out, n, "out")
+        ep.ep_expert_gemm(self._ctx, handle.raw, x, w, n, k, transpose_w, out)
+        return out
+
+    def _fp8_operands(self, x, w):
+        (xq, xs), (wq, ws) = x, w
+        n, k = self._weights(wq, "w")
+        self._rows(xq, k, "x")
+        self._rows(xs, k // 128, "x scales")
+        if tuple(ws.shape) != (self.num_experts, -(-n // 128), k // 128):
+            raise ValueError(f"w scales must be [{self.num_experts}, {-(-n // 128)}, {k // 128}], got {tuple(ws.shape)}")
+        return xq, xs, wq, ws, n, k
+
+    def expert_gemm_fp8(self, x, w, handle: Handle, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The product on FP8 rows: x = (codes [rows, k], scales [rows,
+        k/128]) as low_latency_dispatch returns them, w = (codes [E, n, k],
+        scales [E, ceil(n/128), k/128]) as cast_weights returns them; y
+        [rows, n] bf16."""
+        xq, xs, wq, ws, n, k = self._fp8_operands(x, w)
+        if out is None:
+            out = self._new_rows(n, torch.bfloat16, xq)
+        self._rows(out, n, "out")
+        ep.ep_expert_gemm_fp8(self._ctx, handle.raw, xq, xs, wq, ws, n, k, out)
+        return out
+
+    def expert_gate_fp8(self, x, w, handle: Handle, out=None):
+        """Gate and up products on FP8 rows, SwiGLU and the FP8 cast in one
+        call: w = (codes [E, 2*inner, k] with the gate's rows first, scales);
+        returns (codes [rows, inner], scales [rows, inner/128]), the x of the
+        next expert_gemm_fp8."""
+        xq, xs, wq, ws, n, k = self._fp8_operands(x, w)
+        if n % 2:
+            raise ValueError("w must hold as many gate rows as up rows")
+        inner = n // 2
+        if out is None:
+            out = (self._new_rows(inner, torch.float8_e4m3fn, xq), self._new_rows(inner // 128, torch.float32, xq))
+        self._rows(out[0], inner, "out")
+        self._rows(out[1], inner // 128, "out scales")
+        ep.ep_expert_gate_fp8(self._ctx, handle.raw, xq, xs, wq, ws, inner, k, out[0], out[1])
+        return out
+
+    def expert_wgrad(self, dy: torch.Tensor, x: torch.Tensor, handle: Handle, out: torch.Tensor | None = None,
+                     accumulate: bool = False) -> torch.Tensor:
+        """dW[e] = sum over the rows of e of dy[r] x[r]^T: dy [rows, n], x
+        [rows, k] bf16; out [E, n, k] fp32 (the default) or bf16.
+        accumulate=True adds to an fp32 ``out``."""
+        n, k = dy.shape[-1], x.shape[-1]
+        self._rows(dy, n, "dy")
+        self._rows(x, k, "x")
+        if out is None:
+            if accumulate:
+                raise ValueError("accumulate=True needs out")
+            out = torch.empty(self.num_experts, n, k, dtype=torch.float32, device=x.device)
+        if self._weights(out, "out") != (n, k):
+            raise ValueError(f"out must be [{self.num_experts}, {n}, {k}], got {tuple(out.shape)}")
+        ep.ep_expert_wgrad(self._ctx, handle.raw, dy, x, n, k, accumulate, out)
+        return out
+
+    def expert_swiglu(self, gu: torch.Tensor, handle: Handle, out: torch.Tensor | None = None) -> torch.Tensor:
+        """h = silu(g) * u of gu = [g | u] [rows, 2*inner] bf16; h [rows, inner]."""
+        inner = gu.shape[-1] // 2
+        self._rows(gu, 2 * inner, "gu")
+        if out is None:
+            out = self._new_rows(inner, torch.bfloat16, gu)
+        self._rows(out, inner, "out")
+        ep.ep_expert_swiglu(self._ctx, handle.raw, gu, inner, out)
+        return out
+
+    def expert_swiglu_backward(self, gu: torch.Tensor, dh: torch.Tensor, handle: Handle, out=None):
+        """(dgu [rows, 2*inner], h [rows, inner]) for the gradient dh of h."""
+        inner = gu.shape[-1] // 2
+        self._rows(gu, 2 * inner, "gu")
+        self._rows(dh, inner, "dh")
+        if out is None:
+            out = (self._new_rows(2 * inner, torch.bfloat16, gu), self._new_rows(inner, torch.bfloat16, gu))
+        self._rows(out[0], 2 * inner, "out[0]")
+        self._rows(out[1], inner, "out[1]")
+        ep.ep_expert_swiglu_backward(self._ctx, handle.raw, gu, dh, inner, out[0], out[1])
+        return out
+
+    def cast_weights(self, w: torch.Tensor, out=None):
+        """bf16 [E, n, k] -> (e4m3 codes [E, n, k], fp32 scales [E,
+        ceil(n/128), k/128]), one scale per 128 x 128 block."""
+        n, k = self._weights(w, "w")
+        if out is None:
+            out = (torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device),
+                   torch.empty(self.num_experts, -(-n // 128), k // 128, dtype=torch.float32, device=w.device))
+        if tuple(out[0].shape) != tuple(w.shape) or tuple(out[1].shape) != (self.num_experts, -(-n // 128), k // 128):
+            raise ValueError("out must be codes of w's shape and one scale per 128 x 128 block")
+        ep.ep_cast_weights(self._ctx, w, n, k, out[0], out[1])
+        return out
+
+    def expert_mlp_fp8(self, x, w_gate_up, w_down, handle: Handle, out: torch.Tensor | None = None) -> torch.Tensor:
+        """Gated experts on FP8 rows, between low_latency_dispatch(use_fp8=True)
+        and low_latency_combine: x = (codes, scales) as received, w_gate_up
+        and w_down from cast_weights ([E, 2*inner, H] and [E, H, inner]);
+        returns y [rows, H] bf16."""
+        return self.expert_gemm_fp8(self.expert_gate_fp8(x, w_gate_up, handle), w_down, handle, out=out)
+
+    def expert_mlp(self, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, handle: Handle):
+        """Gated experts in bf16 on the received rows x [rows, H]: w_gate_up
+        [E, 2*inner, H], w_down [E, H, inner].  Returns (y [rows, H], saved)
+        with what expert_mlp_backward needs."""
+        gu = self.expert_gemm(x, w_gate_up, handle)
+        y = self.expert_gemm(self.expert_swiglu(gu, handle), w_down, handle)
+        return y, (x, gu)
+
+    def expert_mlp_backward(self, dy: torch.Tensor, saved, w_gate_up: torch.Tensor, w_down: torch.Tensor,
+                            handle: Handle, grads=None):
+        """Gradients (dx [rows, H] bf16, dw_gate_up, dw_down) of expert_mlp
+        for dy [rows, H].  The weight gradients are fp32; ``grads`` = a pair
+        of fp32 tensors to add them to."""
+        x, gu = saved
+        dgu, h = self.expert_swiglu_backward(gu, self.expert_gemm(dy, w_down, handle, transpose_w=True), handle)
+        acc = grads is not None
+        g_gate_up, g_down = grads if acc else (None, None)
+        dw_down = self.expert_wgrad(dy, h, handle, out=g_down, accumulate=acc)
+        dw_gate_up = self.expert_wgrad(dgu, x, handle, out=g_gate_up, accumulate=acc)
+        return self.expert_gemm(dgu, w_gate_up, handle, transpose_w=True), dw_gate_up, dw_down
+
     def device_status(self) -> int:
         """Synchronise the current stream; return and clear the device status."""
         return ep.ep_get_device_status(self._ctx)

@@ -611,6 +611,53 @@ ep_status median_us(F enqueue, int reps, void *flush, size_t flush_bytes, int sm
     return EP_OK;
 }
 
+// Checks shared by the expert operators: a live context and an expert layout
+// in its handle (a rank-deduplicated one groups rows by rank, not by expert).
+ep_status check_expert(const ep_ctx *ctx, const ep_handle *h) {
+    if (ctx == nullptr || h == nullptr || h->ctx != ctx) return EP_ERR_INVALID_ARG;
+    if (h->tokens_per_rank < 0 || h->rank_mode) return EP_ERR_NO_LAYOUT;
+    if (!on_ctx_device(ctx)) return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
+// Channel counts of an expert product: multiples of `step` from `step` to 65536.
+ep_status check_channels(int32_t c, int32_t step) {
+    if (c < 1 || c % 8 != 0) return EP_ERR_INVALID_ARG;
+    if (c % step != 0 || c > 65536) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+int expert_sms(const ep_ctx *ctx) { return grid_cap(ctx, 1); }
+
+// The parameters every expert product shares.
+ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_t n, int32_t k) {
+    const ep_config &c = ctx->cfg;
+    ep::ExpertGemmParams p = {};
+    p.base = h->base;
+    p.count = h->tokens_per_expert;
+    p.E = c.num_experts;
+    p.n = n;
+    p.k = k;
+    p.rows = ctx->rows;
+    // an expert can be offered every entry; the padded layout keeps R*Tmax
+    p.live = (int64_t)c.num_ranks * h->tokens_per_rank * c.topk;
+    p.max_count = p.live;
+    if (c.layout == EP_LAYOUT_PADDED && p.max_count > (int64_t)c.num_ranks * c.max_tokens_per_rank)
+        p.max_count = (int64_t)c.num_ranks * c.max_tokens_per_rank;
+    p.sms = expert_sms(ctx);
+    p.status = ctx->d_status;
+    return p;
+}
+
+ep_status enqueue_expert(ep::ExpertOp op, const ep::ExpertGemmParams &p, cudaStream_t st) {
+    const cudaError_t e = ep::launch_expert_gemm(op, p, st);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return e == cudaErrorInvalidConfiguration ? EP_ERR_UNSUPPORTED : EP_ERR_CUDA;
+    }
+    return EP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1271,6 +1318,169 @@ ep_status ep_round_trip_auto_chunk(const ep_ctx *ctx, int32_t use_fp8, int32_t r
     if (ctx == nullptr || chunk_tokens == nullptr) return EP_ERR_INVALID_ARG;
     if (use_fp8 != 0 && use_fp8 != 1) return EP_ERR_INVALID_ARG;
     *chunk_tokens = auto_chunk(ctx, use_fp8 != 0, rank_layout != 0);
+    return EP_OK;
+}
+
+ep_status ep_expert_gemm(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const void *d_w, int32_t n, int32_t k,
+                         int32_t transpose_w, void *d_y, void *stream) {
+    NvtxRange nvtx("ep_expert_gemm");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(n, 8);
+    if (s == EP_OK) s = check_channels(k, 8);
+    if (s != EP_OK) return s;
+    if (transpose_w != 0 && transpose_w != 1) return EP_ERR_INVALID_ARG;
+    if (handle->tokens_per_rank == 0) return EP_OK;
+    if (d_x == nullptr || d_w == nullptr || d_y == nullptr) return EP_ERR_INVALID_ARG;
+    if (!aligned(d_x, 16) || !aligned(d_w, 16) || !aligned(d_y, 16)) return EP_ERR_INVALID_ARG;
+    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k);
+    p.x = d_x;
+    p.w = d_w;
+    p.y = d_y;
+    return enqueue_expert(transpose_w ? ep::ExpertOp::kBf16T : ep::ExpertOp::kBf16, p, (cudaStream_t)stream);
+}
+
+ep_status ep_expert_gemm_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const float *d_x_scales,
+                             const void *d_w, const float *d_w_scales, int32_t n, int32_t k, void *d_y, void *stream) {
+    NvtxRange nvtx("ep_expert_gemm_fp8");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(n, 8);
+    if (s == EP_OK) s = check_channels(k, 128);
+    if (s != EP_OK) return s;
+    if (handle->tokens_per_rank == 0) return EP_OK;
+    if (d_x == nullptr || d_x_scales == nullptr || d_w == nullptr || d_w_scales == nullptr || d_y == nullptr)
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(d_x, 16) || !aligned(d_x_scales, 4) || !aligned(d_w, 16) || !aligned(d_w_scales, 4) || !aligned(d_y, 16))
+        return EP_ERR_INVALID_ARG;
+    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k);
+    p.x = d_x;
+    p.xs = d_x_scales;
+    p.w = d_w;
+    p.ws = d_w_scales;
+    p.y = d_y;
+    return enqueue_expert(ep::ExpertOp::kFp8, p, (cudaStream_t)stream);
+}
+
+ep_status ep_expert_gate_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const float *d_x_scales,
+                             const void *d_w, const float *d_w_scales, int32_t inner, int32_t k, void *d_h,
+                             float *d_h_scales, void *stream) {
+    NvtxRange nvtx("ep_expert_gate_fp8");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(inner, 128);
+    if (s == EP_OK) s = check_channels(k, 128);
+    if (s == EP_OK && inner > 32768) s = EP_ERR_UNSUPPORTED;
+    if (s != EP_OK) return s;
+    if (handle->tokens_per_rank == 0) return EP_OK;
+    if (d_x == nullptr || d_x_scales == nullptr || d_w == nullptr || d_w_scales == nullptr || d_h == nullptr ||
+        d_h_scales == nullptr)
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(d_x, 16) || !aligned(d_x_scales, 4) || !aligned(d_w, 16) || !aligned(d_w_scales, 4) ||
+        !aligned(d_h, 16) || !aligned(d_h_scales, 4))
+        return EP_ERR_INVALID_ARG;
+    ep::ExpertGemmParams p = expert_params(ctx, handle, 2 * inner, k);
+    p.x = d_x;
+    p.xs = d_x_scales;
+    p.w = d_w;
+    p.ws = d_w_scales;
+    p.y = d_h;
+    p.ys = d_h_scales;
+    return enqueue_expert(ep::ExpertOp::kGateFp8, p, (cudaStream_t)stream);
+}
+
+ep_status ep_expert_wgrad(ep_ctx *ctx, const ep_handle *handle, const void *d_dy, const void *d_x, int32_t n, int32_t k,
+                          int32_t out_fp32, int32_t accumulate, void *d_dw, void *stream) {
+    NvtxRange nvtx("ep_expert_wgrad");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(n, 8);
+    if (s == EP_OK) s = check_channels(k, 8);
+    if (s != EP_OK) return s;
+    if ((out_fp32 != 0 && out_fp32 != 1) || (accumulate != 0 && accumulate != 1)) return EP_ERR_INVALID_ARG;
+    if (accumulate && !out_fp32) return EP_ERR_INVALID_ARG;
+    if (handle->tokens_per_rank == 0 && accumulate) return EP_OK;
+    // with no tokens dW is zero, and d_dy / d_x are not read
+    if (d_dw == nullptr || !aligned(d_dw, 16)) return EP_ERR_INVALID_ARG;
+    if (handle->tokens_per_rank == 0) {
+        const size_t bytes = (size_t)ctx->cfg.num_experts * n * k * (out_fp32 ? 4 : 2);
+        if (cudaMemsetAsync(d_dw, 0, bytes, (cudaStream_t)stream) != cudaSuccess) {
+            cudaGetLastError();
+            return EP_ERR_CUDA;
+        }
+        return EP_OK;
+    }
+    if (d_dy == nullptr || d_x == nullptr) return EP_ERR_INVALID_ARG;
+    if (!aligned(d_dy, 16) || !aligned(d_x, 16)) return EP_ERR_INVALID_ARG;
+    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k);
+    p.x = d_x;
+    p.dy = d_dy;
+    p.y = d_dw;
+    p.out_fp32 = out_fp32;
+    p.accumulate = accumulate;
+    return enqueue_expert(ep::ExpertOp::kWgrad, p, (cudaStream_t)stream);
+}
+
+ep_status ep_expert_swiglu(ep_ctx *ctx, const ep_handle *handle, const void *d_gu, int32_t inner, void *d_h,
+                           void *stream) {
+    NvtxRange nvtx("ep_expert_swiglu");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(inner, 8);
+    if (s != EP_OK) return s;
+    if (handle->tokens_per_rank == 0) return EP_OK;
+    if (d_gu == nullptr || d_h == nullptr || !aligned(d_gu, 16) || !aligned(d_h, 16)) return EP_ERR_INVALID_ARG;
+    ep::SwigluParams p = {};
+    p.gu = d_gu;
+    p.h = d_h;
+    p.slot = handle->slot;
+    p.n = (int64_t)ctx->cfg.num_ranks * handle->tokens_per_rank * ctx->cfg.topk;
+    p.inner = inner;
+    if (ep::launch_swiglu(p, false, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
+    return EP_OK;
+}
+
+ep_status ep_expert_swiglu_backward(ep_ctx *ctx, const ep_handle *handle, const void *d_gu, const void *d_dh,
+                                    int32_t inner, void *d_dgu, void *d_h, void *stream) {
+    NvtxRange nvtx("ep_expert_swiglu_backward");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(inner, 8);
+    if (s != EP_OK) return s;
+    if (handle->tokens_per_rank == 0) return EP_OK;
+    if (d_gu == nullptr || d_dh == nullptr || d_dgu == nullptr) return EP_ERR_INVALID_ARG;
+    if (!aligned(d_gu, 16) || !aligned(d_dh, 16) || !aligned(d_dgu, 16) || !aligned(d_h, 16)) return EP_ERR_INVALID_ARG;
+    ep::SwigluParams p = {};
+    p.gu = d_gu;
+    p.dh = d_dh;
+    p.dgu = d_dgu;
+    p.h = d_h;
+    p.slot = handle->slot;
+    p.n = (int64_t)ctx->cfg.num_ranks * handle->tokens_per_rank * ctx->cfg.topk;
+    p.inner = inner;
+    if (ep::launch_swiglu(p, true, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
+    return EP_OK;
+}
+
+ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, void *d_q, float *d_scales, void *stream) {
+    NvtxRange nvtx("ep_cast_weights");
+    if (ctx == nullptr || !on_ctx_device(ctx)) return EP_ERR_INVALID_ARG;
+    ep_status s = check_channels(n, 8);
+    if (s == EP_OK) s = check_channels(k, 128);
+    if (s != EP_OK) return s;
+    if (d_w == nullptr || d_q == nullptr || d_scales == nullptr) return EP_ERR_INVALID_ARG;
+    if (!aligned(d_w, 16) || !aligned(d_q, 16) || !aligned(d_scales, 4)) return EP_ERR_INVALID_ARG;
+    ep::CastWeightsParams p = {};
+    p.w = d_w;
+    p.q = static_cast<uint8_t *>(d_q);
+    p.scales = d_scales;
+    p.E = ctx->cfg.num_experts;
+    p.n = n;
+    p.k = k;
+    if (ep::launch_cast_weights(p, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
     return EP_OK;
 }
 

@@ -199,6 +199,48 @@ cudaError_t launch_identity(const IdentityParams &p, bool fp8, int max_blocks, b
                             cudaStream_t stream);
 int identity_blocks_per_sm(bool fp8);
 
+// ------------------------------------------------------------------ expert products
+// Matrix products over the rows of each expert (see expert_gemm.cu).
+enum class ExpertOp : int { kBf16 = 0, kBf16T = 1, kFp8 = 2, kGateFp8 = 3, kWgrad = 4 };
+struct ExpertGemmParams {
+    const void *x;          // bf16 or e4m3 [rows, k]
+    const float *xs;        // [rows, k/128] (FP8)
+    const void *w;          // [E, n, k] (kBf16T: [E, k, n])
+    const float *ws;        // [E, ceil(n/128), k/128] (FP8)
+    const void *dy;         // bf16 [rows, n] (wgrad)
+    void *y;                // bf16 [rows, n]; gate: e4m3 [rows, n/2]; wgrad: [E, n, k]
+    float *ys;              // [rows, n/256] (gate)
+    const int64_t *base;    // [E]
+    const int32_t *count;   // [E]
+    int32_t E, n, k;
+    int64_t rows;           // receive rows
+    int64_t max_count;      // most rows of one expert
+    int64_t live;           // entries of the layout (an upper bound of the rows in use)
+    int32_t out_fp32, accumulate;  // wgrad
+    int32_t sms;            // SMs to spread over
+    uint32_t *status;
+};
+cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream);
+
+// ------------------------------------------------------------------ gated activation, weight cast
+struct SwigluParams {
+    const void *gu;         // bf16 [rows, 2 * inner]
+    const void *dh;         // bf16 [rows, inner] (backward)
+    void *h;                // bf16 [rows, inner] (backward: may be nullptr)
+    void *dgu;              // bf16 [rows, 2 * inner] (backward)
+    const int32_t *slot;    // [n]
+    int64_t n;              // entries
+    int32_t inner;
+};
+cudaError_t launch_swiglu(const SwigluParams &p, bool backward, int sms, cudaStream_t stream);
+struct CastWeightsParams {
+    const void *w;          // bf16 [E, n, k]
+    uint8_t *q;             // e4m3 [E, n, k]
+    float *scales;          // [E, ceil(n/128), k/128]
+    int32_t E, n, k;
+};
+cudaError_t launch_cast_weights(const CastWeightsParams &p, int sms, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device helpers
 #ifdef __CUDACC__
 // Programmatic dependent launch: let the next kernel in the stream start, and

@@ -45,6 +45,8 @@ ENTRY_POINTS = (
     "ep_get_tuning", "ep_set_tuning", "ep_autotune", "ep_get_autotune_log", "ep_set_test_hooks",
     "ep_rank_send_rows", "ep_rank_dispatch_send", "ep_rank_dispatch_recv", "ep_rank_combine_send",
     "ep_rank_combine_recv", "ep_rank_runs",
+    "ep_expert_gemm", "ep_expert_gemm_fp8", "ep_expert_gate_fp8", "ep_expert_wgrad", "ep_expert_swiglu",
+    "ep_expert_swiglu_backward", "ep_cast_weights",
 )
 
 TUNE_KNOBS = {0: "dispatch", 1: "combine_chunks", 2: "round_trip_chunk",
@@ -143,6 +145,13 @@ def lib() -> ctypes.CDLL:
             "ep_rank_combine_send": (I32, [P, P, P, P, I32, P, P]),
             "ep_rank_combine_recv": (I32, [P, P, P, P, P]),
             "ep_rank_runs": (I32, [P, ctypes.POINTER(I32), ctypes.POINTER(I64), ctypes.POINTER(I64)]),
+            "ep_expert_gemm": (I32, [P, P, P, P, I32, I32, I32, P, P]),
+            "ep_expert_gemm_fp8": (I32, [P, P, P, P, P, P, I32, I32, P, P]),
+            "ep_expert_gate_fp8": (I32, [P, P, P, P, P, P, I32, I32, P, P, P]),
+            "ep_expert_wgrad": (I32, [P, P, P, P, I32, I32, I32, I32, P, P]),
+            "ep_expert_swiglu": (I32, [P, P, P, I32, P, P]),
+            "ep_expert_swiglu_backward": (I32, [P, P, P, P, I32, P, P, P]),
+            "ep_cast_weights": (I32, [P, P, I32, I32, P, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -456,3 +465,59 @@ def ep_rank_runs(handle, num_ranks: int):
     _check(lib().ep_rank_runs(handle, cnt, so, ro), "ep_rank_runs")
     mat = lambda a: [list(a[r * num_ranks:(r + 1) * num_ranks]) for r in range(num_ranks)]
     return mat(cnt), mat(so), mat(ro)
+
+
+def ep_expert_gemm(ctx, handle, x: torch.Tensor, w: torch.Tensor, n: int, k: int, transpose_w: bool,
+                   y: torch.Tensor, stream=None) -> None:
+    _check(lib().ep_expert_gemm(
+        ctx, handle, _ptr(x, torch.bfloat16, "x"), _ptr(w, torch.bfloat16, "w"), int(n), int(k),
+        int(bool(transpose_w)), _ptr(y, torch.bfloat16, "y"), _stream(stream)), "ep_expert_gemm")
+
+
+def ep_expert_gemm_fp8(ctx, handle, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                       w_scales: torch.Tensor, n: int, k: int, y: torch.Tensor, stream=None) -> None:
+    _check(lib().ep_expert_gemm_fp8(
+        ctx, handle, _ptr(x, torch.float8_e4m3fn, "x"), _ptr(x_scales, torch.float32, "x_scales"),
+        _ptr(w, torch.float8_e4m3fn, "w"), _ptr(w_scales, torch.float32, "w_scales"), int(n), int(k),
+        _ptr(y, torch.bfloat16, "y"), _stream(stream)), "ep_expert_gemm_fp8")
+
+
+def ep_expert_gate_fp8(ctx, handle, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor,
+                       w_scales: torch.Tensor, inner: int, k: int, h: torch.Tensor, h_scales: torch.Tensor,
+                       stream=None) -> None:
+    _check(lib().ep_expert_gate_fp8(
+        ctx, handle, _ptr(x, torch.float8_e4m3fn, "x"), _ptr(x_scales, torch.float32, "x_scales"),
+        _ptr(w, torch.float8_e4m3fn, "w"), _ptr(w_scales, torch.float32, "w_scales"), int(inner), int(k),
+        _ptr(h, torch.float8_e4m3fn, "h"), _ptr(h_scales, torch.float32, "h_scales"), _stream(stream)),
+        "ep_expert_gate_fp8")
+
+
+def ep_expert_wgrad(ctx, handle, dy: torch.Tensor, x: torch.Tensor, n: int, k: int, accumulate: bool,
+                    dw: torch.Tensor, stream=None) -> None:
+    """dw fp32 or bf16 (accumulate: fp32)."""
+    if dw.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dw must be torch.float32 or torch.bfloat16, got {dw.dtype}")
+    _check(lib().ep_expert_wgrad(
+        ctx, handle, _ptr(dy, torch.bfloat16, "dy"), _ptr(x, torch.bfloat16, "x"), int(n), int(k),
+        int(dw.dtype == torch.float32), int(bool(accumulate)), _ptr(dw, None, "dw"), _stream(stream)),
+        "ep_expert_wgrad")
+
+
+def ep_expert_swiglu(ctx, handle, gu: torch.Tensor, inner: int, h: torch.Tensor, stream=None) -> None:
+    _check(lib().ep_expert_swiglu(ctx, handle, _ptr(gu, torch.bfloat16, "gu"), int(inner),
+                                  _ptr(h, torch.bfloat16, "h"), _stream(stream)), "ep_expert_swiglu")
+
+
+def ep_expert_swiglu_backward(ctx, handle, gu: torch.Tensor, dh: torch.Tensor, inner: int, dgu: torch.Tensor,
+                              h: torch.Tensor | None = None, stream=None) -> None:
+    _check(lib().ep_expert_swiglu_backward(
+        ctx, handle, _ptr(gu, torch.bfloat16, "gu"), _ptr(dh, torch.bfloat16, "dh"), int(inner),
+        _ptr(dgu, torch.bfloat16, "dgu"), _ptr(h, torch.bfloat16, "h"), _stream(stream)),
+        "ep_expert_swiglu_backward")
+
+
+def ep_cast_weights(ctx, w: torch.Tensor, n: int, k: int, q: torch.Tensor, scales: torch.Tensor,
+                    stream=None) -> None:
+    _check(lib().ep_cast_weights(ctx, _ptr(w, torch.bfloat16, "w"), int(n), int(k),
+                                 _ptr(q, torch.float8_e4m3fn, "q"), _ptr(scales, torch.float32, "scales"),
+                                 _stream(stream)), "ep_cast_weights")

@@ -287,6 +287,74 @@ ep_status ep_expert_identity(ep_ctx *ctx, const ep_handle *handle, int32_t use_f
                              const void *d_recv_x, const float *d_recv_scales, void *d_y,
                              int64_t token_begin, int64_t token_end, void *stream);
 
+/* Expert operators: what runs between dispatch and combine on the rows that
+ * the experts received.  The row groups are the handle's: expert e's rows are
+ * base[e] .. base[e] + tokens_per_expert[e] of the receive layout, read on the
+ * device, so a call waits for nothing on the host and can be captured in a
+ * CUDA graph.  Rows outside the groups are neither used nor written (their
+ * bytes may be anything, NaN included); an expert without rows costs nothing
+ * (ep_expert_wgrad writes its zeros).  The handle must hold an expert layout
+ * (ep_get_dispatch_layout / ep_dispatch; a rank-deduplicated layout groups rows
+ * by rank: EP_ERR_NO_LAYOUT).  Row matrices have ep_recv_rows rows, row-major
+ * without gaps; weights are [E, n, k], one matrix per expert; all pointers
+ * 16-byte aligned (scales 4).  Channel counts n, k and inner are multiples of 8
+ * (EP_ERR_INVALID_ARG otherwise) up to 65536, where FP8 blocks run along them
+ * multiples of 128 (EP_ERR_UNSUPPORTED otherwise).  A call uses the context's
+ * SMs (max_sms).  Outputs must not overlap inputs.  Every wait inside the
+ * kernels is bounded (EP_ERR_TIMEOUT through ep_get_device_status).
+ *
+ * ep_expert_gemm: y[r] = W[e] x[r] for every row r of every expert e, products
+ *   of bf16 values summed in fp32, rounded once to bf16.
+ *     d_x  device bf16 [rows, k]
+ *     d_w  device bf16 [E, n, k]; with transpose_w = 1 [E, k, n], i.e.
+ *          y[r] = W[e]^T x[r], the gradient of the input (x is then the
+ *          gradient of the output; n and k stay y's and x's channels)
+ *     d_y  device bf16 [rows, n]
+ * ep_expert_gemm_fp8: the same on what an FP8 dispatch delivers,
+ *   y[r, c] = sum_b xs[r, b] ws[e, c/128, b] sum_{i in block b} xq[r, i] wq[e, c, i]
+ *   (blocks b of 128 channels of k), blocks summed in fp32, one bf16 rounding.
+ *     d_x, d_x_scales  e4m3 [rows, k], fp32 [rows, k/128]
+ *     d_w, d_w_scales  e4m3 [E, n, k], fp32 [E, ceil(n/128), k/128]: one scale
+ *                      per 128 x 128 block (ep_cast_weights makes both)
+ *     d_y              bf16 [rows, n]
+ * ep_expert_gate_fp8: the gate and up products of a gated expert, its SwiGLU
+ *   and the cast for the next product in one call: with W = [Wg; Wu]
+ *   ([E, 2*inner, k]), g and u the two products in fp32 as above,
+ *   h = g / (1 + exp(-g)) * u, cast per 128 channels by the dispatch's rule
+ *   (a = max(amax |h|, 1e-4), scale = a/448, q = e4m3(h * (448/a))).
+ *     d_h, d_h_scales  e4m3 [rows, inner], fp32 [rows, inner/128]
+ * ep_expert_wgrad: dW[e] = sum over the rows of e of dy[r] x[r]^T.
+ *     d_dy   device bf16 [rows, n];  d_x  device bf16 [rows, k]
+ *     d_dw   device [E, n, k], fp32 (out_fp32 = 1) or bf16 (0: one rounding);
+ *            accumulate = 1 (fp32 only) adds to what it holds
+ * ep_expert_swiglu: h = g / (1 + exp(-g)) * u of gu = [g | u] rows, in fp32,
+ *   one bf16 rounding.
+ *     d_gu  device bf16 [rows, 2*inner];  d_h  device bf16 [rows, inner]
+ * ep_expert_swiglu_backward: d_dgu [rows, 2*inner] = [dg | du] for d_dh
+ *   [rows, inner]; with d_h not NULL also writes h again (for the second
+ *   product's ep_expert_wgrad, so that a step need not keep it).
+ * ep_cast_weights: bf16 [E, n, k] -> e4m3 [E, n, k] and a scale per 128 x 128
+ *   block, by the dispatch's FP8 rule with the block's amax; E is the
+ *   context's; a last block of n % 128 rows has its own scale.
+ *
+ * Results do not depend on max_sms, the layout form or the kernels around. */
+ep_status ep_expert_gemm(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const void *d_w,
+                         int32_t n, int32_t k, int32_t transpose_w, void *d_y, void *stream);
+ep_status ep_expert_gemm_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const float *d_x_scales,
+                             const void *d_w, const float *d_w_scales, int32_t n, int32_t k, void *d_y,
+                             void *stream);
+ep_status ep_expert_gate_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const float *d_x_scales,
+                             const void *d_w, const float *d_w_scales, int32_t inner, int32_t k, void *d_h,
+                             float *d_h_scales, void *stream);
+ep_status ep_expert_wgrad(ep_ctx *ctx, const ep_handle *handle, const void *d_dy, const void *d_x, int32_t n,
+                          int32_t k, int32_t out_fp32, int32_t accumulate, void *d_dw, void *stream);
+ep_status ep_expert_swiglu(ep_ctx *ctx, const ep_handle *handle, const void *d_gu, int32_t inner, void *d_h,
+                           void *stream);
+ep_status ep_expert_swiglu_backward(ep_ctx *ctx, const ep_handle *handle, const void *d_gu, const void *d_dh,
+                                    int32_t inner, void *d_dgu, void *d_h, void *stream);
+ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, void *d_q, float *d_scales,
+                          void *stream);
+
 /* Split dispatch and combine: the send half returns and a later "hook" call
  * finishes the receive (the hook-based communication-computation overlap of
  * "如何突破MoE通信瓶颈：DeepEP跨节点优化技术终极指南", section 技术解析,
