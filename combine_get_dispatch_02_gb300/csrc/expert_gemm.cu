@@ -5,156 +5,714 @@
 //   y[r]  = sum_b xs[r,b] ws[e,.,b] (Wq[e] xq[r])_b   (e4m3, 128-channel blocks b)
 //   h[r]  = cast(silu(g) * u), (g, u) = the two halves of the e4m3 product
 //   dW[e] = sum_r dy[r] x[r]^T
-// Plain form: one CTA per output tile of 32 x 128, fp32 accumulation on the
-// CUDA cores.
+//
+// One persistent kernel of CTA pairs (a cluster of 2, one CTA per SM).  A
+// pair's tile is 256 x N of the transposed output: 256 rows of the weights
+// (128 per CTA, the M side of the tensor cores) by N <= 256 rows of one
+// expert (the N side, in steps of 32).  The weights are the dimension without
+// remainders and the tokens the ragged one, so a group of 40 rows costs 64
+// columns of products, not a 128- or 256-row tile; few rows leave the kernel
+// bound by the weights' bytes, many by the tensor cores.  The tiles of an
+// expert are numbered with its token tiles fastest, so pairs that run at the
+// same time share its weights in L2.
+//
+// Warps of a CTA: 0-7 read the accumulators out of tensor memory, 8 loads
+// (one thread, tensor maps, 128-byte swizzle), 9 issues the products (one
+// thread of the pair's first CTA), 10 brings the FP8 scales or clears the
+// rows past the end of an expert (wgrad).  The accumulators are double
+// buffered (2 x 256 columns).  A segment of products shares an accumulator:
+//   bf16       the whole sum over k (the next tile's products run while this
+//              tile is written out)
+//   e4m3       one block of 128 channels, whose partial sums the reading
+//              warps scale and add up in fp32 registers
+//   wgrad      the whole sum over rows; fp32 output: 256 rows, added up in
+//              registers (the tensor cores truncate when they add, and a long
+//              sum would drift: 8e-6 of the result over 7168 terms, measured)
+// All waits are bounded; a wait that gives up sets the status word and ends
+// its role.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "ep_internal.cuh"
+#include "umma.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kBM = 32, kBN = 128, kBK = 16, kT = 256;
+using namespace umma;
 
-__device__ __forceinline__ float e4m3_to_float(uint8_t q) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)q, __NV_E4M3)));
-}
-__device__ __forceinline__ float bf(const void *p, int64_t i) {
-    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
+constexpr int kEpiWarps = 8;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpAux = 10;
+constexpr int kThreads = 11 * 32;
+constexpr int kTileW = 256;       // weight rows of a pair's tile
+constexpr int kScaleGroup = 4;    // 128-channel blocks per fill of the scale buffer
+constexpr int kMaxSmem = 232448;
 
+// Tensor maps: [0] the M-side operand, [1..4] the token rows in boxes of 128,
+// 64, 32 and 16 rows (wgrad: [1] x).
+struct Maps {
+    CUtensorMap m[5];
+};
+
+template <ExpertOp OP, bool F32>
+struct Shape {
+    static constexpr bool FP8 = OP == ExpertOp::kFp8 || OP == ExpertOp::kGateFp8;
+    static constexpr bool GATE = OP == ExpertOp::kGateFp8;
+    static constexpr bool WG = OP == ExpertOp::kWgrad;
+    static constexpr bool A_MN = OP == ExpertOp::kBf16T || WG;
+    static constexpr bool B_MN = WG;
+    static constexpr int NMAX = GATE ? 128 : 256;         // columns of a tile
+    static constexpr int A_BYTES = GATE ? 32768 : 16384;  // per CTA and stage
+    static constexpr int B_BYTES = NMAX / 2 * 128;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int OUT_BYTES = WG && F32 ? 4096 : (GATE ? 1024 : 2048);  // per reading warp
+    static constexpr int STAGES = (WG && F32) || GATE ? 5 : 6;
+    static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
+    static constexpr int AMAX = GATE ? 2 * 2 * 4 * 32 * 4 : 0;
+    // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
+    static constexpr int KSTEP = FP8 ? 128 : 64;
+    // stages per segment; 0: all of them
+    static constexpr int SEG = FP8 ? 1 : (WG && F32 ? 4 : 0);
+    static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE + kEpiWarps * OUT_BYTES + SCALES + AMAX;
+};
+
+struct Bars {
+    uint64_t full[6], empty[6], land[6];
+    uint64_t tfull[2], tempty[2], sfull[2], sempty[2];
+    uint32_t tmem;
+};
+
+struct Tile {
+    int e;
+    int64_t row0;   // first receive row (wgrad: of the expert)
+    int valid;      // rows (wgrad: all rows of the expert)
+    int nt;         // columns of the products, a multiple of 32
+    int w0;         // first weight row of the pair (gate: channel of h)
+    int c0;         // wgrad: first column (channel of x)
+};
+
+// Tile number t.  before[e]: token tiles of the experts before e.
 template <ExpertOp OP>
-__global__ void __launch_bounds__(kT) expert_gemm_plain(const ExpertGemmParams p) {
-    constexpr bool DUAL = OP == ExpertOp::kGateFp8;
-    constexpr int NB = DUAL ? 2 : 1;
-    __shared__ float As[kBK][kBM + 1];
-    __shared__ float Bs[NB][kBK][kBN + 1];
-    const int tid = threadIdx.x, ty = tid >> 5, tx = tid & 31;
-    const bool wg = OP == ExpertOp::kWgrad;
-    const int e = blockIdx.z;
-    const int64_t base = p.base[e];
-    const int cnt = p.count[e];
-    const int mdim = wg ? p.n : cnt;              // rows of this tile's output
-    const int ndim = wg ? p.k : (DUAL ? p.n / 2 : p.n);
-    const int kdim = wg ? cnt : p.k;
-    const int n0 = blockIdx.x * kBN;
-    const int kb = (p.k + 127) / 128;
-    auto load_a = [&](int m, int kk) -> float {   // rows (wgrad: channels of dy)
-        if (m >= mdim || kk >= kdim) return 0.0f;
-        if constexpr (OP == ExpertOp::kWgrad) return bf(p.dy, (base + kk) * p.n + m);
-        const int64_t r = base + m;
-        if constexpr (OP == ExpertOp::kFp8 || OP == ExpertOp::kGateFp8)
-            return e4m3_to_float(static_cast<const uint8_t *>(p.x)[r * p.k + kk]) * p.xs[r * kb + kk / 128];
-        return bf(p.x, r * p.k + kk);
-    };
-    auto load_b = [&](int half, int c, int kk) -> float {
-        if (c >= ndim || kk >= kdim) return 0.0f;
-        if constexpr (OP == ExpertOp::kWgrad) return bf(p.x, (base + kk) * p.k + c);
-        const int64_t w0 = (int64_t)e * p.n * p.k;
-        const int ch = c + half * ndim;
-        if constexpr (OP == ExpertOp::kFp8 || OP == ExpertOp::kGateFp8)
-            return e4m3_to_float(static_cast<const uint8_t *>(p.w)[w0 + (int64_t)ch * p.k + kk]) *
-                   p.ws[((int64_t)e * ((p.n + 127) / 128) + ch / 128) * kb + kk / 128];
-        if constexpr (OP == ExpertOp::kBf16T) return bf(p.w, w0 + (int64_t)kk * p.n + ch);
-        return bf(p.w, w0 + (int64_t)ch * p.k + kk);
-    };
-    for (int m0 = blockIdx.y * kBM; m0 < mdim; m0 += gridDim.y * kBM) {
-        // partial sums of 256 terms, then sums of partial sums: a long fp32 sum
-        // loses fewer bits
-        float acc[NB][4][4] = {}, part[NB][4][4] = {};
-        for (int k0 = 0; k0 < kdim; k0 += kBK) {
-            for (int i = tid; i < kBM * kBK; i += kT) {
-                const int m = wg ? i % kBM : i / kBK, kk = wg ? i / kBM : i % kBK;
-                As[kk][m] = load_a(m0 + m, k0 + kk);
-            }
-            const bool nfast = wg || OP == ExpertOp::kBf16T;
-            for (int h = 0; h < NB; ++h)
-                for (int i = tid; i < kBN * kBK; i += kT) {
-                    const int c = nfast ? i % kBN : i / kBK, kk = nfast ? i / kBN : i % kBK;
-                    Bs[h][kk][c] = load_b(h, n0 + c, k0 + kk);
-                }
-            __syncthreads();
-#pragma unroll
-            for (int kk = 0; kk < kBK; ++kk)
-#pragma unroll
-                for (int h = 0; h < NB; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            part[h][i][j] = fmaf(As[kk][ty * 4 + i], Bs[h][kk][tx + 32 * j], part[h][i][j]);
-            __syncthreads();
-            if ((k0 + kBK) % 256 == 0 || k0 + kBK >= kdim)
-#pragma unroll
-                for (int h = 0; h < NB; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            acc[h][i][j] += part[h][i][j];
-                            part[h][i][j] = 0.0f;
-                        }
+__device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *before, int t, int wtiles) {
+    Tile r;
+    constexpr bool WG = OP == ExpertOp::kWgrad;
+    if constexpr (WG) {
+        const int ctiles = (p.k + 255) / 256;
+        const int per = wtiles * ctiles;
+        r.e = t / per;
+        const int local = t - r.e * per;
+        r.w0 = local / ctiles * kTileW;
+        r.c0 = local % ctiles * 256;
+        r.row0 = __ldg(p.base + r.e);
+        r.valid = __ldg(p.count + r.e);
+        r.nt = p.k - r.c0 > 128 ? 256 : 128;
+    } else {
+        const int q = t / wtiles;
+        int lo = 0, hi = p.E - 1;  // the last e with before[e] <= q
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (before[mid] <= q)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
-        for (int i = 0; i < 4; ++i) {
-            const int m = m0 + ty * 4 + i;
-            if (m >= mdim) continue;
-            if constexpr (DUAL) {
-                float h[4], amax = 0.0f;
-                for (int j = 0; j < 4; ++j) {
-                    const float g = acc[0][i][j];
-                    h[j] = g / (1.0f + expf(-g)) * acc[NB - 1][i][j];
-                    amax = fmaxf(amax, fabsf(h[j]));
+        r.e = lo;
+        const int tt = before[lo + 1] - before[lo];
+        const int local = t - before[lo] * wtiles;
+        const int cnt = __ldg(p.count + lo);
+        // equal token tiles, in steps of 32 rows
+        const int size = ((cnt + tt - 1) / tt + 31) & ~31;
+        const int r0 = local % tt * size;
+        r.w0 = local / tt * (OP == ExpertOp::kGateFp8 ? 256 : kTileW);
+        r.c0 = 0;
+        r.row0 = __ldg(p.base + lo) + r0;
+        r.valid = min(size, cnt - r0);
+        r.nt = (r.valid + 31) & ~31;
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Write 32 tokens x 32 channels of a warp (lane = channel, v[i] = token i) as
+// bf16 rows: neighbouring lanes swap halves so that each holds channel pairs,
+// the pairs go through 2 KB of shared memory (64 bytes per token, free of bank
+// conflicts), and 4 lanes store the 64 bytes of a token.
+__device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf, int lane, __nv_bfloat16 *dst, int64_t ld,
+                                             int tokens, int channels) {
+    const bool odd = lane & 1;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t a = bf16x2(v[4 * j], v[4 * j + 2]), b = bf16x2(v[4 * j + 1], v[4 * j + 3]);
+        const uint32_t keep = odd ? b : a;
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
+        // even lanes: tokens 4j and 4j + 2; odd lanes: 4j + 1 and 4j + 3
+        const uint32_t lo = __byte_perm(keep, got, odd ? 0x1054 : 0x5410);
+        const uint32_t hi = __byte_perm(keep, got, odd ? 0x3276 : 0x7632);
+        const uint32_t at = buf + (4 * j + (odd ? 1 : 0)) * 64 + (lane >> 1) * 4;
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(lo) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 128), "r"(hi) : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int tok = (lane >> 2) + 8 * j, c = (lane & 3) * 8;
+        uint4 q;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "r"(buf + tok * 64 + c * 2));
+        if (tok < tokens && c < channels) *reinterpret_cast<uint4 *>(dst + tok * ld + c) = q;
+    }
+}
+
+// Write 32 rows x 32 columns of a warp (lane = row, v[i] = column i): through
+// shared memory with swizzled 16-byte pieces, then whole 64- (bf16) or
+// 128-byte (fp32) row segments.
+template <bool F32>
+__device__ __forceinline__ void store_rows(const float (&v)[32], uint32_t buf, int lane, void *dst, int64_t ld, int rows,
+                                           int columns, bool accumulate) {
+    __syncwarp();
+    constexpr int P = F32 ? 8 : 4;  // pieces of a row
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+        uint4 q;
+        int at;
+        if constexpr (F32) {
+            q = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                           __float_as_uint(v[4 * c + 3]));
+            at = lane * 128 + (c ^ (lane & 7)) * 16;
+        } else {
+            q = make_uint4(bf16x2(v[8 * c], v[8 * c + 1]), bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                           bf16x2(v[8 * c + 4], v[8 * c + 5]), bf16x2(v[8 * c + 6], v[8 * c + 7]));
+            at = lane * 64 + (c ^ ((lane >> 1) & 3)) * 16;
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                     : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        const int i = lane + 32 * j, row = i / P, c = i % P;
+        const int at = F32 ? row * 128 + (c ^ (row & 7)) * 16 : row * 64 + (c ^ ((row >> 1) & 3)) * 16;
+        uint4 q;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "r"(buf + at));
+        if (row >= rows || c * (F32 ? 4 : 8) >= columns) continue;
+        if constexpr (F32) {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(dst) + row * ld + c * 4);
+            float4 f = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
+            if (accumulate) {
+                const float4 o = *d;
+                f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
+            }
+            *d = f;
+        } else {
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(dst) + row * ld + c * 8) = q;
+        }
+    }
+}
+
+template <ExpertOp OP, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    expert_gemm_kernel(const __grid_constant__ Maps maps, const ExpertGemmParams p) {
+    using S = Shape<OP, F32>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ Bars bars;
+    uint8_t *const smem = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
+    uint8_t *const outs = smem + S::STAGES * S::STAGE;
+    float *const scales = reinterpret_cast<float *>(outs + kEpiWarps * S::OUT_BYTES);
+    float *const amaxs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(scales) + S::SCALES);
+    int *const before = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(amaxs) + S::AMAX);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t b_full = saddr(bars.full), b_empty = saddr(bars.empty), b_land = saddr(bars.land);
+    const uint32_t b_tfull = saddr(bars.tfull), b_tempty = saddr(bars.tempty);
+    const uint32_t b_sfull = saddr(bars.sfull), b_sempty = saddr(bars.sempty);
+
+    if (tid == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            bar_init(b_full + 8 * i, S::WG ? 2 : 1);
+            bar_init(b_empty + 8 * i, 1);
+            bar_init(b_land + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(b_tfull + 8 * i, 1);
+            bar_init(b_tempty + 8 * i, 2 * kEpiWarps);
+            bar_init(b_sfull + 8 * i, 1);
+            bar_init(b_sempty + 8 * i, kEpiWarps);
+        }
+        bar_init_fence();
+        for (int i = 0; i < (S::WG ? 2 : 5); ++i) prefetch_map(&maps.m[i]);
+    }
+    if (warp == kWarpMma) tmem_alloc(saddr(&bars.tmem), 512);
+    pdl_wait();  // the layout, the rows and possibly the weights come from kernels queued before
+    // token tiles of the experts before each one
+    if constexpr (!S::WG) {
+        for (int e = tid; e < p.E; e += kThreads) before[e + 1] = (__ldg(p.count + e) + S::NMAX - 1) / S::NMAX;
+        if (tid == 0) before[0] = 0;
+        __syncthreads();
+        if (warp == 0) {
+            const int per = (p.E + 31) / 32;
+            int sum = 0;
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e < p.E) sum += before[e + 1];
+            }
+            int run = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, run, o);
+                if (lane >= o) run += v;
+            }
+            run -= sum;
+            for (int i = 0; i < per; ++i) {
+                const int e = lane * per + i;
+                if (e < p.E) {
+                    run += before[e + 1];
+                    before[e + 1] = run;
                 }
-                for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                const float a = fmaxf(amax, 1e-4f), inv = __fdiv_rn(448.0f, a);
-                const int64_t r = base + m;
-                for (int j = 0; j < 4; ++j)
-                    static_cast<uint8_t *>(p.y)[r * ndim + n0 + tx + 32 * j] =
-                        __nv_cvt_float_to_fp8(__fmul_rn(h[j], inv), __NV_SATFINITE, __NV_E4M3);
-                if (tx == 0) p.ys[r * (ndim / 128) + n0 / 128] = __fdiv_rn(a, 448.0f);
-            } else {
-                for (int j = 0; j < 4; ++j) {
-                    const int c = n0 + tx + 32 * j;
-                    if (c >= ndim) continue;
-                    if constexpr (OP == ExpertOp::kWgrad) {
-                        const int64_t o = ((int64_t)e * p.n + m) * p.k + c;
-                        if (p.out_fp32) {
-                            float *d = static_cast<float *>(p.y) + o;
-                            *d = p.accumulate ? *d + acc[0][i][j] : acc[0][i][j];
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    const uint32_t tmem = bars.tmem;
+
+    const int width = S::GATE ? p.n / 2 : p.n;
+    const int wtiles = (width + kTileW - 1) / kTileW;
+    const int ctiles = (p.k + 255) / 256;
+    const int total = S::WG ? p.E * wtiles * ctiles : before[p.E] * wtiles;
+    const int kchan = (p.k + S::KSTEP - 1) / S::KSTEP;  // stages of a tile (wgrad: by the expert's rows)
+    auto stages_of = [&](const Tile &ti) { return S::WG ? (ti.valid + 63) / 64 : kchan; };
+    bool ok = true;
+
+    if (warp == kWarpLoad) {
+        if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
+            int used = 0;
+            for (int t = pair; t < total && ok; t += pairs) {
+                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+                const int nk = stages_of(ti);
+                const int half = ti.nt >> 1;
+                const uint32_t bytes = S::A_BYTES + half * 128;
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!(ok = bar_wait(b_empty + 8 * st, ph ^ 1))) break;
+                    const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
+                    const uint32_t full0 = map_rank(b_full + 8 * st, 0);
+                    uint32_t bar = full0;
+                    if constexpr (S::WG) {
+                        if (kb == nk - 1 && (ti.valid & 63) != 0) {
+                            // the rows past the end are cleared before the products see the stage
+                            bar = map_rank(b_land + 8 * st, rank);
+                            bar_expect(b_land + 8 * st, bytes);
+                        } else if (rank == 0) {
+                            bar_expect(b_full + 8 * st, 2 * bytes);
                         } else {
-                            static_cast<__nv_bfloat16 *>(p.y)[o] = __float2bfloat16_rn(acc[0][i][j]);
+                            bar_arrive_cluster(full0);
                         }
+                        const int r = (int)(ti.row0 + kb * 64);
+                        const int n0 = ti.w0 + (int)rank * 128, c0 = ti.c0 + (int)rank * half;
+                        tma_2d(a, &maps.m[0], n0, r, bar);
+                        tma_2d(a + 8192, &maps.m[0], n0 + 64, r, bar);
+                        tma_2d(b, &maps.m[1], c0, r, bar);
+                        if (half > 64) tma_2d(b + 8192, &maps.m[1], c0 + 64, r, bar);
                     } else {
-                        static_cast<__nv_bfloat16 *>(p.y)[(base + m) * p.n + c] = __float2bfloat16_rn(acc[0][i][j]);
+                        if (rank == 0) bar_expect(b_full + 8 * st, 2 * bytes);
+                        const int kc = kb * S::KSTEP, w = ti.w0 + (int)rank * 128;
+                        if constexpr (S::A_MN) {
+                            tma_3d(a, &maps.m[0], w, kc, ti.e, bar);
+                            tma_3d(a + 8192, &maps.m[0], w + 64, kc, ti.e, bar);
+                        } else {
+                            tma_3d(a, &maps.m[0], kc, w, ti.e, bar);
+                            if constexpr (S::GATE) tma_3d(a + 16384, &maps.m[0], kc, width + w, ti.e, bar);
+                        }
+                        int r = (int)ti.row0 + (int)rank * half;
+                        uint32_t d = b;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int h = 128 >> i;
+                            if (half & h) {
+                                tma_2d(d, &maps.m[1 + i], kc, r, bar);
+                                r += h;
+                                d += h * 128;
+                            }
+                        }
+                    }
+                    used = min(used + 1, S::STAGES);
+                    if (++st == S::STAGES) st = 0, ph ^= 1;
+                }
+            }
+            // the stages in flight have been read (nothing lands or arrives here after the kernel's end)
+            for (int i = 0; i < used; ++i) {
+                if (--st < 0) st = S::STAGES - 1, ph ^= 1;
+                if (!bar_wait(b_empty + 8 * st, ph)) {
+                    ok = false;
+                    atomicOr(p.status, kStatusInFlight);
+                    break;
+                }
+            }
+        }
+    } else if (warp == kWarpMma) {
+        if (rank == 0 && lane == 0) {
+            int st = 0;
+            uint32_t ph = 0, seg = 0;
+            for (int t = pair; t < total && ok; t += pairs) {
+                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+                const int nk = stages_of(ti);
+                const uint32_t id = idesc(S::FP8, S::A_MN, S::B_MN, ti.nt);
+                for (int kb = 0; kb < nk; ++kb) {
+                    const int in_seg = S::SEG == 0 ? kb : kb % (S::SEG == 0 ? 1 : S::SEG);
+                    const uint32_t buf = seg & 1;
+                    if (in_seg == 0) {
+                        if (!(ok = bar_wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1))) break;
+                    }
+                    if (!(ok = bar_wait(b_full + 8 * st, ph))) break;
+                    fence_after();
+                    const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
+                    const uint32_t d = tmem + buf * 256;
+                    const int steps = S::WG ? (min(64, ti.valid - kb * 64) + 15) / 16 : 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (S::WG && i >= steps) break;
+                        const uint64_t da = desc(a + i * (S::A_MN ? 2048 : 32), S::A_MN ? 8192 : 16);
+                        const uint64_t db = desc(b + i * (S::B_MN ? 2048 : 32), S::B_MN ? 8192 : 16);
+                        mma<S::FP8>(d, da, db, id, in_seg != 0 || i != 0);
+                        if constexpr (S::GATE)
+                            mma<S::FP8>(d + 128, desc(a + 16384 + i * 32, 16), db, id, in_seg != 0 || i != 0);
+                    }
+                    commit_pair(b_empty + 8 * st);
+                    if (kb == nk - 1 || (S::SEG != 0 && in_seg == S::SEG - 1)) {
+                        commit_pair(b_tfull + 8 * buf);
+                        ++seg;
+                    }
+                    if (++st == S::STAGES) st = 0, ph ^= 1;
+                }
+            }
+        }
+    } else if (warp == kWarpAux) {
+        if constexpr (S::FP8) {
+            // scales of a tile's columns, xs * ws, for kScaleGroup blocks at a time
+            const int nb = (p.n + 127) / 128;
+            uint32_t fill = 0;
+            for (int t = pair; t < total && ok; t += pairs) {
+                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+                const int wb = ti.w0 / 128 + (int)rank;
+                const float *ws = p.ws + ((int64_t)ti.e * nb + min(wb, nb - 1)) * kchan;
+                const float *wu = S::GATE ? p.ws + ((int64_t)ti.e * nb + min(wb + width / 128, nb - 1)) * kchan : ws;
+                for (int g = 0; g < kchan; g += kScaleGroup, ++fill) {
+                    const uint32_t buf = fill & 1;
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
+                    if (!ok) break;
+                    float *out = scales + buf * kScaleGroup * 256;
+                    float w[kScaleGroup], w2[kScaleGroup];
+#pragma unroll
+                    for (int q = 0; q < kScaleGroup; ++q) {
+                        w[q] = g + q < kchan ? __ldg(ws + g + q) : 0.0f;
+                        w2[q] = S::GATE && g + q < kchan ? __ldg(wu + g + q) : 0.0f;
+                    }
+#pragma unroll
+                    for (int j0 = 0; j0 < S::NMAX; j0 += 32) {
+                        if (j0 >= ti.nt) break;
+                        const int j = j0 + lane;
+                        const float *xs = p.xs + (ti.row0 + j) * kchan + g;
+                        float x[kScaleGroup];
+#pragma unroll
+                        for (int q = 0; q < kScaleGroup; ++q) x[q] = j < ti.valid && g + q < kchan ? __ldg(xs + q) : 0.0f;
+#pragma unroll
+                        for (int q = 0; q < kScaleGroup; ++q) {
+                            out[q * 256 + j] = x[q] * w[q];
+                            if constexpr (S::GATE) out[q * 256 + 128 + j] = x[q] * w2[q];
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(b_sfull + 8 * buf);
+                }
+            }
+        } else if constexpr (S::WG) {
+            // an expert's last rows: clear the lines past its end (both operands
+            // hold one 128-byte line per row and 64 channels), up to the 16 rows of a product
+            int st = 0;
+            uint32_t landed = 0;  // parity of each stage's landing barrier
+            for (int t = pair; t < total && ok; t += pairs) {
+                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+                const int nk = stages_of(ti);
+                if ((ti.valid & 63) != 0) {
+                    const int s = (st + nk - 1) % S::STAGES;
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_land + 8 * s, (landed >> s) & 1));
+                    if (!ok) break;
+                    landed ^= 1u << s;
+                    uint8_t *base = smem + s * S::STAGE;
+                    const int r0 = ti.valid & 63, r1 = (r0 + 15) & ~15;
+                    for (int i = lane; i < (r1 - r0) * 32; i += 32) {
+                        const int row = r0 + (i >> 5), piece = i & 31;  // 4 chunks x 8 pieces of 16 bytes
+                        *reinterpret_cast<uint4 *>(base + (piece >> 3) * 8192 + row * 128 + (piece & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(map_rank(b_full + 8 * s, 0));
+                }
+                st = (st + nk) % S::STAGES;
+            }
+        }
+    } else {
+        const int sub = warp & 3, hw = warp >> 2;  // lanes 32 * sub .., every second chunk of 32 columns
+        const uint32_t lanes = tmem + ((uint32_t)(sub * 32) << 16);
+        const uint32_t out = saddr(outs + warp * S::OUT_BYTES);
+        const uint32_t tempty0 = map_rank(b_tempty, 0);
+        uint32_t seg = 0, fill = 0, turn = 0;
+        for (int t = pair; t < total && ok; t += pairs) {
+            const Tile ti = tile_at<OP>(p, before, t, wtiles);
+            const int nk = stages_of(ti);
+            const int chunks = ti.nt >> 5;
+            const int wc = ti.w0 + (int)rank * 128 + sub * 32;  // the warp's first weight row / channel of h
+            if constexpr (S::SEG == 0) {
+                __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
+                const uint32_t buf = seg & 1;
+                if (nk > 0) {
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+                }
+                for (int c = hw; c < chunks; c += 2) {
+                    float v[32];
+                    if (nk > 0) {
+                        tmem_ld32(v, lanes + buf * 256 + c * 32);
+                        tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    }
+                    if constexpr (S::WG)
+                        store_rows<false>(v, out, lane, y + ((int64_t)ti.e * p.n + wc) * p.k + ti.c0 + c * 32, p.k,
+                                          p.n - wc, p.k - ti.c0 - c * 32, false);
+                    else
+                        store_tokens(v, out, lane, y + (ti.row0 + c * 32) * p.n + wc, p.n, ti.valid - c * 32, p.n - wc);
+                }
+                if (nk > 0) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(tempty0 + 8 * buf);
+                    ++seg;
+                }
+            } else {
+                // sums over segments in registers: chunk 2 s + hw of the columns (gate: 2
+                // chunks of the gate's columns, then 2 of the up product's)
+                constexpr int SLOTS = 4;
+                float acc[SLOTS][32];
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[s][i] = 0.0f;
+                const int nseg = (nk + S::SEG - 1) / S::SEG;
+                for (int k = 0; k < nseg; ++k, ++seg) {
+                    const uint32_t buf = seg & 1;
+                    if constexpr (S::FP8) {
+                        if (k % kScaleGroup == 0) {
+                            ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
+                            if (!ok) break;
+                        }
+                    }
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256;
+#pragma unroll
+                    for (int s = 0; s < SLOTS; ++s) {
+                        const int c = S::GATE ? 2 * (s & 1) + hw : 2 * s + hw;
+                        if (c >= chunks) continue;
+                        const int col = c * 32 + (S::GATE && s >= 2 ? 128 : 0);
+                        float v[32];
+                        tmem_ld32(v, lanes + buf * 256 + col);
+                        tmem_wait_ld();
+                        if constexpr (S::FP8) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(sc + col + i);
+                                acc[s][i] = fmaf(v[i], f.x, acc[s][i]);
+                                acc[s][i + 1] = fmaf(v[i + 1], f.y, acc[s][i + 1]);
+                                acc[s][i + 2] = fmaf(v[i + 2], f.z, acc[s][i + 2]);
+                                acc[s][i + 3] = fmaf(v[i + 3], f.w, acc[s][i + 3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) acc[s][i] += v[i];
+                        }
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_cluster(tempty0 + 8 * buf);
+                    if constexpr (S::FP8) {
+                        if (k % kScaleGroup == kScaleGroup - 1 || k == nseg - 1) {
+                            if (lane == 0) bar_arrive(b_sempty + 8 * (fill & 1));
+                            ++fill;
+                        }
+                    }
+                }
+                if (!ok) break;
+                if constexpr (S::GATE) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int c = 2 * s + hw;
+                        if (c >= chunks) continue;  // the same for the 4 warps of this half
+                        float mine = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float g = acc[s][i];
+                            const float h = __fdiv_rn(g, 1.0f + expf(-g)) * acc[s + 2][i];
+                            acc[s][i] = h;
+                            // non-negative floats order like their bits; a NaN counts as 0
+                            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(fabsf(h), 0.0f)));
+                            if (lane == i) mine = __uint_as_float(m);
+                        }
+                        float *am = amaxs + ((turn & 1) * 2 + hw) * 128;
+                        ++turn;
+                        am[sub * 32 + lane] = mine;
+                        asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
+                        const float a = fmaxf(fmaxf(fmaxf(am[lane], am[32 + lane]), fmaxf(am[64 + lane], am[96 + lane])), 1e-4f);
+                        const float inv = __fdiv_rn(448.0f, a);
+                        const int tokens = ti.valid - c * 32;
+                        const int h0 = ti.w0 + (int)rank * 128;
+                        const int64_t row = ti.row0 + c * 32;
+                        uint8_t *buf8 = outs + warp * S::OUT_BYTES;
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            buf8[i * 32 + lane] = __nv_cvt_float_to_fp8(
+                                __fmul_rn(acc[s][i], __shfl_sync(0xFFFFFFFFu, inv, i)), __NV_SATFINITE, __NV_E4M3);
+                        __syncwarp();
+                        if (h0 < width) {
+                            if (sub == 0 && lane < tokens)
+                                p.ys[(row + lane) * (width / 128) + h0 / 128] = __fdiv_rn(a, 448.0f);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int tok = (lane >> 1) + 16 * j, off = (lane & 1) * 16;
+                                const uint4 q = *reinterpret_cast<const uint4 *>(buf8 + tok * 32 + off);
+                                if (tok < tokens)
+                                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) + (row + tok) * width + wc + off) = q;
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < SLOTS; ++s) {
+                        const int c = 2 * s + hw;
+                        if (c >= chunks) continue;
+                        if constexpr (S::WG)
+                            store_rows<true>(acc[s], out, lane,
+                                             static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + ti.c0 + c * 32,
+                                             p.k, p.n - wc, p.k - ti.c0 - c * 32, p.accumulate != 0);
+                        else
+                            store_tokens(acc[s], out, lane,
+                                         static_cast<__nv_bfloat16 *>(p.y) + (ti.row0 + c * 32) * p.n + wc, p.n,
+                                         ti.valid - c * 32, p.n - wc);
                     }
                 }
             }
         }
     }
+    if (!ok) atomicOr(p.status, kStatusTimeout);
+    __syncwarp();
+    fence_before();
+    cluster_sync();
+    fence_after();
+    if (warp == kWarpMma) tmem_free(tmem, 512);
 }
 
-template <ExpertOp OP>
+// ------------------------------------------------------------ host side
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+    static std::atomic<void *> fn{nullptr};
+    void *f = fn.load(std::memory_order_acquire);
+    if (f == nullptr) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeTiled>(f);
+}
+
+// A row-major matrix [rows, cols] (or [planes, rows, cols]) read in boxes of
+// box_rows rows by 128 bytes.
+bool encode(CUtensorMap *m, const void *base, bool fp8, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
+    const EncodeTiled fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t es = fp8 ? 1 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * es, (cuuint64_t)cols * es * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2,
+              const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <ExpertOp OP, bool F32>
+size_t smem_bytes(int E) {
+    return Shape<OP, F32>::fixed + (Shape<OP, F32>::WG ? 0 : ((size_t)E + 1) * 4);
+}
+
+template <ExpertOp OP, bool F32>
 cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
-    const int nd = OP == ExpertOp::kWgrad ? p.k : (OP == ExpertOp::kGateFp8 ? p.n / 2 : p.n);
-    const int64_t md = OP == ExpertOp::kWgrad ? p.n : p.max_count;
-    int64_t my = (md + kBM - 1) / kBM;
-    if (my > 64) my = 64;
-    if (my < 1) my = 1;
-    expert_gemm_plain<OP><<<dim3((nd + kBN - 1) / kBN, (unsigned)my, p.E), kT, 0, stream>>>(p);
-    return cudaGetLastError();
+    using S = Shape<OP, F32>;
+    Maps maps;
+    bool ok;
+    if constexpr (S::WG) {
+        ok = encode(&maps.m[0], p.dy, false, p.n, p.rows, 0, 64) && encode(&maps.m[1], p.x, false, p.k, p.rows, 0, 64);
+    } else {
+        ok = S::A_MN ? encode(&maps.m[0], p.w, S::FP8, p.n, p.k, p.E, 64) : encode(&maps.m[0], p.w, S::FP8, p.k, p.n, p.E, 128);
+        for (int i = 0; i < 4 && ok; ++i) ok = encode(&maps.m[1 + i], p.x, S::FP8, p.k, p.rows, 0, 128 >> i);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    static std::atomic<bool> ready{false};
+    if (!ready.load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(expert_gemm_kernel<OP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
+        if (e != cudaSuccess) return e;
+        ready.store(true, std::memory_order_release);
+    }
+    int pairs = p.sms / 2;
+    if (pairs < 1) pairs = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem_bytes<OP, F32>(p.E);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<OP, F32>, maps, p);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream) {
     switch (op) {
-        case ExpertOp::kBf16: return launch<ExpertOp::kBf16>(p, stream);
-        case ExpertOp::kBf16T: return launch<ExpertOp::kBf16T>(p, stream);
-        case ExpertOp::kFp8: return launch<ExpertOp::kFp8>(p, stream);
-        case ExpertOp::kGateFp8: return launch<ExpertOp::kGateFp8>(p, stream);
-        default: return launch<ExpertOp::kWgrad>(p, stream);
+        case ExpertOp::kBf16: return launch<ExpertOp::kBf16, false>(p, stream);
+        case ExpertOp::kBf16T: return launch<ExpertOp::kBf16T, false>(p, stream);
+        case ExpertOp::kFp8: return launch<ExpertOp::kFp8, false>(p, stream);
+        case ExpertOp::kGateFp8: return launch<ExpertOp::kGateFp8, false>(p, stream);
+        default: return p.out_fp32 ? launch<ExpertOp::kWgrad, true>(p, stream) : launch<ExpertOp::kWgrad, false>(p, stream);
     }
 }
 
