@@ -320,8 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             bar_expect(b_land + 8 * st, bytes);
                         } else if (rank == 0) {
                             bar_expect(b_full + 8 * st, 2 * bytes);
-                        } else {
-                            bar_arrive_cluster(full0);
+                            bar_arrive(b_full + 8 * st);  // for the other CTA
                         }
                         const int r = (int)(ti.row0 + kb * 64);
                         const int n0 = ti.w0 + (int)rank * 128, c0 = ti.c0 + (int)rank * half;
@@ -380,6 +379,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (!(ok = bar_wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1))) break;
                     }
                     if (!(ok = bar_wait(b_full + 8 * st, ph))) break;
+                    if constexpr (S::WG) {
+                        if (kb == nk - 1) fence_acquire_cluster();  // the cleared lines of both CTAs
+                    }
                     fence_after();
                     const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
                     const uint32_t d = tmem + buf * 256;
@@ -505,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (nk > 0) {
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive_cluster(tempty0 + 8 * buf);
+                    if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                     ++seg;
                 }
             } else {
@@ -554,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive_cluster(tempty0 + 8 * buf);
+                    if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                     if constexpr (S::FP8) {
                         if (k % kScaleGroup == kScaleGroup - 1 || k == nseg - 1) {
                             if (lane == 0) bar_arrive(b_sempty + 8 * (fill & 1));

@@ -45,26 +45,42 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on a barrier anywhere in the cluster (address from map_rank).
+// Arrive on a barrier anywhere in the cluster (address from map_rank).  No
+// generic writes are published to the other CTA: what it orders are tensor
+// memory reads, by their own fences.
+__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same, publishing this thread's writes to the cluster.  A release at
+// cluster scope waits for everything the thread has in flight, so it stays out
+// of the loops (wgrad with one per stage: 700 instead of 1380 TFLOP/s).
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
-// Bounded wait for the phase with this parity; false when it gave up.
+__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// Bounded wait for the phase with this parity; false when it gave up.  The
+// clock is read every 1024 polls only: a read costs more than a poll.
 constexpr uint64_t kWaitNs = 2000000000ull;
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     if (bar_try(bar, parity)) return true;
-    const uint64_t t0 = now_ns();
-    while (!bar_try(bar, parity))
-        if (now_ns() - t0 > kWaitNs) return false;
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; !bar_try(bar, parity); ++n) {
+        if ((n & 1023) != 0) continue;
+        const uint64_t t = now_ns();
+        if (t0 == 0)
+            t0 = t;
+        else if (t - t0 > kWaitNs)
+            return false;
+    }
     return true;
 }
 
