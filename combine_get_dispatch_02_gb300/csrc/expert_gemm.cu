@@ -45,8 +45,11 @@ namespace {
 using namespace umma;
 
 constexpr int kEpiWarps = 8;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpAux = 10;
-constexpr int kThreads = 11 * 32;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpAux = 10, kWarpTiles = 11;
+constexpr int kThreads = 12 * 32;
+// registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72
+constexpr int kRegsRead = 216, kRegsRest = 72;
+constexpr int kTileRing = 4;      // tiles looked up ahead
 constexpr int kTileW = 256;       // weight rows of a pair's tile
 constexpr int kScaleGroup = 4;    // 128-channel blocks per fill of the scale buffer
 constexpr int kMaxSmem = 232448;
@@ -68,10 +71,10 @@ struct Shape {
     static constexpr int A_BYTES = GATE ? 32768 : 16384;  // per CTA and stage
     static constexpr int B_BYTES = NMAX / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = WG && F32 ? 4096 : (GATE ? 1024 : 2048);  // per reading warp
-    static constexpr int STAGES = (WG && F32) || GATE ? 5 : 6;
+    static constexpr int OUT_BYTES = GATE ? 1024 : (WG && F32) || OP == ExpertOp::kFp8 ? 4096 : 2048;  // per reading warp
+    static constexpr int STAGES = OP == ExpertOp::kBf16 || OP == ExpertOp::kBf16T || (WG && !F32) ? 6 : 5;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
-    static constexpr int AMAX = GATE ? 2 * 2 * 4 * 32 * 4 : 0;
+    static constexpr int AMAX = GATE ? 2 * 2 * 4 * 64 * 4 : 0;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
     static constexpr int KSTEP = FP8 ? 128 : 64;
     // stages per segment; 0: all of them
@@ -79,19 +82,20 @@ struct Shape {
     static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE + kEpiWarps * OUT_BYTES + SCALES + AMAX;
 };
 
-struct Bars {
-    uint64_t full[6], empty[6], land[6];
-    uint64_t tfull[2], tempty[2], sfull[2], sempty[2];
-    uint32_t tmem;
-};
-
 struct Tile {
-    int e;
     int64_t row0;   // first receive row (wgrad: of the expert)
+    int e;
     int valid;      // rows (wgrad: all rows of the expert)
     int nt;         // columns of the products, a multiple of 32
     int w0;         // first weight row of the pair (gate: channel of h)
     int c0;         // wgrad: first column (channel of x)
+};
+
+struct Bars {
+    uint64_t full[6], empty[6], land[6];
+    uint64_t tfull[2], tempty[2], sfull[2], sempty[2], kfull[kTileRing], kempty[kTileRing];
+    Tile tiles[kTileRing];
+    uint32_t tmem;
 };
 
 // Tile number t.  before[e]: token tiles of the experts before e.
@@ -134,6 +138,17 @@ __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *be
     }
     return r;
 }
+
+// Place of a column's scale in a block's 256: a thread of the fragment layout
+// needs the columns 8 j + 2 (T % 4) + {0, 1} of 64, so they lie together (16
+// floats), in 16-byte pieces swapped so that the four threads' reads of a piece
+// fall into different banks.
+__device__ __forceinline__ int scale_at(int col) {
+    const int c = (col & 7) >> 1, j = (col & 63) >> 3;
+    return (col & ~63) + c * 16 + (((j >> 1) ^ (c >> 1)) << 2) + ((j & 1) << 1) + (col & 1);
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -238,6 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t b_full = saddr(bars.full), b_empty = saddr(bars.empty), b_land = saddr(bars.land);
     const uint32_t b_tfull = saddr(bars.tfull), b_tempty = saddr(bars.tempty);
     const uint32_t b_sfull = saddr(bars.sfull), b_sempty = saddr(bars.sempty);
+    const uint32_t b_kfull = saddr(bars.kfull), b_kempty = saddr(bars.kempty);
 
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
@@ -250,6 +266,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bar_init(b_tempty + 8 * i, 2 * kEpiWarps);
             bar_init(b_sfull + 8 * i, 1);
             bar_init(b_sempty + 8 * i, kEpiWarps);
+        }
+        for (int i = 0; i < kTileRing; ++i) {
+            bar_init(b_kfull + 8 * i, 1);
+            // readers: the reading warps, the loader, the first CTA's product thread, the auxiliary warp
+            bar_init(b_kempty + 8 * i, kEpiWarps + 1 + (rank == 0 ? 1 : 0) + (S::FP8 || S::WG ? 1 : 0));
         }
         bar_init_fence();
         for (int i = 0; i < (S::WG ? 2 : 5); ++i) prefetch_map(&maps.m[i]);
@@ -297,14 +318,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int kchan = (p.k + S::KSTEP - 1) / S::KSTEP;  // stages of a tile (wgrad: by the expert's rows)
     auto stages_of = [&](const Tile &ti) { return S::WG ? (ti.valid + 63) / 64 : kchan; };
     bool ok = true;
-
-    if (warp == kWarpLoad) {
+    // The i-th tile of this pair (whole warps, or one thread of a role).
+    auto next_tile = [&](Tile &ti, int i, bool whole_warp) {
+        const int s = i % kTileRing;
+        ok = bar_wait(b_kfull + 8 * s, (i / kTileRing) & 1);
+        if (whole_warp) ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return false;
+        ti = bars.tiles[s];
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) bar_arrive(b_kempty + 8 * s);
+        return true;
+    };
+    if (warp >= kEpiWarps) {
+    regs_dec<kRegsRest>();
+    if (warp == kWarpTiles) {
+        // looks the tiles up ahead of the others (a search, divisions and two loads from L2)
+        if (lane == 0) {
+            int i = 0;
+            for (int t = pair; t < total; t += pairs, ++i) {
+                const int s = i % kTileRing;
+                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+                if (!(ok = bar_wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
+                bars.tiles[s] = ti;
+                bar_arrive(b_kfull + 8 * s);
+            }
+        }
+    } else if (warp == kWarpLoad) {
         if (lane == 0) {
             int st = 0;
             uint32_t ph = 0;
             int used = 0;
-            for (int t = pair; t < total && ok; t += pairs) {
-                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+            Tile ti;
+            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
+                if (!next_tile(ti, i, false)) break;
                 const int nk = stages_of(ti);
                 const int half = ti.nt >> 1;
                 const uint32_t bytes = S::A_BYTES + half * 128;
@@ -368,8 +414,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0 && lane == 0) {
             int st = 0;
             uint32_t ph = 0, seg = 0;
-            for (int t = pair; t < total && ok; t += pairs) {
-                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+            Tile ti;
+            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
+                if (!next_tile(ti, i, false)) break;
                 const int nk = stages_of(ti);
                 const uint32_t id = idesc(S::FP8, S::A_MN, S::B_MN, ti.nt);
                 for (int kb = 0; kb < nk; ++kb) {
@@ -409,34 +456,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // scales of a tile's columns, xs * ws, for kScaleGroup blocks at a time
             const int nb = (p.n + 127) / 128;
             uint32_t fill = 0;
-            for (int t = pair; t < total && ok; t += pairs) {
-                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+            Tile ti;
+            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
+                if (!next_tile(ti, i, true)) break;
                 const int wb = ti.w0 / 128 + (int)rank;
                 const float *ws = p.ws + ((int64_t)ti.e * nb + min(wb, nb - 1)) * kchan;
                 const float *wu = S::GATE ? p.ws + ((int64_t)ti.e * nb + min(wb + width / 128, nb - 1)) * kchan : ws;
                 for (int g = 0; g < kchan; g += kScaleGroup, ++fill) {
                     const uint32_t buf = fill & 1;
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
-                    if (!ok) break;
-                    float *out = scales + buf * kScaleGroup * 256;
+                    // every load first: the buffer is waited for while they are in flight
+                    float4 x[S::NMAX / 32];
+#pragma unroll
+                    for (int j0 = 0; j0 < S::NMAX; j0 += 32) {
+                        const int j = j0 + lane;
+                        const float *xs = p.xs + (ti.row0 + j) * kchan + g;
+                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (j < ti.valid) {
+                            if (p.xs_vec) {
+                                v = __ldg(reinterpret_cast<const float4 *>(xs));
+                            } else {
+                                v.x = __ldg(xs);
+                                if (g + 1 < kchan) v.y = __ldg(xs + 1);
+                                if (g + 2 < kchan) v.z = __ldg(xs + 2);
+                                if (g + 3 < kchan) v.w = __ldg(xs + 3);
+                            }
+                        }
+                        x[j0 / 32] = v;
+                    }
                     float w[kScaleGroup], w2[kScaleGroup];
 #pragma unroll
                     for (int q = 0; q < kScaleGroup; ++q) {
                         w[q] = g + q < kchan ? __ldg(ws + g + q) : 0.0f;
                         w2[q] = S::GATE && g + q < kchan ? __ldg(wu + g + q) : 0.0f;
                     }
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
+                    if (!ok) break;
+                    float *out = scales + buf * kScaleGroup * 256;
 #pragma unroll
                     for (int j0 = 0; j0 < S::NMAX; j0 += 32) {
-                        if (j0 >= ti.nt) break;
-                        const int j = j0 + lane;
-                        const float *xs = p.xs + (ti.row0 + j) * kchan + g;
-                        float x[kScaleGroup];
-#pragma unroll
-                        for (int q = 0; q < kScaleGroup; ++q) x[q] = j < ti.valid && g + q < kchan ? __ldg(xs + q) : 0.0f;
-#pragma unroll
-                        for (int q = 0; q < kScaleGroup; ++q) {
-                            out[q * 256 + j] = x[q] * w[q];
-                            if constexpr (S::GATE) out[q * 256 + 128 + j] = x[q] * w2[q];
+                        const int at = scale_at(j0 + lane);
+                        const float4 v = x[j0 / 32];
+                        out[at] = v.x * w[0];
+                        out[256 + at] = v.y * w[1];
+                        out[512 + at] = v.z * w[2];
+                        out[768 + at] = v.w * w[3];
+                        if constexpr (S::GATE) {
+                            out[128 + at] = v.x * w2[0];
+                            out[384 + at] = v.y * w2[1];
+                            out[640 + at] = v.z * w2[2];
+                            out[896 + at] = v.w * w2[3];
                         }
                     }
                     __syncwarp();
@@ -448,8 +516,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // hold one 128-byte line per row and 64 channels), up to the 16 rows of a product
             int st = 0;
             uint32_t landed = 0;  // parity of each stage's landing barrier
-            for (int t = pair; t < total && ok; t += pairs) {
-                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+            Tile ti;
+            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
+                if (!next_tile(ti, i, true)) break;
                 const int nk = stages_of(ti);
                 if ((ti.valid & 63) != 0) {
                     const int s = (st + nk - 1) % S::STAGES;
@@ -470,14 +539,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 st = (st + nk) % S::STAGES;
             }
         }
+    }
     } else {
+        regs_inc<kRegsRead>();
         const int sub = warp & 3, hw = warp >> 2;  // lanes 32 * sub .., every second chunk of 32 columns
         const uint32_t lanes = tmem + ((uint32_t)(sub * 32) << 16);
         const uint32_t out = saddr(outs + warp * S::OUT_BYTES);
         const uint32_t tempty0 = map_rank(b_tempty, 0);
         uint32_t seg = 0, fill = 0, turn = 0;
-        for (int t = pair; t < total && ok; t += pairs) {
-            const Tile ti = tile_at<OP>(p, before, t, wtiles);
+        Tile ti;
+        for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
+            if (!next_tile(ti, i, true)) break;
             const int nk = stages_of(ti);
             const int chunks = ti.nt >> 5;
             const int wc = ti.w0 + (int)rank * 128 + sub * 32;  // the warp's first weight row / channel of h
@@ -510,118 +582,206 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                     ++seg;
                 }
-            } else {
-                // sums over segments in registers: chunk 2 s + hw of the columns (gate: 2
-                // chunks of the gate's columns, then 2 of the up product's)
-                constexpr int SLOTS = 4;
-                float acc[SLOTS][32];
+            } else if constexpr (S::FP8) {
+                // Fragments of 64 columns: chunks hw and hw + 2 (gate: the gate's and the up
+                // product's columns of the same tokens), each as lanes 0-15 and 16-31 of the warp.
+                // acc[2 * slot + half][2 j + r]: columns 8 j + 2 (lane % 4) + {0, 1}, weight row
+                // 16 * half + 8 * r + lane / 4.
+                uint64_t acc[4][16];
 #pragma unroll
-                for (int s = 0; s < SLOTS; ++s)
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[s][i] = 0.0f;
-                const int nseg = (nk + S::SEG - 1) / S::SEG;
-                for (int k = 0; k < nseg; ++k, ++seg) {
+                    for (int i2 = 0; i2 < 16; ++i2) acc[q][i2] = 0;
+                const int live = S::GATE ? (hw * 64 < ti.nt ? 4 : 0) : (hw * 64 < ti.nt ? 2 : 0) + ((hw + 2) * 64 < ti.nt ? 2 : 0);
+                const int c4 = lane & 3;
+                for (int k = 0; k < nk; ++k, ++seg) {
                     const uint32_t buf = seg & 1;
-                    if constexpr (S::FP8) {
-                        if (k % kScaleGroup == 0) {
-                            ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
-                            if (!ok) break;
-                        }
+                    if (k % kScaleGroup == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
+                        if (!ok) break;
                     }
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
-                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256;
+                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256 + hw * 64 + c4 * 16;
+                    const uint32_t at = lanes + buf * 256 + hw * 64;
+                    // the next quarter is on its way while one is added up
+                    uint32_t v[2][32];
+                    uint64_t f[8];
+                    if (live > 0) tmem_ld_frag(v[0], at);
 #pragma unroll
-                    for (int s = 0; s < SLOTS; ++s) {
-                        const int c = S::GATE ? 2 * (s & 1) + hw : 2 * s + hw;
-                        if (c >= chunks) continue;
-                        const int col = c * 32 + (S::GATE && s >= 2 ? 128 : 0);
-                        float v[32];
-                        tmem_ld32(v, lanes + buf * 256 + col);
-                        tmem_wait_ld();
-                        if constexpr (S::FP8) {
+                    for (int q = 0; q < 4; ++q) {
+                        if (q >= live) break;
+                        if ((q & 1) == 0) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(sc + col + i);
-                                acc[s][i] = fmaf(v[i], f.x, acc[s][i]);
-                                acc[s][i + 1] = fmaf(v[i + 1], f.y, acc[s][i + 1]);
-                                acc[s][i + 2] = fmaf(v[i + 2], f.z, acc[s][i + 2]);
-                                acc[s][i + 3] = fmaf(v[i + 3], f.w, acc[s][i + 3]);
+                            for (int m = 0; m < 4; ++m) {
+                                const float4 g = *reinterpret_cast<const float4 *>(sc + (q >> 1) * 128 + ((m ^ (c4 >> 1)) << 2));
+                                f[2 * m] = pair2(__float_as_uint(g.x), __float_as_uint(g.y));
+                                f[2 * m + 1] = pair2(__float_as_uint(g.z), __float_as_uint(g.w));
                             }
-                        } else {
+                        }
+                        tmem_wait_ld();
+                        if (q + 1 < 4 && q + 1 < live)
+                            tmem_ld_frag(v[(q + 1) & 1], at + ((q + 1) >> 1) * 128 + (((q + 1) & 1) << 20));
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) acc[s][i] += v[i];
+                        for (int j = 0; j < 8; ++j) {
+                            acc[q][2 * j] = fma2(pair2(v[q & 1][4 * j], v[q & 1][4 * j + 1]), f[j], acc[q][2 * j]);
+                            acc[q][2 * j + 1] = fma2(pair2(v[q & 1][4 * j + 2], v[q & 1][4 * j + 3]), f[j], acc[q][2 * j + 1]);
                         }
                     }
                     fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
-                    if constexpr (S::FP8) {
-                        if (k % kScaleGroup == kScaleGroup - 1 || k == nseg - 1) {
-                            if (lane == 0) bar_arrive(b_sempty + 8 * (fill & 1));
-                            ++fill;
-                        }
+                    if (k % kScaleGroup == kScaleGroup - 1 || k == nk - 1) {
+                        if (lane == 0) bar_arrive(b_sempty + 8 * (fill & 1));
+                        ++fill;
                     }
                 }
                 if (!ok) break;
                 if constexpr (S::GATE) {
+                    const int h0 = ti.w0 + (int)rank * 128;
+                    if (live > 0) {  // the same for the 4 warps of this half
+                        // h in place of the gate's sums, and each column's maximum over the warp's 32 channels
+                        float top[16];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        const int c = 2 * s + hw;
-                        if (c >= chunks) continue;  // the same for the 4 warps of this half
-                        float mine = 0.0f;
+                        for (int j = 0; j < 8; ++j) {
+                            float m0 = 0.0f, m1 = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float g = acc[s][i];
-                            const float h = __fdiv_rn(g, 1.0f + expf(-g)) * acc[s + 2][i];
-                            acc[s][i] = h;
-                            // non-negative floats order like their bits; a NaN counts as 0
-                            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fmaxf(fabsf(h), 0.0f)));
-                            if (lane == i) mine = __uint_as_float(m);
+                            for (int r = 0; r < 4; ++r) {
+                                uint64_t &g = acc[r >> 1][2 * j + (r & 1)];
+                                const uint64_t u = acc[2 + (r >> 1)][2 * j + (r & 1)];
+                                const float a0 = swiglu(lo2(g), lo2(u)), a1 = swiglu(hi2(g), hi2(u));
+                                g = pair2(__float_as_uint(a0), __float_as_uint(a1));
+                                m0 = fmaxf(m0, fabsf(a0));
+                                m1 = fmaxf(m1, fabsf(a1));
+                            }
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) {
+                                m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
+                                m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
+                            }
+                            top[2 * j] = m0;
+                            top[2 * j + 1] = m1;
                         }
-                        float *am = amaxs + ((turn & 1) * 2 + hw) * 128;
+                        // over the block's 128 channels: the four warps of this half
+                        float *am = amaxs + ((turn & 1) * 2 + hw) * 256;
                         ++turn;
-                        am[sub * 32 + lane] = mine;
+                        if (lane < 4) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                *reinterpret_cast<float2 *>(am + sub * 64 + 8 * j + 2 * lane) = make_float2(top[2 * j], top[2 * j + 1]);
+                        }
                         asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
-                        const float a = fmaxf(fmaxf(fmaxf(am[lane], am[32 + lane]), fmaxf(am[64 + lane], am[96 + lane])), 1e-4f);
-                        const float inv = __fdiv_rn(448.0f, a);
-                        const int tokens = ti.valid - c * 32;
-                        const int h0 = ti.w0 + (int)rank * 128;
-                        const int64_t row = ti.row0 + c * 32;
+                        const int tokens = ti.valid - hw * 64;
+                        const int64_t row = ti.row0 + hw * 64;
                         uint8_t *buf8 = outs + warp * S::OUT_BYTES;
-                        __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            buf8[i * 32 + lane] = __nv_cvt_float_to_fp8(
-                                __fmul_rn(acc[s][i], __shfl_sync(0xFFFFFFFFu, inv, i)), __NV_SATFINITE, __NV_E4M3);
-                        __syncwarp();
-                        if (h0 < width) {
-                            if (sub == 0 && lane < tokens)
-                                p.ys[(row + lane) * (width / 128) + h0 / 128] = __fdiv_rn(a, 448.0f);
+                        for (int part = 0; part < 2; ++part) {  // 32 tokens at a time
+                            __syncwarp();
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int tok = (lane >> 1) + 16 * j, off = (lane & 1) * 16;
-                                const uint4 q = *reinterpret_cast<const uint4 *>(buf8 + tok * 32 + off);
-                                if (tok < tokens)
-                                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) + (row + tok) * width + wc + off) = q;
+                            for (int j = 4 * part; j < 4 * part + 4; ++j) {
+                                const int col = 8 * j + 2 * c4;
+                                float2 a = make_float2(1e-4f, 1e-4f);
+#pragma unroll
+                                for (int w = 0; w < 4; ++w) {
+                                    const float2 o = *reinterpret_cast<const float2 *>(am + w * 64 + col);
+                                    a.x = fmaxf(a.x, o.x);
+                                    a.y = fmaxf(a.y, o.y);
+                                }
+                                const float i0 = __fdiv_rn(448.0f, a.x), i1 = __fdiv_rn(448.0f, a.y);
+                                uint8_t *at = buf8 + (col - 32 * part) * 32 + (lane >> 2);
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) {
+                                    const uint64_t g = acc[r >> 1][2 * j + (r & 1)];
+                                    at[8 * r] = __nv_cvt_float_to_fp8(__fmul_rn(lo2(g), i0), __NV_SATFINITE, __NV_E4M3);
+                                    at[8 * r + 32] = __nv_cvt_float_to_fp8(__fmul_rn(hi2(g), i1), __NV_SATFINITE, __NV_E4M3);
+                                }
+                                if (sub == 0 && lane < 4 && h0 < width) {
+                                    float *ys = p.ys + (row + col) * (width / 128) + h0 / 128;
+                                    if (col < tokens) ys[0] = __fdiv_rn(a.x, 448.0f);
+                                    if (col + 1 < tokens) ys[width / 128] = __fdiv_rn(a.y, 448.0f);
+                                }
+                            }
+                            __syncwarp();
+                            if (h0 < width) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const int tok = (lane >> 1) + 16 * j, off = (lane & 1) * 16;
+                                    const uint4 q = *reinterpret_cast<const uint4 *>(buf8 + tok * 32 + off);
+                                    if (tok + 32 * part < tokens)
+                                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) +
+                                                                   (row + 32 * part + tok) * width + wc + off) = q;
+                                }
                             }
                         }
                     }
                 } else {
 #pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (2 * s >= live) break;
+                        const int c0 = (hw + 2 * s) * 64;
+                        // 64 tokens x 32 channels as bf16, 64 bytes per token, 16-byte pieces swapped
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            // the four 8-channel blocks of 8 tokens: rows of the transposed store are tokens
+                            uint32_t h[4];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const uint64_t g = acc[2 * s + (r >> 1)][2 * j + (r & 1)];
+                                h[r] = bf16x2(lo2(g), hi2(g));
+                            }
+                            const int tok = 8 * j + (lane & 7), piece = lane >> 3;
+                            stm_x4_trans(out + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4), h[0], h[1], h[2], h[3]);
+                        }
+                        __syncwarp();
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.y) + (ti.row0 + c0) * p.n + wc;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int tok = (lane >> 2) + 8 * j, piece = lane & 3;
+                            const uint4 q = *reinterpret_cast<const uint4 *>(
+                                outs + warp * S::OUT_BYTES + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4));
+                            if (tok < ti.valid - c0 && piece * 8 < p.n - wc)
+                                *reinterpret_cast<uint4 *>(dst + (int64_t)tok * p.n + piece * 8) = q;
+                        }
+                    }
+                }
+            } else {
+                // wgrad in fp32: sums of 256 rows added up in registers, chunk 2 s + hw of the columns
+                constexpr int SLOTS = 4;
+                float acc[SLOTS][32];
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+                    for (int i2 = 0; i2 < 32; ++i2) acc[s][i2] = 0.0f;
+                const int nseg = (nk + S::SEG - 1) / S::SEG;
+                for (int k = 0; k < nseg; ++k, ++seg) {
+                    const uint32_t buf = seg & 1;
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+#pragma unroll
                     for (int s = 0; s < SLOTS; ++s) {
                         const int c = 2 * s + hw;
                         if (c >= chunks) continue;
-                        if constexpr (S::WG)
-                            store_rows<true>(acc[s], out, lane,
-                                             static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + ti.c0 + c * 32,
-                                             p.k, p.n - wc, p.k - ti.c0 - c * 32, p.accumulate != 0);
-                        else
-                            store_tokens(acc[s], out, lane,
-                                         static_cast<__nv_bfloat16 *>(p.y) + (ti.row0 + c * 32) * p.n + wc, p.n,
-                                         ti.valid - c * 32, p.n - wc);
+                        float v[32];
+                        tmem_ld32(v, lanes + buf * 256 + c * 32);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i2 = 0; i2 < 32; ++i2) acc[s][i2] += v[i2];
                     }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int s = 0; s < SLOTS; ++s) {
+                    const int c = 2 * s + hw;
+                    if (c >= chunks) continue;
+                    store_rows<true>(acc[s], out, lane,
+                                     static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + ti.c0 + c * 32, p.k,
+                                     p.n - wc, p.k - ti.c0 - c * 32, p.accumulate != 0);
                 }
             }
         }
@@ -675,6 +835,8 @@ size_t smem_bytes(int E) {
 template <ExpertOp OP, bool F32>
 cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     using S = Shape<OP, F32>;
+    ExpertGemmParams q = p;
+    q.xs_vec = p.k % (4 * 128) == 0 && (uintptr_t)p.xs % 16 == 0;
     Maps maps;
     bool ok;
     if constexpr (S::WG) {
@@ -703,7 +865,7 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<OP, F32>, maps, p);
+    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<OP, F32>, maps, q);
 }
 
 }  // namespace
