@@ -44,11 +44,6 @@ namespace {
 
 using namespace umma;
 
-constexpr int kEpiWarps = 8;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpAux = 10, kWarpTiles = 11;
-constexpr int kThreads = 12 * 32;
-// registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72
-constexpr int kRegsRead = 216, kRegsRest = 72;
 constexpr int kTileRing = 4;      // tiles looked up ahead
 constexpr int kTileW = 256;       // weight rows of a pair's tile
 constexpr int kScaleGroup = 4;    // 128-channel blocks per fill of the scale buffer
@@ -67,11 +62,15 @@ struct Shape {
     static constexpr bool WG = OP == ExpertOp::kWgrad;
     static constexpr bool A_MN = OP == ExpertOp::kBf16T || WG;
     static constexpr bool B_MN = WG;
+    static constexpr int READ = 8;                  // warps that read the accumulators
+    static constexpr int THREADS = (READ + 4) * 32;
+    // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72
+    static constexpr int REGS_READ = 216, REGS_REST = 72;
     static constexpr int NMAX = GATE ? 128 : 256;         // columns of a tile
     static constexpr int A_BYTES = GATE ? 32768 : 16384;  // per CTA and stage
     static constexpr int B_BYTES = NMAX / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = GATE ? 1024 : (WG && F32) || OP == ExpertOp::kFp8 ? 4096 : 2048;  // per reading warp
+    static constexpr int OUT_BYTES = GATE ? 1024 : OP == ExpertOp::kFp8 || (WG && F32) ? 4096 : 2048;  // per reading warp
     static constexpr int STAGES = OP == ExpertOp::kBf16 || OP == ExpertOp::kBf16T || (WG && !F32) ? 6 : 5;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
     static constexpr int AMAX = GATE ? 2 * 2 * 4 * 64 * 4 : 0;
@@ -79,7 +78,7 @@ struct Shape {
     static constexpr int KSTEP = FP8 ? 128 : 64;
     // stages per segment; 0: all of them
     static constexpr int SEG = FP8 ? 1 : (WG && F32 ? 4 : 0);
-    static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE + kEpiWarps * OUT_BYTES + SCALES + AMAX;
+    static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE + READ * OUT_BYTES + SCALES + AMAX;
 };
 
 struct Tile {
@@ -139,13 +138,13 @@ __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *be
     return r;
 }
 
-// Place of a column's scale in a block's 256: a thread of the fragment layout
-// needs the columns 8 j + 2 (T % 4) + {0, 1} of 64, so they lie together (16
-// floats), in 16-byte pieces swapped so that the four threads' reads of a piece
-// fall into different banks.
+// Place of a column's scale in a block's 256: a thread T of the fragment
+// layout needs the columns 4 j + T % 4 of 64, so they lie together (16 floats),
+// in 16-byte pieces swapped so that the four threads' reads of a piece fall
+// into different banks.
 __device__ __forceinline__ int scale_at(int col) {
-    const int c = (col & 7) >> 1, j = (col & 63) >> 3;
-    return (col & ~63) + c * 16 + (((j >> 1) ^ (c >> 1)) << 2) + ((j & 1) << 1) + (col & 1);
+    const int c = col & 3, j = (col & 63) >> 2;
+    return (col & ~63) + c * 16 + (((j >> 2) ^ (c >> 1)) << 2) + (j & 3);
 }
 
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
@@ -236,18 +235,19 @@ __device__ __forceinline__ void store_rows(const float (&v)[32], uint32_t buf, i
 }
 
 template <ExpertOp OP, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THREADS, 1)
     expert_gemm_kernel(const __grid_constant__ Maps maps, const ExpertGemmParams p) {
     using S = Shape<OP, F32>;
     extern __shared__ uint8_t dyn[];
     __shared__ Bars bars;
     uint8_t *const smem = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
     uint8_t *const outs = smem + S::STAGES * S::STAGE;
-    float *const scales = reinterpret_cast<float *>(outs + kEpiWarps * S::OUT_BYTES);
+    float *const scales = reinterpret_cast<float *>(outs + S::READ * S::OUT_BYTES);
     float *const amaxs = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(scales) + S::SCALES);
     int *const before = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(amaxs) + S::AMAX);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kWarpLoad = S::READ, kWarpMma = S::READ + 1, kWarpAux = S::READ + 2, kWarpTiles = S::READ + 3;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const uint32_t b_full = saddr(bars.full), b_empty = saddr(bars.empty), b_land = saddr(bars.land);
@@ -263,14 +263,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(b_tfull + 8 * i, 1);
-            bar_init(b_tempty + 8 * i, 2 * kEpiWarps);
+            bar_init(b_tempty + 8 * i, 2 * S::READ);
             bar_init(b_sfull + 8 * i, 1);
-            bar_init(b_sempty + 8 * i, kEpiWarps);
+            bar_init(b_sempty + 8 * i, S::READ);
         }
         for (int i = 0; i < kTileRing; ++i) {
             bar_init(b_kfull + 8 * i, 1);
             // readers: the reading warps, the loader, the first CTA's product thread, the auxiliary warp
-            bar_init(b_kempty + 8 * i, kEpiWarps + 1 + (rank == 0 ? 1 : 0) + (S::FP8 || S::WG ? 1 : 0));
+            bar_init(b_kempty + 8 * i, S::READ + 1 + (rank == 0 ? 1 : 0) + (S::FP8 || S::WG ? 1 : 0));
         }
         bar_init_fence();
         for (int i = 0; i < (S::WG ? 2 : 5); ++i) prefetch_map(&maps.m[i]);
@@ -279,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_wait();  // the layout, the rows and possibly the weights come from kernels queued before
     // token tiles of the experts before each one
     if constexpr (!S::WG) {
-        for (int e = tid; e < p.E; e += kThreads) before[e + 1] = (__ldg(p.count + e) + S::NMAX - 1) / S::NMAX;
+        for (int e = tid; e < p.E; e += S::THREADS) before[e + 1] = (__ldg(p.count + e) + S::NMAX - 1) / S::NMAX;
         if (tid == 0) before[0] = 0;
         __syncthreads();
         if (warp == 0) {
@@ -329,8 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!whole_warp || lane == 0) bar_arrive(b_kempty + 8 * s);
         return true;
     };
-    if (warp >= kEpiWarps) {
-    regs_dec<kRegsRest>();
+    if (warp >= S::READ) {
+    regs_dec<S::REGS_REST>();
     if (warp == kWarpTiles) {
         // looks the tiles up ahead of the others (a search, divisions and two loads from L2)
         if (lane == 0) {
@@ -541,7 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     } else {
-        regs_inc<kRegsRead>();
+        regs_inc<S::REGS_READ>();
         const int sub = warp & 3, hw = warp >> 2;  // lanes 32 * sub .., every second chunk of 32 columns
         const uint32_t lanes = tmem + ((uint32_t)(sub * 32) << 16);
         const uint32_t out = saddr(outs + warp * S::OUT_BYTES);
@@ -564,8 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int c = hw; c < chunks; c += 2) {
                     float v[32];
                     if (nk > 0) {
-                        tmem_ld32(v, lanes + buf * 256 + c * 32);
-                        tmem_wait_ld();
+                        tmem_get32(v, lanes + buf * 256 + c * 32);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.0f;
@@ -583,17 +582,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ++seg;
                 }
             } else if constexpr (S::FP8) {
-                // Fragments of 64 columns: chunks hw and hw + 2 (gate: the gate's and the up
-                // product's columns of the same tokens), each as lanes 0-15 and 16-31 of the warp.
-                // acc[2 * slot + half][2 j + r]: columns 8 j + 2 (lane % 4) + {0, 1}, weight row
-                // 16 * half + 8 * r + lane / 4.
+                // Fragments of 64 columns: columns 64 hw and 64 hw + 128 on (gate: the gate's and
+                // the up product's columns of the same tokens), each as lanes 0-15 and 16-31.
+                // acc[2 * piece + half][j]: column 4 j + lane % 4, weight rows
+                // 16 * half + lane / 4 + {0, 8}.
+                const int col0 = hw * 64;
+                const int live = S::GATE ? (col0 < ti.nt ? 4 : 0) : (col0 < ti.nt ? 2 : 0) + (col0 + 128 < ti.nt ? 2 : 0);
+                const int c4 = lane & 3;
                 uint64_t acc[4][16];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int i2 = 0; i2 < 16; ++i2) acc[q][i2] = 0;
-                const int live = S::GATE ? (hw * 64 < ti.nt ? 4 : 0) : (hw * 64 < ti.nt ? 2 : 0) + ((hw + 2) * 64 < ti.nt ? 2 : 0);
-                const int c4 = lane & 3;
+                    for (int j = 0; j < 16; ++j) acc[q][j] = 0;
                 for (int k = 0; k < nk; ++k, ++seg) {
                     const uint32_t buf = seg & 1;
                     if (k % kScaleGroup == 0) {
@@ -603,30 +603,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
-                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256 + hw * 64 + c4 * 16;
-                    const uint32_t at = lanes + buf * 256 + hw * 64;
+                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256 + col0 + c4 * 16;
+                    const uint32_t at = lanes + buf * 256 + col0;
                     // the next quarter is on its way while one is added up
                     uint32_t v[2][32];
-                    uint64_t f[8];
+                    float f[16];
                     if (live > 0) tmem_ld_frag(v[0], at);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         if (q >= live) break;
                         if ((q & 1) == 0) {
 #pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const float4 g = *reinterpret_cast<const float4 *>(sc + (q >> 1) * 128 + ((m ^ (c4 >> 1)) << 2));
-                                f[2 * m] = pair2(__float_as_uint(g.x), __float_as_uint(g.y));
-                                f[2 * m + 1] = pair2(__float_as_uint(g.z), __float_as_uint(g.w));
-                            }
+                            for (int m = 0; m < 4; ++m)
+                                *reinterpret_cast<float4 *>(f + 4 * m) =
+                                    *reinterpret_cast<const float4 *>(sc + (q >> 1) * 128 + ((m ^ (c4 >> 1)) << 2));
                         }
-                        tmem_wait_ld();
+                        tmem_wait(v[q & 1]);
                         if (q + 1 < 4 && q + 1 < live)
                             tmem_ld_frag(v[(q + 1) & 1], at + ((q + 1) >> 1) * 128 + (((q + 1) & 1) << 20));
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            acc[q][2 * j] = fma2(pair2(v[q & 1][4 * j], v[q & 1][4 * j + 1]), f[j], acc[q][2 * j]);
-                            acc[q][2 * j + 1] = fma2(pair2(v[q & 1][4 * j + 2], v[q & 1][4 * j + 3]), f[j], acc[q][2 * j + 1]);
+                        for (int j = 0; j < 16; ++j) {
+                            const uint32_t g = __float_as_uint(f[j]);
+                            acc[q][j] = fma2(pair2(v[q & 1][2 * j], v[q & 1][2 * j + 1]), pair2(g, g), acc[q][j]);
                         }
                     }
                     fence_before();
@@ -638,80 +636,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!ok) break;
+                uint8_t *const own = outs + warp * S::OUT_BYTES;
                 if constexpr (S::GATE) {
                     const int h0 = ti.w0 + (int)rank * 128;
-                    if (live > 0) {  // the same for the 4 warps of this half
+                    if (live > 0) {  // the same for the 4 warps of these columns
                         // h in place of the gate's sums, and each column's maximum over the warp's 32 channels
-                        float top[16];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float m0 = 0.0f, m1 = 0.0f;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                uint64_t &g = acc[r >> 1][2 * j + (r & 1)];
-                                const uint64_t u = acc[2 + (r >> 1)][2 * j + (r & 1)];
-                                const float a0 = swiglu(lo2(g), lo2(u)), a1 = swiglu(hi2(g), hi2(u));
-                                g = pair2(__float_as_uint(a0), __float_as_uint(a1));
-                                m0 = fmaxf(m0, fabsf(a0));
-                                m1 = fmaxf(m1, fabsf(a1));
-                            }
-#pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) {
-                                m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
-                                m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
-                            }
-                            top[2 * j] = m0;
-                            top[2 * j + 1] = m1;
-                        }
-                        // over the block's 128 channels: the four warps of this half
                         float *am = amaxs + ((turn & 1) * 2 + hw) * 256;
                         ++turn;
-                        if (lane < 4) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                *reinterpret_cast<float2 *>(am + sub * 64 + 8 * j + 2 * lane) = make_float2(top[2 * j], top[2 * j + 1]);
+                        for (int j = 0; j < 16; ++j) {
+                            float m = 0.0f;
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const float a0 = swiglu(lo2(acc[r][j]), lo2(acc[2 + r][j]));
+                                const float a1 = swiglu(hi2(acc[r][j]), hi2(acc[2 + r][j]));
+                                acc[r][j] = pair2(__float_as_uint(a0), __float_as_uint(a1));
+                                m = fmaxf(m, fmaxf(fabsf(a0), fabsf(a1)));
+                            }
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                            if (lane < 4) am[sub * 64 + 4 * j + lane] = m;
                         }
+                        // over the block's 128 channels: the four warps of these columns
                         asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
-                        const int tokens = ti.valid - hw * 64;
-                        const int64_t row = ti.row0 + hw * 64;
-                        uint8_t *buf8 = outs + warp * S::OUT_BYTES;
+                        const int tokens = ti.valid - col0;
+                        const int64_t row = ti.row0 + col0;
 #pragma unroll
                         for (int part = 0; part < 2; ++part) {  // 32 tokens at a time
                             __syncwarp();
 #pragma unroll
-                            for (int j = 4 * part; j < 4 * part + 4; ++j) {
-                                const int col = 8 * j + 2 * c4;
-                                float2 a = make_float2(1e-4f, 1e-4f);
+                            for (int j = 8 * part; j < 8 * part + 8; ++j) {
+                                const int col = 4 * j + c4;
+                                float a = 1e-4f;
 #pragma unroll
-                                for (int w = 0; w < 4; ++w) {
-                                    const float2 o = *reinterpret_cast<const float2 *>(am + w * 64 + col);
-                                    a.x = fmaxf(a.x, o.x);
-                                    a.y = fmaxf(a.y, o.y);
-                                }
-                                const float i0 = __fdiv_rn(448.0f, a.x), i1 = __fdiv_rn(448.0f, a.y);
-                                uint8_t *at = buf8 + (col - 32 * part) * 32 + (lane >> 2);
+                                for (int w = 0; w < 4; ++w) a = fmaxf(a, am[w * 64 + col]);
+                                const float inv = __fdiv_rn(448.0f, a);
+                                uint8_t *at = own + (col - 32 * part) * 32 + (lane >> 2);
 #pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const uint64_t g = acc[r >> 1][2 * j + (r & 1)];
-                                    at[8 * r] = __nv_cvt_float_to_fp8(__fmul_rn(lo2(g), i0), __NV_SATFINITE, __NV_E4M3);
-                                    at[8 * r + 32] = __nv_cvt_float_to_fp8(__fmul_rn(hi2(g), i1), __NV_SATFINITE, __NV_E4M3);
+                                for (int r = 0; r < 2; ++r) {
+                                    at[16 * r] = __nv_cvt_float_to_fp8(__fmul_rn(lo2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
+                                    at[16 * r + 8] = __nv_cvt_float_to_fp8(__fmul_rn(hi2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
                                 }
-                                if (sub == 0 && lane < 4 && h0 < width) {
-                                    float *ys = p.ys + (row + col) * (width / 128) + h0 / 128;
-                                    if (col < tokens) ys[0] = __fdiv_rn(a.x, 448.0f);
-                                    if (col + 1 < tokens) ys[width / 128] = __fdiv_rn(a.y, 448.0f);
-                                }
+                                if (sub == 0 && lane < 4 && h0 < width && col < tokens)
+                                    p.ys[(row + col) * (width / 128) + h0 / 128] = __fdiv_rn(a, 448.0f);
                             }
                             __syncwarp();
-                            if (h0 < width) {
 #pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    const int tok = (lane >> 1) + 16 * j, off = (lane & 1) * 16;
-                                    const uint4 q = *reinterpret_cast<const uint4 *>(buf8 + tok * 32 + off);
-                                    if (tok + 32 * part < tokens)
-                                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) +
-                                                                   (row + 32 * part + tok) * width + wc + off) = q;
-                                }
+                            for (int j = 0; j < 2; ++j) {
+                                const int t32 = (lane >> 1) + 16 * j, tok = 32 * part + t32, off = (lane & 1) * 16;
+                                const uint4 q = *reinterpret_cast<const uint4 *>(own + t32 * 32 + off);
+                                if (h0 < width && tok < tokens)
+                                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) + (row + tok) * width + wc + off) = q;
                             }
                         }
                     }
@@ -719,19 +694,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         if (2 * s >= live) break;
-                        const int c0 = (hw + 2 * s) * 64;
+                        const int c0 = col0 + 128 * s;
                         // 64 tokens x 32 channels as bf16, 64 bytes per token, 16-byte pieces swapped
                         __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            // the four 8-channel blocks of 8 tokens: rows of the transposed store are tokens
+                            // the four 8-channel blocks of 8 tokens, stored transposed: a thread's values are
+                            // the tokens 8 j + lane % 4 and + 4, so row i of the store is token 8 j + i / 2 + 4 (i % 2)
                             uint32_t h[4];
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const uint64_t g = acc[2 * s + (r >> 1)][2 * j + (r & 1)];
-                                h[r] = bf16x2(lo2(g), hi2(g));
+                            for (int r = 0; r < 2; ++r) {
+                                const uint64_t a = acc[2 * s + r][2 * j], b = acc[2 * s + r][2 * j + 1];
+                                h[2 * r] = bf16x2(lo2(a), lo2(b));
+                                h[2 * r + 1] = bf16x2(hi2(a), hi2(b));
                             }
-                            const int tok = 8 * j + (lane & 7), piece = lane >> 3;
+                            const int i8 = lane & 7, tok = 8 * j + (i8 >> 1) + 4 * (i8 & 1), piece = lane >> 3;
                             stm_x4_trans(out + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4), h[0], h[1], h[2], h[3]);
                         }
                         __syncwarp();
@@ -739,8 +716,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const int tok = (lane >> 2) + 8 * j, piece = lane & 3;
-                            const uint4 q = *reinterpret_cast<const uint4 *>(
-                                outs + warp * S::OUT_BYTES + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4));
+                            const uint4 q = *reinterpret_cast<const uint4 *>(own + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4));
                             if (tok < ti.valid - c0 && piece * 8 < p.n - wc)
                                 *reinterpret_cast<uint4 *>(dst + (int64_t)tok * p.n + piece * 8) = q;
                         }
@@ -765,8 +741,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const int c = 2 * s + hw;
                         if (c >= chunks) continue;
                         float v[32];
-                        tmem_ld32(v, lanes + buf * 256 + c * 32);
-                        tmem_wait_ld();
+                        tmem_get32(v, lanes + buf * 256 + c * 32);
 #pragma unroll
                         for (int i2 = 0; i2 < 32; ++i2) acc[s][i2] += v[i2];
                     }
@@ -857,7 +832,7 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     if (pairs < 1) pairs = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(S::THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem_bytes<OP, F32>(p.E);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
