@@ -45,9 +45,10 @@ namespace {
 using namespace umma;
 
 constexpr int kTileRing = 4;      // tiles looked up ahead
-constexpr int kTileW = 256;       // weight rows of a pair's tile
 constexpr int kScaleGroup = 4;    // 128-channel blocks per fill of the scale buffer
 constexpr int kMaxSmem = 232448;
+// mean rows per expert from which the e4m3 products take the row form
+constexpr int kRowFormRows = 160;
 
 // Tensor maps: [0] the M-side operand, [1..4] the token rows in boxes of 128,
 // 64, 32 and 16 rows (wgrad: [1] x).
@@ -55,29 +56,38 @@ struct Maps {
     CUtensorMap m[5];
 };
 
-template <ExpertOp OP, bool F32>
+// ALT: wgrad with fp32 output; e4m3 products in row form.
+template <ExpertOp OP, bool ALT>
 struct Shape {
     static constexpr bool FP8 = OP == ExpertOp::kFp8 || OP == ExpertOp::kGateFp8;
     static constexpr bool GATE = OP == ExpertOp::kGateFp8;
     static constexpr bool WG = OP == ExpertOp::kWgrad;
+    static constexpr bool F32 = WG && ALT;
+    static constexpr bool ROW = FP8 && ALT;
+    static constexpr bool GATE_COL = GATE && !ROW;   // gate and up product as two M-side operands
     static constexpr bool A_MN = OP == ExpertOp::kBf16T || WG;
     static constexpr bool B_MN = WG;
     static constexpr int READ = 8;                  // warps that read the accumulators
     static constexpr int THREADS = (READ + 4) * 32;
     // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72
     static constexpr int REGS_READ = 216, REGS_REST = 72;
-    static constexpr int NMAX = GATE ? 128 : 256;         // columns of a tile
-    static constexpr int A_BYTES = GATE ? 32768 : 16384;  // per CTA and stage
-    static constexpr int B_BYTES = NMAX / 2 * 128;
+    static constexpr int TOKENS = GATE_COL ? 128 : 256;       // most rows of a tile
+    static constexpr int WROWS = GATE && ROW ? 128 : 256;     // weight rows (gate: channels of h) of a pair's tile
+    static constexpr int A_BYTES = GATE_COL ? 32768 : 16384;  // per CTA and stage
+    static constexpr int B_BYTES = ROW ? 16384 : TOKENS / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = GATE ? 1024 : OP == ExpertOp::kFp8 || (WG && F32) ? 4096 : 2048;  // per reading warp
-    static constexpr int STAGES = OP == ExpertOp::kBf16 || OP == ExpertOp::kBf16T || (WG && !F32) ? 6 : 5;
+    static constexpr int OUT_BYTES = GATE_COL ? 1024 : (OP == ExpertOp::kFp8 && !ROW) || F32 ? 4096 : 2048;  // per reading warp
+    static constexpr int STAGES = GATE_COL || (OP == ExpertOp::kFp8 && !ROW) || F32 ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
-    static constexpr int AMAX = GATE ? 2 * 2 * 4 * 64 * 4 : 0;
+    static constexpr int AMAX = !GATE ? 0 : ROW ? 2 * 2 * 128 * 4 : 2 * 2 * 4 * 64 * 4;
+    // e4m3: rows (of a CTA, or columns of the pair) that the scale warp serves
+    [[maybe_unused]] static constexpr int SROWS = ROW ? 128 : TOKENS;
+    // two scales per row: gate and up, or the two 128-channel blocks of a row-form tile
+    [[maybe_unused]] static constexpr bool TWO = GATE || ROW;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
     static constexpr int KSTEP = FP8 ? 128 : 64;
     // stages per segment; 0: all of them
-    static constexpr int SEG = FP8 ? 1 : (WG && F32 ? 4 : 0);
+    static constexpr int SEG = FP8 ? 1 : (F32 ? 4 : 0);
     static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE + READ * OUT_BYTES + SCALES + AMAX;
 };
 
@@ -98,16 +108,16 @@ struct Bars {
 };
 
 // Tile number t.  before[e]: token tiles of the experts before e.
-template <ExpertOp OP>
+template <ExpertOp OP, bool ALT>
 __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *before, int t, int wtiles) {
+    using S = Shape<OP, ALT>;
     Tile r;
-    constexpr bool WG = OP == ExpertOp::kWgrad;
-    if constexpr (WG) {
+    if constexpr (S::WG) {
         const int ctiles = (p.k + 255) / 256;
         const int per = wtiles * ctiles;
         r.e = t / per;
         const int local = t - r.e * per;
-        r.w0 = local / ctiles * kTileW;
+        r.w0 = local / ctiles * S::WROWS;
         r.c0 = local % ctiles * 256;
         r.row0 = __ldg(p.base + r.e);
         r.valid = __ldg(p.count + r.e);
@@ -126,14 +136,14 @@ __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *be
         const int tt = before[lo + 1] - before[lo];
         const int local = t - before[lo] * wtiles;
         const int cnt = __ldg(p.count + lo);
-        // equal token tiles, in steps of 32 rows
-        const int size = ((cnt + tt - 1) / tt + 31) & ~31;
+        // equal token tiles, in steps of 32 rows (row form: whole ones and the rest)
+        const int size = S::ROW ? S::TOKENS : ((cnt + tt - 1) / tt + 31) & ~31;
         const int r0 = local % tt * size;
-        r.w0 = local / tt * (OP == ExpertOp::kGateFp8 ? 256 : kTileW);
+        r.w0 = local / tt * S::WROWS;
         r.c0 = 0;
         r.row0 = __ldg(p.base + lo) + r0;
         r.valid = min(size, cnt - r0);
-        r.nt = (r.valid + 31) & ~31;
+        r.nt = S::ROW ? 256 : (r.valid + 31) & ~31;
     }
     return r;
 }
@@ -186,58 +196,47 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf,
     }
 }
 
-// Write 32 rows x 32 columns of a warp (lane = row, v[i] = column i): through
-// shared memory with swizzled 16-byte pieces, then whole 64- (bf16) or
-// 128-byte (fp32) row segments.
-template <bool F32>
-__device__ __forceinline__ void store_rows(const float (&v)[32], uint32_t buf, int lane, void *dst, int64_t ld, int rows,
-                                           int columns, bool accumulate) {
+// Write 32 lines of P pieces of 16 bytes (lane = line): through shared memory,
+// pieces swapped against bank conflicts, then P lanes store a line's 64 (P = 4)
+// or 128 (P = 8) bytes.  pitch: bytes from line to line of dst.  ADD: fp32
+// values added to what dst holds.
+template <int P, bool ADD = false>
+__device__ __forceinline__ void store_lines(const uint4 (&v)[P], uint32_t buf, int lane, void *dst, int64_t pitch, int lines,
+                                            int pieces) {
+    auto place = [](int line, int c) {
+        return P == 8 ? line * 128 + (c ^ (line & 7)) * 16 : line * 64 + (c ^ ((line >> 1) & 3)) * 16;
+    };
     __syncwarp();
-    constexpr int P = F32 ? 8 : 4;  // pieces of a row
 #pragma unroll
-    for (int c = 0; c < P; ++c) {
-        uint4 q;
-        int at;
-        if constexpr (F32) {
-            q = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
-                           __float_as_uint(v[4 * c + 3]));
-            at = lane * 128 + (c ^ (lane & 7)) * 16;
-        } else {
-            q = make_uint4(bf16x2(v[8 * c], v[8 * c + 1]), bf16x2(v[8 * c + 2], v[8 * c + 3]),
-                           bf16x2(v[8 * c + 4], v[8 * c + 5]), bf16x2(v[8 * c + 6], v[8 * c + 7]));
-            at = lane * 64 + (c ^ ((lane >> 1) & 3)) * 16;
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+    for (int c = 0; c < P; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + place(lane, c)), "r"(v[c].x), "r"(v[c].y),
+                     "r"(v[c].z), "r"(v[c].w)
                      : "memory");
-    }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < P; ++j) {
-        const int i = lane + 32 * j, row = i / P, c = i % P;
-        const int at = F32 ? row * 128 + (c ^ (row & 7)) * 16 : row * 64 + (c ^ ((row >> 1) & 3)) * 16;
+        const int i = lane + 32 * j, line = i / P, c = i % P;
         uint4 q;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                     : "r"(buf + at));
-        if (row >= rows || c * (F32 ? 4 : 8) >= columns) continue;
-        if constexpr (F32) {
-            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(dst) + row * ld + c * 4);
-            float4 f = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z), __uint_as_float(q.w));
-            if (accumulate) {
-                const float4 o = *d;
-                f = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
-            }
-            *d = f;
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(dst) + row * ld + c * 8) = q;
+                     : "r"(buf + place(line, c)));
+        if (line >= lines || c >= pieces) continue;
+        uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(dst) + line * pitch + c * 16);
+        if constexpr (ADD) {
+            const uint4 o = *d;
+            q.x = __float_as_uint(__uint_as_float(o.x) + __uint_as_float(q.x));
+            q.y = __float_as_uint(__uint_as_float(o.y) + __uint_as_float(q.y));
+            q.z = __float_as_uint(__uint_as_float(o.z) + __uint_as_float(q.z));
+            q.w = __float_as_uint(__uint_as_float(o.w) + __uint_as_float(q.w));
         }
+        *d = q;
     }
 }
 
-template <ExpertOp OP, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THREADS, 1)
+template <ExpertOp OP, bool ALT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THREADS, 1)
     expert_gemm_kernel(const __grid_constant__ Maps maps, const ExpertGemmParams p) {
-    using S = Shape<OP, F32>;
+    using S = Shape<OP, ALT>;
     extern __shared__ uint8_t dyn[];
     __shared__ Bars bars;
     uint8_t *const smem = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
@@ -279,7 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
     pdl_wait();  // the layout, the rows and possibly the weights come from kernels queued before
     // token tiles of the experts before each one
     if constexpr (!S::WG) {
-        for (int e = tid; e < p.E; e += S::THREADS) before[e + 1] = (__ldg(p.count + e) + S::NMAX - 1) / S::NMAX;
+        for (int e = tid; e < p.E; e += S::THREADS) before[e + 1] = (__ldg(p.count + e) + S::TOKENS - 1) / S::TOKENS;
         if (tid == 0) before[0] = 0;
         __syncthreads();
         if (warp == 0) {
@@ -312,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
     const uint32_t tmem = bars.tmem;
 
     const int width = S::GATE ? p.n / 2 : p.n;
-    const int wtiles = (width + kTileW - 1) / kTileW;
+    const int wtiles = (width + S::WROWS - 1) / S::WROWS;
     const int ctiles = (p.k + 255) / 256;
     const int total = S::WG ? p.E * wtiles * ctiles : before[p.E] * wtiles;
     const int kchan = (p.k + S::KSTEP - 1) / S::KSTEP;  // stages of a tile (wgrad: by the expert's rows)
@@ -337,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
             int i = 0;
             for (int t = pair; t < total; t += pairs, ++i) {
                 const int s = i % kTileRing;
-                const Tile ti = tile_at<OP>(p, before, t, wtiles);
+                const Tile ti = tile_at<OP, ALT>(p, before, t, wtiles);
                 if (!(ok = bar_wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
                 bars.tiles[s] = ti;
                 bar_arrive(b_kfull + 8 * s);
@@ -352,8 +351,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
             for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
                 if (!next_tile(ti, i, false)) break;
                 const int nk = stages_of(ti);
+                // rows that each CTA loads on the token side
                 const int half = ti.nt >> 1;
-                const uint32_t bytes = S::A_BYTES + half * 128;
+                const int mine = S::ROW ? min(128, max(0, (ti.valid - (int)rank * 128 + 15) & ~15)) : half;
+                const uint32_t bytes = (S::ROW ? S::B_BYTES : S::A_BYTES) + mine * 128;
+                const uint32_t both = S::ROW ? 2 * S::B_BYTES + min(256, (ti.valid + 15) & ~15) * 128 : 2 * bytes;
                 for (int kb = 0; kb < nk; ++kb) {
                     if (!(ok = bar_wait(b_empty + 8 * st, ph ^ 1))) break;
                     const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
@@ -375,21 +377,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
                         tma_2d(b, &maps.m[1], c0, r, bar);
                         if (half > 64) tma_2d(b + 8192, &maps.m[1], c0 + 64, r, bar);
                     } else {
-                        if (rank == 0) bar_expect(b_full + 8 * st, 2 * bytes);
+                        if (rank == 0) bar_expect(b_full + 8 * st, both);
                         const int kc = kb * S::KSTEP, w = ti.w0 + (int)rank * 128;
-                        if constexpr (S::A_MN) {
+                        if constexpr (S::ROW) {
+                            // gate: the first CTA's half of the columns is the gate's, the second's the up product's
+                            tma_3d(b, &maps.m[0], kc, S::GATE ? ti.w0 + (int)rank * width : w, ti.e, bar);
+                        } else if constexpr (S::A_MN) {
                             tma_3d(a, &maps.m[0], w, kc, ti.e, bar);
                             tma_3d(a + 8192, &maps.m[0], w + 64, kc, ti.e, bar);
                         } else {
                             tma_3d(a, &maps.m[0], kc, w, ti.e, bar);
                             if constexpr (S::GATE) tma_3d(a + 16384, &maps.m[0], kc, width + w, ti.e, bar);
                         }
-                        int r = (int)ti.row0 + (int)rank * half;
-                        uint32_t d = b;
+                        int r = (int)ti.row0 + (int)rank * (S::ROW ? 128 : half);
+                        uint32_t d = S::ROW ? a : b;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int h = 128 >> i;
-                            if (half & h) {
+                            if (mine & h) {
                                 tma_2d(d, &maps.m[1 + i], kc, r, bar);
                                 r += h;
                                 d += h * 128;
@@ -439,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
                         const uint64_t da = desc(a + i * (S::A_MN ? 2048 : 32), S::A_MN ? 8192 : 16);
                         const uint64_t db = desc(b + i * (S::B_MN ? 2048 : 32), S::B_MN ? 8192 : 16);
                         mma<S::FP8>(d, da, db, id, in_seg != 0 || i != 0);
-                        if constexpr (S::GATE)
+                        if constexpr (S::GATE_COL)
                             mma<S::FP8>(d + 128, desc(a + 16384 + i * 32, 16), db, id, in_seg != 0 || i != 0);
                     }
                     commit_pair(b_empty + 8 * st);
@@ -453,63 +458,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
         }
     } else if (warp == kWarpAux) {
         if constexpr (S::FP8) {
-            // scales of a tile's columns, xs * ws, for kScaleGroup blocks at a time
+            // scales of a tile's rows, xs * ws, for kScaleGroup blocks at a time; the next group's
+            // (or tile's) loads are in flight while one is stored
             const int nb = (p.n + 127) / 128;
+            struct Group {
+                float4 x[S::SROWS / 32], w, w2;
+            } cur, nxt;
             uint32_t fill = 0;
-            Tile ti;
-            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
-                if (!next_tile(ti, i, true)) break;
-                const int wb = ti.w0 / 128 + (int)rank;
-                const float *ws = p.ws + ((int64_t)ti.e * nb + min(wb, nb - 1)) * kchan;
-                const float *wu = S::GATE ? p.ws + ((int64_t)ti.e * nb + min(wb + width / 128, nb - 1)) * kchan : ws;
-                for (int g = 0; g < kchan; g += kScaleGroup, ++fill) {
-                    const uint32_t buf = fill & 1;
-                    // every load first: the buffer is waited for while they are in flight
-                    float4 x[S::NMAX / 32];
-#pragma unroll
-                    for (int j0 = 0; j0 < S::NMAX; j0 += 32) {
-                        const int j = j0 + lane;
-                        const float *xs = p.xs + (ti.row0 + j) * kchan + g;
-                        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (j < ti.valid) {
-                            if (p.xs_vec) {
-                                v = __ldg(reinterpret_cast<const float4 *>(xs));
-                            } else {
-                                v.x = __ldg(xs);
-                                if (g + 1 < kchan) v.y = __ldg(xs + 1);
-                                if (g + 2 < kchan) v.z = __ldg(xs + 2);
-                                if (g + 3 < kchan) v.w = __ldg(xs + 3);
-                            }
-                        }
-                        x[j0 / 32] = v;
+            Tile ti = {};
+            int i = 0, t = pair, g = 0;
+            auto fetch = [&](Group &o) {
+                const int r0 = S::ROW ? (int)rank * 128 : 0;
+                const int b0 = S::ROW ? ti.w0 / 128 : ti.w0 / 128 + (int)rank;
+                const int b1 = S::GATE ? b0 + width / 128 : b0 + 1;
+                auto four = [&](const float *q, bool vec) {
+                    float4 v;
+                    if (vec) {
+                        v = __ldg(reinterpret_cast<const float4 *>(q));
+                    } else {
+                        v.x = __ldg(q);
+                        v.y = g + 1 < kchan ? __ldg(q + 1) : 0.0f;
+                        v.z = g + 2 < kchan ? __ldg(q + 2) : 0.0f;
+                        v.w = g + 3 < kchan ? __ldg(q + 3) : 0.0f;
                     }
-                    float w[kScaleGroup], w2[kScaleGroup];
+                    return v;
+                };
+                const float *ws = p.ws + (int64_t)ti.e * nb * kchan + g;
+                o.w = four(ws + (int64_t)min(b0, nb - 1) * kchan, p.ws_vec);
+                if constexpr (S::TWO) o.w2 = four(ws + (int64_t)min(b1, nb - 1) * kchan, p.ws_vec);
 #pragma unroll
-                    for (int q = 0; q < kScaleGroup; ++q) {
-                        w[q] = g + q < kchan ? __ldg(ws + g + q) : 0.0f;
-                        w2[q] = S::GATE && g + q < kchan ? __ldg(wu + g + q) : 0.0f;
-                    }
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
-                    if (!ok) break;
-                    float *out = scales + buf * kScaleGroup * 256;
-#pragma unroll
-                    for (int j0 = 0; j0 < S::NMAX; j0 += 32) {
-                        const int at = scale_at(j0 + lane);
-                        const float4 v = x[j0 / 32];
-                        out[at] = v.x * w[0];
-                        out[256 + at] = v.y * w[1];
-                        out[512 + at] = v.z * w[2];
-                        out[768 + at] = v.w * w[3];
-                        if constexpr (S::GATE) {
-                            out[128 + at] = v.x * w2[0];
-                            out[384 + at] = v.y * w2[1];
-                            out[640 + at] = v.z * w2[2];
-                            out[896 + at] = v.w * w2[3];
-                        }
-                    }
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(b_sfull + 8 * buf);
+                for (int j0 = 0; j0 < S::SROWS; j0 += 32) {
+                    const int j = r0 + j0 + lane;
+                    o.x[j0 / 32] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (j < ti.valid) o.x[j0 / 32] = four(p.xs + (ti.row0 + j) * kchan + g, p.xs_vec);
                 }
+            };
+            bool more = t < total && next_tile(ti, 0, true);
+            if (more) fetch(cur);
+            while (more) {
+                // on to the next group
+                g += kScaleGroup;
+                if (g >= kchan) {
+                    g = 0;
+                    t += pairs;
+                    more = t < total && next_tile(ti, ++i, true);
+                    if (!ok) break;
+                }
+                if (more) fetch(nxt);
+                const uint32_t buf = fill & 1;
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
+                if (!ok) break;
+                float *out = scales + buf * kScaleGroup * 256;
+#pragma unroll
+                for (int j0 = 0; j0 < S::SROWS; j0 += 32) {
+                    const int at = S::ROW ? j0 + lane : scale_at(j0 + lane);
+                    const float4 v = cur.x[j0 / 32];
+                    out[at] = v.x * cur.w.x;
+                    out[256 + at] = v.y * cur.w.y;
+                    out[512 + at] = v.z * cur.w.z;
+                    out[768 + at] = v.w * cur.w.w;
+                    if constexpr (S::TWO) {
+                        out[128 + at] = v.x * cur.w2.x;
+                        out[384 + at] = v.y * cur.w2.y;
+                        out[640 + at] = v.z * cur.w2.z;
+                        out[896 + at] = v.w * cur.w2.w;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(b_sfull + 8 * buf);
+                ++fill;
+                cur = nxt;
             }
         } else if constexpr (S::WG) {
             // an expert's last rows: clear the lines past its end (both operands
@@ -569,10 +587,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0.0f;
                     }
-                    if constexpr (S::WG)
-                        store_rows<false>(v, out, lane, y + ((int64_t)ti.e * p.n + wc) * p.k + ti.c0 + c * 32, p.k,
-                                          p.n - wc, p.k - ti.c0 - c * 32, false);
-                    else
+                    if constexpr (S::WG) {
+                        uint4 line[4];
+                        uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) b4[j] = bf16x2(v[2 * j], v[2 * j + 1]);
+                        const int col = ti.c0 + c * 32;
+                        store_lines<4>(line, out, lane, y + ((int64_t)ti.e * p.n + wc) * p.k + col, (int64_t)p.k * 2, p.n - wc,
+                                       (p.k - col) / 8);
+                    } else
                         store_tokens(v, out, lane, y + (ti.row0 + c * 32) * p.n + wc, p.n, ti.valid - c * 32, p.n - wc);
                 }
                 if (nk > 0) {
@@ -580,6 +603,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
                     __syncwarp();
                     if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                     ++seg;
+                }
+            } else if constexpr (S::ROW) {
+                // The row form: lane = row, so a block's scale is one number per thread and the
+                // shape with the full rate serves.  Four chunks of 32 columns: 128 hw on (gate: the
+                // gate's and the up product's 64 hw on).
+                const int rows = ti.valid - (int)rank * 128 - sub * 32;  // of this warp
+                const int row = sub * 32 + lane;
+                uint64_t acc[4][16];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[q][j] = 0;
+                for (int k = 0; k < nk; ++k, ++seg) {
+                    const uint32_t buf = seg & 1;
+                    if (k % kScaleGroup == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
+                        if (!ok) break;
+                    }
+                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256 + row;
+                    const uint32_t s0 = __float_as_uint(sc[S::GATE ? 0 : hw * 128]), s1 = S::GATE ? __float_as_uint(sc[128]) : s0;
+                    const uint64_t f0 = pair2(s0, s0), f1 = S::GATE ? pair2(s1, s1) : f0;
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t at = lanes + buf * 256 + hw * (S::GATE ? 64 : 128);
+                    uint32_t v[2][32];
+                    if (rows > 0) tmem_ld32(v[0], at);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (rows > 0) {
+                            tmem_wait(v[q & 1]);
+                            if (q < 3) tmem_ld32(v[(q + 1) & 1], at + (S::GATE && q + 1 >= 2 ? 64 + (q + 1) * 32 : (q + 1) * 32));
+                        }
+                        if (q == 3) {  // all read: the buffer can be written again
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
+                        }
+                        if (rows > 0) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                acc[q][j] = fma2(pair2(v[q & 1][2 * j], v[q & 1][2 * j + 1]), q < 2 ? f0 : f1, acc[q][j]);
+                        }
+                    }
+                    if (k % kScaleGroup == kScaleGroup - 1 || k == nk - 1) {
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(b_sempty + 8 * (fill & 1));
+                        ++fill;
+                    }
+                }
+                if (!ok) break;
+                const int64_t row0 = ti.row0 + (int)rank * 128 + sub * 32;
+                if constexpr (S::GATE) {
+                    // 64 of the block's 128 channels here, the others in the warp of the other half
+                    float top = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float a0 = swiglu(lo2(acc[q][j]), lo2(acc[2 + q][j]));
+                            const float a1 = swiglu(hi2(acc[q][j]), hi2(acc[2 + q][j]));
+                            acc[q][j] = pair2(__float_as_uint(a0), __float_as_uint(a1));
+                            top = fmaxf(top, fmaxf(fabsf(a0), fabsf(a1)));
+                        }
+                    float *am = amaxs + (turn & 1) * 256;
+                    ++turn;
+                    am[hw * 128 + row] = top;
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + sub) : "memory");
+                    const float a = fmaxf(fmaxf(top, am[(hw ^ 1) * 128 + row]), 1e-4f);
+                    const float inv = __fdiv_rn(448.0f, a);
+                    if (hw == 0 && lane < rows) p.ys[(row0 + lane) * (width / 128) + ti.w0 / 128] = __fdiv_rn(a, 448.0f);
+                    uint4 line[4];
+                    uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const uint32_t b0 = __nv_cvt_float2_to_fp8x2(
+                                make_float2(__fmul_rn(lo2(acc[q][j]), inv), __fmul_rn(hi2(acc[q][j]), inv)), __NV_SATFINITE, __NV_E4M3);
+                            const uint32_t b1 = __nv_cvt_float2_to_fp8x2(
+                                make_float2(__fmul_rn(lo2(acc[q][j + 1]), inv), __fmul_rn(hi2(acc[q][j + 1]), inv)), __NV_SATFINITE,
+                                __NV_E4M3);
+                            b4[q * 8 + j / 2] = b0 | b1 << 16;
+                        }
+                    store_lines<4>(line, out, lane, static_cast<uint8_t *>(p.y) + row0 * width + ti.w0 + hw * 64, width, rows, 4);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint4 line[4];
+                        uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) b4[j] = bf16x2(lo2(acc[q][j]), hi2(acc[q][j]));
+                        const int c = ti.w0 + hw * 128 + q * 32;
+                        store_lines<4>(line, out, lane, static_cast<__nv_bfloat16 *>(p.y) + row0 * p.n + c, (int64_t)p.n * 2, rows,
+                                       (p.n - c) / 8);
+                    }
                 }
             } else if constexpr (S::FP8) {
                 // Fragments of 64 columns: columns 64 hw and 64 hw + 128 on (gate: the gate's and
@@ -724,39 +843,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, F32>::THRE
                 }
             } else {
                 // wgrad in fp32: sums of 256 rows added up in registers, chunk 2 s + hw of the columns
-                constexpr int SLOTS = 4;
-                float acc[SLOTS][32];
+                uint64_t acc[4][16];
 #pragma unroll
-                for (int s = 0; s < SLOTS; ++s)
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int i2 = 0; i2 < 32; ++i2) acc[s][i2] = 0.0f;
+                    for (int j = 0; j < 16; ++j) acc[q][j] = 0;
                 const int nseg = (nk + S::SEG - 1) / S::SEG;
                 for (int k = 0; k < nseg; ++k, ++seg) {
                     const uint32_t buf = seg & 1;
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
+                    const uint32_t at = lanes + buf * 256 + hw * 32;
+                    uint32_t v[2][32];
+                    tmem_ld32(v[0], at);
 #pragma unroll
-                    for (int s = 0; s < SLOTS; ++s) {
-                        const int c = 2 * s + hw;
-                        if (c >= chunks) continue;
-                        float v[32];
-                        tmem_get32(v, lanes + buf * 256 + c * 32);
+                    for (int q = 0; q < 4; ++q) {
+                        // columns past ti.nt are read (they lie in the buffer) and not written out
+                        tmem_wait(v[q & 1]);
+                        if (q < 3) {
+                            tmem_ld32(v[(q + 1) & 1], at + (q + 1) * 64);
+                        } else {
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
+                        }
 #pragma unroll
-                        for (int i2 = 0; i2 < 32; ++i2) acc[s][i2] += v[i2];
+                        for (int j = 0; j < 16; ++j)
+                            acc[q][j] = add2(pair2(v[q & 1][2 * j], v[q & 1][2 * j + 1]), acc[q][j]);
                     }
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int s = 0; s < SLOTS; ++s) {
-                    const int c = 2 * s + hw;
+                for (int q = 0; q < 4; ++q) {
+                    const int c = 2 * q + hw;
                     if (c >= chunks) continue;
-                    store_rows<true>(acc[s], out, lane,
-                                     static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + ti.c0 + c * 32, p.k,
-                                     p.n - wc, p.k - ti.c0 - c * 32, p.accumulate != 0);
+                    const int col = ti.c0 + c * 32;
+                    uint4 line[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        line[j] = make_uint4((uint32_t)acc[q][2 * j], (uint32_t)(acc[q][2 * j] >> 32), (uint32_t)acc[q][2 * j + 1],
+                                             (uint32_t)(acc[q][2 * j + 1] >> 32));
+                    float *dst = static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + col;
+                    if (p.accumulate)
+                        store_lines<8, true>(line, out, lane, dst, (int64_t)p.k * 4, p.n - wc, (p.k - col) / 4);
+                    else
+                        store_lines<8>(line, out, lane, dst, (int64_t)p.k * 4, p.n - wc, (p.k - col) / 4);
                 }
             }
         }
@@ -802,16 +934,17 @@ bool encode(CUtensorMap *m, const void *base, bool fp8, int64_t cols, int64_t ro
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <ExpertOp OP, bool F32>
+template <ExpertOp OP, bool ALT>
 size_t smem_bytes(int E) {
-    return Shape<OP, F32>::fixed + (Shape<OP, F32>::WG ? 0 : ((size_t)E + 1) * 4);
+    return Shape<OP, ALT>::fixed + (Shape<OP, ALT>::WG ? 0 : ((size_t)E + 1) * 4);
 }
 
-template <ExpertOp OP, bool F32>
+template <ExpertOp OP, bool ALT>
 cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
-    using S = Shape<OP, F32>;
+    using S = Shape<OP, ALT>;
     ExpertGemmParams q = p;
     q.xs_vec = p.k % (4 * 128) == 0 && (uintptr_t)p.xs % 16 == 0;
+    q.ws_vec = p.k % (4 * 128) == 0 && (uintptr_t)p.ws % 16 == 0;
     Maps maps;
     bool ok;
     if constexpr (S::WG) {
@@ -824,7 +957,7 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     static std::atomic<bool> ready{false};
     if (!ready.load(std::memory_order_acquire)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(expert_gemm_kernel<OP, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
+            cudaFuncSetAttribute(expert_gemm_kernel<OP, ALT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
         if (e != cudaSuccess) return e;
         ready.store(true, std::memory_order_release);
     }
@@ -833,24 +966,26 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(S::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = smem_bytes<OP, F32>(p.E);
+    cfg.dynamicSmemBytes = smem_bytes<OP, ALT>(p.E);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<OP, F32>, maps, q);
+    return cudaLaunchKernelEx(&cfg, expert_gemm_kernel<OP, ALT>, maps, q);
 }
 
 }  // namespace
 
 cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream) {
+    const bool row = p.live > (int64_t)p.E * kRowFormRows;
     switch (op) {
         case ExpertOp::kBf16: return launch<ExpertOp::kBf16, false>(p, stream);
         case ExpertOp::kBf16T: return launch<ExpertOp::kBf16T, false>(p, stream);
-        case ExpertOp::kFp8: return launch<ExpertOp::kFp8, false>(p, stream);
-        case ExpertOp::kGateFp8: return launch<ExpertOp::kGateFp8, false>(p, stream);
+        case ExpertOp::kFp8: return row ? launch<ExpertOp::kFp8, true>(p, stream) : launch<ExpertOp::kFp8, false>(p, stream);
+        case ExpertOp::kGateFp8:
+            return row ? launch<ExpertOp::kGateFp8, true>(p, stream) : launch<ExpertOp::kGateFp8, false>(p, stream);
         default: return p.out_fp32 ? launch<ExpertOp::kWgrad, true>(p, stream) : launch<ExpertOp::kWgrad, false>(p, stream);
     }
 }

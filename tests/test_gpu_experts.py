@@ -16,6 +16,8 @@ pytestmark = pytest.mark.gpu
 EDGES = [0, 1, 31, 32, 33, 127, 128, 129, 0, 255, 256, 257, 520]
 # n, k: below one tile, no tile divides them, exact tiles, long
 SHAPES = [(8, 8), (24, 72), (136, 64), (264, 200), (256, 256), (1000, 328)]
+# the same with many rows per expert on average, where the FP8 products put the rows on the other side
+EDGES_MANY = [0, 1, 16, 17, 127, 128, 129, 0, 144, 255, 256, 257, 300, 520, 1000, 777]
 SHAPES_FP8 = [(8, 128), (136, 256), (264, 384), (256, 128), (1000, 1152)]
 
 
@@ -110,6 +112,12 @@ def test_gemm_fp8_edges(n, k):
     check_fp8(buf, h, grp, n, k)
 
 
+@pytest.mark.parametrize("n,k", SHAPES_FP8)
+def test_gemm_fp8_edges_of_many_rows(n, k):
+    buf, h, grp = group(EDGES_MANY, padded=(n == 264))
+    check_fp8(buf, h, grp, n, k)
+
+
 def test_gemm_fp8_few_tokens_and_long_sums():
     buf, h, grp = group([1, 0, 2, 1, 0, 0, 4, 1], padded=True, ranks=4)
     check_fp8(buf, h, grp, 776, 7168)
@@ -148,6 +156,12 @@ def check_gate(buf, h, grp, inner, k, seed=1):
 @pytest.mark.parametrize("inner,k", [(128, 128), (256, 384), (384, 1152), (640, 256)])
 def test_gate_fp8_edges(inner, k):
     buf, h, grp = group(EDGES, padded=(inner == 384))
+    check_gate(buf, h, grp, inner, k)
+
+
+@pytest.mark.parametrize("inner,k", [(128, 128), (256, 384), (384, 1152), (640, 256)])
+def test_gate_fp8_edges_of_many_rows(inner, k):
+    buf, h, grp = group(EDGES_MANY, padded=(inner == 384))
     check_gate(buf, h, grp, inner, k)
 
 
