@@ -343,23 +343,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             }
         }
     } else if (warp == kWarpLoad) {
-        if (lane == 0) {
-            int st = 0;
-            uint32_t ph = 0;
-            int used = 0;
-            Tile ti;
-            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
-                if (!next_tile(ti, i, false)) break;
-                const int nk = stages_of(ti);
-                // rows that each CTA loads on the token side
-                const int half = ti.nt >> 1;
-                const int mine = S::ROW ? min(128, max(0, (ti.valid - (int)rank * 128 + 15) & ~15)) : half;
-                const uint32_t bytes = (S::ROW ? S::B_BYTES : S::A_BYTES) + mine * 128;
-                const uint32_t both = S::ROW ? 2 * S::B_BYTES + min(256, (ti.valid + 15) & ~15) * 128 : 2 * bytes;
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!(ok = bar_wait(b_empty + 8 * st, ph ^ 1))) break;
-                    const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
-                    const uint32_t full0 = map_rank(b_full + 8 * st, 0);
+        int st = 0;
+        uint32_t ph = 0;
+        int used = 0;
+        Tile ti;
+        for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
+            if (!next_tile(ti, i, true)) break;
+            const int nk = stages_of(ti);
+            // rows that each CTA loads on the token side
+            const int half = ti.nt >> 1;
+            const int mine = S::ROW ? min(128, max(0, (ti.valid - (int)rank * 128 + 15) & ~15)) : half;
+            const uint32_t bytes = (S::ROW ? S::B_BYTES : S::A_BYTES) + mine * 128;
+            const uint32_t both = S::ROW ? 2 * S::B_BYTES + min(256, (ti.valid + 15) & ~15) * 128 : 2 * bytes;
+            for (int kb = 0; kb < nk; ++kb) {
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph ^ 1));
+                if (!ok) break;
+                const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
+                const uint32_t full0 = map_rank(b_full + 8 * st, 0);
+                if (elect()) {
                     uint32_t bar = full0;
                     if constexpr (S::WG) {
                         if (kb == nk - 1 && (ti.valid & 63) != 0) {
@@ -392,45 +393,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         int r = (int)ti.row0 + (int)rank * (S::ROW ? 128 : half);
                         uint32_t d = S::ROW ? a : b;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int h = 128 >> i;
+                        for (int j = 0; j < 4; ++j) {
+                            const int h = 128 >> j;
                             if (mine & h) {
-                                tma_2d(d, &maps.m[1 + i], kc, r, bar);
+                                tma_2d(d, &maps.m[1 + j], kc, r, bar);
                                 r += h;
                                 d += h * 128;
                             }
                         }
                     }
-                    used = min(used + 1, S::STAGES);
-                    if (++st == S::STAGES) st = 0, ph ^= 1;
                 }
+                __syncwarp();
+                used = min(used + 1, S::STAGES);
+                if (++st == S::STAGES) st = 0, ph ^= 1;
             }
-            // the stages in flight have been read (nothing lands or arrives here after the kernel's end)
-            for (int i = 0; i < used; ++i) {
-                if (--st < 0) st = S::STAGES - 1, ph ^= 1;
-                if (!bar_wait(b_empty + 8 * st, ph)) {
-                    ok = false;
-                    atomicOr(p.status, kStatusInFlight);
-                    break;
-                }
+        }
+        // the stages in flight have been read (nothing lands or arrives here after the kernel's end)
+        for (int i = 0; i < used; ++i) {
+            if (--st < 0) st = S::STAGES - 1, ph ^= 1;
+            if (!__all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph))) {
+                ok = false;
+                atomicOr(p.status, kStatusInFlight);
+                break;
             }
         }
     } else if (warp == kWarpMma) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             int st = 0;
             uint32_t ph = 0, seg = 0;
             Tile ti;
             for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
-                if (!next_tile(ti, i, false)) break;
+                if (!next_tile(ti, i, true)) break;
                 const int nk = stages_of(ti);
                 const uint32_t id = idesc(S::FP8, S::A_MN, S::B_MN, ti.nt);
                 for (int kb = 0; kb < nk; ++kb) {
                     const int in_seg = S::SEG == 0 ? kb : kb % (S::SEG == 0 ? 1 : S::SEG);
                     const uint32_t buf = seg & 1;
+                    // the operands first: they are there long before the accumulator is read out
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_full + 8 * st, ph));
+                    if (!ok) break;
                     if (in_seg == 0) {
-                        if (!(ok = bar_wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1))) break;
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1));
+                        if (!ok) break;
                     }
-                    if (!(ok = bar_wait(b_full + 8 * st, ph))) break;
                     if constexpr (S::WG) {
                         if (kb == nk - 1) fence_acquire_cluster();  // the cleared lines of both CTAs
                     }
@@ -438,20 +443,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
                     const uint32_t d = tmem + buf * 256;
                     const int steps = S::WG ? (min(64, ti.valid - kb * 64) + 15) / 16 : 4;
+                    const bool ends = kb == nk - 1 || (S::SEG != 0 && in_seg == S::SEG - 1);
+                    if (elect()) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (S::WG && i >= steps) break;
-                        const uint64_t da = desc(a + i * (S::A_MN ? 2048 : 32), S::A_MN ? 8192 : 16);
-                        const uint64_t db = desc(b + i * (S::B_MN ? 2048 : 32), S::B_MN ? 8192 : 16);
-                        mma<S::FP8>(d, da, db, id, in_seg != 0 || i != 0);
-                        if constexpr (S::GATE_COL)
-                            mma<S::FP8>(d + 128, desc(a + 16384 + i * 32, 16), db, id, in_seg != 0 || i != 0);
+                        for (int j = 0; j < 4; ++j) {
+                            if (S::WG && j >= steps) break;
+                            const uint64_t da = desc(a + j * (S::A_MN ? 2048 : 32), S::A_MN ? 8192 : 16);
+                            const uint64_t db = desc(b + j * (S::B_MN ? 2048 : 32), S::B_MN ? 8192 : 16);
+                            mma<S::FP8>(d, da, db, id, in_seg != 0 || j != 0);
+                            if constexpr (S::GATE_COL)
+                                mma<S::FP8>(d + 128, desc(a + 16384 + j * 32, 16), db, id, in_seg != 0 || j != 0);
+                        }
+                        commit_pair(b_empty + 8 * st);
+                        if (ends) commit_pair(b_tfull + 8 * buf);
                     }
-                    commit_pair(b_empty + 8 * st);
-                    if (kb == nk - 1 || (S::SEG != 0 && in_seg == S::SEG - 1)) {
-                        commit_pair(b_tfull + 8 * buf);
-                        ++seg;
-                    }
+                    __syncwarp();
+                    if (ends) ++seg;
                     if (++st == S::STAGES) st = 0, ph ^= 1;
                 }
             }
@@ -627,24 +634,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
+                    // 64 columns at a time, so that the buffer is free again after two reads and half the sums
                     const uint32_t at = lanes + buf * 256 + hw * (S::GATE ? 64 : 128);
-                    uint32_t v[2][32];
-                    if (rows > 0) tmem_ld32(v[0], at);
+                    uint32_t v[64];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (rows > 0) {
-                            tmem_wait(v[q & 1]);
-                            if (q < 3) tmem_ld32(v[(q + 1) & 1], at + (S::GATE && q + 1 >= 2 ? 64 + (q + 1) * 32 : (q + 1) * 32));
-                        }
-                        if (q == 3) {  // all read: the buffer can be written again
+                    for (int q = 0; q < 4; q += 2) {
+                        if (rows > 0) tmem_get64(v, at + (q == 0 ? 0 : S::GATE ? 128 : 64));
+                        if (q == 2) {
                             fence_before();
                             __syncwarp();
                             if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                         }
                         if (rows > 0) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                acc[q][j] = fma2(pair2(v[q & 1][2 * j], v[q & 1][2 * j + 1]), q < 2 ? f0 : f1, acc[q][j]);
+                            for (int j = 0; j < 16; ++j) {
+                                acc[q][j] = fma2(pair2(v[2 * j], v[2 * j + 1]), q < 2 ? f0 : f1, acc[q][j]);
+                                acc[q + 1][j] = fma2(pair2(v[32 + 2 * j], v[33 + 2 * j]), q < 2 ? f0 : f1, acc[q + 1][j]);
+                            }
                         }
                     }
                     if (k % kScaleGroup == kScaleGroup - 1 || k == nk - 1) {
