@@ -67,19 +67,20 @@ struct Shape {
     static constexpr bool GATE_COL = GATE && !ROW;   // gate and up product as two M-side operands
     static constexpr bool A_MN = OP == ExpertOp::kBf16T || WG;
     static constexpr bool B_MN = WG;
-    static constexpr int READ = 8;                  // warps that read the accumulators
+    static constexpr int READ = ROW ? 16 : 8;       // warps that read the accumulators
     static constexpr int THREADS = (READ + 4) * 32;
-    // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72
-    static constexpr int REGS_READ = 216, REGS_REST = 72;
+    // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72 (row form: 640 x 96,
+    // split 512 x 104 + 128 x 64)
+    static constexpr int REGS_READ = ROW ? 104 : 216, REGS_REST = ROW ? 64 : 72;
     static constexpr int TOKENS = GATE_COL ? 128 : 256;       // most rows of a tile
     static constexpr int WROWS = GATE && ROW ? 128 : 256;     // weight rows (gate: channels of h) of a pair's tile
     static constexpr int A_BYTES = GATE_COL ? 32768 : 16384;  // per CTA and stage
     static constexpr int B_BYTES = ROW ? 16384 : TOKENS / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = GATE_COL ? 1024 : (OP == ExpertOp::kFp8 && !ROW) || F32 ? 4096 : 2048;  // per reading warp
-    static constexpr int STAGES = GATE_COL || (OP == ExpertOp::kFp8 && !ROW) || F32 ? 5 : 6;
+    static constexpr int OUT_BYTES = GATE ? 1024 : (OP == ExpertOp::kFp8 && !ROW) || F32 ? 4096 : 2048;  // per reading warp
+    static constexpr int STAGES = GATE_COL || OP == ExpertOp::kFp8 || F32 ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
-    static constexpr int AMAX = !GATE ? 0 : ROW ? 2 * 2 * 128 * 4 : 2 * 2 * 4 * 64 * 4;
+    static constexpr int AMAX = !GATE ? 0 : ROW ? 2 * 4 * 128 * 4 : 2 * 2 * 4 * 64 * 4;
     // e4m3: rows (of a CTA, or columns of the pair) that the scale warp serves
     [[maybe_unused]] static constexpr int SROWS = ROW ? 128 : TOKENS;
     // two scales per row: gate and up, or the two 128-channel blocks of a row-form tile
@@ -197,14 +198,14 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf,
 }
 
 // Write 32 lines of P pieces of 16 bytes (lane = line): through shared memory,
-// pieces swapped against bank conflicts, then P lanes store a line's 64 (P = 4)
-// or 128 (P = 8) bytes.  pitch: bytes from line to line of dst.  ADD: fp32
+// pieces swapped against bank conflicts, then P lanes store a line's 32 (P = 2),
+// 64 (P = 4) or 128 (P = 8) bytes.  pitch: bytes from line to line of dst.  ADD: fp32
 // values added to what dst holds.
 template <int P, bool ADD = false>
 __device__ __forceinline__ void store_lines(const uint4 (&v)[P], uint32_t buf, int lane, void *dst, int64_t pitch, int lines,
                                             int pieces) {
     auto place = [](int line, int c) {
-        return P == 8 ? line * 128 + (c ^ (line & 7)) * 16 : line * 64 + (c ^ ((line >> 1) & 3)) * 16;
+        return line * P * 16 + (c ^ (line / (8 / P) & (P - 1))) * 16;
     };
     __syncwarp();
 #pragma unroll
@@ -613,15 +614,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 }
             } else if constexpr (S::ROW) {
                 // The row form: lane = row, so a block's scale is one number per thread and the
-                // shape with the full rate serves.  Four chunks of 32 columns: 128 hw on (gate: the
-                // gate's and the up product's 64 hw on).
+                // shape with the full rate serves.  64 columns per warp in 4 chunks of 16: 64 hw on
+                // (gate: the gate's and the up product's 32 hw on).  16 warps, because a read takes
+                // 200 cycles beside the products and nothing else hides it.
                 const int rows = ti.valid - (int)rank * 128 - sub * 32;  // of this warp
                 const int row = sub * 32 + lane;
-                uint64_t acc[4][16];
+                uint64_t acc[4][8];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[q][j] = 0;
+                    for (int j = 0; j < 8; ++j) acc[q][j] = 0;
                 for (int k = 0; k < nk; ++k, ++seg) {
                     const uint32_t buf = seg & 1;
                     if (k % kScaleGroup == 0) {
@@ -629,28 +631,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         if (!ok) break;
                     }
                     const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256 + row;
-                    const uint32_t s0 = __float_as_uint(sc[S::GATE ? 0 : hw * 128]), s1 = S::GATE ? __float_as_uint(sc[128]) : s0;
+                    const uint32_t s0 = __float_as_uint(sc[S::GATE ? 0 : (hw >> 1) * 128]), s1 = S::GATE ? __float_as_uint(sc[128]) : s0;
                     const uint64_t f0 = pair2(s0, s0), f1 = S::GATE ? pair2(s1, s1) : f0;
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
-                    // 64 columns at a time, so that the buffer is free again after two reads and half the sums
-                    const uint32_t at = lanes + buf * 256 + hw * (S::GATE ? 64 : 128);
-                    uint32_t v[64];
+                    const uint32_t at = lanes + buf * 256 + hw * (S::GATE ? 32 : 64);
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        if (rows > 0) tmem_get64(v, at + (q == 0 ? 0 : S::GATE ? 128 : 64));
-                        if (q == 2) {
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t v[16];
+                        if (rows > 0) tmem_get16(v, at + q * 16 + (S::GATE && q >= 2 ? 96 : 0));
+                        if (q == 3) {  // all read: the buffer can be written again
                             fence_before();
                             __syncwarp();
                             if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                         }
                         if (rows > 0) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                acc[q][j] = fma2(pair2(v[2 * j], v[2 * j + 1]), q < 2 ? f0 : f1, acc[q][j]);
-                                acc[q + 1][j] = fma2(pair2(v[32 + 2 * j], v[33 + 2 * j]), q < 2 ? f0 : f1, acc[q + 1][j]);
-                            }
+                            for (int j = 0; j < 8; ++j) acc[q][j] = fma2(pair2(v[2 * j], v[2 * j + 1]), q < 2 ? f0 : f1, acc[q][j]);
                         }
                     }
                     if (k % kScaleGroup == kScaleGroup - 1 || k == nk - 1) {
@@ -662,46 +660,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 if (!ok) break;
                 const int64_t row0 = ti.row0 + (int)rank * 128 + sub * 32;
                 if constexpr (S::GATE) {
-                    // 64 of the block's 128 channels here, the others in the warp of the other half
+                    // 32 of the block's 128 channels here, the others in the three warps of the same rows
                     float top = 0.0f;
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < 8; ++j) {
                             const float a0 = swiglu(lo2(acc[q][j]), lo2(acc[2 + q][j]));
                             const float a1 = swiglu(hi2(acc[q][j]), hi2(acc[2 + q][j]));
                             acc[q][j] = pair2(__float_as_uint(a0), __float_as_uint(a1));
                             top = fmaxf(top, fmaxf(fabsf(a0), fabsf(a1)));
                         }
-                    float *am = amaxs + (turn & 1) * 256;
+                    float *am = amaxs + (turn & 1) * 512;
                     ++turn;
                     am[hw * 128 + row] = top;
-                    asm volatile("bar.sync %0, 64;" ::"r"(1 + sub) : "memory");
-                    const float a = fmaxf(fmaxf(top, am[(hw ^ 1) * 128 + row]), 1e-4f);
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + sub) : "memory");
+                    const float a = fmaxf(fmaxf(fmaxf(am[row], am[128 + row]), fmaxf(am[256 + row], am[384 + row])), 1e-4f);
                     const float inv = __fdiv_rn(448.0f, a);
                     if (hw == 0 && lane < rows) p.ys[(row0 + lane) * (width / 128) + ti.w0 / 128] = __fdiv_rn(a, 448.0f);
-                    uint4 line[4];
+                    uint4 line[2];
                     uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
+                        for (int j = 0; j < 8; j += 2) {
                             const uint32_t b0 = __nv_cvt_float2_to_fp8x2(
                                 make_float2(__fmul_rn(lo2(acc[q][j]), inv), __fmul_rn(hi2(acc[q][j]), inv)), __NV_SATFINITE, __NV_E4M3);
                             const uint32_t b1 = __nv_cvt_float2_to_fp8x2(
                                 make_float2(__fmul_rn(lo2(acc[q][j + 1]), inv), __fmul_rn(hi2(acc[q][j + 1]), inv)), __NV_SATFINITE,
                                 __NV_E4M3);
-                            b4[q * 8 + j / 2] = b0 | b1 << 16;
+                            b4[q * 4 + j / 2] = b0 | b1 << 16;
                         }
-                    store_lines<4>(line, out, lane, static_cast<uint8_t *>(p.y) + row0 * width + ti.w0 + hw * 64, width, rows, 4);
+                    store_lines<2>(line, out, lane, static_cast<uint8_t *>(p.y) + row0 * width + ti.w0 + hw * 32, width, rows, 2);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 4; q += 2) {
                         uint4 line[4];
                         uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) b4[j] = bf16x2(lo2(acc[q][j]), hi2(acc[q][j]));
-                        const int c = ti.w0 + hw * 128 + q * 32;
+                        for (int j = 0; j < 16; ++j) b4[j] = bf16x2(lo2(acc[q + j / 8][j % 8]), hi2(acc[q + j / 8][j % 8]));
+                        const int c = ti.w0 + hw * 64 + q * 16;
                         store_lines<4>(line, out, lane, static_cast<__nv_bfloat16 *>(p.y) + row0 * p.n + c, (int64_t)p.n * 2, rows,
                                        (p.n - c) / 8);
                     }
