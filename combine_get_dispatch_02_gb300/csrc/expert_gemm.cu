@@ -64,27 +64,24 @@ struct Shape {
     static constexpr bool WG = OP == ExpertOp::kWgrad;
     static constexpr bool F32 = WG && ALT;
     static constexpr bool ROW = FP8 && ALT;
-    static constexpr bool GATE_COL = GATE && !ROW;   // gate and up product as two M-side operands
+    static constexpr bool COL = FP8 && !ALT;         // two M-side operands: gate and up product, or 2 x 256 weight rows
     static constexpr bool A_MN = OP == ExpertOp::kBf16T || WG;
     static constexpr bool B_MN = WG;
     static constexpr int READ = ROW ? 16 : 8;       // warps that read the accumulators
     static constexpr int THREADS = (READ + 4) * 32;
-    // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72 (row form: 640 x 96,
-    // split 512 x 104 + 128 x 64)
+    // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72 (row form: 640 x 96, split
+    // 512 x 104 + 128 x 64)
     static constexpr int REGS_READ = ROW ? 104 : 216, REGS_REST = ROW ? 64 : 72;
-    static constexpr int TOKENS = GATE_COL ? 128 : 256;       // most rows of a tile
-    static constexpr int WROWS = GATE && ROW ? 128 : 256;     // weight rows (gate: channels of h) of a pair's tile
-    static constexpr int A_BYTES = GATE_COL ? 32768 : 16384;  // per CTA and stage
+    static constexpr int TOKENS = COL ? 128 : 256;            // most rows of a tile
+    // weight rows (gate: channels of h) of a pair's tile
+    static constexpr int WROWS = COL && !GATE ? 512 : GATE && ROW ? 128 : 256;
+    static constexpr int A_BYTES = COL ? 32768 : 16384;       // per CTA and stage
     static constexpr int B_BYTES = ROW ? 16384 : TOKENS / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = GATE ? 1024 : (OP == ExpertOp::kFp8 && !ROW) || F32 ? 4096 : 2048;  // per reading warp
-    static constexpr int STAGES = GATE_COL || OP == ExpertOp::kFp8 || F32 ? 5 : 6;
+    static constexpr int OUT_BYTES = COL ? 512 : GATE ? 1024 : F32 ? 4096 : 2048;  // per reading warp
+    static constexpr int STAGES = COL || OP == ExpertOp::kFp8 || F32 ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
-    static constexpr int AMAX = !GATE ? 0 : ROW ? 2 * 4 * 128 * 4 : 2 * 2 * 4 * 64 * 4;
-    // e4m3: rows (of a CTA, or columns of the pair) that the scale warp serves
-    [[maybe_unused]] static constexpr int SROWS = ROW ? 128 : TOKENS;
-    // two scales per row: gate and up, or the two 128-channel blocks of a row-form tile
-    [[maybe_unused]] static constexpr bool TWO = GATE || ROW;
+    static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 : 0;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
     static constexpr int KSTEP = FP8 ? 128 : 64;
     // stages per segment; 0: all of them
@@ -149,10 +146,10 @@ __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *be
     return r;
 }
 
-// Place of a column's scale in a block's 256: a thread T of the fragment
-// layout needs the columns 4 j + T % 4 of 64, so they lie together (16 floats),
-// in 16-byte pieces swapped so that the four threads' reads of a piece fall
-// into different banks.
+// Place of a column's scale in a block's 256 (column form): a thread T of the
+// fragment layout needs the columns 4 j + T % 4 of 64, so they lie together (16
+// floats), in 16-byte pieces swapped so that the four threads' reads of a piece
+// fall into different banks.
 __device__ __forceinline__ int scale_at(int col) {
     const int c = col & 3, j = (col & 63) >> 2;
     return (col & ~63) + c * 16 + (((j >> 2) ^ (c >> 1)) << 2) + (j & 3);
@@ -389,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             tma_3d(a + 8192, &maps.m[0], w + 64, kc, ti.e, bar);
                         } else {
                             tma_3d(a, &maps.m[0], kc, w, ti.e, bar);
-                            if constexpr (S::GATE) tma_3d(a + 16384, &maps.m[0], kc, width + w, ti.e, bar);
+                            if constexpr (S::COL) tma_3d(a + 16384, &maps.m[0], kc, w + (S::GATE ? width : 256), ti.e, bar);
                         }
                         int r = (int)ti.row0 + (int)rank * (S::ROW ? 128 : half);
                         uint32_t d = S::ROW ? a : b;
@@ -452,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             const uint64_t da = desc(a + j * (S::A_MN ? 2048 : 32), S::A_MN ? 8192 : 16);
                             const uint64_t db = desc(b + j * (S::B_MN ? 2048 : 32), S::B_MN ? 8192 : 16);
                             mma<S::FP8>(d, da, db, id, in_seg != 0 || j != 0);
-                            if constexpr (S::GATE_COL)
+                            if constexpr (S::COL)
                                 mma<S::FP8>(d + 128, desc(a + 16384 + j * 32, 16), db, id, in_seg != 0 || j != 0);
                         }
                         commit_pair(b_empty + 8 * st);
@@ -466,11 +463,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
         }
     } else if (warp == kWarpAux) {
         if constexpr (S::FP8) {
-            // scales of a tile's rows, xs * ws, for kScaleGroup blocks at a time; the next group's
-            // (or tile's) loads are in flight while one is stored
+            // scales of 128 rows (row form: of this CTA), xs * ws with the two blocks of weight rows, for
+            // kScaleGroup blocks at a time; the next group's (or tile's) loads are in flight while one is stored
             const int nb = (p.n + 127) / 128;
             struct Group {
-                float4 x[S::SROWS / 32], w, w2;
+                float4 x[4], w, w2;
             } cur, nxt;
             uint32_t fill = 0;
             Tile ti = {};
@@ -478,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             auto fetch = [&](Group &o) {
                 const int r0 = S::ROW ? (int)rank * 128 : 0;
                 const int b0 = S::ROW ? ti.w0 / 128 : ti.w0 / 128 + (int)rank;
-                const int b1 = S::GATE ? b0 + width / 128 : b0 + 1;
+                const int b1 = b0 + (S::GATE ? width / 128 : S::ROW ? 1 : 2);
                 auto four = [&](const float *q, bool vec) {
                     float4 v;
                     if (vec) {
@@ -493,9 +490,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 };
                 const float *ws = p.ws + (int64_t)ti.e * nb * kchan + g;
                 o.w = four(ws + (int64_t)min(b0, nb - 1) * kchan, p.ws_vec);
-                if constexpr (S::TWO) o.w2 = four(ws + (int64_t)min(b1, nb - 1) * kchan, p.ws_vec);
+                o.w2 = four(ws + (int64_t)min(b1, nb - 1) * kchan, p.ws_vec);
 #pragma unroll
-                for (int j0 = 0; j0 < S::SROWS; j0 += 32) {
+                for (int j0 = 0; j0 < 128; j0 += 32) {
                     const int j = r0 + j0 + lane;
                     o.x[j0 / 32] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (j < ti.valid) o.x[j0 / 32] = four(p.xs + (ti.row0 + j) * kchan + g, p.xs_vec);
@@ -518,19 +515,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 if (!ok) break;
                 float *out = scales + buf * kScaleGroup * 256;
 #pragma unroll
-                for (int j0 = 0; j0 < S::SROWS; j0 += 32) {
+                for (int j0 = 0; j0 < 128; j0 += 32) {
                     const int at = S::ROW ? j0 + lane : scale_at(j0 + lane);
                     const float4 v = cur.x[j0 / 32];
                     out[at] = v.x * cur.w.x;
                     out[256 + at] = v.y * cur.w.y;
                     out[512 + at] = v.z * cur.w.z;
                     out[768 + at] = v.w * cur.w.w;
-                    if constexpr (S::TWO) {
-                        out[128 + at] = v.x * cur.w2.x;
-                        out[384 + at] = v.y * cur.w2.y;
-                        out[640 + at] = v.z * cur.w2.z;
-                        out[896 + at] = v.w * cur.w2.w;
-                    }
+                    out[128 + at] = v.x * cur.w2.x;
+                    out[384 + at] = v.y * cur.w2.y;
+                    out[640 + at] = v.z * cur.w2.z;
+                    out[896 + at] = v.w * cur.w2.w;
                 }
                 __syncwarp();
                 if (lane == 0) bar_arrive(b_sfull + 8 * buf);
@@ -612,43 +607,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                     ++seg;
                 }
-            } else if constexpr (S::ROW) {
-                // The row form: lane = row, so a block's scale is one number per thread and the
-                // shape with the full rate serves.  64 columns per warp in 4 chunks of 16: 64 hw on
-                // (gate: the gate's and the up product's 32 hw on).  16 warps, because a read takes
-                // 200 cycles beside the products and nothing else hides it.
-                const int rows = ti.valid - (int)rank * 128 - sub * 32;  // of this warp
+            } else if constexpr (S::FP8) {
+                // A block's products are scaled and added up here.
+                //   row form: lane = row, one or two scales per thread and block; columns 64 hw on
+                //     (gate: the gate's and the up product's 32 hw on) in 4 chunks of 16.  16 warps,
+                //     because a read takes 200 cycles beside the products and nothing else hides it
+                //     (8 warps: 572 instead of 492 us at 8192^3).
+                //   column form: tokens 64 hw on of both operands, as fragments of 16 lanes: a thread has
+                //     16 columns and needs their scales only (as whole lanes all 64: 4 times the reads of
+                //     shared memory, 666 instead of 400 us at 76 x 128 rows x 4096 x 7168)
+                //     acc[2 * operand + half][j]: column 4 j + lane % 4, weight rows 16 * half + lane / 4
+                //     and + 8
+                const int rows = ti.valid - (int)rank * 128 - sub * 32;  // row form: of this warp
                 const int row = sub * 32 + lane;
-                uint64_t acc[4][8];
+                const int c4 = lane & 3;
+                const int col0 = hw * (S::GATE && S::ROW ? 32 : 64);
+                const bool live = S::ROW ? rows > 0 : col0 < ti.nt;
+                constexpr int J = S::COL ? 16 : 8;
+                uint64_t acc[4][J];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[q][j] = 0;
+                    for (int j = 0; j < J; ++j) acc[q][j] = 0;
                 for (int k = 0; k < nk; ++k, ++seg) {
                     const uint32_t buf = seg & 1;
                     if (k % kScaleGroup == 0) {
                         ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
                         if (!ok) break;
                     }
-                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256 + row;
-                    const uint32_t s0 = __float_as_uint(sc[S::GATE ? 0 : (hw >> 1) * 128]), s1 = S::GATE ? __float_as_uint(sc[128]) : s0;
-                    const uint64_t f0 = pair2(s0, s0), f1 = S::GATE ? pair2(s1, s1) : f0;
+                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256;
+                    uint64_t f0 = 0, f1 = 0;
+                    if constexpr (S::ROW) {
+                        const uint32_t s0 = __float_as_uint(sc[row + (S::GATE ? 0 : (hw >> 1) * 128)]);
+                        const uint32_t s1 = S::GATE ? __float_as_uint(sc[row + 128]) : s0;
+                        f0 = pair2(s0, s0);
+                        f1 = pair2(s1, s1);
+                    }
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
-                    const uint32_t at = lanes + buf * 256 + hw * (S::GATE ? 32 : 64);
+                    const uint32_t at = lanes + buf * 256 + col0;
+                    [[maybe_unused]] float cs[16];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        uint32_t v[16];
-                        if (rows > 0) tmem_get16(v, at + q * 16 + (S::GATE && q >= 2 ? 96 : 0));
+                        uint32_t v[2 * J];
+                        if (live) {
+                            if constexpr (S::COL) {
+                                tmem_get_frag(v, at + (q >> 1) * 128 + ((q & 1) << 20));
+                                if ((q & 1) == 0) {
+#pragma unroll
+                                    for (int m = 0; m < 4; ++m)
+                                        *reinterpret_cast<float4 *>(cs + 4 * m) = *reinterpret_cast<const float4 *>(
+                                            sc + (q >> 1) * 128 + col0 + c4 * 16 + ((m ^ (c4 >> 1)) << 2));
+                                }
+                            } else {
+                                tmem_get16(v, at + q * 16 + (S::GATE && q >= 2 ? 96 : 0));
+                            }
+                        }
                         if (q == 3) {  // all read: the buffer can be written again
                             fence_before();
                             __syncwarp();
                             if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                         }
-                        if (rows > 0) {
+                        if (live) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) acc[q][j] = fma2(pair2(v[2 * j], v[2 * j + 1]), q < 2 ? f0 : f1, acc[q][j]);
+                            for (int j = 0; j < J; ++j) {
+                                uint64_t f = q < 2 ? f0 : f1;
+                                if constexpr (S::COL) {
+                                    const uint32_t c = __float_as_uint(cs[j]);
+                                    f = pair2(c, c);
+                                }
+                                acc[q][j] = fma2(pair2(v[2 * j], v[2 * j + 1]), f, acc[q][j]);
+                            }
                         }
                     }
                     if (k % kScaleGroup == kScaleGroup - 1 || k == nk - 1) {
@@ -658,6 +688,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     }
                 }
                 if (!ok) break;
+                if constexpr (S::COL) {
+                    const int tokens = ti.valid - col0;
+                    const int64_t first = ti.row0 + col0;
+                    uint8_t *const own = outs + warp * S::OUT_BYTES;
+                    if constexpr (S::GATE) {
+                        if (live) {  // the same for the 4 warps of these tokens
+                            // h in place of the gate's sums, and each column's maximum over the warp's 32 channels
+                            float *am = amaxs + ((turn & 1) * 2 + hw) * 256;
+                            ++turn;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float m = 0.0f;
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    const float a0 = swiglu(lo2(acc[r][j]), lo2(acc[2 + r][j]));
+                                    const float a1 = swiglu(hi2(acc[r][j]), hi2(acc[2 + r][j]));
+                                    acc[r][j] = pair2(__float_as_uint(a0), __float_as_uint(a1));
+                                    m = fmaxf(m, fmaxf(fabsf(a0), fabsf(a1)));
+                                }
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                                if (lane < 4) am[sub * 64 + 4 * j + lane] = m;
+                            }
+                            // over the block's 128 channels: the four warps of these tokens
+                            asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
+                            const int h0 = ti.w0 + (int)rank * 128;
+#pragma unroll
+                            for (int part = 0; part < 4; ++part) {  // 16 tokens at a time
+                                __syncwarp();
+#pragma unroll
+                                for (int j = 4 * part; j < 4 * part + 4; ++j) {
+                                    const int col = 4 * j + c4;
+                                    const float a = fmaxf(fmaxf(fmaxf(am[col], am[64 + col]), fmaxf(am[128 + col], am[192 + col])), 1e-4f);
+                                    const float inv = __fdiv_rn(448.0f, a);
+                                    uint8_t *at = own + (col - 16 * part) * 32 + (lane >> 2);
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) {
+                                        at[16 * r] = __nv_cvt_float_to_fp8(__fmul_rn(lo2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
+                                        at[16 * r + 8] = __nv_cvt_float_to_fp8(__fmul_rn(hi2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
+                                    }
+                                    if (sub == 0 && lane < 4 && h0 < width && col < tokens)
+                                        p.ys[(first + col) * (width / 128) + h0 / 128] = __fdiv_rn(a, 448.0f);
+                                }
+                                __syncwarp();
+                                const int tok = 16 * part + (lane >> 1), off = (lane & 1) * 16;
+                                const uint4 q = *reinterpret_cast<const uint4 *>(own + (lane >> 1) * 32 + off);
+                                if (h0 < width && tok < tokens)
+                                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) + (first + tok) * width + wc + off) = q;
+                            }
+                        }
+                    } else if (live) {
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            const int c0 = wc + o * 256;
+                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.y) + first * p.n + c0;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                // 8 tokens x 32 channels as bf16, 64 bytes per token, 16-byte pieces swapped.
+                                // Stored transposed: a thread's values are the tokens 8 j + lane % 4 and + 4, so
+                                // row i of the store is token 8 j + i / 2 + 4 (i % 2)
+                                uint32_t h[4];
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    const uint64_t a = acc[2 * o + r][2 * j], b = acc[2 * o + r][2 * j + 1];
+                                    h[2 * r] = bf16x2(lo2(a), lo2(b));
+                                    h[2 * r + 1] = bf16x2(hi2(a), hi2(b));
+                                }
+                                __syncwarp();
+                                const int i8 = lane & 7, t8 = (i8 >> 1) + 4 * (i8 & 1);
+                                stm_x4_trans(out + t8 * 64 + (((lane >> 3) ^ ((t8 >> 1) & 3)) << 4), h[0], h[1], h[2], h[3]);
+                                __syncwarp();
+                                const int t = lane >> 2, piece = lane & 3;
+                                const uint4 q = *reinterpret_cast<const uint4 *>(own + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4));
+                                if (8 * j + t < tokens && piece * 8 < p.n - c0)
+                                    *reinterpret_cast<uint4 *>(dst + (int64_t)(8 * j + t) * p.n + piece * 8) = q;
+                            }
+                        }
+                    }
+                    continue;
+                }
                 const int64_t row0 = ti.row0 + (int)rank * 128 + sub * 32;
                 if constexpr (S::GATE) {
                     // 32 of the block's 128 channels here, the others in the three warps of the same rows
@@ -702,147 +812,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         const int c = ti.w0 + hw * 64 + q * 16;
                         store_lines<4>(line, out, lane, static_cast<__nv_bfloat16 *>(p.y) + row0 * p.n + c, (int64_t)p.n * 2, rows,
                                        (p.n - c) / 8);
-                    }
-                }
-            } else if constexpr (S::FP8) {
-                // Fragments of 64 columns: columns 64 hw and 64 hw + 128 on (gate: the gate's and
-                // the up product's columns of the same tokens), each as lanes 0-15 and 16-31.
-                // acc[2 * piece + half][j]: column 4 j + lane % 4, weight rows
-                // 16 * half + lane / 4 + {0, 8}.
-                const int col0 = hw * 64;
-                const int live = S::GATE ? (col0 < ti.nt ? 4 : 0) : (col0 < ti.nt ? 2 : 0) + (col0 + 128 < ti.nt ? 2 : 0);
-                const int c4 = lane & 3;
-                uint64_t acc[4][16];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[q][j] = 0;
-                for (int k = 0; k < nk; ++k, ++seg) {
-                    const uint32_t buf = seg & 1;
-                    if (k % kScaleGroup == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
-                        if (!ok) break;
-                    }
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
-                    if (!ok) break;
-                    fence_after();
-                    const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256 + col0 + c4 * 16;
-                    const uint32_t at = lanes + buf * 256 + col0;
-                    // the next quarter is on its way while one is added up
-                    uint32_t v[2][32];
-                    float f[16];
-                    if (live > 0) tmem_ld_frag(v[0], at);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (q >= live) break;
-                        if ((q & 1) == 0) {
-#pragma unroll
-                            for (int m = 0; m < 4; ++m)
-                                *reinterpret_cast<float4 *>(f + 4 * m) =
-                                    *reinterpret_cast<const float4 *>(sc + (q >> 1) * 128 + ((m ^ (c4 >> 1)) << 2));
-                        }
-                        tmem_wait(v[q & 1]);
-                        if (q + 1 < 4 && q + 1 < live)
-                            tmem_ld_frag(v[(q + 1) & 1], at + ((q + 1) >> 1) * 128 + (((q + 1) & 1) << 20));
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const uint32_t g = __float_as_uint(f[j]);
-                            acc[q][j] = fma2(pair2(v[q & 1][2 * j], v[q & 1][2 * j + 1]), pair2(g, g), acc[q][j]);
-                        }
-                    }
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
-                    if (k % kScaleGroup == kScaleGroup - 1 || k == nk - 1) {
-                        if (lane == 0) bar_arrive(b_sempty + 8 * (fill & 1));
-                        ++fill;
-                    }
-                }
-                if (!ok) break;
-                uint8_t *const own = outs + warp * S::OUT_BYTES;
-                if constexpr (S::GATE) {
-                    const int h0 = ti.w0 + (int)rank * 128;
-                    if (live > 0) {  // the same for the 4 warps of these columns
-                        // h in place of the gate's sums, and each column's maximum over the warp's 32 channels
-                        float *am = amaxs + ((turn & 1) * 2 + hw) * 256;
-                        ++turn;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float m = 0.0f;
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const float a0 = swiglu(lo2(acc[r][j]), lo2(acc[2 + r][j]));
-                                const float a1 = swiglu(hi2(acc[r][j]), hi2(acc[2 + r][j]));
-                                acc[r][j] = pair2(__float_as_uint(a0), __float_as_uint(a1));
-                                m = fmaxf(m, fmaxf(fabsf(a0), fabsf(a1)));
-                            }
-#pragma unroll
-                            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                            if (lane < 4) am[sub * 64 + 4 * j + lane] = m;
-                        }
-                        // over the block's 128 channels: the four warps of these columns
-                        asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
-                        const int tokens = ti.valid - col0;
-                        const int64_t row = ti.row0 + col0;
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {  // 32 tokens at a time
-                            __syncwarp();
-#pragma unroll
-                            for (int j = 8 * part; j < 8 * part + 8; ++j) {
-                                const int col = 4 * j + c4;
-                                float a = 1e-4f;
-#pragma unroll
-                                for (int w = 0; w < 4; ++w) a = fmaxf(a, am[w * 64 + col]);
-                                const float inv = __fdiv_rn(448.0f, a);
-                                uint8_t *at = own + (col - 32 * part) * 32 + (lane >> 2);
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    at[16 * r] = __nv_cvt_float_to_fp8(__fmul_rn(lo2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
-                                    at[16 * r + 8] = __nv_cvt_float_to_fp8(__fmul_rn(hi2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
-                                }
-                                if (sub == 0 && lane < 4 && h0 < width && col < tokens)
-                                    p.ys[(row + col) * (width / 128) + h0 / 128] = __fdiv_rn(a, 448.0f);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int t32 = (lane >> 1) + 16 * j, tok = 32 * part + t32, off = (lane & 1) * 16;
-                                const uint4 q = *reinterpret_cast<const uint4 *>(own + t32 * 32 + off);
-                                if (h0 < width && tok < tokens)
-                                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.y) + (row + tok) * width + wc + off) = q;
-                            }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (2 * s >= live) break;
-                        const int c0 = col0 + 128 * s;
-                        // 64 tokens x 32 channels as bf16, 64 bytes per token, 16-byte pieces swapped
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            // the four 8-channel blocks of 8 tokens, stored transposed: a thread's values are
-                            // the tokens 8 j + lane % 4 and + 4, so row i of the store is token 8 j + i / 2 + 4 (i % 2)
-                            uint32_t h[4];
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const uint64_t a = acc[2 * s + r][2 * j], b = acc[2 * s + r][2 * j + 1];
-                                h[2 * r] = bf16x2(lo2(a), lo2(b));
-                                h[2 * r + 1] = bf16x2(hi2(a), hi2(b));
-                            }
-                            const int i8 = lane & 7, tok = 8 * j + (i8 >> 1) + 4 * (i8 & 1), piece = lane >> 3;
-                            stm_x4_trans(out + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4), h[0], h[1], h[2], h[3]);
-                        }
-                        __syncwarp();
-                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.y) + (ti.row0 + c0) * p.n + wc;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int tok = (lane >> 2) + 8 * j, piece = lane & 3;
-                            const uint4 q = *reinterpret_cast<const uint4 *>(own + tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4));
-                            if (tok < ti.valid - c0 && piece * 8 < p.n - wc)
-                                *reinterpret_cast<uint4 *>(dst + (int64_t)tok * p.n + piece * 8) = q;
-                        }
                     }
                 }
             } else {

@@ -133,16 +133,6 @@ __device__ __forceinline__ void tmem_get32(float (&v)[32], uint32_t addr) {
         : "r"(addr)
         : "memory");
 }
-// 16 lanes x 64 fp32 columns as fragments: r[2 j + i] = lane T / 4 + 8 i,
-// column 4 j + T % 4 (T = thread of the warp).  The rates of the shapes, 2
-// warps per lane group: 32x32b 870, 16x128b 504, 16x256b 255 bytes per clock
-// and SM.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t (&r)[32], uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x128b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-}
 // 32 consecutive columns of the warp's 32 lanes: r[i] = column i of the
 // thread's lane; complete after tmem_wait.
 __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
@@ -157,6 +147,18 @@ __device__ __forceinline__ void tmem_get16(uint32_t (&r)[16], uint32_t addr) {
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+// 16 lanes x 64 columns as fragments, complete on return: r[2 j + i] = lane
+// T / 4 + 8 i, column 4 j + T % 4 (T = thread of the warp).  The shapes' rates
+// with 2 warps per lane group: 32x32b 870, 16x128b 504, 16x256b 255 bytes per
+// clock and SM.
+__device__ __forceinline__ void tmem_get_frag(uint32_t (&r)[32], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr)
         : "memory");
 }
