@@ -217,7 +217,8 @@ struct ExpertGemmParams {
     int64_t max_count;      // most rows of one expert
     int64_t live;           // entries of the layout (an upper bound of the rows in use)
     int32_t out_fp32, accumulate;  // wgrad
-    int32_t xs_vec, ws_vec; // set by the launcher: rows of xs / ws can be read 16 bytes at a time
+    int32_t xs_vec, ws_vec, y_vec;  // set by the launcher: rows of xs / ws can be read 16 bytes, rows of
+                                    // y written 32 bytes at a time
     int32_t sms;            // SMs to spread over
     uint32_t *status;
 };

@@ -51,9 +51,9 @@ constexpr int kMaxSmem = 232448;
 constexpr int kRowFormRows = 160;
 
 // Tensor maps: [0] the M-side operand, [1..4] the token rows in boxes of 128,
-// 64, 32 and 16 rows (wgrad: [1] x).
+// 64, 32 and 16 rows (wgrad: [1] x), [5] the output of the e4m3 row form.
 struct Maps {
-    CUtensorMap m[5];
+    CUtensorMap m[6];
 };
 
 // ALT: wgrad with fp32 output; e4m3 products in row form.
@@ -78,8 +78,8 @@ struct Shape {
     static constexpr int A_BYTES = COL ? 32768 : 16384;       // per CTA and stage
     static constexpr int B_BYTES = ROW ? 16384 : TOKENS / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = COL ? 512 : GATE ? 1024 : F32 ? 4096 : 2048;  // per reading warp
-    static constexpr int STAGES = COL || OP == ExpertOp::kFp8 || F32 ? 5 : 6;
+    static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : F32 ? 4096 : 2048;  // per reading warp
+    static constexpr int STAGES = ROW && !GATE ? 4 : COL || F32 ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
     static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 : 0;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
@@ -155,7 +155,9 @@ __device__ __forceinline__ int scale_at(int col) {
     return (col & ~63) + c * 16 + (((j >> 2) ^ (c >> 1)) << 2) + (j & 3);
 }
 
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
+// g / (1 + exp(-g)) * u with the fast exponential and division (2 ulp each, an
+// eighth of the instructions): far inside what the sums before it are good to.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -194,9 +196,22 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf,
     }
 }
 
+// Two pieces of 16 bytes of one row, as one 32-byte store where `whole` (the
+// rows are 32-byte aligned); pieces: how many of them lie in the row.
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8], bool whole, int pieces) {
+    if (whole && pieces >= 2) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+        return;
+    }
+    if (pieces >= 1) static_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    if (pieces >= 2) static_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
 // Write 32 lines of P pieces of 16 bytes (lane = line): through shared memory,
-// pieces swapped against bank conflicts, then P lanes store a line's 32 (P = 2),
-// 64 (P = 4) or 128 (P = 8) bytes.  pitch: bytes from line to line of dst.  ADD: fp32
+// pieces swapped against bank conflicts, then P lanes store a line's 64 (P = 4)
+// or 128 (P = 8) bytes.  pitch: bytes from line to line of dst.  ADD: fp32
 // values added to what dst holds.
 template <int P, bool ADD = false>
 __device__ __forceinline__ void store_lines(const uint4 (&v)[P], uint32_t buf, int lane, void *dst, int64_t pitch, int lines,
@@ -699,6 +714,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             ++turn;
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
+                                if (4 * j >= tokens) break;
                                 float m = 0.0f;
 #pragma unroll
                                 for (int r = 0; r < 2; ++r) {
@@ -716,6 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             const int h0 = ti.w0 + (int)rank * 128;
 #pragma unroll
                             for (int part = 0; part < 4; ++part) {  // 16 tokens at a time
+                                if (16 * part >= tokens) break;
                                 __syncwarp();
 #pragma unroll
                                 for (int j = 4 * part; j < 4 * part + 4; ++j) {
@@ -788,8 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     const float a = fmaxf(fmaxf(fmaxf(am[row], am[128 + row]), fmaxf(am[256 + row], am[384 + row])), 1e-4f);
                     const float inv = __fdiv_rn(448.0f, a);
                     if (hw == 0 && lane < rows) p.ys[(row0 + lane) * (width / 128) + ti.w0 / 128] = __fdiv_rn(a, 448.0f);
-                    uint4 line[2];
-                    uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
+                    uint32_t b4[8];
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -801,17 +817,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                                 __NV_E4M3);
                             b4[q * 4 + j / 2] = b0 | b1 << 16;
                         }
-                    store_lines<2>(line, out, lane, static_cast<uint8_t *>(p.y) + row0 * width + ti.w0 + hw * 32, width, rows, 2);
+                    if (lane < rows)
+                        store32(static_cast<uint8_t *>(p.y) + (row0 + lane) * width + ti.w0 + hw * 32, b4, p.y_vec, 2);
                 } else {
+                    // 32 rows x 64 columns.  All rows in use: a box of shared memory (128 bytes per row,
+                    // 16-byte pieces swizzled as the tensor map has it), stored while the next tile is
+                    // added up; ordinary stores of 64 KB held the tile's end up for 3600 cycles.
+                    const int c = ti.w0 + hw * 64;
+                    if (rows >= 32) {
+                        if (lane == 0) store_read_wait();
+                        __syncwarp();
 #pragma unroll
-                    for (int q = 0; q < 4; q += 2) {
-                        uint4 line[4];
-                        uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
+                        for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) b4[j] = bf16x2(lo2(acc[q + j / 8][j % 8]), hi2(acc[q + j / 8][j % 8]));
-                        const int c = ti.w0 + hw * 64 + q * 16;
-                        store_lines<4>(line, out, lane, static_cast<__nv_bfloat16 *>(p.y) + row0 * p.n + c, (int64_t)p.n * 2, rows,
-                                       (p.n - c) / 8);
+                            for (int o = 0; o < 2; ++o) {
+                                uint32_t b4[4];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) b4[j] = bf16x2(lo2(acc[q][4 * o + j]), hi2(acc[q][4 * o + j]));
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 128 +
+                                                                                              (((2 * q + o) ^ (lane & 7)) << 4)),
+                                             "r"(b4[0]), "r"(b4[1]), "r"(b4[2]), "r"(b4[3])
+                                             : "memory");
+                            }
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0 && c < p.n) tma_store_2d(&maps.m[5], out, c, (int)row0);
+                    } else if (lane < rows) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t b4[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) b4[j] = bf16x2(lo2(acc[q][j]), hi2(acc[q][j]));
+                            store32(static_cast<__nv_bfloat16 *>(p.y) + (row0 + lane) * p.n + c + q * 16, b4, p.y_vec,
+                                    (p.n - c - q * 16) / 8);
+                        }
                     }
                 }
             } else {
@@ -866,6 +905,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             }
         }
     }
+    if constexpr (S::ROW && !S::GATE) {
+        if (warp < S::READ && lane == 0) store_wait();
+    }
     if (!ok) atomicOr(p.status, kStatusTimeout);
     __syncwarp();
     fence_before();
@@ -917,6 +959,8 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     using S = Shape<OP, ALT>;
     ExpertGemmParams q = p;
     q.xs_vec = p.k % (4 * 128) == 0 && (uintptr_t)p.xs % 16 == 0;
+    const int64_t ybytes = S::GATE ? p.n / 2 : (int64_t)p.n * 2;
+    q.y_vec = ybytes % 32 == 0 && (uintptr_t)p.y % 32 == 0;
     q.ws_vec = p.k % (4 * 128) == 0 && (uintptr_t)p.ws % 16 == 0;
     Maps maps;
     bool ok;
@@ -925,6 +969,7 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     } else {
         ok = S::A_MN ? encode(&maps.m[0], p.w, S::FP8, p.n, p.k, p.E, 64) : encode(&maps.m[0], p.w, S::FP8, p.k, p.n, p.E, 128);
         for (int i = 0; i < 4 && ok; ++i) ok = encode(&maps.m[1 + i], p.x, S::FP8, p.k, p.rows, 0, 128 >> i);
+        if constexpr (S::ROW && !S::GATE) ok = ok && encode(&maps.m[5], p.y, false, p.n, p.rows, 0, 32);
     }
     if (!ok) return cudaErrorInvalidValue;
     static std::atomic<bool> ready{false};
