@@ -379,12 +379,13 @@ class Buffer:
     # -------------------------------------------------------- expert operators
     def _weights(self, w: torch.Tensor, name: str) -> tuple[int, int]:
         """The two channel counts of an [E, ., .] weight tensor."""
-        if w.dim() != 3 or w.shape[0] != self.num_experts:
-            raise ValueError(f"{name} must be [E={self.num_experts}, ., .], got {tuple(w.shape)}")
-        return w.shape[1], w.shape[2]
+        shape = w.shape
+        if len(shape) != 3 or shape[0] != self.num_experts:
+            raise ValueError(f"{name} must be [E={self.num_experts}, ., .], got {tuple(shape)}")
+        return shape[1], shape[2]
 
     def _rows(self, t: torch.Tensor, width: int, name: str) -> None:
-        if t.dim() != 2 or t.shape[0] != self.rows or t.shape[1] != width:
+        if t.shape != (self.rows, width):
             raise ValueError(f"{name} must be [{self.rows}, {width}], got {tuple(t.shape)}")
 
     def _new_rows(self, width: int, dtype: torch.dtype, like: torch.Tensor) -> torch.Tensor:

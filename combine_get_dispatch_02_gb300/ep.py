@@ -178,12 +178,16 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    """The cudaStream_t of ``stream``, or of the current one.  The raw getter
+    costs 0.2 us, torch.cuda.current_stream() 3 us: as much as a small call's
+    launch."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def make_config(num_ranks, max_tokens_per_rank, hidden, num_experts, topk,
