@@ -51,7 +51,8 @@ constexpr int kMaxSmem = 232448;
 constexpr int kRowFormRows = 160;
 
 // Tensor maps: [0] the M-side operand, [1..4] the token rows in boxes of 128,
-// 64, 32 and 16 rows (wgrad: [1] x), [5] the output of the e4m3 row form.
+// 64, 32 and 16 rows (wgrad: [1] x), [5] the output of the e4m3 row form
+// and of wgrad.
 struct Maps {
     CUtensorMap m[6];
 };
@@ -78,7 +79,7 @@ struct Shape {
     static constexpr int A_BYTES = COL ? 32768 : 16384;       // per CTA and stage
     static constexpr int B_BYTES = ROW ? 16384 : TOKENS / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : F32 ? 4096 : 2048;  // per reading warp
+    static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : F32 ? 8192 : WG ? 4096 : 2048;  // per reading warp
     static constexpr int STAGES = ROW && !GATE ? 4 : COL || F32 ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
     static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 : 0;
@@ -209,40 +210,36 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8], bool 
     if (pieces >= 2) static_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
-// Write 32 lines of P pieces of 16 bytes (lane = line): through shared memory,
-// pieces swapped against bank conflicts, then P lanes store a line's 64 (P = 4)
-// or 128 (P = 8) bytes.  pitch: bytes from line to line of dst.  ADD: fp32
-// values added to what dst holds.
-template <int P, bool ADD = false>
-__device__ __forceinline__ void store_lines(const uint4 (&v)[P], uint32_t buf, int lane, void *dst, int64_t pitch, int lines,
-                                            int pieces) {
-    auto place = [](int line, int c) {
-        return line * P * 16 + (c ^ (line / (8 / P) & (P - 1))) * 16;
-    };
-    __syncwarp();
+// 32 lines of 8 pieces of 16 bytes (lane = line) into a box of shared memory as
+// a 128-byte swizzled tensor map has it.
+__device__ __forceinline__ void fill_box(const uint4 (&v)[8], uint32_t box, int lane) {
 #pragma unroll
-    for (int c = 0; c < P; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + place(lane, c)), "r"(v[c].x), "r"(v[c].y),
-                     "r"(v[c].z), "r"(v[c].w)
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(v[c].x),
+                     "r"(v[c].y), "r"(v[c].z), "r"(v[c].w)
                      : "memory");
+    fence_async_shared();
     __syncwarp();
+}
+
+// Add 32 lines of 32 fp32 values (lane = line) to what dst holds: through shared
+// memory, so that 8 lanes take a line's 128 bytes.  pitch: bytes from line to
+// line; pieces: how many 16-byte pieces of a line exist.
+__device__ __forceinline__ void add_lines(const uint4 (&v)[8], uint32_t buf, int lane, float *dst, int64_t pitch, int lines,
+                                          int pieces) {
+    __syncwarp();
+    fill_box(v, buf, lane);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const int i = lane + 32 * j, line = i / P, c = i % P;
-        uint4 q;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                     : "r"(buf + place(line, c)));
+    for (int j = 0; j < 8; ++j) {
+        const int i = lane + 32 * j, line = i / 8, c = i % 8;
+        float4 q;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                     : "r"(buf + line * 128 + ((c ^ (line & 7)) << 4)));
         if (line >= lines || c >= pieces) continue;
-        uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(dst) + line * pitch + c * 16);
-        if constexpr (ADD) {
-            const uint4 o = *d;
-            q.x = __float_as_uint(__uint_as_float(o.x) + __uint_as_float(q.x));
-            q.y = __float_as_uint(__uint_as_float(o.y) + __uint_as_float(q.y));
-            q.z = __float_as_uint(__uint_as_float(o.z) + __uint_as_float(q.z));
-            q.w = __float_as_uint(__uint_as_float(o.w) + __uint_as_float(q.w));
-        }
-        *d = q;
+        float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<uint8_t *>(dst) + line * pitch + c * 16);
+        const float4 o = *d;
+        *d = make_float4(o.x + q.x, o.y + q.y, o.z + q.z, o.w + q.w);
     }
 }
 
@@ -589,39 +586,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             const int nk = stages_of(ti);
             const int chunks = ti.nt >> 5;
             const int wc = ti.w0 + (int)rank * 128 + sub * 32;  // the warp's first weight row / channel of h
-            if constexpr (S::SEG == 0) {
-                __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
+            if constexpr (S::WG && !S::F32) {
+                // columns 128 hw on, as two boxes of 64 (128 bytes of bf16) that the tensor map stores
+                // while the next tile is summed; what lies past n or k it leaves out
                 const uint32_t buf = seg & 1;
                 if (nk > 0) {
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
                 }
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const int col = hw * 128 + o * 64;
+                    uint4 line[8];
+                    uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
+#pragma unroll
+                    for (int i2 = 0; i2 < 2; ++i2) {
+                        float v[32];
+                        if (nk > 0) {
+                            tmem_get32(v, lanes + buf * 256 + col + i2 * 32);  // past ti.nt: in the buffer, not stored
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) b4[16 * i2 + j] = bf16x2(v[2 * j], v[2 * j + 1]);
+                    }
+                    if (o == 1 && nk > 0) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
+                        ++seg;
+                    }
+                    if (lane == 0) store_read_wait();
+                    __syncwarp();
+                    fill_box(line, out, lane);
+                    if (lane == 0 && wc < p.n && ti.c0 + col < p.k) tma_store_3d(&maps.m[5], out, ti.c0 + col, wc, ti.e);
+                }
+            } else if constexpr (S::SEG == 0) {
+                __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
+                const uint32_t buf = seg & 1;
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                if (!ok) break;
+                fence_after();
                 for (int c = hw; c < chunks; c += 2) {
                     float v[32];
-                    if (nk > 0) {
-                        tmem_get32(v, lanes + buf * 256 + c * 32);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-                    }
-                    if constexpr (S::WG) {
-                        uint4 line[4];
-                        uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) b4[j] = bf16x2(v[2 * j], v[2 * j + 1]);
-                        const int col = ti.c0 + c * 32;
-                        store_lines<4>(line, out, lane, y + ((int64_t)ti.e * p.n + wc) * p.k + col, (int64_t)p.k * 2, p.n - wc,
-                                       (p.k - col) / 8);
-                    } else
-                        store_tokens(v, out, lane, y + (ti.row0 + c * 32) * p.n + wc, p.n, ti.valid - c * 32, p.n - wc);
+                    tmem_get32(v, lanes + buf * 256 + c * 32);
+                    store_tokens(v, out, lane, y + (ti.row0 + c * 32) * p.n + wc, p.n, ti.valid - c * 32, p.n - wc);
                 }
-                if (nk > 0) {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
-                    ++seg;
-                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
+                ++seg;
             } else if constexpr (S::FP8) {
                 // A block's products are scaled and added up here.
                 //   row form: lane = row, one or two scales per thread and block; columns 64 hw on
@@ -827,20 +843,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if (rows >= 32) {
                         if (lane == 0) store_read_wait();
                         __syncwarp();
+                        uint4 line[8];
+                        uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int o = 0; o < 2; ++o) {
-                                uint32_t b4[4];
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) b4[j] = bf16x2(lo2(acc[q][4 * o + j]), hi2(acc[q][4 * o + j]));
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 128 +
-                                                                                              (((2 * q + o) ^ (lane & 7)) << 4)),
-                                             "r"(b4[0]), "r"(b4[1]), "r"(b4[2]), "r"(b4[3])
-                                             : "memory");
-                            }
-                        fence_async_shared();
-                        __syncwarp();
+                        for (int j = 0; j < 32; ++j) b4[j] = bf16x2(lo2(acc[j / 8][j % 8]), hi2(acc[j / 8][j % 8]));
+                        fill_box(line, out, lane);
                         if (lane == 0 && c < p.n) tma_store_2d(&maps.m[5], out, c, (int)row0);
                     } else if (lane < rows) {
 #pragma unroll
@@ -854,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     }
                 }
             } else {
-                // wgrad in fp32: sums of 256 rows added up in registers, chunk 2 s + hw of the columns
+                // wgrad in fp32: sums of 256 rows added up in registers, columns 128 hw on
                 uint64_t acc[4][16];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -866,46 +873,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
-                    const uint32_t at = lanes + buf * 256 + hw * 32;
-                    uint32_t v[2][32];
-                    tmem_ld32(v[0], at);
+                    const uint32_t at = lanes + buf * 256 + hw * 128;
+                    uint32_t v[32];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         // columns past ti.nt are read (they lie in the buffer) and not written out
-                        tmem_wait(v[q & 1]);
-                        if (q < 3) {
-                            tmem_ld32(v[(q + 1) & 1], at + (q + 1) * 64);
-                        } else {
+                        tmem_ld32(v, at + q * 32);
+                        tmem_wait(v);
+                        if (q == 3) {
                             fence_before();
                             __syncwarp();
                             if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            acc[q][j] = add2(pair2(v[q & 1][2 * j], v[q & 1][2 * j + 1]), acc[q][j]);
+                        for (int j = 0; j < 16; ++j) acc[q][j] = add2(pair2(v[2 * j], v[2 * j + 1]), acc[q][j]);
                     }
                 }
                 if (!ok) break;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int c = 2 * q + hw;
-                    if (c >= chunks) continue;
-                    const int col = ti.c0 + c * 32;
+                    const int col = ti.c0 + hw * 128 + q * 32;
+                    if (wc >= p.n || col >= p.k) continue;
                     uint4 line[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         line[j] = make_uint4((uint32_t)acc[q][2 * j], (uint32_t)(acc[q][2 * j] >> 32), (uint32_t)acc[q][2 * j + 1],
                                              (uint32_t)(acc[q][2 * j + 1] >> 32));
-                    float *dst = static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + col;
-                    if (p.accumulate)
-                        store_lines<8, true>(line, out, lane, dst, (int64_t)p.k * 4, p.n - wc, (p.k - col) / 4);
-                    else
-                        store_lines<8>(line, out, lane, dst, (int64_t)p.k * 4, p.n - wc, (p.k - col) / 4);
+                    if (p.accumulate) {
+                        float *dst = static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + col;
+                        add_lines(line, out, lane, dst, (int64_t)p.k * 4, p.n - wc, (p.k - col) / 4);
+                    } else {
+                        // a box of 32 columns in the buffer that the store before the last one read, stored
+                        // while the next one is filled
+                        const uint32_t box = out + (turn & 1) * 4096;
+                        ++turn;
+                        if (lane == 0) store_read_wait<1>();
+                        __syncwarp();
+                        fill_box(line, box, lane);
+                        if (lane == 0) tma_store_3d(&maps.m[5], box, col, wc, ti.e);
+                    }
                 }
             }
         }
     }
-    if constexpr (S::ROW && !S::GATE) {
+    if constexpr (S::WG || (S::ROW && !S::GATE)) {
         if (warp < S::READ && lane == 0) store_wait();
     }
     if (!ok) atomicOr(p.status, kStatusTimeout);
@@ -936,15 +947,14 @@ EncodeTiled encode_fn() {
 
 // A row-major matrix [rows, cols] (or [planes, rows, cols]) read in boxes of
 // box_rows rows by 128 bytes.
-bool encode(CUtensorMap *m, const void *base, bool fp8, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
+bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
     const EncodeTiled fn = encode_fn();
     if (fn == nullptr) return false;
-    const cuuint64_t es = fp8 ? 1 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {(cuuint64_t)cols * es, (cuuint64_t)cols * es * (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)(cols * es), (cuuint64_t)(cols * es * rows)};
     const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
-    return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes > 0 ? 3 : 2,
+    return fn(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, planes > 0 ? 3 : 2,
               const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -965,11 +975,13 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     Maps maps;
     bool ok;
     if constexpr (S::WG) {
-        ok = encode(&maps.m[0], p.dy, false, p.n, p.rows, 0, 64) && encode(&maps.m[1], p.x, false, p.k, p.rows, 0, 64);
+        ok = encode(&maps.m[0], p.dy, 2, p.n, p.rows, 0, 64) && encode(&maps.m[1], p.x, 2, p.k, p.rows, 0, 64) &&
+             encode(&maps.m[5], p.y, S::F32 ? 4 : 2, p.k, p.n, p.E, 32);
     } else {
-        ok = S::A_MN ? encode(&maps.m[0], p.w, S::FP8, p.n, p.k, p.E, 64) : encode(&maps.m[0], p.w, S::FP8, p.k, p.n, p.E, 128);
-        for (int i = 0; i < 4 && ok; ++i) ok = encode(&maps.m[1 + i], p.x, S::FP8, p.k, p.rows, 0, 128 >> i);
-        if constexpr (S::ROW && !S::GATE) ok = ok && encode(&maps.m[5], p.y, false, p.n, p.rows, 0, 32);
+        constexpr int es = S::FP8 ? 1 : 2;
+        ok = S::A_MN ? encode(&maps.m[0], p.w, es, p.n, p.k, p.E, 64) : encode(&maps.m[0], p.w, es, p.k, p.n, p.E, 128);
+        for (int i = 0; i < 4 && ok; ++i) ok = encode(&maps.m[1 + i], p.x, es, p.k, p.rows, 0, 128 >> i);
+        if constexpr (S::ROW && !S::GATE) ok = ok && encode(&maps.m[5], p.y, 2, p.n, p.rows, 0, 32);
     }
     if (!ok) return cudaErrorInvalidValue;
     static std::atomic<bool> ready{false};
