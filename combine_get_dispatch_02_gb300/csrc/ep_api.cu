@@ -74,6 +74,8 @@ struct ep_handle {
     cudaEvent_t runs_ev;      // recorded after the copy of the run sizes to h_runs
     int32_t runs_state;       // 0: none, 1: copy queued (wait on runs_ev), 2: on the host
     int32_t has_send;         // send_slot / runs belong to the layout held
+    // tile counters of the expert products, behind the layout's barrier counter
+    mutable uint32_t tile_counter;  // the next one to take
 };
 
 namespace {
@@ -646,6 +648,8 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
         p.max_count = (int64_t)c.num_ranks * c.max_tokens_per_rank;
     p.sms = expert_sms(ctx);
     p.status = ctx->d_status;
+    p.next = reinterpret_cast<uint32_t *>(h->cta_hist + grid_hist_ints(ctx) + 16) +
+             2 * (h->tile_counter++ % ep::kTileCounters);
     return p;
 }
 
@@ -795,7 +799,7 @@ ep_status ep_handle_create(ep_ctx *ctx, ep_handle **out) {
               cudaMalloc(&h->off_er, er * sizeof(int32_t)) == cudaSuccess &&
               cudaMalloc(&h->base, (size_t)c.num_experts * sizeof(int64_t)) == cudaSuccess &&
               cudaMalloc(&h->tokens_per_expert, (size_t)c.num_experts * sizeof(int32_t)) == cudaSuccess &&
-              cudaMalloc(&h->cta_hist, (grid_hist_ints(ctx) + 16) * sizeof(int32_t)) == cudaSuccess &&
+              cudaMalloc(&h->cta_hist, (grid_hist_ints(ctx) + 16 + 2 * ep::kTileCounters) * sizeof(int32_t)) == cudaSuccess &&
               cudaMalloc(&h->send_slot, nk * sizeof(int32_t)) == cudaSuccess;
     if (ok && c.num_ranks <= ep::kRankRunsMaxRanks)
         ok = cudaMallocHost(&h->h_runs, (size_t)c.num_ranks * c.num_ranks * sizeof(int32_t)) == cudaSuccess &&
@@ -805,8 +809,9 @@ ep_status ep_handle_create(ep_ctx *ctx, ep_handle **out) {
         ep_handle_destroy(h);
         return EP_ERR_OOM;
     }
-    // the grid-form layout's barrier counter starts at zero (each launch puts it back)
-    if (cudaMemset(h->cta_hist + grid_hist_ints(ctx), 0, 16 * sizeof(int32_t)) != cudaSuccess) {
+    // the grid-form layout's barrier counter and the tile counters start at zero (each launch puts
+    // them back)
+    if (cudaMemset(h->cta_hist + grid_hist_ints(ctx), 0, (16 + 2 * ep::kTileCounters) * sizeof(int32_t)) != cudaSuccess) {
         cudaGetLastError();
         ep_handle_destroy(h);
         return EP_ERR_CUDA;

@@ -221,7 +221,12 @@ struct ExpertGemmParams {
                                     // y written 32 bytes at a time
     int32_t sms;            // SMs to spread over
     uint32_t *status;
+    uint32_t *next;         // tile counter and count of the pairs that are done with it: both zero
+                            // between launches, each launch puts them back
 };
+// Tile counters of a handle (two words each), taken in turn, so that operators
+// of one handle may run side by side.
+constexpr int kTileCounters = 32;
 cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream);
 
 // ------------------------------------------------------------------ gated activation, weight cast

@@ -44,9 +44,11 @@ namespace {
 
 using namespace umma;
 
-constexpr int kTileRing = 4;      // tiles looked up ahead
+constexpr int kTileRing = 2;      // tiles looked up ahead
+constexpr int kNextRing = 4;      // tile numbers on their way to the second CTA
 constexpr int kScaleGroup = 4;    // 128-channel blocks per fill of the scale buffer
 constexpr int kMaxSmem = 232448;
+constexpr int kSortExperts = 256;  // wgrad: most experts that are put in order
 // mean rows per expert from which the e4m3 products take the row form
 constexpr int kRowFormRows = 160;
 
@@ -102,11 +104,14 @@ struct Tile {
 struct Bars {
     uint64_t full[6], empty[6], land[6];
     uint64_t tfull[2], tempty[2], sfull[2], sempty[2], kfull[kTileRing], kempty[kTileRing];
+    uint64_t nfull[kNextRing], nempty[kNextRing];
     Tile tiles[kTileRing];
+    int next[kNextRing];
     uint32_t tmem;
 };
 
-// Tile number t.  before[e]: token tiles of the experts before e.
+// Tile number t.  before[e]: token tiles of the experts before e (wgrad: the
+// experts by falling row count).
 template <ExpertOp OP, bool ALT>
 __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *before, int t, int wtiles) {
     using S = Shape<OP, ALT>;
@@ -114,8 +119,9 @@ __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *be
     if constexpr (S::WG) {
         const int ctiles = (p.k + 255) / 256;
         const int per = wtiles * ctiles;
-        r.e = t / per;
-        const int local = t - r.e * per;
+        const int i = t / per;
+        const int local = t - i * per;
+        r.e = p.E <= kSortExperts ? before[i] : i;
         r.w0 = local / ctiles * S::WROWS;
         r.c0 = local % ctiles * 256;
         r.row0 = __ldg(p.base + r.e);
@@ -281,6 +287,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             // readers: the reading warps, the loader, the first CTA's product thread, the auxiliary warp
             bar_init(b_kempty + 8 * i, S::READ + 1 + (rank == 0 ? 1 : 0) + (S::FP8 || S::WG ? 1 : 0));
         }
+        for (int i = 0; i < kNextRing; ++i) {
+            bar_init(saddr(&bars.nfull[i]), 1);
+            bar_init(saddr(&bars.nempty[i]), 1);
+        }
         bar_init_fence();
         for (int i = 0; i < (S::WG ? 2 : 5); ++i) prefetch_map(&maps.m[i]);
     }
@@ -314,6 +324,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             }
         }
     }
+    if constexpr (S::WG) {
+        // long sums first: tiles are handed out in this order, and a long one at the end would be
+        // waited for alone
+        if (p.E <= kSortExperts) {
+            const int c = tid < p.E ? __ldg(p.count + tid) : -1;
+            if (tid < p.E) before[tid] = c;
+            __syncthreads();
+            int at = 0;
+            if (tid < p.E)
+                for (int e = 0; e < p.E; ++e) {
+                    const int o = before[e];
+                    at += o > c || (o == c && e < tid) ? 1 : 0;
+                }
+            __syncthreads();
+            if (tid < p.E) before[at] = tid;
+        }
+    }
     fence_before();
     __syncthreads();
     cluster_sync();
@@ -327,29 +354,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
     const int kchan = (p.k + S::KSTEP - 1) / S::KSTEP;  // stages of a tile (wgrad: by the expert's rows)
     auto stages_of = [&](const Tile &ti) { return S::WG ? (ti.valid + 63) / 64 : kchan; };
     bool ok = true;
-    // The i-th tile of this pair (whole warps, or one thread of a role).
-    auto next_tile = [&](Tile &ti, int i, bool whole_warp) {
+    // The i-th tile of this pair, for a whole warp; false after the last one.
+    auto next_tile = [&](Tile &ti, int i) {
         const int s = i % kTileRing;
-        ok = bar_wait(b_kfull + 8 * s, (i / kTileRing) & 1);
-        if (whole_warp) ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_kfull + 8 * s, (i / kTileRing) & 1));
         if (!ok) return false;
         ti = bars.tiles[s];
-        if (whole_warp) __syncwarp();
-        if (!whole_warp || lane == 0) bar_arrive(b_kempty + 8 * s);
-        return true;
+        __syncwarp();
+        if (lane == 0) bar_arrive(b_kempty + 8 * s);
+        return ti.e >= 0;
     };
     if (warp >= S::READ) {
     regs_dec<S::REGS_REST>();
     if (warp == kWarpTiles) {
-        // looks the tiles up ahead of the others (a search, divisions and two loads from L2)
+        // Hands the pair's tiles out, looked up ahead of the others (a search, divisions and two
+        // loads from L2).  The first tile is the pair's own number, the others come from a counter in
+        // global memory, so that pairs with short tiles take more of them and the tiles of one
+        // expert, which share its weights in L2, start together.  The first CTA draws the numbers and
+        // sends them to the second.
         if (lane == 0) {
-            int i = 0;
-            for (int t = pair; t < total; t += pairs, ++i) {
+            const bool drawn = total > pairs;
+            int t = pair;
+            for (int i = 0; ok; ++i) {
+                const int n = i % kNextRing;
+                if (drawn && i > 0) {
+                    const uint32_t full = saddr(&bars.nfull[n]), empty = saddr(&bars.nempty[n]);
+                    if (rank == 0) {
+                        t = pairs + (int)atomicAdd(p.next, 1u);
+                        if (!(ok = bar_wait(empty, ((i / kNextRing) & 1) ^ 1))) break;
+                        send_u32(map_rank(saddr(&bars.next[n]), 1), (uint32_t)t, map_rank(full, 1));
+                    } else {
+                        bar_expect(full, 4);
+                        if (!(ok = bar_wait(full, (i / kNextRing) & 1))) break;
+                        t = bars.next[n];
+                        bar_arrive_cluster(map_rank(empty, 0));
+                    }
+                } else if (drawn) {
+                    // the first round of ring place 0 stands for the first tile, which nobody sends
+                    if (rank == 1) {
+                        bar_arrive(saddr(&bars.nfull[0]));
+                        bar_arrive_cluster(map_rank(saddr(&bars.nempty[0]), 0));
+                    }
+                } else if (i > 0) {
+                    t = total;
+                }
                 const int s = i % kTileRing;
-                const Tile ti = tile_at<OP, ALT>(p, before, t, wtiles);
+                Tile ti;
+                ti.e = -1;
+                if (t < total) ti = tile_at<OP, ALT>(p, before, t, wtiles);
                 if (!(ok = bar_wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
                 bars.tiles[s] = ti;
                 bar_arrive(b_kfull + 8 * s);
+                if (t >= total) break;
+            }
+            // the last pair to stop drawing puts the counter back for the next launch
+            if (drawn && rank == 0 && atomicAdd(p.next + 1, 1u) == (uint32_t)pairs - 1) {
+                p.next[0] = 0;
+                p.next[1] = 0;
             }
         }
     } else if (warp == kWarpLoad) {
@@ -357,8 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
         uint32_t ph = 0;
         int used = 0;
         Tile ti;
-        for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
-            if (!next_tile(ti, i, true)) break;
+        for (int i = 0; ok; ++i) {
+            if (!next_tile(ti, i)) break;
             const int nk = stages_of(ti);
             // rows that each CTA loads on the token side
             const int half = ti.nt >> 1;
@@ -432,8 +493,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             int st = 0;
             uint32_t ph = 0, seg = 0;
             Tile ti;
-            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
-                if (!next_tile(ti, i, true)) break;
+            for (int i = 0; ok; ++i) {
+                if (!next_tile(ti, i)) break;
                 const int nk = stages_of(ti);
                 const uint32_t id = idesc(S::FP8, S::A_MN, S::B_MN, ti.nt);
                 for (int kb = 0; kb < nk; ++kb) {
@@ -483,7 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             } cur, nxt;
             uint32_t fill = 0;
             Tile ti = {};
-            int i = 0, t = pair, g = 0;
+            int i = 0, g = 0;
             auto fetch = [&](Group &o) {
                 const int r0 = S::ROW ? (int)rank * 128 : 0;
                 const int b0 = S::ROW ? ti.w0 / 128 : ti.w0 / 128 + (int)rank;
@@ -510,15 +571,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if (j < ti.valid) o.x[j0 / 32] = four(p.xs + (ti.row0 + j) * kchan + g, p.xs_vec);
                 }
             };
-            bool more = t < total && next_tile(ti, 0, true);
+            bool more = next_tile(ti, 0);
             if (more) fetch(cur);
             while (more) {
                 // on to the next group
                 g += kScaleGroup;
                 if (g >= kchan) {
                     g = 0;
-                    t += pairs;
-                    more = t < total && next_tile(ti, ++i, true);
+                    more = next_tile(ti, ++i);
                     if (!ok) break;
                 }
                 if (more) fetch(nxt);
@@ -550,8 +610,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             int st = 0;
             uint32_t landed = 0;  // parity of each stage's landing barrier
             Tile ti;
-            for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
-                if (!next_tile(ti, i, true)) break;
+            for (int i = 0; ok; ++i) {
+                if (!next_tile(ti, i)) break;
                 const int nk = stages_of(ti);
                 if ((ti.valid & 63) != 0) {
                     const int s = (st + nk - 1) % S::STAGES;
@@ -581,8 +641,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
         const uint32_t tempty0 = map_rank(b_tempty, 0);
         uint32_t seg = 0, fill = 0, turn = 0;
         Tile ti;
-        for (int t = pair, i = 0; t < total && ok; t += pairs, ++i) {
-            if (!next_tile(ti, i, true)) break;
+        for (int i = 0; ok; ++i) {
+            if (!next_tile(ti, i)) break;
             const int nk = stages_of(ti);
             const int chunks = ti.nt >> 5;
             const int wc = ti.w0 + (int)rank * 128 + sub * 32;  // the warp's first weight row / channel of h
@@ -961,7 +1021,7 @@ bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows
 
 template <ExpertOp OP, bool ALT>
 size_t smem_bytes(int E) {
-    return Shape<OP, ALT>::fixed + (Shape<OP, ALT>::WG ? 0 : ((size_t)E + 1) * 4);
+    return Shape<OP, ALT>::fixed + (Shape<OP, ALT>::WG ? (size_t)kSortExperts * 4 : ((size_t)E + 1) * 4);
 }
 
 template <ExpertOp OP, bool ALT>

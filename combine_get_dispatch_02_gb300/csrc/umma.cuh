@@ -88,6 +88,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
     return true;
 }
 
+// Four bytes into another CTA's shared memory, counted on a barrier of the same
+// CTA (both addresses from map_rank).
+__device__ __forceinline__ void send_u32(uint32_t addr, uint32_t value, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(value), "r"(bar)
+                 : "memory");
+}
+
 // ------------------------------------------------------------ tensor-map loads
 // `bar` may be the barrier of either CTA of the pair (cta_group::2).
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
