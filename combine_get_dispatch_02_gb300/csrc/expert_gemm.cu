@@ -81,8 +81,8 @@ struct Shape {
     static constexpr int A_BYTES = COL ? 32768 : 16384;       // per CTA and stage
     static constexpr int B_BYTES = ROW ? 16384 : TOKENS / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : F32 ? 8192 : WG ? 4096 : 2048;  // per reading warp
-    static constexpr int STAGES = ROW && !GATE ? 4 : COL || F32 ? 5 : 6;
+    static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : WG ? 4096 : 2048;  // per reading warp
+    static constexpr int STAGES = ROW && !GATE ? 4 : COL ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
     static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 : 0;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
@@ -216,12 +216,15 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8], bool 
     if (pieces >= 2) static_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
-// 32 lines of 8 pieces of 16 bytes (lane = line) into a box of shared memory as
-// a 128-byte swizzled tensor map has it.
-__device__ __forceinline__ void fill_box(const uint4 (&v)[8], uint32_t box, int lane) {
+// 32 lines of P pieces of 16 bytes (lane = line) into a box of shared memory as
+// a tensor map with lines of P * 16 bytes has it: swizzled over 128 (P = 8) or
+// 64 bytes (P = 4).
+template <int P>
+__device__ __forceinline__ void fill_box(const uint4 (&v)[P], uint32_t box, int lane) {
+    const int swap = P == 8 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(v[c].x),
+    for (int c = 0; c < P; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * P * 16 + ((c ^ swap) << 4)), "r"(v[c].x),
                      "r"(v[c].y), "r"(v[c].z), "r"(v[c].w)
                      : "memory");
     fence_async_shared();
@@ -234,7 +237,7 @@ __device__ __forceinline__ void fill_box(const uint4 (&v)[8], uint32_t box, int 
 __device__ __forceinline__ void add_lines(const uint4 (&v)[8], uint32_t buf, int lane, float *dst, int64_t pitch, int lines,
                                           int pieces) {
     __syncwarp();
-    fill_box(v, buf, lane);
+    fill_box<8>(v, buf, lane);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int i = lane + 32 * j, line = i / 8, c = i % 8;
@@ -647,8 +650,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             const int chunks = ti.nt >> 5;
             const int wc = ti.w0 + (int)rank * 128 + sub * 32;  // the warp's first weight row / channel of h
             if constexpr (S::WG && !S::F32) {
-                // columns 128 hw on, as two boxes of 64 (128 bytes of bf16) that the tensor map stores
-                // while the next tile is summed; what lies past n or k it leaves out
+                // columns 128 hw on, as four boxes of 32 (64 bytes of bf16) that the tensor map stores
+                // while the next ones are filled and the next tile is summed; what lies past n or k it
+                // leaves out
                 const uint32_t buf = seg & 1;
                 if (nk > 0) {
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
@@ -656,32 +660,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     fence_after();
                 }
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const int col = hw * 128 + o * 64;
-                    uint4 line[8];
+                for (int q = 0; q < 4; ++q) {
+                    const int col = hw * 128 + q * 32;
+                    uint4 line[4];
                     uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
+                    float v[32];
+                    if (nk > 0) {
+                        tmem_get32(v, lanes + buf * 256 + col);  // past ti.nt: in the buffer, not stored
+                    } else {
 #pragma unroll
-                    for (int i2 = 0; i2 < 2; ++i2) {
-                        float v[32];
-                        if (nk > 0) {
-                            tmem_get32(v, lanes + buf * 256 + col + i2 * 32);  // past ti.nt: in the buffer, not stored
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) b4[16 * i2 + j] = bf16x2(v[2 * j], v[2 * j + 1]);
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                     }
-                    if (o == 1 && nk > 0) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) b4[j] = bf16x2(v[2 * j], v[2 * j + 1]);
+                    if (q == 3 && nk > 0) {
                         fence_before();
                         __syncwarp();
                         if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                         ++seg;
                     }
-                    if (lane == 0) store_read_wait();
+                    if (wc >= p.n || ti.c0 + col >= p.k) continue;
+                    const uint32_t box = out + (turn & 1) * 2048;  // read by the store before the last one
+                    ++turn;
+                    if (lane == 0) store_read_wait<1>();
                     __syncwarp();
-                    fill_box(line, out, lane);
-                    if (lane == 0 && wc < p.n && ti.c0 + col < p.k) tma_store_3d(&maps.m[5], out, ti.c0 + col, wc, ti.e);
+                    fill_box<4>(line, box, lane);
+                    if (lane == 0) tma_store_3d(&maps.m[5], box, ti.c0 + col, wc, ti.e);
                 }
             } else if constexpr (S::SEG == 0) {
                 __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
@@ -907,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) b4[j] = bf16x2(lo2(acc[j / 8][j % 8]), hi2(acc[j / 8][j % 8]));
-                        fill_box(line, out, lane);
+                        fill_box<8>(line, out, lane);
                         if (lane == 0 && c < p.n) tma_store_2d(&maps.m[5], out, c, (int)row0);
                     } else if (lane < rows) {
 #pragma unroll
@@ -963,14 +967,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         float *dst = static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + col;
                         add_lines(line, out, lane, dst, (int64_t)p.k * 4, p.n - wc, (p.k - col) / 4);
                     } else {
-                        // a box of 32 columns in the buffer that the store before the last one read, stored
-                        // while the next one is filled
-                        const uint32_t box = out + (turn & 1) * 4096;
-                        ++turn;
-                        if (lane == 0) store_read_wait<1>();
-                        __syncwarp();
-                        fill_box(line, box, lane);
-                        if (lane == 0) tma_store_3d(&maps.m[5], box, col, wc, ti.e);
+                        // boxes of 16 columns, stored while the next ones are filled
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            if (col + 16 * o >= p.k) continue;
+                            const uint4 half[4] = {line[4 * o], line[4 * o + 1], line[4 * o + 2], line[4 * o + 3]};
+                            const uint32_t box = out + (turn & 1) * 2048;  // read by the store before the last one
+                            ++turn;
+                            if (lane == 0) store_read_wait<1>();
+                            __syncwarp();
+                            fill_box<4>(half, box, lane);
+                            if (lane == 0) tma_store_3d(&maps.m[5], box, col + 16 * o, wc, ti.e);
+                        }
                     }
                 }
             }
@@ -1005,18 +1013,18 @@ EncodeTiled encode_fn() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// A row-major matrix [rows, cols] (or [planes, rows, cols]) read in boxes of
-// box_rows rows by 128 bytes.
-bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
+// A row-major matrix [rows, cols] (or [planes, rows, cols]) in boxes of box_rows
+// rows by box_bytes (64 or 128), swizzled over as many bytes.
+bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows, int box_bytes = 128) {
     const EncodeTiled fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)(cols * es), (cuuint64_t)(cols * es * rows)};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(box_bytes / es), (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     return fn(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, planes > 0 ? 3 : 2,
               const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <ExpertOp OP, bool ALT>
@@ -1036,7 +1044,7 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     bool ok;
     if constexpr (S::WG) {
         ok = encode(&maps.m[0], p.dy, 2, p.n, p.rows, 0, 64) && encode(&maps.m[1], p.x, 2, p.k, p.rows, 0, 64) &&
-             encode(&maps.m[5], p.y, S::F32 ? 4 : 2, p.k, p.n, p.E, 32);
+             encode(&maps.m[5], p.y, S::F32 ? 4 : 2, p.k, p.n, p.E, 32, 64);
     } else {
         constexpr int es = S::FP8 ? 1 : 2;
         ok = S::A_MN ? encode(&maps.m[0], p.w, es, p.n, p.k, p.E, 64) : encode(&maps.m[0], p.w, es, p.k, p.n, p.E, 128);
