@@ -84,7 +84,7 @@ struct Shape {
     static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : WG ? 4096 : 2048;  // per reading warp
     static constexpr int STAGES = ROW && !GATE ? 4 : COL ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
-    static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 : 0;
+    static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 + (COL ? READ * 64 * 4 : 0) : 0;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
     static constexpr int KSTEP = FP8 ? 128 : 64;
     // stages per segment; 0: all of them
@@ -738,23 +738,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         f0 = pair2(s0, s0);
                         f1 = pair2(s1, s1);
                     }
+                    // (column form: the first operand's here, the second's between its reads)
+                    [[maybe_unused]] float cs[16];
+                    auto column_scales = [&](int operand) {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            *reinterpret_cast<float4 *>(cs + 4 * m) =
+                                *reinterpret_cast<const float4 *>(sc + operand * 128 + col0 + c4 * 16 + ((m ^ (c4 >> 1)) << 2));
+                    };
+                    if constexpr (S::COL) {
+                        if (live) column_scales(0);
+                    }
                     ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
                     const uint32_t at = lanes + buf * 256 + col0;
-                    [[maybe_unused]] float cs[16];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t v[2 * J];
                         if (live) {
                             if constexpr (S::COL) {
+                                if (q == 2) column_scales(1);
                                 tmem_get_frag(v, at + (q >> 1) * 128 + ((q & 1) << 20));
-                                if ((q & 1) == 0) {
-#pragma unroll
-                                    for (int m = 0; m < 4; ++m)
-                                        *reinterpret_cast<float4 *>(cs + 4 * m) = *reinterpret_cast<const float4 *>(
-                                            sc + (q >> 1) * 128 + col0 + c4 * 16 + ((m ^ (c4 >> 1)) << 2));
-                                }
                             } else {
                                 tmem_get16(v, at + q * 16 + (S::GATE && q >= 2 ? 96 : 0));
                             }
@@ -789,44 +794,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     uint8_t *const own = outs + warp * S::OUT_BYTES;
                     if constexpr (S::GATE) {
                         if (live) {  // the same for the 4 warps of these tokens
-                            // h in place of the gate's sums, and each column's maximum over the warp's 32 channels
-                            float *am = amaxs + ((turn & 1) * 2 + hw) * 256;
-                            ++turn;
+                            // h in place of the gate's sums, and each column's maximum over the thread's 4
+                            // channels; 16 tokens at a time, as many as there are
+                            float top[16];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                if (4 * j >= tokens) break;
-                                float m = 0.0f;
+                            for (int j = 0; j < 16; ++j) top[j] = 0.0f;
 #pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    const float a0 = swiglu(lo2(acc[r][j]), lo2(acc[2 + r][j]));
-                                    const float a1 = swiglu(hi2(acc[r][j]), hi2(acc[2 + r][j]));
-                                    acc[r][j] = pair2(__float_as_uint(a0), __float_as_uint(a1));
-                                    m = fmaxf(m, fmaxf(fabsf(a0), fabsf(a1)));
-                                }
-#pragma unroll
-                                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                                if (lane < 4) am[sub * 64 + 4 * j + lane] = m;
-                            }
-                            // over the block's 128 channels: the four warps of these tokens
-                            asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
-                            const int h0 = ti.w0 + (int)rank * 128;
-#pragma unroll
-                            for (int part = 0; part < 4; ++part) {  // 16 tokens at a time
+                            for (int part = 0; part < 4; ++part) {
                                 if (16 * part >= tokens) break;
-                                __syncwarp();
 #pragma unroll
                                 for (int j = 4 * part; j < 4 * part + 4; ++j) {
-                                    const int col = 4 * j + c4;
-                                    const float a = fmaxf(fmaxf(fmaxf(am[col], am[64 + col]), fmaxf(am[128 + col], am[192 + col])), 1e-4f);
-                                    const float inv = __fdiv_rn(448.0f, a);
-                                    uint8_t *at = own + (col - 16 * part) * 32 + (lane >> 2);
 #pragma unroll
                                     for (int r = 0; r < 2; ++r) {
-                                        at[16 * r] = __nv_cvt_float_to_fp8(__fmul_rn(lo2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
-                                        at[16 * r + 8] = __nv_cvt_float_to_fp8(__fmul_rn(hi2(acc[r][j]), inv), __NV_SATFINITE, __NV_E4M3);
+                                        const float a0 = swiglu(lo2(acc[r][j]), lo2(acc[2 + r][j]));
+                                        const float a1 = swiglu(hi2(acc[r][j]), hi2(acc[2 + r][j]));
+                                        acc[r][j] = pair2(__float_as_uint(a0), __float_as_uint(a1));
+                                        top[j] = fmaxf(top[j], fmaxf(fabsf(a0), fabsf(a1)));
                                     }
-                                    if (sub == 0 && lane < 4 && h0 < width && col < tokens)
-                                        p.ys[(first + col) * (width / 128) + h0 / 128] = __fdiv_rn(a, 448.0f);
+                                }
+                            }
+                            // over the warp's 32 channels: 8 lanes hold a column's; each step hands the half
+                            // that the other lane will keep over, so that a lane ends with two columns
+#pragma unroll
+                            for (int o = 16, half = 8; o >= 4; o >>= 1, half >>= 1) {
+                                const bool up = lane & o;
+#pragma unroll
+                                for (int j = 0; j < half; ++j) {
+                                    const float give = up ? top[j] : top[j + half], keep = up ? top[j + half] : top[j];
+                                    top[j] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+                                }
+                            }
+                            float *am = amaxs + ((turn & 1) * 2 + hw) * 256;
+                            ++turn;
+                            const int j0 = (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2;
+                            am[sub * 64 + 4 * j0 + c4] = top[0];
+                            am[sub * 64 + 4 * j0 + 4 + c4] = top[1];
+                            // over the block's 128 channels: the four warps of these columns
+                            asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
+                            const int h0 = ti.w0 + (int)rank * 128;
+                            float *inv = amaxs + 1024 + warp * 64;  // [column % 4][column / 4]
+#pragma unroll
+                            for (int i2 = 0; i2 < 2; ++i2) {
+                                const int col = lane + 32 * i2;
+                                const float a = fmaxf(fmaxf(fmaxf(am[col], am[64 + col]), fmaxf(am[128 + col], am[192 + col])), 1e-4f);
+                                inv[(col & 3) * 16 + (col >> 2)] = __fdiv_rn(448.0f, a);
+                                if (sub == 0 && h0 < width && col < tokens)
+                                    p.ys[(first + col) * (width / 128) + h0 / 128] = __fdiv_rn(a, 448.0f);
+                            }
+#pragma unroll
+                            for (int part = 0; part < 4; ++part) {
+                                if (16 * part >= tokens) break;
+                                __syncwarp();
+                                const float4 f4 = *reinterpret_cast<const float4 *>(inv + c4 * 16 + 4 * part);
+                                const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    uint8_t *at = own + (4 * j + c4) * 32 + (lane >> 2);
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r) {
+                                        const uint64_t h = acc[r][4 * part + j];
+                                        const uint32_t q = __nv_cvt_float2_to_fp8x2(
+                                            make_float2(__fmul_rn(lo2(h), f[j]), __fmul_rn(hi2(h), f[j])), __NV_SATFINITE, __NV_E4M3);
+                                        at[16 * r] = (uint8_t)q;
+                                        at[16 * r + 8] = (uint8_t)(q >> 8);
+                                    }
                                 }
                                 __syncwarp();
                                 const int tok = 16 * part + (lane >> 1), off = (lane & 1) * 16;
