@@ -49,35 +49,52 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) 
     const __nv_bfloat16 *dh = static_cast<const __nv_bfloat16 *>(p.dh);
     __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(p.h);
     __nv_bfloat16 *dgu = static_cast<__nv_bfloat16 *>(p.dgu);
-    for (int64_t it = warp; it < items; it += nwarp) {
-        const int64_t i = it / nch;
-        const int32_t s = p.slot[i];
-        if (s < 0) continue;  // warp-uniform
-        const int c = (int)(it - i * nch) * kChunk + lane * 8;
-        if (c >= I) continue;
-        const int64_t row = s;
-        const uint4 vg = ld_nc_na_v4(gu + row * 2 * I + c), vu = ld_nc_na_v4(gu + row * 2 * I + I + c);
-        uint4 vd = make_uint4(0, 0, 0, 0);
-        if constexpr (BWD) vd = ld_nc_na_v4(dh + row * I + c);
-        const uint32_t g4[4] = {vg.x, vg.y, vg.z, vg.w}, u4[4] = {vu.x, vu.y, vu.z, vu.w};
-        const uint32_t d4[4] = {vd.x, vd.y, vd.z, vd.w};
-        uint32_t oh[4], og[4], ou[4];
+    constexpr int U = BWD ? 2 : 1;  // items at a time: all their loads before the first is computed
+    for (int64_t it0 = warp; it0 < items; it0 += U * nwarp) {
+        int64_t row[U];
+        int ch[U];
+        uint4 vg[U], vu[U], vd[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float ga = bf16_lo(g4[j]), gb = bf16_hi(g4[j]), ua = bf16_lo(u4[j]), ub = bf16_hi(u4[j]);
-            const float sa = sigmoid(ga), sb = sigmoid(gb);
-            const float fa = ga * sa, fb = gb * sb;
-            oh[j] = pack_bf16(fa * ua, fb * ub);
-            if constexpr (BWD) {
-                const float da = bf16_lo(d4[j]), db = bf16_hi(d4[j]);
-                ou[j] = pack_bf16(da * fa, db * fb);
-                og[j] = pack_bf16(da * ua * sa * fmaf(ga, 1.0f - sa, 1.0f), db * ub * sb * fmaf(gb, 1.0f - sb, 1.0f));
-            }
+        for (int t = 0; t < U; ++t) {
+            const int64_t it = it0 + t * nwarp;
+            const int64_t i = it / nch;
+            row[t] = it < items ? p.slot[i] : -1;
+            ch[t] = (int)(it - i * nch) * kChunk + lane * 8;
+            if (ch[t] >= I) row[t] = -1;
         }
-        if (!BWD || h != nullptr) *reinterpret_cast<uint4 *>(h + row * I + c) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-        if constexpr (BWD) {
-            *reinterpret_cast<uint4 *>(dgu + row * 2 * I + c) = make_uint4(og[0], og[1], og[2], og[3]);
-            *reinterpret_cast<uint4 *>(dgu + row * 2 * I + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+#pragma unroll
+        for (int t = 0; t < U; ++t) {
+            if (row[t] < 0) continue;
+            vg[t] = ld_nc_na_v4(gu + row[t] * 2 * I + ch[t]);
+            vu[t] = ld_nc_na_v4(gu + row[t] * 2 * I + I + ch[t]);
+            if constexpr (BWD) vd[t] = ld_nc_na_v4(dh + row[t] * I + ch[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < U; ++t) {
+            if (row[t] < 0) continue;
+            const int c = ch[t];
+            const uint32_t g4[4] = {vg[t].x, vg[t].y, vg[t].z, vg[t].w}, u4[4] = {vu[t].x, vu[t].y, vu[t].z, vu[t].w};
+            uint32_t d4[4] = {};
+            if constexpr (BWD) d4[0] = vd[t].x, d4[1] = vd[t].y, d4[2] = vd[t].z, d4[3] = vd[t].w;
+            uint32_t oh[4], og[4], ou[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float ga = bf16_lo(g4[j]), gb = bf16_hi(g4[j]), ua = bf16_lo(u4[j]), ub = bf16_hi(u4[j]);
+                const float sa = sigmoid(ga), sb = sigmoid(gb);
+                const float fa = ga * sa, fb = gb * sb;
+                oh[j] = pack_bf16(fa * ua, fb * ub);
+                if constexpr (BWD) {
+                    const float da = bf16_lo(d4[j]), db = bf16_hi(d4[j]);
+                    ou[j] = pack_bf16(da * fa, db * fb);
+                    og[j] = pack_bf16(da * ua * sa * fmaf(ga, 1.0f - sa, 1.0f), db * ub * sb * fmaf(gb, 1.0f - sb, 1.0f));
+                }
+            }
+            if (!BWD || h != nullptr)
+                *reinterpret_cast<uint4 *>(h + row[t] * I + c) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+            if constexpr (BWD) {
+                *reinterpret_cast<uint4 *>(dgu + row[t] * 2 * I + c) = make_uint4(og[0], og[1], og[2], og[3]);
+                *reinterpret_cast<uint4 *>(dgu + row[t] * 2 * I + I + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+            }
         }
     }
 }
@@ -145,12 +162,23 @@ cudaError_t launch_pdl(K kernel, const P &p, int64_t blocks, cudaStream_t stream
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <typename K>
+int occupancy(K kernel) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != cudaSuccess) {
+        cudaGetLastError();
+        return 1;
+    }
+    return n > 0 ? n : 1;
+}
+
 }  // namespace
 
 cudaError_t launch_swiglu(const SwigluParams &p, bool backward, int sms, cudaStream_t stream) {
     const int64_t warps = p.n * ((p.inner + kChunk - 1) / kChunk);
     int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > (int64_t)sms * 8) blocks = (int64_t)sms * 8;
+    static const int resident[2] = {occupancy(swiglu_kernel<false>), occupancy(swiglu_kernel<true>)};
+    if (blocks > (int64_t)sms * resident[backward]) blocks = (int64_t)sms * resident[backward];
     return backward ? launch_pdl(swiglu_kernel<true>, p, blocks, stream)
                     : launch_pdl(swiglu_kernel<false>, p, blocks, stream);
 }

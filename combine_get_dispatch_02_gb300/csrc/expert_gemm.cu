@@ -48,9 +48,12 @@ constexpr int kTileRing = 2;      // tiles looked up ahead
 constexpr int kNextRing = 4;      // tile numbers on their way to the second CTA
 constexpr int kScaleGroup = 4;    // 128-channel blocks per fill of the scale buffer
 constexpr int kMaxSmem = 232448;
+// Mean rows per expert from which the e4m3 products take the row form.  Up to 128
+// rows the column form needs one tile and the weights' bytes bound it (64
+// experts x 4096 x 7168, gate: 305 us, row form 461); with 144 rows in two
+// tiles it takes 508 us, the row form 463.
+constexpr int kRowFormRows = 136;
 constexpr int kSortExperts = 256;  // wgrad: most experts that are put in order
-// mean rows per expert from which the e4m3 products take the row form
-constexpr int kRowFormRows = 160;
 
 // Tensor maps: [0] the M-side operand, [1..4] the token rows in boxes of 128,
 // 64, 32 and 16 rows (wgrad: [1] x), [5] the output of the e4m3 row form
