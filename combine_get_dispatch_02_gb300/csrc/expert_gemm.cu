@@ -54,6 +54,7 @@ constexpr int kMaxSmem = 232448;
 // tiles it takes 508 us, the row form 463.
 constexpr int kRowFormRows = 136;
 constexpr int kSortExperts = 256;  // wgrad: most experts that are put in order
+constexpr int kKeepExperts = 256;  // most experts whose counts and bases are kept in shared memory
 
 // Tensor maps: [0] the M-side operand, [1..4] the token rows in boxes of 128,
 // 64, 32 and 16 rows (wgrad: [1] x), [5] the output of the e4m3 row form
@@ -113,10 +114,17 @@ struct Bars {
     uint32_t tmem;
 };
 
+// The layout's counts and bases in shared memory (nullptr: too many experts,
+// they are read from global memory).
+struct Kept {
+    const int64_t *base;
+    const int *count;
+};
+
 // Tile number t.  before[e]: token tiles of the experts before e (wgrad: the
 // experts by falling row count).
 template <ExpertOp OP, bool ALT>
-__device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *before, int t, int wtiles) {
+__device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *before, const Kept &kept, int t, int wtiles) {
     using S = Shape<OP, ALT>;
     Tile r;
     if constexpr (S::WG) {
@@ -127,8 +135,8 @@ __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *be
         r.e = p.E <= kSortExperts ? before[i] : i;
         r.w0 = local / ctiles * S::WROWS;
         r.c0 = local % ctiles * 256;
-        r.row0 = __ldg(p.base + r.e);
-        r.valid = __ldg(p.count + r.e);
+        r.row0 = kept.base != nullptr ? kept.base[r.e] : __ldg(p.base + r.e);
+        r.valid = kept.base != nullptr ? kept.count[r.e] : __ldg(p.count + r.e);
         r.nt = p.k - r.c0 > 128 ? 256 : 128;
     } else {
         const int q = t / wtiles;
@@ -143,13 +151,13 @@ __device__ __forceinline__ Tile tile_at(const ExpertGemmParams &p, const int *be
         r.e = lo;
         const int tt = before[lo + 1] - before[lo];
         const int local = t - before[lo] * wtiles;
-        const int cnt = __ldg(p.count + lo);
+        const int cnt = kept.base != nullptr ? kept.count[lo] : __ldg(p.count + lo);
         // equal token tiles, in steps of 32 rows (row form: whole ones and the rest)
         const int size = S::ROW ? S::TOKENS : ((cnt + tt - 1) / tt + 31) & ~31;
         const int r0 = local % tt * size;
         r.w0 = local / tt * S::WROWS;
         r.c0 = 0;
-        r.row0 = __ldg(p.base + lo) + r0;
+        r.row0 = (kept.base != nullptr ? kept.base[lo] : __ldg(p.base + lo)) + r0;
         r.valid = min(size, cnt - r0);
         r.nt = S::ROW ? 256 : (r.valid + 31) & ~31;
     }
@@ -300,11 +308,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
         bar_init_fence();
         for (int i = 0; i < (S::WG ? 2 : 5); ++i) prefetch_map(&maps.m[i]);
     }
+    __syncwarp();
+    cluster_arrive();  // the barriers are initialised; waited for below
     if (warp == kWarpMma) tmem_alloc(saddr(&bars.tmem), 512);
     pdl_wait();  // the layout, the rows and possibly the weights come from kernels queued before
-    // token tiles of the experts before each one
+    // token tiles of the experts before each one, and behind them the counts and bases (wgrad: the
+    // experts in order, and no room for those)
+    Kept kept = {nullptr, nullptr};
+    if (!S::WG && p.E <= kKeepExperts) {
+        int64_t *kb = reinterpret_cast<int64_t *>(before + ((p.E + 2) & ~1));
+        int *kc = reinterpret_cast<int *>(kb + p.E);
+        kept.base = kb;
+        kept.count = kc;
+        if (tid < p.E) {
+            kc[tid] = __ldg(p.count + tid);
+            kb[tid] = __ldg(p.base + tid);
+        }
+        __syncthreads();
+    }
     if constexpr (!S::WG) {
-        for (int e = tid; e < p.E; e += S::THREADS) before[e + 1] = (__ldg(p.count + e) + S::TOKENS - 1) / S::TOKENS;
+        for (int e = tid; e < p.E; e += S::THREADS)
+            before[e + 1] = ((kept.base != nullptr ? kept.count[e] : __ldg(p.count + e)) + S::TOKENS - 1) / S::TOKENS;
         if (tid == 0) before[0] = 0;
         __syncthreads();
         if (warp == 0) {
@@ -329,27 +353,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 }
             }
         }
-    }
-    if constexpr (S::WG) {
+    } else if (p.E <= kSortExperts) {
         // long sums first: tiles are handed out in this order, and a long one at the end would be
         // waited for alone
-        if (p.E <= kSortExperts) {
-            const int c = tid < p.E ? __ldg(p.count + tid) : -1;
-            if (tid < p.E) before[tid] = c;
-            __syncthreads();
-            int at = 0;
-            if (tid < p.E)
-                for (int e = 0; e < p.E; ++e) {
-                    const int o = before[e];
-                    at += o > c || (o == c && e < tid) ? 1 : 0;
-                }
-            __syncthreads();
-            if (tid < p.E) before[at] = tid;
-        }
+        const int c = tid < p.E ? __ldg(p.count + tid) : -1;
+        if (tid < p.E) before[tid] = c;
+        __syncthreads();
+        int at = 0;
+        if (tid < p.E)
+            for (int e = 0; e < p.E; ++e) {
+                const int o = before[e];
+                at += o > c || (o == c && e < tid) ? 1 : 0;
+            }
+        __syncthreads();
+        if (tid < p.E) before[at] = tid;
     }
     fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_wait();
     fence_after();
     const uint32_t tmem = bars.tmem;
 
@@ -407,11 +428,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 const int s = i % kTileRing;
                 Tile ti;
                 ti.e = -1;
-                if (t < total) ti = tile_at<OP, ALT>(p, before, t, wtiles);
+                if (t < total) ti = tile_at<OP, ALT>(p, before, kept, t, wtiles);
                 if (!(ok = bar_wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
                 bars.tiles[s] = ti;
                 bar_arrive(b_kfull + 8 * s);
-                if (t >= total) break;
+                if (t >= total) {
+                    // the second CTA's arrivals are here before this CTA ends
+                    if (drawn && rank == 0)
+                        for (int j = max(0, i - kNextRing + 1); j <= i && ok; ++j)
+                            ok = bar_wait(saddr(&bars.nempty[j % kNextRing]), (j / kNextRing) & 1);
+                    break;
+                }
             }
             // the last pair to stop drawing puts the counter back for the next launch
             if (drawn && rank == 0 && atomicAdd(p.next + 1, 1u) == (uint32_t)pairs - 1) {
@@ -539,6 +566,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if (++st == S::STAGES) st = 0, ph ^= 1;
                 }
             }
+            // the last accumulators have been read: the second CTA's arrivals are here before this CTA ends
+            for (uint32_t i = 1; i <= 2 && i <= seg && ok; ++i)
+                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * ((seg - i) & 1), ((seg - i) >> 1) & 1));
         }
     } else if (warp == kWarpAux) {
         if constexpr (S::FP8) {
@@ -1024,7 +1054,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
     if (!ok) atomicOr(p.status, kStatusTimeout);
     __syncwarp();
     fence_before();
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
     fence_after();
     if (warp == kWarpMma) tmem_free(tmem, 512);
 }
@@ -1063,7 +1094,8 @@ bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows
 
 template <ExpertOp OP, bool ALT>
 size_t smem_bytes(int E) {
-    return Shape<OP, ALT>::fixed + (Shape<OP, ALT>::WG ? (size_t)kSortExperts * 4 : ((size_t)E + 1) * 4);
+    if (Shape<OP, ALT>::WG) return Shape<OP, ALT>::fixed + (size_t)kSortExperts * 4;
+    return Shape<OP, ALT>::fixed + (((size_t)E + 2) & ~(size_t)1) * 4 + (E <= kKeepExperts ? (size_t)E * 12 : 0);
 }
 
 template <ExpertOp OP, bool ALT>
