@@ -739,6 +739,7 @@ ep_status ep_create(const ep_config *cfg, ep_ctx **out) {
     ctx->identity_bps_fp8 = ep::identity_blocks_per_sm(true);
     ep::dispatch_init();
     ep::move_init();
+    ep::expert_gemm_init();
     if (cudaMalloc(&ctx->d_status, sizeof(uint32_t)) != cudaSuccess) {
         cudaGetLastError();
         free(ctx);

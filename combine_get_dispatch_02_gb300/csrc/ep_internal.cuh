@@ -227,6 +227,8 @@ struct ExpertGemmParams {
 // Tile counters of a handle (two words each), taken in turn, so that operators
 // of one handle may run side by side.
 constexpr int kTileCounters = 32;
+// One-time set-up with the device current (shared memory limits).
+void expert_gemm_init();
 cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream);
 
 // ------------------------------------------------------------------ gated activation, weight cast

@@ -109,6 +109,7 @@ struct Bars {
     uint64_t full[6], empty[6], land[6];
     uint64_t tfull[2], tempty[2], sfull[2], sempty[2], kfull[kTileRing], kempty[kTileRing];
     uint64_t nfull[kNextRing], nempty[kNextRing];
+    uint64_t amax[4];
     Tile tiles[kTileRing];
     int next[kNextRing];
     uint32_t tmem;
@@ -298,13 +299,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
         }
         for (int i = 0; i < kTileRing; ++i) {
             bar_init(b_kfull + 8 * i, 1);
-            // readers: the reading warps, the loader, the first CTA's product thread, the auxiliary warp
+            // readers: the reading warps, the loader, the first CTA's product warp, the auxiliary warp
             bar_init(b_kempty + 8 * i, S::READ + 1 + (rank == 0 ? 1 : 0) + (S::FP8 || S::WG ? 1 : 0));
         }
         for (int i = 0; i < kNextRing; ++i) {
             bar_init(saddr(&bars.nfull[i]), 1);
             bar_init(saddr(&bars.nempty[i]), 1);
         }
+        for (int i = 0; i < 4; ++i) bar_init(saddr(&bars.amax[i]), 4);
         bar_init_fence();
         for (int i = 0; i < (S::WG ? 2 : 5); ++i) prefetch_map(&maps.m[i]);
     }
@@ -391,284 +393,291 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
         if (lane == 0) bar_arrive(b_kempty + 8 * s);
         return ti.e >= 0;
     };
+    // The four warps that share a block's maximum (gate): all have written theirs.
+    auto amax_ready = [&](int group, uint32_t turn) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(saddr(&bars.amax[group]));
+        ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(&bars.amax[group]), turn & 1));
+        return ok;
+    };
     if (warp >= S::READ) {
-    regs_dec<S::REGS_REST>();
-    if (warp == kWarpTiles) {
-        // Hands the pair's tiles out, looked up ahead of the others (a search, divisions and two
-        // loads from L2).  The first tile is the pair's own number, the others come from a counter in
-        // global memory, so that pairs with short tiles take more of them and the tiles of one
-        // expert, which share its weights in L2, start together.  The first CTA draws the numbers and
-        // sends them to the second.
-        if (lane == 0) {
-            const bool drawn = total > pairs;
-            int t = pair;
-            for (int i = 0; ok; ++i) {
-                const int n = i % kNextRing;
-                if (drawn && i > 0) {
-                    const uint32_t full = saddr(&bars.nfull[n]), empty = saddr(&bars.nempty[n]);
-                    if (rank == 0) {
-                        t = pairs + (int)atomicAdd(p.next, 1u);
-                        if (!(ok = bar_wait(empty, ((i / kNextRing) & 1) ^ 1))) break;
-                        send_u32(map_rank(saddr(&bars.next[n]), 1), (uint32_t)t, map_rank(full, 1));
-                    } else {
-                        bar_expect(full, 4);
-                        if (!(ok = bar_wait(full, (i / kNextRing) & 1))) break;
-                        t = bars.next[n];
-                        bar_arrive_cluster(map_rank(empty, 0));
-                    }
-                } else if (drawn) {
-                    // the first round of ring place 0 stands for the first tile, which nobody sends
-                    if (rank == 1) {
-                        bar_arrive(saddr(&bars.nfull[0]));
-                        bar_arrive_cluster(map_rank(saddr(&bars.nempty[0]), 0));
-                    }
-                } else if (i > 0) {
-                    t = total;
-                }
-                const int s = i % kTileRing;
-                Tile ti;
-                ti.e = -1;
-                if (t < total) ti = tile_at<OP, ALT>(p, before, kept, t, wtiles);
-                if (!(ok = bar_wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
-                bars.tiles[s] = ti;
-                bar_arrive(b_kfull + 8 * s);
-                if (t >= total) {
-                    // the second CTA's arrivals are here before this CTA ends
-                    if (drawn && rank == 0)
-                        for (int j = max(0, i - kNextRing + 1); j <= i && ok; ++j)
-                            ok = bar_wait(saddr(&bars.nempty[j % kNextRing]), (j / kNextRing) & 1);
-                    break;
-                }
-            }
-            // the last pair to stop drawing puts the counter back for the next launch
-            if (drawn && rank == 0 && atomicAdd(p.next + 1, 1u) == (uint32_t)pairs - 1) {
-                p.next[0] = 0;
-                p.next[1] = 0;
-            }
-        }
-    } else if (warp == kWarpLoad) {
-        int st = 0;
-        uint32_t ph = 0;
-        int used = 0;
-        Tile ti;
-        for (int i = 0; ok; ++i) {
-            if (!next_tile(ti, i)) break;
-            const int nk = stages_of(ti);
-            // rows that each CTA loads on the token side
-            const int half = ti.nt >> 1;
-            const int mine = S::ROW ? min(128, max(0, (ti.valid - (int)rank * 128 + 15) & ~15)) : half;
-            const uint32_t bytes = (S::ROW ? S::B_BYTES : S::A_BYTES) + mine * 128;
-            const uint32_t both = S::ROW ? 2 * S::B_BYTES + min(256, (ti.valid + 15) & ~15) * 128 : 2 * bytes;
-            for (int kb = 0; kb < nk; ++kb) {
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph ^ 1));
-                if (!ok) break;
-                const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
-                const uint32_t full0 = map_rank(b_full + 8 * st, 0);
-                if (elect()) {
-                    uint32_t bar = full0;
-                    if constexpr (S::WG) {
-                        if (kb == nk - 1 && (ti.valid & 63) != 0) {
-                            // the rows past the end are cleared before the products see the stage
-                            bar = map_rank(b_land + 8 * st, rank);
-                            bar_expect(b_land + 8 * st, bytes);
-                        } else if (rank == 0) {
-                            bar_expect(b_full + 8 * st, 2 * bytes);
-                            bar_arrive(b_full + 8 * st);  // for the other CTA
-                        }
-                        const int r = (int)(ti.row0 + kb * 64);
-                        const int n0 = ti.w0 + (int)rank * 128, c0 = ti.c0 + (int)rank * half;
-                        tma_2d(a, &maps.m[0], n0, r, bar);
-                        tma_2d(a + 8192, &maps.m[0], n0 + 64, r, bar);
-                        tma_2d(b, &maps.m[1], c0, r, bar);
-                        if (half > 64) tma_2d(b + 8192, &maps.m[1], c0 + 64, r, bar);
-                    } else {
-                        if (rank == 0) bar_expect(b_full + 8 * st, both);
-                        const int kc = kb * S::KSTEP, w = ti.w0 + (int)rank * 128;
-                        if constexpr (S::ROW) {
-                            // gate: the first CTA's half of the columns is the gate's, the second's the up product's
-                            tma_3d(b, &maps.m[0], kc, S::GATE ? ti.w0 + (int)rank * width : w, ti.e, bar);
-                        } else if constexpr (S::A_MN) {
-                            tma_3d(a, &maps.m[0], w, kc, ti.e, bar);
-                            tma_3d(a + 8192, &maps.m[0], w + 64, kc, ti.e, bar);
+        regs_dec<S::REGS_REST>();
+        if (warp == kWarpTiles) {
+            // Hands the pair's tiles out, looked up ahead of the others (a search, divisions and two
+            // loads from L2).  The first tile is the pair's own number, the others come from a counter in
+            // global memory, so that pairs with short tiles take more of them and the tiles of one
+            // expert, which share its weights in L2, start together.  The first CTA draws the numbers and
+            // sends them to the second.
+            if (lane == 0) {
+                const bool drawn = total > pairs;
+                int t = pair;
+                for (int i = 0; ok; ++i) {
+                    const int n = i % kNextRing;
+                    if (drawn && i > 0) {
+                        const uint32_t full = saddr(&bars.nfull[n]), empty = saddr(&bars.nempty[n]);
+                        if (rank == 0) {
+                            t = pairs + (int)atomicAdd(p.next, 1u);
+                            if (!(ok = bar_wait(empty, ((i / kNextRing) & 1) ^ 1))) break;
+                            send_u32(map_rank(saddr(&bars.next[n]), 1), (uint32_t)t, map_rank(full, 1));
                         } else {
-                            tma_3d(a, &maps.m[0], kc, w, ti.e, bar);
-                            if constexpr (S::COL) tma_3d(a + 16384, &maps.m[0], kc, w + (S::GATE ? width : 256), ti.e, bar);
+                            bar_expect(full, 4);
+                            if (!(ok = bar_wait(full, (i / kNextRing) & 1))) break;
+                            t = bars.next[n];
+                            bar_arrive_cluster(map_rank(empty, 0));
                         }
-                        int r = (int)ti.row0 + (int)rank * (S::ROW ? 128 : half);
-                        uint32_t d = S::ROW ? a : b;
+                    } else if (drawn) {
+                        // the first round of ring place 0 stands for the first tile, which nobody sends
+                        if (rank == 1) {
+                            bar_arrive(saddr(&bars.nfull[0]));
+                            bar_arrive_cluster(map_rank(saddr(&bars.nempty[0]), 0));
+                        }
+                    } else if (i > 0) {
+                        t = total;
+                    }
+                    const int s = i % kTileRing;
+                    Tile ti;
+                    ti.e = -1;
+                    if (t < total) ti = tile_at<OP, ALT>(p, before, kept, t, wtiles);
+                    if (!(ok = bar_wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
+                    bars.tiles[s] = ti;
+                    bar_arrive(b_kfull + 8 * s);
+                    if (t >= total) {
+                        // the second CTA's arrivals are here before this CTA ends
+                        if (drawn && rank == 0)
+                            for (int j = max(0, i - kNextRing + 1); j <= i && ok; ++j)
+                                ok = bar_wait(saddr(&bars.nempty[j % kNextRing]), (j / kNextRing) & 1);
+                        break;
+                    }
+                }
+                // the last pair to stop drawing puts the counter back for the next launch
+                if (drawn && rank == 0 && atomicAdd(p.next + 1, 1u) == (uint32_t)pairs - 1) {
+                    p.next[0] = 0;
+                    p.next[1] = 0;
+                }
+            }
+        } else if (warp == kWarpLoad) {
+            int st = 0;
+            uint32_t ph = 0;
+            int used = 0;
+            Tile ti;
+            for (int i = 0; ok; ++i) {
+                if (!next_tile(ti, i)) break;
+                const int nk = stages_of(ti);
+                // rows that each CTA loads on the token side
+                const int half = ti.nt >> 1;
+                const int mine = S::ROW ? min(128, max(0, (ti.valid - (int)rank * 128 + 15) & ~15)) : half;
+                const uint32_t bytes = (S::ROW ? S::B_BYTES : S::A_BYTES) + mine * 128;
+                const uint32_t both = S::ROW ? 2 * S::B_BYTES + min(256, (ti.valid + 15) & ~15) * 128 : 2 * bytes;
+                for (int kb = 0; kb < nk; ++kb) {
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph ^ 1));
+                    if (!ok) break;
+                    const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
+                    const uint32_t full0 = map_rank(b_full + 8 * st, 0);
+                    if (elect()) {
+                        uint32_t bar = full0;
+                        if constexpr (S::WG) {
+                            if (kb == nk - 1 && (ti.valid & 63) != 0) {
+                                // the rows past the end are cleared before the products see the stage
+                                bar = map_rank(b_land + 8 * st, rank);
+                                bar_expect(b_land + 8 * st, bytes);
+                            } else if (rank == 0) {
+                                bar_expect(b_full + 8 * st, 2 * bytes);
+                                bar_arrive(b_full + 8 * st);  // for the other CTA
+                            }
+                            const int r = (int)(ti.row0 + kb * 64);
+                            const int n0 = ti.w0 + (int)rank * 128, c0 = ti.c0 + (int)rank * half;
+                            tma_2d(a, &maps.m[0], n0, r, bar);
+                            tma_2d(a + 8192, &maps.m[0], n0 + 64, r, bar);
+                            tma_2d(b, &maps.m[1], c0, r, bar);
+                            if (half > 64) tma_2d(b + 8192, &maps.m[1], c0 + 64, r, bar);
+                        } else {
+                            if (rank == 0) bar_expect(b_full + 8 * st, both);
+                            const int kc = kb * S::KSTEP, w = ti.w0 + (int)rank * 128;
+                            if constexpr (S::ROW) {
+                                // gate: the first CTA's half of the columns is the gate's, the second's the up product's
+                                tma_3d(b, &maps.m[0], kc, S::GATE ? ti.w0 + (int)rank * width : w, ti.e, bar);
+                            } else if constexpr (S::A_MN) {
+                                tma_3d(a, &maps.m[0], w, kc, ti.e, bar);
+                                tma_3d(a + 8192, &maps.m[0], w + 64, kc, ti.e, bar);
+                            } else {
+                                tma_3d(a, &maps.m[0], kc, w, ti.e, bar);
+                                if constexpr (S::COL) tma_3d(a + 16384, &maps.m[0], kc, w + (S::GATE ? width : 256), ti.e, bar);
+                            }
+                            int r = (int)ti.row0 + (int)rank * (S::ROW ? 128 : half);
+                            uint32_t d = S::ROW ? a : b;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int h = 128 >> j;
-                            if (mine & h) {
-                                tma_2d(d, &maps.m[1 + j], kc, r, bar);
-                                r += h;
-                                d += h * 128;
+                            for (int j = 0; j < 4; ++j) {
+                                const int h = 128 >> j;
+                                if (mine & h) {
+                                    tma_2d(d, &maps.m[1 + j], kc, r, bar);
+                                    r += h;
+                                    d += h * 128;
+                                }
                             }
                         }
                     }
-                }
-                __syncwarp();
-                used = min(used + 1, S::STAGES);
-                if (++st == S::STAGES) st = 0, ph ^= 1;
-            }
-        }
-        // the stages in flight have been read (nothing lands or arrives here after the kernel's end)
-        for (int i = 0; i < used; ++i) {
-            if (--st < 0) st = S::STAGES - 1, ph ^= 1;
-            if (!__all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph))) {
-                ok = false;
-                atomicOr(p.status, kStatusInFlight);
-                break;
-            }
-        }
-    } else if (warp == kWarpMma) {
-        if (rank == 0) {
-            int st = 0;
-            uint32_t ph = 0, seg = 0;
-            Tile ti;
-            for (int i = 0; ok; ++i) {
-                if (!next_tile(ti, i)) break;
-                const int nk = stages_of(ti);
-                const uint32_t id = idesc(S::FP8, S::A_MN, S::B_MN, ti.nt);
-                for (int kb = 0; kb < nk; ++kb) {
-                    const int in_seg = S::SEG == 0 ? kb : kb % (S::SEG == 0 ? 1 : S::SEG);
-                    const uint32_t buf = seg & 1;
-                    // the operands first: they are there long before the accumulator is read out
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_full + 8 * st, ph));
-                    if (!ok) break;
-                    if (in_seg == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1));
-                        if (!ok) break;
-                    }
-                    if constexpr (S::WG) {
-                        if (kb == nk - 1) fence_acquire_cluster();  // the cleared lines of both CTAs
-                    }
-                    fence_after();
-                    const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
-                    const uint32_t d = tmem + buf * 256;
-                    const int steps = S::WG ? (min(64, ti.valid - kb * 64) + 15) / 16 : 4;
-                    const bool ends = kb == nk - 1 || (S::SEG != 0 && in_seg == S::SEG - 1);
-                    if (elect()) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (S::WG && j >= steps) break;
-                            const uint64_t da = desc(a + j * (S::A_MN ? 2048 : 32), S::A_MN ? 8192 : 16);
-                            const uint64_t db = desc(b + j * (S::B_MN ? 2048 : 32), S::B_MN ? 8192 : 16);
-                            mma<S::FP8>(d, da, db, id, in_seg != 0 || j != 0);
-                            if constexpr (S::COL)
-                                mma<S::FP8>(d + 128, desc(a + 16384 + j * 32, 16), db, id, in_seg != 0 || j != 0);
-                        }
-                        commit_pair(b_empty + 8 * st);
-                        if (ends) commit_pair(b_tfull + 8 * buf);
-                    }
                     __syncwarp();
-                    if (ends) ++seg;
+                    used = min(used + 1, S::STAGES);
                     if (++st == S::STAGES) st = 0, ph ^= 1;
                 }
             }
-            // the last accumulators have been read: the second CTA's arrivals are here before this CTA ends
-            for (uint32_t i = 1; i <= 2 && i <= seg && ok; ++i)
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * ((seg - i) & 1), ((seg - i) >> 1) & 1));
-        }
-    } else if (warp == kWarpAux) {
-        if constexpr (S::FP8) {
-            // scales of 128 rows (row form: of this CTA), xs * ws with the two blocks of weight rows, for
-            // kScaleGroup blocks at a time; the next group's (or tile's) loads are in flight while one is stored
-            const int nb = (p.n + 127) / 128;
-            struct Group {
-                float4 x[4], w, w2;
-            } cur, nxt;
-            uint32_t fill = 0;
-            Tile ti = {};
-            int i = 0, g = 0;
-            auto fetch = [&](Group &o) {
-                const int r0 = S::ROW ? (int)rank * 128 : 0;
-                const int b0 = S::ROW ? ti.w0 / 128 : ti.w0 / 128 + (int)rank;
-                const int b1 = b0 + (S::GATE ? width / 128 : S::ROW ? 1 : 2);
-                auto four = [&](const float *q, bool vec) {
-                    float4 v;
-                    if (vec) {
-                        v = __ldg(reinterpret_cast<const float4 *>(q));
-                    } else {
-                        v.x = __ldg(q);
-                        v.y = g + 1 < kchan ? __ldg(q + 1) : 0.0f;
-                        v.z = g + 2 < kchan ? __ldg(q + 2) : 0.0f;
-                        v.w = g + 3 < kchan ? __ldg(q + 3) : 0.0f;
+            // the stages in flight have been read (nothing lands or arrives here after the kernel's end)
+            for (int i = 0; i < used; ++i) {
+                if (--st < 0) st = S::STAGES - 1, ph ^= 1;
+                if (!__all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph))) {
+                    ok = false;
+                    atomicOr(p.status, kStatusInFlight);
+                    break;
+                }
+            }
+        } else if (warp == kWarpMma) {
+            if (rank == 0) {
+                int st = 0;
+                uint32_t ph = 0, seg = 0;
+                Tile ti;
+                for (int i = 0; ok; ++i) {
+                    if (!next_tile(ti, i)) break;
+                    const int nk = stages_of(ti);
+                    const uint32_t id = idesc(S::FP8, S::A_MN, S::B_MN, ti.nt);
+                    for (int kb = 0; kb < nk; ++kb) {
+                        const int in_seg = S::SEG == 0 ? kb : kb % (S::SEG == 0 ? 1 : S::SEG);
+                        const uint32_t buf = seg & 1;
+                        // the operands first: they are there long before the accumulator is read out
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_full + 8 * st, ph));
+                        if (!ok) break;
+                        if (in_seg == 0) {
+                            ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1));
+                            if (!ok) break;
+                        }
+                        if constexpr (S::WG) {
+                            if (kb == nk - 1) fence_acquire_cluster();  // the cleared lines of both CTAs
+                        }
+                        fence_after();
+                        const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
+                        const uint32_t d = tmem + buf * 256;
+                        const int steps = S::WG ? (min(64, ti.valid - kb * 64) + 15) / 16 : 4;
+                        const bool ends = kb == nk - 1 || (S::SEG != 0 && in_seg == S::SEG - 1);
+                        if (elect()) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if (S::WG && j >= steps) break;
+                                const uint64_t da = desc(a + j * (S::A_MN ? 2048 : 32), S::A_MN ? 8192 : 16);
+                                const uint64_t db = desc(b + j * (S::B_MN ? 2048 : 32), S::B_MN ? 8192 : 16);
+                                mma<S::FP8>(d, da, db, id, in_seg != 0 || j != 0);
+                                if constexpr (S::COL)
+                                    mma<S::FP8>(d + 128, desc(a + 16384 + j * 32, 16), db, id, in_seg != 0 || j != 0);
+                            }
+                            commit_pair(b_empty + 8 * st);
+                            if (ends) commit_pair(b_tfull + 8 * buf);
+                        }
+                        __syncwarp();
+                        if (ends) ++seg;
+                        if (++st == S::STAGES) st = 0, ph ^= 1;
                     }
-                    return v;
+                }
+                // the last accumulators have been read: the second CTA's arrivals are here before this CTA ends
+                for (uint32_t i = 1; i <= 2 && i <= seg && ok; ++i)
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * ((seg - i) & 1), ((seg - i) >> 1) & 1));
+            }
+        } else if (warp == kWarpAux) {
+            if constexpr (S::FP8) {
+                // scales of 128 rows (row form: of this CTA), xs * ws with the two blocks of weight rows, for
+                // kScaleGroup blocks at a time; the next group's (or tile's) loads are in flight while one is stored
+                const int nb = (p.n + 127) / 128;
+                struct Group {
+                    float4 x[4], w, w2;
+                } cur, nxt;
+                uint32_t fill = 0;
+                Tile ti = {};
+                int i = 0, g = 0;
+                auto fetch = [&](Group &o) {
+                    const int r0 = S::ROW ? (int)rank * 128 : 0;
+                    const int b0 = S::ROW ? ti.w0 / 128 : ti.w0 / 128 + (int)rank;
+                    const int b1 = b0 + (S::GATE ? width / 128 : S::ROW ? 1 : 2);
+                    auto four = [&](const float *q, bool vec) {
+                        float4 v;
+                        if (vec) {
+                            v = __ldg(reinterpret_cast<const float4 *>(q));
+                        } else {
+                            v.x = __ldg(q);
+                            v.y = g + 1 < kchan ? __ldg(q + 1) : 0.0f;
+                            v.z = g + 2 < kchan ? __ldg(q + 2) : 0.0f;
+                            v.w = g + 3 < kchan ? __ldg(q + 3) : 0.0f;
+                        }
+                        return v;
+                    };
+                    const float *ws = p.ws + (int64_t)ti.e * nb * kchan + g;
+                    o.w = four(ws + (int64_t)min(b0, nb - 1) * kchan, p.ws_vec);
+                    o.w2 = four(ws + (int64_t)min(b1, nb - 1) * kchan, p.ws_vec);
+#pragma unroll
+                    for (int j0 = 0; j0 < 128; j0 += 32) {
+                        const int j = r0 + j0 + lane;
+                        o.x[j0 / 32] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (j < ti.valid) o.x[j0 / 32] = four(p.xs + (ti.row0 + j) * kchan + g, p.xs_vec);
+                    }
                 };
-                const float *ws = p.ws + (int64_t)ti.e * nb * kchan + g;
-                o.w = four(ws + (int64_t)min(b0, nb - 1) * kchan, p.ws_vec);
-                o.w2 = four(ws + (int64_t)min(b1, nb - 1) * kchan, p.ws_vec);
-#pragma unroll
-                for (int j0 = 0; j0 < 128; j0 += 32) {
-                    const int j = r0 + j0 + lane;
-                    o.x[j0 / 32] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (j < ti.valid) o.x[j0 / 32] = four(p.xs + (ti.row0 + j) * kchan + g, p.xs_vec);
-                }
-            };
-            bool more = next_tile(ti, 0);
-            if (more) fetch(cur);
-            while (more) {
-                // on to the next group
-                g += kScaleGroup;
-                if (g >= kchan) {
-                    g = 0;
-                    more = next_tile(ti, ++i);
-                    if (!ok) break;
-                }
-                if (more) fetch(nxt);
-                const uint32_t buf = fill & 1;
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
-                if (!ok) break;
-                float *out = scales + buf * kScaleGroup * 256;
-#pragma unroll
-                for (int j0 = 0; j0 < 128; j0 += 32) {
-                    const int at = S::ROW ? j0 + lane : scale_at(j0 + lane);
-                    const float4 v = cur.x[j0 / 32];
-                    out[at] = v.x * cur.w.x;
-                    out[256 + at] = v.y * cur.w.y;
-                    out[512 + at] = v.z * cur.w.z;
-                    out[768 + at] = v.w * cur.w.w;
-                    out[128 + at] = v.x * cur.w2.x;
-                    out[384 + at] = v.y * cur.w2.y;
-                    out[640 + at] = v.z * cur.w2.z;
-                    out[896 + at] = v.w * cur.w2.w;
-                }
-                __syncwarp();
-                if (lane == 0) bar_arrive(b_sfull + 8 * buf);
-                ++fill;
-                cur = nxt;
-            }
-        } else if constexpr (S::WG) {
-            // an expert's last rows: clear the lines past its end (both operands
-            // hold one 128-byte line per row and 64 channels), up to the 16 rows of a product
-            int st = 0;
-            uint32_t landed = 0;  // parity of each stage's landing barrier
-            Tile ti;
-            for (int i = 0; ok; ++i) {
-                if (!next_tile(ti, i)) break;
-                const int nk = stages_of(ti);
-                if ((ti.valid & 63) != 0) {
-                    const int s = (st + nk - 1) % S::STAGES;
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_land + 8 * s, (landed >> s) & 1));
-                    if (!ok) break;
-                    landed ^= 1u << s;
-                    uint8_t *base = smem + s * S::STAGE;
-                    const int r0 = ti.valid & 63, r1 = (r0 + 15) & ~15;
-                    for (int i = lane; i < (r1 - r0) * 32; i += 32) {
-                        const int row = r0 + (i >> 5), piece = i & 31;  // 4 chunks x 8 pieces of 16 bytes
-                        *reinterpret_cast<uint4 *>(base + (piece >> 3) * 8192 + row * 128 + (piece & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
+                bool more = next_tile(ti, 0);
+                if (more) fetch(cur);
+                while (more) {
+                    // on to the next group
+                    g += kScaleGroup;
+                    if (g >= kchan) {
+                        g = 0;
+                        more = next_tile(ti, ++i);
+                        if (!ok) break;
                     }
-                    fence_async_shared();
+                    if (more) fetch(nxt);
+                    const uint32_t buf = fill & 1;
+                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
+                    if (!ok) break;
+                    float *out = scales + buf * kScaleGroup * 256;
+#pragma unroll
+                    for (int j0 = 0; j0 < 128; j0 += 32) {
+                        const int at = S::ROW ? j0 + lane : scale_at(j0 + lane);
+                        const float4 v = cur.x[j0 / 32];
+                        out[at] = v.x * cur.w.x;
+                        out[256 + at] = v.y * cur.w.y;
+                        out[512 + at] = v.z * cur.w.z;
+                        out[768 + at] = v.w * cur.w.w;
+                        out[128 + at] = v.x * cur.w2.x;
+                        out[384 + at] = v.y * cur.w2.y;
+                        out[640 + at] = v.z * cur.w2.z;
+                        out[896 + at] = v.w * cur.w2.w;
+                    }
                     __syncwarp();
-                    if (lane == 0) bar_arrive_cluster(map_rank(b_full + 8 * s, 0));
+                    if (lane == 0) bar_arrive(b_sfull + 8 * buf);
+                    ++fill;
+                    cur = nxt;
                 }
-                st = (st + nk) % S::STAGES;
+            } else if constexpr (S::WG) {
+                // an expert's last rows: clear the lines past its end (both operands
+                // hold one 128-byte line per row and 64 channels), up to the 16 rows of a product
+                int st = 0;
+                uint32_t landed = 0;  // parity of each stage's landing barrier
+                Tile ti;
+                for (int i = 0; ok; ++i) {
+                    if (!next_tile(ti, i)) break;
+                    const int nk = stages_of(ti);
+                    if ((ti.valid & 63) != 0) {
+                        const int s = (st + nk - 1) % S::STAGES;
+                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_land + 8 * s, (landed >> s) & 1));
+                        if (!ok) break;
+                        landed ^= 1u << s;
+                        uint8_t *base = smem + s * S::STAGE;
+                        const int r0 = ti.valid & 63, r1 = (r0 + 15) & ~15;
+                        for (int i = lane; i < (r1 - r0) * 32; i += 32) {
+                            const int row = r0 + (i >> 5), piece = i & 31;  // 4 chunks x 8 pieces of 16 bytes
+                            *reinterpret_cast<uint4 *>(base + (piece >> 3) * 8192 + row * 128 + (piece & 7) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_shared();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive_cluster(map_rank(b_full + 8 * s, 0));
+                    }
+                    st = (st + nk) % S::STAGES;
+                }
             }
         }
-    }
     } else {
         regs_inc<S::REGS_READ>();
         const int sub = warp & 3, hw = warp >> 2;  // lanes 32 * sub .., every second chunk of 32 columns
@@ -858,12 +867,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                                 }
                             }
                             float *am = amaxs + ((turn & 1) * 2 + hw) * 256;
-                            ++turn;
                             const int j0 = (lane >> 4 & 1) * 8 + (lane >> 3 & 1) * 4 + (lane >> 2 & 1) * 2;
                             am[sub * 64 + 4 * j0 + c4] = top[0];
                             am[sub * 64 + 4 * j0 + 4 + c4] = top[1];
                             // over the block's 128 channels: the four warps of these columns
-                            asm volatile("bar.sync %0, 128;" ::"r"(1 + hw) : "memory");
+                            if (!amax_ready(hw, turn++)) break;
                             const int h0 = ti.w0 + (int)rank * 128;
                             float *inv = amaxs + 1024 + warp * 64;  // [column % 4][column / 4]
 #pragma unroll
@@ -943,9 +951,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             top = fmaxf(top, fmaxf(fabsf(a0), fabsf(a1)));
                         }
                     float *am = amaxs + (turn & 1) * 512;
-                    ++turn;
                     am[hw * 128 + row] = top;
-                    asm volatile("bar.sync %0, 128;" ::"r"(1 + sub) : "memory");
+                    if (!amax_ready(sub, turn++)) break;
                     const float a = fmaxf(fmaxf(fmaxf(am[row], am[128 + row]), fmaxf(am[256 + row], am[384 + row])), 1e-4f);
                     const float inv = __fdiv_rn(448.0f, a);
                     if (hw == 0 && lane < rows) p.ys[(row0 + lane) * (width / 128) + ti.w0 / 128] = __fdiv_rn(a, 448.0f);
@@ -1118,13 +1125,6 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
         if constexpr (S::ROW && !S::GATE) ok = ok && encode(&maps.m[5], p.y, 2, p.n, p.rows, 0, 32);
     }
     if (!ok) return cudaErrorInvalidValue;
-    static std::atomic<bool> ready{false};
-    if (!ready.load(std::memory_order_acquire)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(expert_gemm_kernel<OP, ALT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
-        if (e != cudaSuccess) return e;
-        ready.store(true, std::memory_order_release);
-    }
     int pairs = p.sms / 2;
     if (pairs < 1) pairs = 1;
     cudaLaunchConfig_t cfg = {};
@@ -1141,6 +1141,27 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+namespace {
+template <ExpertOp OP, bool ALT>
+void allow_smem() {
+    // failing here means failing at the launch, which reports it
+    if (cudaFuncSetAttribute(expert_gemm_kernel<OP, ALT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024) !=
+        cudaSuccess)
+        cudaGetLastError();
+}
+}  // namespace
+
+void expert_gemm_init() {
+    allow_smem<ExpertOp::kBf16, false>();
+    allow_smem<ExpertOp::kBf16T, false>();
+    allow_smem<ExpertOp::kFp8, false>();
+    allow_smem<ExpertOp::kFp8, true>();
+    allow_smem<ExpertOp::kGateFp8, false>();
+    allow_smem<ExpertOp::kGateFp8, true>();
+    allow_smem<ExpertOp::kWgrad, false>();
+    allow_smem<ExpertOp::kWgrad, true>();
+}
 
 cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream) {
     const bool row = p.live > (int64_t)p.E * kRowFormRows;

@@ -340,6 +340,55 @@ def test_same_bits_every_time_on_any_sm_count():
         assert torch.equal(o[2], outs[0][2])
 
 
+@pytest.mark.parametrize("many", [False, True])
+def test_fp8_same_bits_every_time_on_any_sm_count(many):
+    counts = EDGES_MANY if many else EDGES
+    outs = []
+    for sms in (0, 0, 2, 37):
+        buf, h, grp = group(counts, max_sms=sms)
+        xq = cast_rows(receive(buf.rows, 512, grp, 1).float())
+        w = buf.cast_weights(weights(len(counts), 768, 512, 2))
+        y, (hq, hs) = buf.expert_gemm_fp8(xq, w, h), buf.expert_gate_fp8(xq, w, h)
+        done(buf)
+        used = in_use(buf.rows, grp)
+        outs.append((y[used], hq.view(torch.uint8)[used], hs[used]))
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+def test_more_experts_than_the_kernels_keep_at_hand():
+    """Past 256 experts counts and bases are read as they are needed, and the
+    weights' gradient takes the experts in their own order."""
+    counts = [(7 * e) % 5 for e in range(600)]
+    counts[3], counts[599] = 260, 40
+    buf, h, grp = group(counts)
+    check_gemm(buf, h, grp, 72, 136, False)
+    check_gemm(buf, h, grp, 72, 136, True)
+    check_wgrad(buf, h, grp, 40, 72, torch.float32)
+    check_fp8(buf, h, grp, 72, 128)
+    check_gate(buf, h, grp, 128, 128)
+
+
+def test_operators_of_one_handle_side_by_side():
+    """A step's independent products on two streams: input and weight gradient
+    of one handle, launched over and over without a wait between them."""
+    buf, h, grp = group([300, 0, 17, 640, 128, 1, 77, 256] * 4)
+    used = in_use(buf.rows, grp)
+    dy, x, w = receive(buf.rows, 512, grp, 1), receive(buf.rows, 256, grp, 2), weights(32, 512, 256, 3)
+    want_dx, want_dw = buf.expert_gemm(dy, w, h, transpose_w=True), buf.expert_wgrad(dy, x, h)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    dx, dw = sentinel((buf.rows, 256)), sentinel((32, 512, 256), torch.float32)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        buf.expert_gemm(dy, w, h, transpose_w=True, out=dx)
+        with torch.cuda.stream(side):
+            buf.expert_wgrad(dy, x, h, out=dw)
+    torch.cuda.synchronize()
+    done(buf)
+    assert torch.equal(dx[used], want_dx[used]) and torch.equal(dw, want_dw)
+
+
 def test_on_another_stream_and_in_a_graph():
     buf, h, grp = group([10, 0, 200, 33])
     x, w = receive(buf.rows, 256, grp, 1), weights(4, 512, 256, 2)
