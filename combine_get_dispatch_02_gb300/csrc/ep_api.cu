@@ -647,6 +647,9 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
     if (c.layout == EP_LAYOUT_PADDED && p.max_count > (int64_t)c.num_ranks * c.max_tokens_per_rank)
         p.max_count = (int64_t)c.num_ranks * c.max_tokens_per_rank;
     p.sms = expert_sms(ctx);
+    p.withhold = ctx->hooks.move_withhold_item < c.num_experts ? (int32_t)ctx->hooks.move_withhold_item : -1;
+    // 2 clocks a ns (a little over the fastest clock)
+    p.wait_cycles = ctx->hooks.move_wait_ns > 0 ? 2 * ctx->hooks.move_wait_ns : 1ll << 32;
     p.status = ctx->d_status;
     p.next = reinterpret_cast<uint32_t *>(h->cta_hist + grid_hist_ints(ctx) + 16) +
              2 * (h->tile_counter++ % ep::kTileCounters);

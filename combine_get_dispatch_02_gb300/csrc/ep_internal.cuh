@@ -220,6 +220,8 @@ struct ExpertGemmParams {
     int32_t xs_vec, ws_vec, y_vec;  // set by the launcher: rows of xs / ws can be read 16 bytes, rows of
                                     // y written 32 bytes at a time
     int32_t sms;            // SMs to spread over
+    int32_t withhold;       // test hook: expert whose rows are never loaded (-1: none)
+    int64_t wait_cycles;    // bound of each wait in SM clocks
     uint32_t *status;
     uint32_t *next;         // tile counter and count of the pairs that are done with it: both zero
                             // between launches, each launch puts them back

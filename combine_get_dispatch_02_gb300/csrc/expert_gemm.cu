@@ -383,10 +383,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
     const int kchan = (p.k + S::KSTEP - 1) / S::KSTEP;  // stages of a tile (wgrad: by the expert's rows)
     auto stages_of = [&](const Tile &ti) { return S::WG ? (ti.valid + 63) / 64 : kchan; };
     bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.wait_cycles); };
     // The i-th tile of this pair, for a whole warp; false after the last one.
     auto next_tile = [&](Tile &ti, int i) {
         const int s = i % kTileRing;
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_kfull + 8 * s, (i / kTileRing) & 1));
+        ok = __all_sync(0xFFFFFFFFu, wait(b_kfull + 8 * s, (i / kTileRing) & 1));
         if (!ok) return false;
         ti = bars.tiles[s];
         __syncwarp();
@@ -397,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
     auto amax_ready = [&](int group, uint32_t turn) {
         __syncwarp();
         if (lane == 0) bar_arrive(saddr(&bars.amax[group]));
-        ok = __all_sync(0xFFFFFFFFu, bar_wait(saddr(&bars.amax[group]), turn & 1));
+        ok = __all_sync(0xFFFFFFFFu, wait(saddr(&bars.amax[group]), turn & 1));
         return ok;
     };
     if (warp >= S::READ) {
@@ -417,11 +418,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         const uint32_t full = saddr(&bars.nfull[n]), empty = saddr(&bars.nempty[n]);
                         if (rank == 0) {
                             t = pairs + (int)atomicAdd(p.next, 1u);
-                            if (!(ok = bar_wait(empty, ((i / kNextRing) & 1) ^ 1))) break;
+                            if (!(ok = wait(empty, ((i / kNextRing) & 1) ^ 1))) break;
                             send_u32(map_rank(saddr(&bars.next[n]), 1), (uint32_t)t, map_rank(full, 1));
                         } else {
                             bar_expect(full, 4);
-                            if (!(ok = bar_wait(full, (i / kNextRing) & 1))) break;
+                            if (!(ok = wait(full, (i / kNextRing) & 1))) break;
                             t = bars.next[n];
                             bar_arrive_cluster(map_rank(empty, 0));
                         }
@@ -438,14 +439,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     Tile ti;
                     ti.e = -1;
                     if (t < total) ti = tile_at<OP, ALT>(p, before, kept, t, wtiles);
-                    if (!(ok = bar_wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
+                    if (!(ok = wait(b_kempty + 8 * s, ((i / kTileRing) & 1) ^ 1))) break;
                     bars.tiles[s] = ti;
                     bar_arrive(b_kfull + 8 * s);
                     if (t >= total) {
                         // the second CTA's arrivals are here before this CTA ends
                         if (drawn && rank == 0)
                             for (int j = max(0, i - kNextRing + 1); j <= i && ok; ++j)
-                                ok = bar_wait(saddr(&bars.nempty[j % kNextRing]), (j / kNextRing) & 1);
+                                ok = wait(saddr(&bars.nempty[j % kNextRing]), (j / kNextRing) & 1);
                         break;
                     }
                 }
@@ -469,10 +470,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 const uint32_t bytes = (S::ROW ? S::B_BYTES : S::A_BYTES) + mine * 128;
                 const uint32_t both = S::ROW ? 2 * S::B_BYTES + min(256, (ti.valid + 15) & ~15) * 128 : 2 * bytes;
                 for (int kb = 0; kb < nk; ++kb) {
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph ^ 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(b_empty + 8 * st, ph ^ 1));
                     if (!ok) break;
                     const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
                     const uint32_t full0 = map_rank(b_full + 8 * st, 0);
+                    if (ti.e == p.withhold) {  // test hook
+                        ok = false;
+                        break;
+                    }
                     if (elect()) {
                         uint32_t bar = full0;
                         if constexpr (S::WG) {
@@ -524,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             // the stages in flight have been read (nothing lands or arrives here after the kernel's end)
             for (int i = 0; i < used; ++i) {
                 if (--st < 0) st = S::STAGES - 1, ph ^= 1;
-                if (!__all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * st, ph))) {
+                if (!__all_sync(0xFFFFFFFFu, wait(b_empty + 8 * st, ph))) {
                     ok = false;
                     atomicOr(p.status, kStatusInFlight);
                     break;
@@ -543,10 +548,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         const int in_seg = S::SEG == 0 ? kb : kb % (S::SEG == 0 ? 1 : S::SEG);
                         const uint32_t buf = seg & 1;
                         // the operands first: they are there long before the accumulator is read out
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_full + 8 * st, ph));
+                        ok = __all_sync(0xFFFFFFFFu, wait(b_full + 8 * st, ph));
                         if (!ok) break;
                         if (in_seg == 0) {
-                            ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1));
+                            ok = __all_sync(0xFFFFFFFFu, wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1));
                             if (!ok) break;
                         }
                         if constexpr (S::WG) {
@@ -577,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 }
                 // the last accumulators have been read: the second CTA's arrivals are here before this CTA ends
                 for (uint32_t i = 1; i <= 2 && i <= seg && ok; ++i)
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tempty + 8 * ((seg - i) & 1), ((seg - i) >> 1) & 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(b_tempty + 8 * ((seg - i) & 1), ((seg - i) >> 1) & 1));
             }
         } else if (warp == kWarpAux) {
             if constexpr (S::FP8) {
@@ -628,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     }
                     if (more) fetch(nxt);
                     const uint32_t buf = fill & 1;
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(b_sempty + 8 * buf, ((fill >> 1) & 1) ^ 1));
                     if (!ok) break;
                     float *out = scales + buf * kScaleGroup * 256;
 #pragma unroll
@@ -660,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     const int nk = stages_of(ti);
                     if ((ti.valid & 63) != 0) {
                         const int s = (st + nk - 1) % S::STAGES;
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_land + 8 * s, (landed >> s) & 1));
+                        ok = __all_sync(0xFFFFFFFFu, wait(b_land + 8 * s, (landed >> s) & 1));
                         if (!ok) break;
                         landed ^= 1u << s;
                         uint8_t *base = smem + s * S::STAGE;
@@ -697,7 +702,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 // leaves out
                 const uint32_t buf = seg & 1;
                 if (nk > 0) {
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
                 }
@@ -732,7 +737,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             } else if constexpr (S::SEG == 0) {
                 __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
                 const uint32_t buf = seg & 1;
-                ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                 if (!ok) break;
                 fence_after();
                 for (int c = hw; c < chunks; c += 2) {
@@ -769,7 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 for (int k = 0; k < nk; ++k, ++seg) {
                     const uint32_t buf = seg & 1;
                     if (k % kScaleGroup == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, bar_wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
+                        ok = __all_sync(0xFFFFFFFFu, wait(b_sfull + 8 * (fill & 1), (fill >> 1) & 1));
                         if (!ok) break;
                     }
                     const float *sc = scales + ((fill & 1) * kScaleGroup + k % kScaleGroup) * 256;
@@ -791,7 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if constexpr (S::COL) {
                         if (live) column_scales(0);
                     }
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
                     const uint32_t at = lanes + buf * 256 + col0;
@@ -1005,7 +1010,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 const int nseg = (nk + S::SEG - 1) / S::SEG;
                 for (int k = 0; k < nseg; ++k, ++seg) {
                     const uint32_t buf = seg & 1;
-                    ok = __all_sync(0xFFFFFFFFu, bar_wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                    ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
                     fence_after();
                     const uint32_t at = lanes + buf * 256 + hw * 128;

@@ -74,10 +74,11 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 __device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-// Bounded wait for the phase with this parity; false when it gave up: after
-// 2^32 cycles of the SM's own counter (about 2 s; it never steps back, unlike
-// the global timer), read every 1024 polls.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+// Bounded wait for the phase with this parity; false when it gave up, after
+// `cycles` of the SM's own counter (it never steps back, unlike the global
+// timer), which is read every 1024 polls.
+constexpr long long kWaitCycles = 1ll << 32;  // about 2 s
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, long long cycles) {
     if (bar_try(bar, parity)) return true;
     long long t0 = 0;
     for (uint32_t n = 1; !bar_try(bar, parity); ++n) {
@@ -85,7 +86,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
         const long long t = clock64();
         if (t0 == 0)
             t0 = t;
-        else if (t - t0 > (1ll << 32))
+        else if (t - t0 > cycles)
             return false;
     }
     return true;

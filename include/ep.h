@@ -616,9 +616,12 @@ ep_status ep_get_device_status(ep_ctx *ctx, void *stream);
  *                       g) and ep_combine_send (entry g*K + k) whose row load
  *                       is never issued, so the bounded wait for it runs out
  *                       and ep_get_device_status reports EP_ERR_TIMEOUT (no
- *                       load is in flight for it); -1 = none (the default)
- *   move_wait_ns        bound of each of those waits in ns; 0 = 1 s (the
- *                       default), at most 10 s
+ *                       load is in flight for it); -1 = none (the default).
+ *                       The expert products (ep_expert_gemm, _gemm_fp8,
+ *                       _gate_fp8, _wgrad) take it as an expert whose operands
+ *                       are never loaded
+ *   move_wait_ns        bound of each of those waits in ns; 0 = the default (1 s,
+ *                       expert products 2 s), at most 10 s
  * Values out of range: EP_ERR_INVALID_ARG and the switches are unchanged.
  * Host only. */
 typedef struct ep_test_hooks {

@@ -502,6 +502,41 @@ def test_refusals():
     done(buf)
 
 
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "wgrad", "wgrad_fp32", "fp8", "gate"])
+@pytest.mark.parametrize("counts", [[40, 0, 3, 130, 128, 9], [300, 700, 1, 256, 513, 40]])
+def test_waits_run_out_then_the_context_works_again(op, counts):
+    """An expert whose operands are never loaded: every wait in the kernel gives
+    up after a millisecond, the call reports it, and the same calls afterwards
+    give the same bits as before."""
+    buf, h, grp = group(counts)
+    E, used = len(counts), in_use(buf.rows, grp)
+    x, dy, w = receive(buf.rows, 1024, grp, 1), receive(buf.rows, 1024, grp, 2), weights(E, 1024, 1024, 3)
+    xq, wq = cast_rows(x.float()), buf.cast_weights(w)
+
+    def call():
+        if op == "gemm":
+            return (buf.expert_gemm(x, w, h)[used],)
+        if op == "dgrad":
+            return (buf.expert_gemm(dy, w, h, transpose_w=True)[used],)
+        if op == "fp8":
+            return (buf.expert_gemm_fp8(xq, wq, h)[used],)
+        if op == "gate":
+            q, s = buf.expert_gate_fp8(xq, wq, h)
+            return q.view(torch.uint8)[used], s[used]
+        dtype = torch.float32 if op == "wgrad_fp32" else torch.bfloat16
+        return (buf.expert_wgrad(dy, x, h, out=torch.empty(E, 1024, 1024, dtype=dtype, device="cuda")),)
+
+    want = call()
+    done(buf)
+    ep.ep_set_test_hooks(buf.ctx, move_withhold_item=3, move_wait_ns=1_000_000)
+    call()
+    assert buf.device_status() == ep.EP_ERR_TIMEOUT
+    ep.ep_set_test_hooks(buf.ctx)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    done(buf)
+
+
 # ------------------------------------------------------------------ the operators as they are used together
 
 def test_fp8_serving_path_from_dispatch_to_combine():
