@@ -54,15 +54,11 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 }
 // Arrive on a barrier anywhere in the cluster (address from map_rank).  No
 // generic writes are published to the other CTA: what it orders are tensor
-// memory reads, by their own fences.
+// memory reads and a CTA's own shared memory, by their own fences.  A release at
+// cluster scope would wait for everything the thread has in flight (wgrad with
+// one per stage: 700 instead of 1380 TFLOP/s).
 __device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// The same, publishing this thread's writes to the cluster.  A release at
-// cluster scope waits for everything the thread has in flight, so it stays out
-// of the loops (wgrad with one per stage: 700 instead of 1380 TFLOP/s).
-__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -73,7 +69,6 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 // Bounded wait for the phase with this parity; false when it gave up, after
 // `cycles` of the SM's own counter (it never steps back, unlike the global
 // timer), which is read every 1024 polls.
