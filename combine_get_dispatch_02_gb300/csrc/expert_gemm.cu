@@ -243,27 +243,6 @@ __device__ __forceinline__ void fill_box(const uint4 (&v)[P], uint32_t box, int 
     __syncwarp();
 }
 
-// Add 32 lines of 32 fp32 values (lane = line) to what dst holds: through shared
-// memory, so that 8 lanes take a line's 128 bytes.  pitch: bytes from line to
-// line; pieces: how many 16-byte pieces of a line exist.
-__device__ __forceinline__ void add_lines(const uint4 (&v)[8], uint32_t buf, int lane, float *dst, int64_t pitch, int lines,
-                                          int pieces) {
-    __syncwarp();
-    fill_box<8>(v, buf, lane);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int i = lane + 32 * j, line = i / 8, c = i % 8;
-        float4 q;
-        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
-                     : "r"(buf + line * 128 + ((c ^ (line & 7)) << 4)));
-        if (line >= lines || c >= pieces) continue;
-        float4 *d = reinterpret_cast<float4 *>(reinterpret_cast<uint8_t *>(dst) + line * pitch + c * 16);
-        const float4 o = *d;
-        *d = make_float4(o.x + q.x, o.y + q.y, o.z + q.z, o.w + q.w);
-    }
-}
-
 template <ExpertOp OP, bool ALT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THREADS, 1)
     expert_gemm_kernel(const __grid_constant__ Maps maps, const ExpertGemmParams p) {
@@ -1040,21 +1019,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     for (int j = 0; j < 8; ++j)
                         line[j] = make_uint4((uint32_t)acc[q][2 * j], (uint32_t)(acc[q][2 * j] >> 32), (uint32_t)acc[q][2 * j + 1],
                                              (uint32_t)(acc[q][2 * j + 1] >> 32));
-                    if (p.accumulate) {
-                        float *dst = static_cast<float *>(p.y) + ((int64_t)ti.e * p.n + wc) * p.k + col;
-                        add_lines(line, out, lane, dst, (int64_t)p.k * 4, p.n - wc, (p.k - col) / 4);
-                    } else {
-                        // boxes of 16 columns, stored while the next ones are filled
+                    // boxes of 16 columns, stored (or added) while the next ones are filled
 #pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            if (col + 16 * o >= p.k) continue;
-                            const uint4 half[4] = {line[4 * o], line[4 * o + 1], line[4 * o + 2], line[4 * o + 3]};
-                            const uint32_t box = out + (turn & 1) * 2048;  // read by the store before the last one
-                            ++turn;
-                            if (lane == 0) store_read_wait<1>();
-                            __syncwarp();
-                            fill_box<4>(half, box, lane);
-                            if (lane == 0) tma_store_3d(&maps.m[5], box, col + 16 * o, wc, ti.e);
+                    for (int o = 0; o < 2; ++o) {
+                        const int x = col + 16 * o;
+                        if (x >= p.k || (p.accumulate && nk == 0)) continue;
+                        const uint4 half[4] = {line[4 * o], line[4 * o + 1], line[4 * o + 2], line[4 * o + 3]};
+                        const uint32_t box = out + (turn & 1) * 2048;  // read by the store before the last one
+                        ++turn;
+                        if (lane == 0) store_read_wait<1>();
+                        __syncwarp();
+                        fill_box<4>(half, box, lane);
+                        if (lane == 0) {
+                            if (p.accumulate)
+                                tma_add_3d(&maps.m[5], box, x, wc, ti.e);
+                            else
+                                tma_store_3d(&maps.m[5], box, x, wc, ti.e);
                         }
                     }
                 }
