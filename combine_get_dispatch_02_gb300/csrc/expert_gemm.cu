@@ -109,7 +109,7 @@ struct Bars {
     uint64_t full[6], empty[6], land[6];
     uint64_t tfull[2], tempty[2], sfull[2], sempty[2], kfull[kTileRing], kempty[kTileRing];
     uint64_t nfull[kNextRing], nempty[kNextRing];
-    uint64_t amax[4];
+    uint64_t amax[4], want;
     Tile tiles[kTileRing];
     int next[kNextRing];
     uint32_t tmem;
@@ -286,6 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             bar_init(saddr(&bars.nempty[i]), 1);
         }
         for (int i = 0; i < 4; ++i) bar_init(saddr(&bars.amax[i]), 4);
+        bar_init(saddr(&bars.want), 1);
         bar_init_fence();
         for (int i = 0; i < (S::WG ? 2 : 5); ++i) prefetch_map(&maps.m[i]);
     }
@@ -396,6 +397,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if (drawn && i > 0) {
                         const uint32_t full = saddr(&bars.nfull[n]), empty = saddr(&bars.nempty[n]);
                         if (rank == 0) {
+                            // not before the loader is near the end of the tile before: a number drawn
+                            // early starts late, and the tiles of one expert no longer together
+                            if (!(ok = wait(saddr(&bars.want), (i - 1) & 1))) break;
                             t = pairs + (int)atomicAdd(p.next, 1u);
                             if (!(ok = wait(empty, ((i / kNextRing) & 1) ^ 1))) break;
                             send_u32(map_rank(saddr(&bars.next[n]), 1), (uint32_t)t, map_rank(full, 1));
@@ -448,7 +452,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                 const int mine = S::ROW ? min(128, max(0, (ti.valid - (int)rank * 128 + 15) & ~15)) : half;
                 const uint32_t bytes = (S::ROW ? S::B_BYTES : S::A_BYTES) + mine * 128;
                 const uint32_t both = S::ROW ? 2 * S::B_BYTES + min(256, (ti.valid + 15) & ~15) * 128 : 2 * bytes;
+                const int want = nk - S::STAGES - 2;  // stages loaded when the next tile is asked for
+                if (want <= 0 && rank == 0 && lane == 0) bar_arrive(saddr(&bars.want));
                 for (int kb = 0; kb < nk; ++kb) {
+                    if (kb == want && kb > 0 && rank == 0 && lane == 0) bar_arrive(saddr(&bars.want));
                     ok = __all_sync(0xFFFFFFFFu, wait(b_empty + 8 * st, ph ^ 1));
                     if (!ok) break;
                     const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
