@@ -74,8 +74,10 @@ struct ep_handle {
     cudaEvent_t runs_ev;      // recorded after the copy of the run sizes to h_runs
     int32_t runs_state;       // 0: none, 1: copy queued (wait on runs_ev), 2: on the host
     int32_t has_send;         // send_slot / runs belong to the layout held
-    // tile counters of the expert products, behind the layout's barrier counter
-    mutable uint32_t tile_counter;  // the next one to take
+    // who holds which tile counter of the expert products (they lie behind the layout's barrier
+    // counter): the streams by their ids, in the order of their first call, and captured calls
+    mutable unsigned long long counter_stream[ep::kStreamCounters];
+    mutable uint32_t counter_streams, counter_captured;
 };
 
 namespace {
@@ -631,8 +633,36 @@ ep_status check_channels(int32_t c, int32_t step) {
 
 int expert_sms(const ep_ctx *ctx) { return grid_cap(ctx, 1); }
 
+// The tile counter of a product on `st`: two launches that can run side by side
+// must not draw from one.  A stream's launches follow each other, so each stream has
+// one; a captured call has one of its own, because its graph can run beside
+// anything (but not beside itself: it writes the same output).  nullptr when
+// they are all taken: the tiles are then dealt out in a fixed order.
+uint32_t *tile_counter(const ep_ctx *ctx, const ep_handle *h, cudaStream_t st) {
+    uint32_t *const first = reinterpret_cast<uint32_t *>(h->cta_hist + grid_hist_ints(ctx) + 16);
+    cudaStreamCaptureStatus capture;
+    unsigned long long id;
+    if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) {
+        cudaGetLastError();  // the launch reports it
+        return nullptr;
+    }
+    if (capture != cudaStreamCaptureStatusNone) {
+        if (h->counter_captured == ep::kCapturedCounters) return nullptr;
+        return first + 2 * (ep::kStreamCounters + h->counter_captured++);
+    }
+    if (cudaStreamGetId(st, &id) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    for (uint32_t i = 0; i < h->counter_streams; ++i)
+        if (h->counter_stream[i] == id) return first + 2 * i;
+    if (h->counter_streams == ep::kStreamCounters) return nullptr;
+    h->counter_stream[h->counter_streams] = id;
+    return first + 2 * h->counter_streams++;
+}
+
 // The parameters every expert product shares.
-ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_t n, int32_t k) {
+ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_t n, int32_t k, cudaStream_t st) {
     const ep_config &c = ctx->cfg;
     ep::ExpertGemmParams p = {};
     p.base = h->base;
@@ -651,8 +681,7 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
     // 2 clocks a ns (a little over the fastest clock)
     p.wait_cycles = ctx->hooks.move_wait_ns > 0 ? 2 * ctx->hooks.move_wait_ns : 1ll << 32;
     p.status = ctx->d_status;
-    p.next = reinterpret_cast<uint32_t *>(h->cta_hist + grid_hist_ints(ctx) + 16) +
-             2 * (h->tile_counter++ % ep::kTileCounters);
+    p.next = tile_counter(ctx, h, st);
     return p;
 }
 
@@ -803,7 +832,7 @@ ep_status ep_handle_create(ep_ctx *ctx, ep_handle **out) {
               cudaMalloc(&h->off_er, er * sizeof(int32_t)) == cudaSuccess &&
               cudaMalloc(&h->base, (size_t)c.num_experts * sizeof(int64_t)) == cudaSuccess &&
               cudaMalloc(&h->tokens_per_expert, (size_t)c.num_experts * sizeof(int32_t)) == cudaSuccess &&
-              cudaMalloc(&h->cta_hist, (grid_hist_ints(ctx) + 16 + 2 * ep::kTileCounters) * sizeof(int32_t)) == cudaSuccess &&
+              cudaMalloc(&h->cta_hist, (grid_hist_ints(ctx) + 16 + 2 * (ep::kStreamCounters + ep::kCapturedCounters)) * sizeof(int32_t)) == cudaSuccess &&
               cudaMalloc(&h->send_slot, nk * sizeof(int32_t)) == cudaSuccess;
     if (ok && c.num_ranks <= ep::kRankRunsMaxRanks)
         ok = cudaMallocHost(&h->h_runs, (size_t)c.num_ranks * c.num_ranks * sizeof(int32_t)) == cudaSuccess &&
@@ -815,7 +844,7 @@ ep_status ep_handle_create(ep_ctx *ctx, ep_handle **out) {
     }
     // the grid-form layout's barrier counter and the tile counters start at zero (each launch puts
     // them back)
-    if (cudaMemset(h->cta_hist + grid_hist_ints(ctx), 0, (16 + 2 * ep::kTileCounters) * sizeof(int32_t)) != cudaSuccess) {
+    if (cudaMemset(h->cta_hist + grid_hist_ints(ctx), 0, (16 + 2 * (ep::kStreamCounters + ep::kCapturedCounters)) * sizeof(int32_t)) != cudaSuccess) {
         cudaGetLastError();
         ep_handle_destroy(h);
         return EP_ERR_CUDA;
@@ -1341,7 +1370,7 @@ ep_status ep_expert_gemm(ep_ctx *ctx, const ep_handle *handle, const void *d_x, 
     if (handle->tokens_per_rank == 0) return EP_OK;
     if (d_x == nullptr || d_w == nullptr || d_y == nullptr) return EP_ERR_INVALID_ARG;
     if (!aligned(d_x, 16) || !aligned(d_w, 16) || !aligned(d_y, 16)) return EP_ERR_INVALID_ARG;
-    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k);
+    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k, (cudaStream_t)stream);
     p.x = d_x;
     p.w = d_w;
     p.y = d_y;
@@ -1360,7 +1389,7 @@ ep_status ep_expert_gemm_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d
         return EP_ERR_INVALID_ARG;
     if (!aligned(d_x, 16) || !aligned(d_x_scales, 4) || !aligned(d_w, 16) || !aligned(d_w_scales, 4) || !aligned(d_y, 16))
         return EP_ERR_INVALID_ARG;
-    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k);
+    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k, (cudaStream_t)stream);
     p.x = d_x;
     p.xs = d_x_scales;
     p.w = d_w;
@@ -1385,7 +1414,7 @@ ep_status ep_expert_gate_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d
     if (!aligned(d_x, 16) || !aligned(d_x_scales, 4) || !aligned(d_w, 16) || !aligned(d_w_scales, 4) ||
         !aligned(d_h, 16) || !aligned(d_h_scales, 4))
         return EP_ERR_INVALID_ARG;
-    ep::ExpertGemmParams p = expert_params(ctx, handle, 2 * inner, k);
+    ep::ExpertGemmParams p = expert_params(ctx, handle, 2 * inner, k, (cudaStream_t)stream);
     p.x = d_x;
     p.xs = d_x_scales;
     p.w = d_w;
@@ -1417,7 +1446,7 @@ ep_status ep_expert_wgrad(ep_ctx *ctx, const ep_handle *handle, const void *d_dy
     }
     if (d_dy == nullptr || d_x == nullptr) return EP_ERR_INVALID_ARG;
     if (!aligned(d_dy, 16) || !aligned(d_x, 16)) return EP_ERR_INVALID_ARG;
-    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k);
+    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k, (cudaStream_t)stream);
     p.x = d_x;
     p.dy = d_dy;
     p.y = d_dw;

@@ -224,11 +224,11 @@ struct ExpertGemmParams {
     int64_t wait_cycles;    // bound of each wait in SM clocks
     uint32_t *status;
     uint32_t *next;         // tile counter and count of the pairs that are done with it: both zero
-                            // between launches, each launch puts them back
+                            // between launches, each launch puts them back; nullptr: none free
 };
-// Tile counters of a handle (two words each), taken in turn, so that operators
-// of one handle may run side by side.
-constexpr int kTileCounters = 32;
+// Tile counters of a handle (two words each), for its streams and for calls
+// captured into graphs.
+constexpr int kStreamCounters = 64, kCapturedCounters = 4032;
 // One-time set-up with the device current (shared memory limits).
 void expert_gemm_init();
 cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream);

@@ -387,10 +387,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             // Hands the pair's tiles out, looked up ahead of the others (a search, divisions and two
             // loads from L2).  The first tile is the pair's own number, the others come from a counter in
             // global memory, so that pairs with short tiles take more of them and the tiles of one
-            // expert, which share its weights in L2, start together.  The first CTA draws the numbers and
-            // sends them to the second.
+            // expert, which share its weights in L2, start together (every 76th tile instead: 262144 rows x
+            // 2048 x 7168 5.8 instead of 4.9 ms, 32 x 128 tokens' FP8 gate 1.81 instead of 1.52).  The first
+            // CTA draws the numbers and sends them to the second.
             if (lane == 0) {
-                const bool drawn = total > pairs;
+                const bool drawn = p.next != nullptr && total > pairs;
                 int t = pair;
                 for (int i = 0; ok; ++i) {
                     const int n = i % kNextRing;
@@ -416,7 +417,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             bar_arrive_remote(map_rank(saddr(&bars.nempty[0]), 0));
                         }
                     } else if (i > 0) {
-                        t = total;
+                        t += pairs;
                     }
                     const int s = i % kTileRing;
                     Tile ti;

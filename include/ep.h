@@ -57,7 +57,8 @@
  *   - A context and its handles belong to the device current at ep_create;
  *     calls must be made with that device current.  A context is not
  *     thread-safe; calls on one context must not overlap on the GPU unless
- *     they use different handles and output buffers.
+ *     they use different handles and output buffers (the expert operators
+ *     below may share a handle).
  */
 #ifndef EP_H
 #define EP_H
@@ -337,7 +338,9 @@ ep_status ep_expert_identity(ep_ctx *ctx, const ep_handle *handle, int32_t use_f
  *   block, by the dispatch's FP8 rule with the block's amax; E is the
  *   context's; a last block of n % 128 rows has its own scale.
  *
- * Results do not depend on max_sms, the layout form or the kernels around. */
+ * Operators of one handle may run side by side (several streams, graphs) as
+ * long as none writes what another reads or writes.  Results do not depend on
+ * max_sms, the layout form or the kernels around. */
 ep_status ep_expert_gemm(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const void *d_w,
                          int32_t n, int32_t k, int32_t transpose_w, void *d_y, void *stream);
 ep_status ep_expert_gemm_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const float *d_x_scales,

@@ -389,6 +389,58 @@ def test_operators_of_one_handle_side_by_side():
     assert torch.equal(dx[used], want_dx[used]) and torch.equal(dw, want_dw)
 
 
+def test_graphs_beside_eager_calls_and_each_other():
+    """Products that draw their tiles from a counter: two graphs and an eager
+    stream of one handle at once, each launched many times over."""
+    buf, h, grp = group([300, 0, 17, 640, 128, 1, 77, 256] * 4)
+    used = in_use(buf.rows, grp)
+    x, w = receive(buf.rows, 256, grp, 1), weights(32, 2048, 256, 2)
+    want = buf.expert_gemm(x, w, h)
+    outs = [sentinel((buf.rows, 2048)) for _ in range(3)]
+    torch.cuda.synchronize()
+    graphs = []
+    for out in outs[:2]:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(8):
+                buf.expert_gemm(x, w, h, out=out)
+    side = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, g in zip(side, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        for _ in range(8):
+            buf.expert_gemm(x, w, h, out=outs[2])
+    torch.cuda.synchronize()
+    done(buf)
+    for out in outs:
+        assert torch.equal(out[used], want[used])
+
+
+def test_more_captured_calls_than_counters():
+    """Past the tile counters of a handle the tiles come in a fixed order, with
+    the same bits (and the weights' gradient adds each tile once)."""
+    buf, h, grp = group([40, 0, 17, 64, 128, 1, 77, 56] * 4)
+    used = in_use(buf.rows, grp)
+    x, w = receive(buf.rows, 256, grp, 1), weights(32, 1024, 256, 2)
+    dy = receive(buf.rows, 1024, grp, 3)
+    want, want_dw = buf.expert_gemm(x, w, h), buf.expert_wgrad(dy, x, h)
+    out, dw = sentinel((buf.rows, 1024)), torch.zeros((32, 1024, 256), dtype=torch.float32, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(4040):
+            buf.expert_gemm(x, w, h, out=out)
+        out.fill_(0)
+        buf.expert_gemm(x, w, h, out=out)
+        buf.expert_wgrad(dy, x, h, accumulate=True, out=dw)
+    g.replay()
+    torch.cuda.synchronize()
+    done(buf)
+    assert torch.equal(out[used], want[used]) and torch.equal(dw, want_dw)
+
+
 def test_on_another_stream_and_in_a_graph():
     buf, h, grp = group([10, 0, 200, 33])
     x, w = receive(buf.rows, 256, grp, 1), weights(4, 512, 256, 2)
