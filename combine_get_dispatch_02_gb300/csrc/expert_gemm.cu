@@ -6,30 +6,55 @@
 //   h[r]  = cast(silu(g) * u), (g, u) = the two halves of the e4m3 product
 //   dW[e] = sum_r dy[r] x[r]^T
 //
-// One persistent kernel of CTA pairs (a cluster of 2, one CTA per SM).  A
-// pair's tile is 256 x N of the transposed output: 256 rows of the weights
-// (128 per CTA, the M side of the tensor cores) by N <= 256 rows of one
-// expert (the N side, in steps of 32).  The weights are the dimension without
-// remainders and the tokens the ragged one, so a group of 40 rows costs 64
-// columns of products, not a 128- or 256-row tile; few rows leave the kernel
-// bound by the weights' bytes, many by the tensor cores.  The tiles of an
-// expert are numbered with its token tiles fastest, so pairs that run at the
+// One persistent kernel of CTA pairs (a cluster of 2, one CTA per SM).  Tiles:
+//   bf16, wgrad      256 rows of the weights (the M side of the tensor cores, 128
+//                    per CTA) by up to 256 rows of one expert (the N side, in
+//                    steps of 32; wgrad: columns of x)
+//   e4m3, column form  the same with two operands of weight rows (gate: 256
+//                    channels of the gate and of the up product; else 512 rows) by
+//                    up to 128 rows of an expert
+//   e4m3, row form   256 rows of an expert on the M side by 256 weight rows
+//                    (gate: 128 + 128)
+// The weights have no remainders and the tokens are ragged, so with the tokens
+// on the N side a group of 40 rows costs 64 columns of products, not a tile of
+// 128 or 256 rows; few rows leave the kernel bound by the weights' bytes, many
+// by the tensor cores.  The e4m3 products have a scale per row and 128
+// channels, so their partial sums leave tensor memory every 128 channels and are
+// scaled and added up in fp32 registers; that reading bounds them, and with many
+// rows it is cheaper where a thread holds one row and needs one scale (row form,
+// from kRowFormRows rows per expert on).  The tiles of an expert are numbered
+// with its token tiles fastest and drawn in that order, so pairs that run at the
 // same time share its weights in L2.
 //
-// Warps of a CTA: 0-7 read the accumulators out of tensor memory, 8 loads
-// (one thread, tensor maps, 128-byte swizzle), 9 issues the products (one
-// thread of the pair's first CTA), 10 brings the FP8 scales or clears the
-// rows past the end of an expert (wgrad).  The accumulators are double
-// buffered (2 x 256 columns).  A segment of products shares an accumulator:
+// Warps of a CTA: READ (8, e4m3 row form 16) that read the accumulators out of
+// tensor memory, then one that loads (tensor maps, 128-byte swizzle), one that
+// issues the products (in the pair's first CTA), one that brings the e4m3
+// scales or clears the rows past the end of an expert (wgrad), one that draws
+// the tiles.  The accumulators are double buffered (2 x 256 columns).  A segment
+// of products shares an accumulator:
 //   bf16       the whole sum over k (the next tile's products run while this
 //              tile is written out)
-//   e4m3       one block of 128 channels, whose partial sums the reading
-//              warps scale and add up in fp32 registers
+//   e4m3       one block of 128 channels
 //   wgrad      the whole sum over rows; fp32 output: 256 rows, added up in
 //              registers (the tensor cores truncate when they add, and a long
-//              sum would drift: 8e-6 of the result over 7168 terms, measured)
+//              sum would drift: 8e-6 of the result over 7168 terms, measured);
+//              stored, or added to what is there, by tensor map from shared
+//              memory, which also leaves out what lies past the matrix
 // All waits are bounded; a wait that gives up sets the status word and ends
 // its role.
+//
+// Measured (one GB300, rows spread evenly unless said; of the 6.78 TB/s copy and
+// the 1913 TFLOP/s bf16 peak, 1706 over seconds):
+//   bf16   262144 rows x 2048 x 7168    4.9 ms, 1.57 PFLOP/s (power limit), 4.1 ms cold
+//          256 experts x 16 rows x 7168 x 2048   1.10 ms, 6.9 TB/s
+//   wgrad  16 x 1000 rows x 2048 x 7168   263 us, 1.79 PFLOP/s; fp32 output 360 us
+//          (its sums leave tensor memory every 256 rows)
+//   e4m3   8192^3   485 us, 2.27 PFLOP/s (row form: reading the partial sums takes
+//          about 950 cycles a block, the products 512)
+//          76 experts x 16 rows x 4096 x 7168   327 us, 6.9 TB/s
+//   gate   256 experts x 128 rows x 2 * 2048 x 7168   1.15 ms, 6.9 TB/s; 32768
+//          entries drawn over 256 experts 1.54 ms (half the experts have more than
+//          128 rows and take two tiles, whose weights come through L2 twice)
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -570,11 +595,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             }
         } else if (warp == kWarpAux) {
             if constexpr (S::FP8) {
-                // scales of 128 rows (row form: of this CTA), xs * ws with the two blocks of weight rows, for
-                // kScaleGroup blocks at a time; the next group's (or tile's) loads are in flight while one is stored
+                // Scales of 128 rows for kScaleGroup blocks at a time; the next group's (or tile's) loads
+                // are in flight while one is stored.  Row form: of this CTA's rows, xs * ws with the two
+                // blocks of weight rows.  Column form: xs, and apart from them the two ws, because each
+                // thread needs 16 rows' and the reading warps' share of shared memory bounds them (products
+                // of both operands read from here 334 instead of 327 us at 76 x 16 rows x 4096 x 7168).
                 const int nb = (p.n + 127) / 128;
                 struct Group {
-                    float4 x[4], w, w2;
+                    float4 x[4];
+                    float4 w, w2;  // row form
+                    float wl;      // column form: lane j < 8 has that of block j / 2, operand j % 2
                 } cur, nxt;
                 uint32_t fill = 0;
                 Tile ti = {};
@@ -596,8 +626,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         return v;
                     };
                     const float *ws = p.ws + (int64_t)ti.e * nb * kchan + g;
-                    o.w = four(ws + (int64_t)min(b0, nb - 1) * kchan, p.ws_vec);
-                    o.w2 = four(ws + (int64_t)min(b1, nb - 1) * kchan, p.ws_vec);
+                    if constexpr (S::COL) {
+                        o.wl = 0.0f;
+                        if (lane < 8 && g + (lane >> 1) < kchan)
+                            o.wl = __ldg(ws + (int64_t)min(lane & 1 ? b1 : b0, nb - 1) * kchan + (lane >> 1));
+                    } else {
+                        o.w = four(ws + (int64_t)min(b0, nb - 1) * kchan, p.ws_vec);
+                        o.w2 = four(ws + (int64_t)min(b1, nb - 1) * kchan, p.ws_vec);
+                    }
 #pragma unroll
                     for (int j0 = 0; j0 < 128; j0 += 32) {
                         const int j = r0 + j0 + lane;
@@ -624,6 +660,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     for (int j0 = 0; j0 < 128; j0 += 32) {
                         const int at = S::ROW ? j0 + lane : scale_at(j0 + lane);
                         const float4 v = cur.x[j0 / 32];
+                        if constexpr (S::COL) {
+                            out[at] = v.x;
+                            out[256 + at] = v.y;
+                            out[512 + at] = v.z;
+                            out[768 + at] = v.w;
+                            continue;
+                        }
                         out[at] = v.x * cur.w.x;
                         out[256 + at] = v.y * cur.w.y;
                         out[512 + at] = v.z * cur.w.z;
@@ -632,6 +675,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         out[384 + at] = v.y * cur.w2.y;
                         out[640 + at] = v.z * cur.w2.z;
                         out[896 + at] = v.w * cur.w2.w;
+                    }
+                    if constexpr (S::COL) {
+                        // behind each block's 128: those of its two blocks of weight rows
+                        if (lane < 8) out[(lane >> 1) * 256 + 128 + (lane & 1)] = cur.wl;
                     }
                     __syncwarp();
                     if (lane == 0) bar_arrive(b_sfull + 8 * buf);
@@ -773,16 +820,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         f0 = pair2(s0, s0);
                         f1 = pair2(s1, s1);
                     }
-                    // (column form: the first operand's here, the second's between its reads)
-                    [[maybe_unused]] float cs[16];
-                    auto column_scales = [&](int operand) {
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            *reinterpret_cast<float4 *>(cs + 4 * m) =
-                                *reinterpret_cast<const float4 *>(sc + operand * 128 + col0 + c4 * 16 + ((m ^ (c4 >> 1)) << 2));
-                    };
+                    [[maybe_unused]] float xs[16];
+                    [[maybe_unused]] float2 ws = {0.0f, 0.0f};
                     if constexpr (S::COL) {
-                        if (live) column_scales(0);
+                        if (live) {
+                            ws = *reinterpret_cast<const float2 *>(sc + 128);
+#pragma unroll
+                            for (int m = 0; m < 4; ++m)
+                                *reinterpret_cast<float4 *>(xs + 4 * m) =
+                                    *reinterpret_cast<const float4 *>(sc + col0 + c4 * 16 + ((m ^ (c4 >> 1)) << 2));
+                        }
                     }
                     ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                     if (!ok) break;
@@ -793,7 +840,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         uint32_t v[2 * J];
                         if (live) {
                             if constexpr (S::COL) {
-                                if (q == 2) column_scales(1);
                                 tmem_get_frag(v, at + (q >> 1) * 128 + ((q & 1) << 20));
                             } else {
                                 tmem_get16(v, at + q * 16 + (S::GATE && q >= 2 ? 96 : 0));
@@ -809,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             for (int j = 0; j < J; ++j) {
                                 uint64_t f = q < 2 ? f0 : f1;
                                 if constexpr (S::COL) {
-                                    const uint32_t c = __float_as_uint(cs[j]);
+                                    const uint32_t c = __float_as_uint(__fmul_rn(xs[j], q < 2 ? ws.x : ws.y));
                                     f = pair2(c, c);
                                 }
                                 acc[q][j] = fma2(pair2(v[2 * j], v[2 * j + 1]), f, acc[q][j]);
@@ -1081,16 +1127,20 @@ EncodeTiled encode_fn() {
 
 // A row-major matrix [rows, cols] (or [planes, rows, cols]) in boxes of box_rows
 // rows by box_bytes (64 or 128), swizzled over as many bytes.
-bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows, int box_bytes = 128) {
+bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows,
+            int box_bytes = 128) {
     const EncodeTiled fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)(cols * es), (cuuint64_t)(cols * es * rows)};
     const cuuint32_t box[3] = {(cuuint32_t)(box_bytes / es), (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
-    return fn(m, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, planes > 0 ? 3 : 2,
-              const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const CUtensorMapDataType type = es == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return fn(m, type, planes > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <ExpertOp OP, bool ALT>
