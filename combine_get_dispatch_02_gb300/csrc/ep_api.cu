@@ -671,11 +671,7 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
     p.n = n;
     p.k = k;
     p.rows = ctx->rows;
-    // an expert can be offered every entry; the padded layout keeps R*Tmax
     p.live = (int64_t)c.num_ranks * h->tokens_per_rank * c.topk;
-    p.max_count = p.live;
-    if (c.layout == EP_LAYOUT_PADDED && p.max_count > (int64_t)c.num_ranks * c.max_tokens_per_rank)
-        p.max_count = (int64_t)c.num_ranks * c.max_tokens_per_rank;
     p.sms = expert_sms(ctx);
     p.withhold = ctx->hooks.move_withhold_item < c.num_experts ? (int32_t)ctx->hooks.move_withhold_item : -1;
     // 2 clocks a ns (a little over the fastest clock)

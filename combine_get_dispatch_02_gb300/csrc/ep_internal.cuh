@@ -214,7 +214,6 @@ struct ExpertGemmParams {
     const int32_t *count;   // [E]
     int32_t E, n, k;
     int64_t rows;           // receive rows
-    int64_t max_count;      // most rows of one expert
     int64_t live;           // entries of the layout (an upper bound of the rows in use)
     int32_t out_fp32, accumulate;  // wgrad
     int32_t xs_vec, ws_vec, y_vec;  // set by the launcher: rows of xs / ws can be read 16 bytes, rows of
