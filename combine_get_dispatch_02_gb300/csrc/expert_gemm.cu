@@ -35,7 +35,7 @@
 //   bf16       the whole sum over k (the next tile's products run while this
 //              tile is written out)
 //   e4m3       one block of 128 channels
-//   wgrad      the whole sum over rows; fp32 output: 256 rows, added up in
+//   wgrad      the whole sum over rows; fp32 output: 384 rows, added up in
 //              registers (the tensor cores truncate when they add, and a long
 //              sum would drift: 8e-6 of the result over 7168 terms, measured);
 //              stored, or added to what is there, by tensor map from shared
@@ -47,8 +47,8 @@
 // the 1913 TFLOP/s bf16 peak, 1706 over seconds):
 //   bf16   262144 rows x 2048 x 7168    4.9 ms, 1.57 PFLOP/s (power limit), 4.1 ms cold
 //          256 experts x 16 rows x 7168 x 2048   1.10 ms, 6.9 TB/s
-//   wgrad  16 x 1000 rows x 2048 x 7168   263 us, 1.79 PFLOP/s; fp32 output 360 us
-//          (its sums leave tensor memory every 256 rows)
+//   wgrad  16 x 1024 rows x 2048 x 7168   266 us, 1.81 PFLOP/s; fp32 output 338 us
+//          (0.94 GB, which the tensor cores' work only partly covers)
 //   e4m3   8192^3   485 us, 2.27 PFLOP/s (row form: reading the partial sums takes
 //          about 950 cycles a block, the products 512)
 //          76 experts x 16 rows x 4096 x 7168   327 us, 6.9 TB/s
@@ -116,8 +116,10 @@ struct Shape {
     static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 + (COL ? READ * 64 * 4 : 0) : 0;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
     static constexpr int KSTEP = FP8 ? 128 : 64;
-    // stages per segment; 0: all of them
-    static constexpr int SEG = FP8 ? 1 : (F32 ? 4 : 0);
+    // stages per segment; 0: all of them.  fp32 wgrad: 384 rows.  With 256 the tensor cores wait for the
+    // registers while those are stored (16 x 1024 rows x 2048 x 7168: 354 instead of 338 us), with 512 the
+    // drift of 6000 equal-signed terms is over 2^-20.
+    static constexpr int SEG = FP8 ? 1 : (F32 ? 6 : 0);
     static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE + READ * OUT_BYTES + SCALES + AMAX;
 };
 
@@ -253,15 +255,14 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&v)[8], bool 
     if (pieces >= 2) static_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
-// 32 lines of P pieces of 16 bytes (lane = line) into a box of shared memory as
-// a tensor map with lines of P * 16 bytes has it: swizzled over 128 (P = 8) or
-// 64 bytes (P = 4).
-template <int P>
-__device__ __forceinline__ void fill_box(const uint4 (&v)[P], uint32_t box, int lane) {
-    const int swap = P == 8 ? lane & 7 : (lane >> 1) & 3;
+// 32 lines of 128 bytes (lane = line) into a box of shared memory as a tensor
+// map with such lines, swizzled over 128 bytes, has it.  Whole lines of 128
+// bytes: the copy unit takes a line at a time, and with lines of 64 the fp32
+// weights' gradient of 64 x 256 rows x 2048 x 7168 took 741 us instead of 664.
+__device__ __forceinline__ void fill_box(const uint4 (&v)[8], uint32_t box, int lane) {
 #pragma unroll
-    for (int c = 0; c < P; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * P * 16 + ((c ^ swap) << 4)), "r"(v[c].x),
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(v[c].x),
                      "r"(v[c].y), "r"(v[c].z), "r"(v[c].w)
                      : "memory");
     fence_async_shared();
@@ -732,8 +733,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             const int chunks = ti.nt >> 5;
             const int wc = ti.w0 + (int)rank * 128 + sub * 32;  // the warp's first weight row / channel of h
             if constexpr (S::WG && !S::F32) {
-                // columns 128 hw on, as four boxes of 32 (64 bytes of bf16) that the tensor map stores
-                // while the next ones are filled and the next tile is summed; what lies past n or k it
+                // columns 128 hw on, as two boxes of 64 (128 bytes of bf16) that the tensor map stores
+                // while the next one is read and the next tile is summed; what lies past n or k it
                 // leaves out
                 const uint32_t buf = seg & 1;
                 if (nk > 0) {
@@ -742,32 +743,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     fence_after();
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = hw * 128 + q * 32;
-                    uint4 line[4];
+                for (int q = 0; q < 2; ++q) {
+                    const int col = hw * 128 + q * 64;
+                    uint4 line[8];
                     uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
-                    float v[32];
-                    if (nk > 0) {
-                        tmem_get32(v, lanes + buf * 256 + col);  // past ti.nt: in the buffer, not stored
-                    } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    for (int o = 0; o < 2; ++o) {
+                        float v[32];
+                        if (nk > 0) {
+                            tmem_get32(v, lanes + buf * 256 + col + o * 32);  // past ti.nt: in the buffer, not stored
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) b4[o * 16 + j] = bf16x2(v[2 * j], v[2 * j + 1]);
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) b4[j] = bf16x2(v[2 * j], v[2 * j + 1]);
-                    if (q == 3 && nk > 0) {
+                    if (q == 1 && nk > 0) {
                         fence_before();
                         __syncwarp();
                         if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
                         ++seg;
                     }
                     if (wc >= p.n || ti.c0 + col >= p.k) continue;
-                    const uint32_t box = out + (turn & 1) * 2048;  // read by the store before the last one
-                    ++turn;
-                    if (lane == 0) store_read_wait<1>();
+                    if (lane == 0) store_read_wait();
                     __syncwarp();
-                    fill_box<4>(line, box, lane);
-                    if (lane == 0) tma_store_3d(&maps.m[5], box, ti.c0 + col, wc, ti.e);
+                    fill_box(line, out, lane);
+                    if (lane == 0) tma_store_3d(&maps.m[5], out, ti.c0 + col, wc, ti.e);
                 }
             } else if constexpr (S::SEG == 0) {
                 __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
@@ -1021,7 +1023,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         uint32_t *b4 = reinterpret_cast<uint32_t *>(line);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) b4[j] = bf16x2(lo2(acc[j / 8][j % 8]), hi2(acc[j / 8][j % 8]));
-                        fill_box<8>(line, out, lane);
+                        fill_box(line, out, lane);
                         if (lane == 0 && c < p.n) tma_store_2d(&maps.m[5], out, c, (int)row0);
                     } else if (lane < rows) {
 #pragma unroll
@@ -1035,7 +1037,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     }
                 }
             } else {
-                // wgrad in fp32: sums of 256 rows added up in registers, columns 128 hw on
+                // wgrad in fp32: sums of 384 rows added up in registers, columns 128 hw on
                 uint64_t acc[4][16];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -1073,23 +1075,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     for (int j = 0; j < 8; ++j)
                         line[j] = make_uint4((uint32_t)acc[q][2 * j], (uint32_t)(acc[q][2 * j] >> 32), (uint32_t)acc[q][2 * j + 1],
                                              (uint32_t)(acc[q][2 * j + 1] >> 32));
-                    // boxes of 16 columns, stored (or added) while the next ones are filled
-#pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        const int x = col + 16 * o;
-                        if (x >= p.k || (p.accumulate && nk == 0)) continue;
-                        const uint4 half[4] = {line[4 * o], line[4 * o + 1], line[4 * o + 2], line[4 * o + 3]};
-                        const uint32_t box = out + (turn & 1) * 2048;  // read by the store before the last one
-                        ++turn;
-                        if (lane == 0) store_read_wait<1>();
-                        __syncwarp();
-                        fill_box<4>(half, box, lane);
-                        if (lane == 0) {
-                            if (p.accumulate)
-                                tma_add_3d(&maps.m[5], box, x, wc, ti.e);
-                            else
-                                tma_store_3d(&maps.m[5], box, x, wc, ti.e);
-                        }
+                    if (p.accumulate && nk == 0) continue;
+                    if (lane == 0) store_read_wait();
+                    __syncwarp();
+                    fill_box(line, out, lane);
+                    if (lane == 0) {
+                        if (p.accumulate)
+                            tma_add_3d(&maps.m[5], out, col, wc, ti.e);
+                        else
+                            tma_store_3d(&maps.m[5], out, col, wc, ti.e);
                     }
                 }
             }
@@ -1126,21 +1120,19 @@ EncodeTiled encode_fn() {
 }
 
 // A row-major matrix [rows, cols] (or [planes, rows, cols]) in boxes of box_rows
-// rows by box_bytes (64 or 128), swizzled over as many bytes.
-bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows,
-            int box_bytes = 128) {
+// rows by 128 bytes, swizzled.
+bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
     const EncodeTiled fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)(cols * es), (cuuint64_t)(cols * es * rows)};
-    const cuuint32_t box[3] = {(cuuint32_t)(box_bytes / es), (cuuint32_t)box_rows, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUtensorMapDataType type = es == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     return fn(m, type, planes > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <ExpertOp OP, bool ALT>
@@ -1161,7 +1153,7 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     bool ok;
     if constexpr (S::WG) {
         ok = encode(&maps.m[0], p.dy, 2, p.n, p.rows, 0, 64) && encode(&maps.m[1], p.x, 2, p.k, p.rows, 0, 64) &&
-             encode(&maps.m[5], p.y, S::F32 ? 4 : 2, p.k, p.n, p.E, 32, 64);
+             encode(&maps.m[5], p.y, S::F32 ? 4 : 2, p.k, p.n, p.E, 32);
     } else {
         constexpr int es = S::FP8 ? 1 : 2;
         ok = S::A_MN ? encode(&maps.m[0], p.w, es, p.n, p.k, p.E, 64) : encode(&maps.m[0], p.w, es, p.k, p.n, p.E, 128);

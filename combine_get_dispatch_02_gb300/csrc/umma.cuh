@@ -132,9 +132,8 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, uint32_t src,
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
-// All but the newest N stores of this thread have read their boxes.
-template <int N = 0>
-__device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+// The stores of this thread have read their boxes.
+__device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
