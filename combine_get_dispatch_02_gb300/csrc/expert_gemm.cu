@@ -203,6 +203,8 @@ __device__ __forceinline__ int scale_at(int col) {
 
 // g / (1 + exp(-g)) * u with the fast exponential and division (2 ulp each, an
 // eighth of the instructions): far inside what the sums before it are good to.
+// Of 3.6 million codes 11 differ from those of 64 bits with these and 12 with
+// the exact functions, which cost 64 x 128 rows x 4096 x 512 66 instead of 47 us.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
