@@ -47,7 +47,7 @@
 // the 1913 TFLOP/s bf16 peak, 1706 over seconds):
 //   bf16   262144 rows x 2048 x 7168    4.9 ms, 1.57 PFLOP/s (power limit), 4.1 ms cold
 //          256 experts x 16 rows x 7168 x 2048   1.10 ms, 6.9 TB/s
-//   wgrad  16 x 1024 rows x 2048 x 7168   266 us, 1.81 PFLOP/s; fp32 output 338 us
+//   wgrad  16 x 1024 rows x 2048 x 7168   278 us, 1.73 PFLOP/s; fp32 output 343 us
 //          (0.94 GB, which the tensor cores' work only partly covers)
 //   e4m3   8192^3   485 us, 2.27 PFLOP/s (row form: reading the partial sums takes
 //          about 950 cycles a block, the products 512)
@@ -392,6 +392,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
     auto stages_of = [&](const Tile &ti) { return S::WG ? (ti.valid + 63) / 64 : kchan; };
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) { return bar_wait(bar, parity, p.wait_cycles); };
+    // for a barrier behind which the other CTA has touched shared memory
+    auto wait_cluster = [&](uint32_t bar, uint32_t parity) { return bar_wait<true>(bar, parity, p.wait_cycles); };
     // The i-th tile of this pair, for a whole warp; false after the last one.
     auto next_tile = [&](Tile &ti, int i) {
         const int s = i % kTileRing;
@@ -430,19 +432,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             // early starts late, and the tiles of one expert no longer together
                             if (!(ok = wait(saddr(&bars.want), (i - 1) & 1))) break;
                             t = pairs + (int)atomicAdd(p.next, 1u);
-                            if (!(ok = wait(empty, ((i / kNextRing) & 1) ^ 1))) break;
+                            if (!(ok = wait_cluster(empty, ((i / kNextRing) & 1) ^ 1))) break;
                             send_u32(map_rank(saddr(&bars.next[n]), 1), (uint32_t)t, map_rank(full, 1));
                         } else {
                             bar_expect(full, 4);
-                            if (!(ok = wait(full, (i / kNextRing) & 1))) break;
+                            if (!(ok = wait_cluster(full, (i / kNextRing) & 1))) break;
                             t = bars.next[n];
-                            bar_arrive_remote(map_rank(empty, 0));
+                            bar_arrive_cluster(map_rank(empty, 0));
                         }
                     } else if (drawn) {
                         // the first round of ring place 0 stands for the first tile, which nobody sends
                         if (rank == 1) {
                             bar_arrive(saddr(&bars.nfull[0]));
-                            bar_arrive_remote(map_rank(saddr(&bars.nempty[0]), 0));
+                            bar_arrive_cluster(map_rank(saddr(&bars.nempty[0]), 0));
                         }
                     } else if (i > 0) {
                         t += pairs;
@@ -496,15 +498,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if (elect()) {
                         uint32_t bar = full0;
                         if constexpr (S::WG) {
-                            if (kb == nk - 1 && (ti.valid & 63) != 0) {
-                                // the rows past the end are cleared before the products see the stage
+                            const int part = ti.valid & 63;  // rows of the last 64 that are not full
+                            if (kb == 0 && part != 0) {
+                                // these come first: the rows past the end are cleared before the products
+                                // see the stage, while they still work on the tile before
                                 bar = map_rank(b_land + 8 * st, rank);
                                 bar_expect(b_land + 8 * st, bytes);
                             } else if (rank == 0) {
                                 bar_expect(b_full + 8 * st, 2 * bytes);
                                 bar_arrive(b_full + 8 * st);  // for the other CTA
                             }
-                            const int r = (int)(ti.row0 + kb * 64);
+                            const int r = (int)(ti.row0 + (part == 0 ? kb : kb == 0 ? nk - 1 : kb - 1) * 64);
                             const int n0 = ti.w0 + (int)rank * 128, c0 = ti.c0 + (int)rank * half;
                             tma_2d(a, &maps.m[0], n0, r, bar);
                             tma_2d(a + 8192, &maps.m[0], n0 + 64, r, bar);
@@ -563,7 +567,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         const int in_seg = S::SEG == 0 ? kb : kb % (S::SEG == 0 ? 1 : S::SEG);
                         const uint32_t buf = seg & 1;
                         // the operands first: they are there long before the accumulator is read out
-                        ok = __all_sync(0xFFFFFFFFu, wait(b_full + 8 * st, ph));
+                        const bool part = S::WG && kb == 0 && (ti.valid & 63) != 0;
+                        ok = __all_sync(0xFFFFFFFFu, part ? wait_cluster(b_full + 8 * st, ph) : wait(b_full + 8 * st, ph));
                         if (!ok) break;
                         if (in_seg == 0) {
                             ok = __all_sync(0xFFFFFFFFu, wait(b_tempty + 8 * buf, ((seg >> 1) & 1) ^ 1));
@@ -572,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                         fence_after();
                         const uint32_t a = saddr(smem + st * S::STAGE), b = a + S::A_BYTES;
                         const uint32_t d = tmem + buf * 256;
-                        const int steps = S::WG ? (min(64, ti.valid - kb * 64) + 15) / 16 : 4;
+                        const int steps = part ? ((ti.valid & 63) + 15) / 16 : 4;
                         const bool ends = kb == nk - 1 || (S::SEG != 0 && in_seg == S::SEG - 1);
                         if (elect()) {
 #pragma unroll
@@ -689,8 +694,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     cur = nxt;
                 }
             } else if constexpr (S::WG) {
-                // an expert's last rows: clear the lines past its end (both operands
-                // hold one 128-byte line per row and 64 channels), up to the 16 rows of a product
+                // an expert's last rows, in its tile's first stage: clear the lines past its end
+                // (both operands hold one 128-byte line per row and 64 channels), up to the 16 rows of a
+                // product
                 int st = 0;
                 uint32_t landed = 0;  // parity of each stage's landing barrier
                 Tile ti;
@@ -698,24 +704,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     if (!next_tile(ti, i)) break;
                     const int nk = stages_of(ti);
                     if ((ti.valid & 63) != 0) {
-                        const int s = (st + nk - 1) % S::STAGES;
-                        ok = __all_sync(0xFFFFFFFFu, wait(b_land + 8 * s, (landed >> s) & 1));
+                        ok = __all_sync(0xFFFFFFFFu, wait(b_land + 8 * st, (landed >> st) & 1));
                         if (!ok) break;
-                        landed ^= 1u << s;
-                        uint8_t *base = smem + s * S::STAGE;
+                        landed ^= 1u << st;
+                        uint8_t *base = smem + st * S::STAGE;
                         const int r0 = ti.valid & 63, r1 = (r0 + 15) & ~15;
                         for (int i = lane; i < (r1 - r0) * 32; i += 32) {
                             const int row = r0 + (i >> 5), piece = i & 31;  // 4 chunks x 8 pieces of 16 bytes
                             *reinterpret_cast<uint4 *>(base + (piece >> 3) * 8192 + row * 128 + (piece & 7) * 16) =
                                 make_uint4(0, 0, 0, 0);
                         }
-                        // The lines are read by this SM's tensor core only: the fence puts the zeros before
-                        // that, the arrival just carries the signal to the CTA that issues the products (with
-                        // a release and an acquire at cluster scope, 264 -> 313 us at 16 x 1000 rows x 2048 x
-                        // 7168).
+                        // The first CTA issues the products that read the lines of both: the zeros go before
+                        // the tensor core's reads by the fence, and to that CTA's thread by a release at
+                        // cluster scope.  Nothing waits for it: the loader is up to STAGES stages ahead of
+                        // the products here (16 experts x 2048 x 7168: 280 us at 1000 rows each, 278 at 1024,
+                        // where nothing is cleared; in a tile's last stage the release and its acquire took
+                        // 2000 cycles a tile, 313 us).
                         fence_async_shared();
                         __syncwarp();
-                        if (lane == 0) bar_arrive_remote(map_rank(b_full + 8 * s, 0));
+                        if (lane == 0) bar_arrive_cluster(map_rank(b_full + 8 * st, 0));
                     }
                     st = (st + nk) % S::STAGES;
                 }

@@ -52,31 +52,47 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Arrive on a barrier anywhere in the cluster (address from map_rank).  No
-// generic writes are published to the other CTA: what it orders are tensor
-// memory reads and a CTA's own shared memory, by their own fences.  A release at
-// cluster scope would wait for everything the thread has in flight (wgrad with
-// one per stage: 700 instead of 1380 TFLOP/s).
+// Arrive on a barrier anywhere in the cluster (address from map_rank).  For
+// arrivals that publish no memory: what they order are tensor memory reads, by
+// their own fences.
 __device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same for an arrival behind which this thread has written or read shared
+// memory that the other CTA reads or writes next: a release at cluster scope,
+// met by bar_wait<true>.  It waits for everything the thread has in flight, so it
+// has no place where something waits for it at once (wgrad with one per stage:
+// 700 instead of 1380 TFLOP/s).
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// CLUSTER: acquires at cluster scope what the other CTA's threads released.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 // Bounded wait for the phase with this parity; false when it gave up, after
 // `cycles` of the SM's own counter (it never steps back, unlike the global
 // timer), which is read every 1024 polls.
 constexpr long long kWaitCycles = 1ll << 32;  // about 2 s
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, long long cycles) {
-    if (bar_try(bar, parity)) return true;
+    if (bar_try<CLUSTER>(bar, parity)) return true;
     long long t0 = 0;
-    for (uint32_t n = 1; !bar_try(bar, parity); ++n) {
+    for (uint32_t n = 1; !bar_try<CLUSTER>(bar, parity); ++n) {
         if ((n & 1023) != 0) continue;
         const long long t = clock64();
         if (t0 == 0)
