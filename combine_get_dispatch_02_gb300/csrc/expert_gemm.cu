@@ -35,7 +35,7 @@
 //   bf16       the whole sum over k (the next tile's products run while this
 //              tile is written out)
 //   e4m3       one block of 128 channels
-//   wgrad      the whole sum over rows; fp32 output: 384 rows, added up in
+//   wgrad      the whole sum over rows; fp32 output: 256 rows, added up in
 //              registers (the tensor cores truncate when they add, and a long
 //              sum would drift: 8e-6 of the result over 7168 terms, measured);
 //              stored, or added to what is there, by tensor map from shared
@@ -47,7 +47,7 @@
 // the 1913 TFLOP/s bf16 peak, 1706 over seconds):
 //   bf16   262144 rows x 2048 x 7168    4.9 ms, 1.57 PFLOP/s (power limit), 4.1 ms cold
 //          256 experts x 16 rows x 7168 x 2048   1.10 ms, 6.9 TB/s
-//   wgrad  16 x 1024 rows x 2048 x 7168   278 us, 1.73 PFLOP/s; fp32 output 343 us
+//   wgrad  16 x 1024 rows x 2048 x 7168   278 us, 1.73 PFLOP/s; fp32 output 356 us
 //          (0.94 GB, which the tensor cores' work only partly covers)
 //   e4m3   8192^3   485 us, 2.27 PFLOP/s (row form: reading the partial sums takes
 //          about 950 cycles a block, the products 512)
@@ -116,10 +116,12 @@ struct Shape {
     static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 + (COL ? READ * 64 * 4 : 0) : 0;
     // channels (bf16: 64, e4m3: 128) or rows (wgrad: 64) of one stage
     static constexpr int KSTEP = FP8 ? 128 : 64;
-    // stages per segment; 0: all of them.  fp32 wgrad: 384 rows.  With 256 the tensor cores wait for the
-    // registers while those are stored (16 x 1024 rows x 2048 x 7168: 354 instead of 338 us), with 512 the
-    // drift of 6000 equal-signed terms is over 2^-20.
-    static constexpr int SEG = FP8 ? 1 : (F32 ? 6 : 0);
+    // stages per segment; 0: all of them.  fp32 wgrad: 256 rows, 16 additions that truncate, whose drift
+    // (2-norm of the error of equal-signed sums of 384 to 6000 rows: 3.1 to 3.8e-7) is what a plain fp32
+    // product of the library is off by (1.8 to 4.3e-7).  384 rows drift by 5.6e-7, 128 by 1.9e-7.  16 x 1024
+    // rows x 2048 x 7168: 339 / 356 / 404 us with 384 / 256 / 128 (the tensor cores run two segments ahead
+    // and wait for the registers while those are stored), 64 x 256 rows 644 / 644 / 658.
+    static constexpr int SEG = FP8 ? 1 : (F32 ? 4 : 0);
     static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE + READ * OUT_BYTES + SCALES + AMAX;
 };
 
@@ -1046,7 +1048,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     }
                 }
             } else {
-                // wgrad in fp32: sums of 384 rows added up in registers, columns 128 hw on
+                // wgrad in fp32: sums of 256 rows added up in registers, columns 128 hw on
                 uint64_t acc[4][16];
 #pragma unroll
                 for (int q = 0; q < 4; ++q)

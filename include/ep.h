@@ -328,6 +328,11 @@ ep_status ep_expert_identity(ep_ctx *ctx, const ep_handle *handle, int32_t use_f
  *     d_dy   device bf16 [rows, n];  d_x  device bf16 [rows, k]
  *     d_dw   device [E, n, k], fp32 (out_fp32 = 1) or bf16 (0: one rounding);
  *            accumulate = 1 (fp32 only) adds to what it holds
+ *   The tensor cores truncate when they add: fp32 sums leave them every 256 rows
+ *   and are added up with rounding, so sums of equal sign come out low by up to
+ *   2^-21 of themselves (mean over the outputs), as a plain fp32 product is off
+ *   either way.  bf16 outputs take the whole sum (8e-6 low over 7168 equal-signed
+ *   terms), like the other bf16 products; their rounding is 2^-9.
  * ep_expert_swiglu: h = g / (1 + exp(-g)) * u of gu = [g | u] rows, in fp32,
  *   one bf16 rounding.
  *     d_gu  device bf16 [rows, 2*inner];  d_h  device bf16 [rows, inner]
