@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from expert_reference import receive
+from expert_reference import BF16, assert_close, receive, silu
 from test_gpu_experts import _setup, check_wgrad, done, group  # noqa: F401  (_setup: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -34,3 +34,51 @@ def test_wgrad_in_fp32_drifts_no_more_than_an_fp32_product(rows):
     done(buf)
     want = dy.double().T @ x.double()
     assert float((dw[0].double() - want).norm() / want.norm()) < 2.0 ** -21
+
+
+@pytest.mark.parametrize("counts", [[3, 0, 40], [300, 700]])
+def test_gate_is_good_to_24_bits_however_far_out(counts):
+    """One gate value per block of 128 channels, the others zero: the block's scale is
+    |h| / 448 in fp32.  exp is good to 1 ulp, 1 + e, g e and u to half a one, the
+    division to 2 and the scale to half: 5 ulp of 2^-23, below 2^-20.  The last gates
+    are past the range where a fast division by 1 + exp(-g) gives 0."""
+    gates = [-1.0, -6.5, -12.0, -20.0, -26.0, -44.0, -60.0, -72.0, -80.0, -88.0, 1.0, 20.0, 60.0, 88.0]
+    buf, h, _ = group(counts)
+    E, inner = len(counts), 128 * len(gates)
+    g = torch.tensor(gates, dtype=torch.float64)
+    up = 2.0 ** (1 - silu(g).abs().log2().ceil())     # so that h lies between 1 and 4
+    want = (silu(g) * up).abs().cuda()
+    xq = torch.zeros(buf.rows, 128, device="cuda")
+    xq[:, 0] = 1.0
+    wq, ws = torch.zeros(E, 2 * inner, 128, device="cuda"), torch.ones(E, 2 * len(gates), 1, device="cuda")
+    wq[:, 0:inner:128, 0] = g.float().cuda()
+    wq[:, inner::128, 0] = 1.0
+    ws[:, len(gates):, 0] = up.float().cuda()
+    fp8 = torch.float8_e4m3fn
+    hq, hs = buf.expert_gate_fp8((xq.to(fp8), torch.ones(buf.rows, 1, device="cuda")), (wq.to(fp8), ws), h)
+    done(buf)
+    assert_close(hs * 448.0, want.expand_as(hs), 2.0 ** -20 * want, "scales")
+    assert bool((hq[:, ::128].float() == 448.0 * torch.sign(g.float()).cuda()).all())
+
+
+def test_swiglu_far_out_with_large_factors():
+    """Gates where exp(-g) overflows in fp32 while h and its gradient do not.  exp(g)
+    is subnormal there, good to half of 2^-149; everything else to a few ulp."""
+    gates = [-30.0, -60.0, -87.0, -88.5, -89.0, -92.0, -95.0, -98.0, 30.0, 60.0, 89.0, 98.0]
+    g = torch.tensor(gates, dtype=torch.float64).cuda()
+    u = torch.where(g < 0, 2.0 ** 100, 1.5)
+    dh = torch.where(g < 0, 2.0 ** 30, 0.75)         # u dh alone is past fp32's range
+    pad = torch.zeros(4, dtype=torch.float64, device="cuda")
+    row = torch.cat((g, pad, u, pad)).bfloat16().expand(5, -1).contiguous()
+    buf, h, _ = group([2, 3])
+    out = buf.expert_swiglu(row, h)
+    dgu, again = buf.expert_swiglu_backward(row, torch.cat((dh, pad)).bfloat16().expand(5, -1).contiguous(), h)
+    done(buf)
+    assert torch.equal(out, again)
+    s, low = torch.sigmoid(g), 2.0 ** -149 * (1.0 + g.abs()) * u
+    want = silu(g) * u
+    assert_close(out[:, :12], want.expand(5, -1), (BF16 + 2.0 ** -19) * want.abs() + low, "h")
+    want = dh * silu(g)
+    assert_close(dgu[:, 16:28], want.expand(5, -1), (BF16 + 2.0 ** -19) * want.abs() + low / u * dh, "du")
+    want = dh * u * s * (1 + g * (1 - s))
+    assert_close(dgu[:, :12], want.expand(5, -1), (BF16 + 2.0 ** -19) * want.abs() + low * dh, "dg")
