@@ -2,7 +2,9 @@
 
 serve: FP8 dispatch -> gate and up products, SwiGLU and cast -> down product -> combine
 train: bf16 dispatch -> gate and up -> SwiGLU -> down -> combine, and back: the gradient of the
-       combine is a dispatch, the experts' backward pass, the gradient of the dispatch is a combine
+       combine is a dispatch whose rows take their entry's routing weight (and, for those weights, a
+       product of each token's gradient with its experts' outputs), the experts' backward pass, the
+       gradient of the dispatch is a combine
 
 Usage: python examples/expert_mlp.py serve|train [--ranks R] [--tokens T] [--hidden H] [--experts E]
        [--topk K] [--inner I] [--padded] [--steps N]
@@ -49,7 +51,23 @@ def serve_step(buf, h, x, idx, wts, w_gate_up, w_down, clock):
     return out
 
 
-def train_step(buf, h, x, idx, wts, w_gate_up, w_down, grads, clock):
+def combine_backward(buf, h, dout, y, wts):
+    """Gradients of out[t] = sum_k wts[t, k] * y[row(t, k)]: (dy in the receive layout, dwts [N, K]);
+    masked entries have none."""
+    slot = h.tensors()["slot"].long()
+    dy, _, _ = buf.low_latency_dispatch(dout, None, buf.max_tokens_per_rank, buf.num_experts, use_fp8=False, handle=h)
+    # the weight of each row's entry; masked entries write behind the last row
+    w = torch.zeros(buf.rows + 1, 1, device=dy.device)
+    w[torch.where(slot < 0, buf.rows, slot).view(-1)] = wts.view(-1, 1)
+    wide = dout.float()
+    dw = torch.stack([(wide * y.index_select(0, s.clamp_min(0))).sum(1) for s in slot.unbind(1)], 1)
+    return torch.mul(dy, w[:-1], out=dy), torch.where(slot < 0, 0.0, dw)
+
+
+def train_step(buf, h, x, idx, wts, w_gate_up, w_down, grads, clock, loss_grad=lambda out: out):
+    """Forward and backward of out = combine(experts(dispatch(x)), wts); loss_grad(out) [N, H] bf16 is the
+    loss's gradient (the default: of half the sum of out's squares).  Adds the weights' gradients to
+    ``grads``; returns (out, dx [N, H], dwts [N, K])."""
     clock("start")
     recv, _, h = buf.low_latency_dispatch(x, idx, buf.max_tokens_per_rank, buf.num_experts, use_fp8=False, handle=h)
     clock("dispatch")
@@ -57,15 +75,13 @@ def train_step(buf, h, x, idx, wts, w_gate_up, w_down, grads, clock):
     clock("experts")
     out = buf.low_latency_combine(y, idx, wts, h, buf.num_experts)
     clock("combine")
-    # a loss whose gradient is the output itself; the combine's gradient is a dispatch of it (its
-    # weights left to the caller: here all experts of a token get the same gradient)
-    dy, _, _ = buf.low_latency_dispatch(out, None, buf.max_tokens_per_rank, buf.num_experts, use_fp8=False, handle=h)
+    dy, dwts = combine_backward(buf, h, loss_grad(out), y, wts)
     clock("combine backward")
     dx, *_ = buf.expert_mlp_backward(dy, saved, w_gate_up, w_down, h, grads=grads)
     clock("experts backward")
     dtok = buf.low_latency_combine(dx, idx, None, h, buf.num_experts)
     clock("dispatch backward")
-    return dtok
+    return out, dtok, dwts
 
 
 def main():
@@ -88,7 +104,7 @@ def main():
     h = buf.new_handle()
     if a.mode == "serve":
         qgu, qd = buf.cast_weights(w_gate_up), buf.cast_weights(w_down)
-        step = lambda clock: serve_step(buf, h, x, idx, wts, qgu, qd, clock)  # noqa: E731
+        step = lambda clock: (serve_step(buf, h, x, idx, wts, qgu, qd, clock),)  # noqa: E731
     else:
         grads = (torch.zeros(w_gate_up.shape, device=dev), torch.zeros(w_down.shape, device=dev))
         step = lambda clock: train_step(buf, h, x, idx, wts, w_gate_up, w_down, grads, clock)  # noqa: E731
@@ -98,7 +114,7 @@ def main():
     for c in clocks:
         out = step(c)
     rows = [c.parts() for c in clocks]
-    if buf.device_status() != ep.EP_OK or not bool(torch.isfinite(out.float()).all()):
+    if buf.device_status() != ep.EP_OK or not all(bool(torch.isfinite(t.float()).all()) for t in out):
         raise SystemExit("the step failed")
     n = a.ranks * a.tokens
     total = sum(us for r in rows for _, us in r) / len(rows)
