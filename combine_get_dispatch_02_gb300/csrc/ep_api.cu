@@ -18,6 +18,7 @@
 
 #include "ep.h"
 #include "ep_internal.cuh"
+#include "tile_counters.h"
 
 namespace {
 constexpr int kCeStreams = 2;  // device wire: copies spread over two streams (measured: 1 stream 2.5,
@@ -75,9 +76,8 @@ struct ep_handle {
     int32_t runs_state;       // 0: none, 1: copy queued (wait on runs_ev), 2: on the host
     int32_t has_send;         // send_slot / runs belong to the layout held
     // who holds which tile counter of the expert products (they lie behind the layout's barrier
-    // counter): the streams by their ids, in the order of their first call, and captured calls
-    mutable unsigned long long counter_stream[ep::kStreamCounters];
-    mutable uint32_t counter_streams, counter_captured;
+    // counter)
+    ep::TileCounters *counters;
 };
 
 namespace {
@@ -633,32 +633,46 @@ ep_status check_channels(int32_t c, int32_t step) {
 
 int expert_sms(const ep_ctx *ctx) { return grid_cap(ctx, 1); }
 
-// The tile counter of a product on `st`: two launches that can run side by side
-// must not draw from one.  A stream's launches follow each other, so each stream has
-// one; a captured call has one of its own, because its graph can run beside
-// anything (but not beside itself: it writes the same output).  nullptr when
+// The tile counter of a product on `st` (see tile_counters.h); nullptr when
 // they are all taken: the tiles are then dealt out in a fixed order.
 uint32_t *tile_counter(const ep_ctx *ctx, const ep_handle *h, cudaStream_t st) {
     uint32_t *const first = reinterpret_cast<uint32_t *>(h->cta_hist + grid_hist_ints(ctx) + 16);
     cudaStreamCaptureStatus capture;
-    unsigned long long id;
     if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) {
         cudaGetLastError();  // the launch reports it
         return nullptr;
     }
     if (capture != cudaStreamCaptureStatusNone) {
-        if (h->counter_captured == ep::kCapturedCounters) return nullptr;
-        return first + 2 * (ep::kStreamCounters + h->counter_captured++);
+        // the graph keeps the counter, and hands it to its copies
+        cudaGraph_t graph = nullptr;
+        cudaUserObject_t object;
+        if (cudaStreamGetCaptureInfo(st, &capture, nullptr, &graph, nullptr, nullptr, nullptr) != cudaSuccess ||
+            capture != cudaStreamCaptureStatusActive) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        ep::TileCounters::Captured *const c = h->counters->take();
+        if (c == nullptr) return nullptr;
+        const int index = c->index;
+        if (cudaUserObjectCreate(&object, c, ep::TileCounters::give_back, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+            cudaGetLastError();
+            ep::TileCounters::give_back(c);
+            return nullptr;
+        }
+        if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) != cudaSuccess) {
+            cudaGetLastError();
+            cudaUserObjectRelease(object, 1);  // gives the counter back
+            return nullptr;
+        }
+        return first + 2 * index;
     }
+    unsigned long long id;
     if (cudaStreamGetId(st, &id) != cudaSuccess) {
         cudaGetLastError();
         return nullptr;
     }
-    for (uint32_t i = 0; i < h->counter_streams; ++i)
-        if (h->counter_stream[i] == id) return first + 2 * i;
-    if (h->counter_streams == ep::kStreamCounters) return nullptr;
-    h->counter_stream[h->counter_streams] = id;
-    return first + 2 * h->counter_streams++;
+    const int i = h->counters->of_stream(id);
+    return i < 0 ? nullptr : first + 2 * i;
 }
 
 // The parameters every expert product shares.
@@ -820,6 +834,11 @@ ep_status ep_handle_create(ep_ctx *ctx, ep_handle **out) {
     h->ctx = ctx;
     h->tokens_per_rank = -1;
     h->num_keys = c.num_experts;
+    h->counters = ep::TileCounters::create();
+    if (h->counters == nullptr) {
+        free(h);
+        return EP_ERR_OOM;
+    }
     const size_t nk = (size_t)c.num_ranks * c.max_tokens_per_rank * c.topk;
     const size_t er = (size_t)c.num_experts * c.num_ranks;
     bool ok = cudaMalloc(&h->slot, nk * sizeof(int32_t)) == cudaSuccess &&
@@ -863,6 +882,7 @@ ep_status ep_handle_destroy(ep_handle *h) {
     if (h->h_runs) cudaFreeHost(h->h_runs);
     if (h->runs_ev) cudaEventDestroy(h->runs_ev);
     cudaGetLastError();
+    if (h->counters) h->counters->release();
     free(h);
     return EP_OK;
 }
@@ -1721,6 +1741,13 @@ ep_status ep_get_device_status(ep_ctx *ctx, void *stream) {
     if (bits & ep::kStatusCapacity) return EP_ERR_CAPACITY;
     if (bits & ep::kStatusInFlight) return EP_ERR_TIMEOUT_IN_FLIGHT;
     if (bits & ep::kStatusTimeout) return EP_ERR_TIMEOUT;
+    return EP_OK;
+}
+
+ep_status ep_get_test_counters(const ep_handle *handle, int32_t *streams, int32_t *captured) {
+    if (handle == nullptr || streams == nullptr || captured == nullptr) return EP_ERR_INVALID_ARG;
+    *streams = handle->counters->streams();
+    *captured = handle->counters->captured();
     return EP_OK;
 }
 

@@ -225,9 +225,6 @@ struct ExpertGemmParams {
     uint32_t *next;         // tile counter and count of the pairs that are done with it: both zero
                             // between launches, each launch puts them back; nullptr: none free
 };
-// Tile counters of a handle (two words each), for its streams and for calls
-// captured into graphs.
-constexpr int kStreamCounters = 64, kCapturedCounters = 4032;
 // One-time set-up with the device current (shared memory limits).
 void expert_gemm_init();
 cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStream_t stream);

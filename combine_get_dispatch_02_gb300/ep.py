@@ -42,7 +42,7 @@ ENTRY_POINTS = (
     "ep_get_device_status", "ep_dispatch_noalloc", "ep_get_rank_layout", "ep_rank_recv_rows",
     "ep_dispatch_range", "ep_combine_range", "ep_expert_identity", "ep_round_trip",
     "ep_round_trip_auto_chunk", "ep_dispatch_send", "ep_dispatch_recv", "ep_combine_send", "ep_combine_recv",
-    "ep_get_tuning", "ep_set_tuning", "ep_autotune", "ep_get_autotune_log", "ep_set_test_hooks",
+    "ep_get_tuning", "ep_set_tuning", "ep_autotune", "ep_get_autotune_log", "ep_set_test_hooks", "ep_get_test_counters",
     "ep_rank_send_rows", "ep_rank_dispatch_send", "ep_rank_dispatch_recv", "ep_rank_combine_send",
     "ep_rank_combine_recv", "ep_rank_runs",
     "ep_expert_gemm", "ep_expert_gemm_fp8", "ep_expert_gate_fp8", "ep_expert_wgrad", "ep_expert_swiglu",
@@ -139,6 +139,7 @@ def lib() -> ctypes.CDLL:
             "ep_autotune": (I32, [P, P, P, I32, P, I32, P, P, P, P, I32, ctypes.POINTER(ep_tuning), P]),
             "ep_get_autotune_log": (I32, [P, ctypes.POINTER(ep_tune_record), I32, ctypes.POINTER(I32)]),
             "ep_set_test_hooks": (I32, [P, ctypes.POINTER(ep_test_hooks)]),
+            "ep_get_test_counters": (I32, [P, ctypes.POINTER(I32), ctypes.POINTER(I32)]),
             "ep_rank_send_rows": (I32, [CFG, ctypes.POINTER(I64)]),
             "ep_rank_dispatch_send": (I32, [P, P, P, P, I32, I32, P, P, P, P, P, P]),
             "ep_rank_dispatch_recv": (I32, [P, P, I32, P, P, P, P, P, I32, P, P]),
@@ -412,6 +413,13 @@ def ep_set_test_hooks(ctx, move_withhold_item: int = -1, move_wait_ns: int = 0) 
     load is never issued, and the bound of their waits."""
     h = ep_test_hooks(int(move_withhold_item), int(move_wait_ns))
     _check(lib().ep_set_test_hooks(ctx, ctypes.byref(h)), "ep_set_test_hooks")
+
+
+def ep_get_test_counters(handle) -> tuple[int, int]:
+    """Test-only: tile counters of the expert products held by (streams, captured calls)."""
+    streams, captured = ctypes.c_int32(), ctypes.c_int32()
+    _check(lib().ep_get_test_counters(handle, ctypes.byref(streams), ctypes.byref(captured)), "ep_get_test_counters")
+    return streams.value, captured.value
 
 
 def ep_rank_send_rows(cfg: ep_config) -> int:

@@ -345,7 +345,13 @@ ep_status ep_expert_identity(ep_ctx *ctx, const ep_handle *handle, int32_t use_f
  *
  * Operators of one handle may run side by side (several streams, graphs) as
  * long as none writes what another reads or writes.  Results do not depend on
- * max_sms, the layout form or the kernels around. */
+ * max_sms, the layout form or the kernels around.
+ *
+ * A handle has tile counters for 512 streams, by the streams' ids, and for 3584
+ * captured calls in graphs that exist; a captured call's comes back when its graph
+ * and what was instantiated from it are destroyed.  Products on further streams and in
+ * further captured calls take their tiles in a fixed order, with the same
+ * results, up to a fifth slower. */
 ep_status ep_expert_gemm(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const void *d_w,
                          int32_t n, int32_t k, int32_t transpose_w, void *d_y, void *stream);
 ep_status ep_expert_gemm_fp8(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const float *d_x_scales,
@@ -637,6 +643,9 @@ typedef struct ep_test_hooks {
     int64_t move_wait_ns;
 } ep_test_hooks;
 ep_status ep_set_test_hooks(ep_ctx *ctx, const ep_test_hooks *hooks);
+/* Test-only: how many of a handle's tile counters (expert operators) its streams
+ * and its captured calls hold.  Host only. */
+ep_status ep_get_test_counters(const ep_handle *handle, int32_t *streams, int32_t *captured);
 
 #ifdef __cplusplus
 }

@@ -1,9 +1,13 @@
 """GPU checks of the expert operators at the edges of their groups, ranges and handles."""
+import ctypes
+import time
+
 import pytest
 import torch
 
-from expert_reference import BF16, assert_close, receive, silu
-from test_gpu_experts import _setup, check_wgrad, done, group  # noqa: F401  (_setup: the module's fixture)
+from combine_get_dispatch_02_gb300 import ep
+from expert_reference import BF16, assert_close, in_use, receive, silu, weights
+from test_gpu_experts import _setup, check_wgrad, done, group, sentinel  # noqa: F401  (_setup: the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +86,69 @@ def test_swiglu_far_out_with_large_factors():
     assert_close(dgu[:, 16:28], want.expand(5, -1), (BF16 + 2.0 ** -19) * want.abs() + low / u * dh, "du")
     want = dh * u * s * (1 + g * (1 - s))
     assert_close(dgu[:, :12], want.expand(5, -1), (BF16 + 2.0 ** -19) * want.abs() + low * dh, "dg")
+
+
+def held_by_captured_calls(h, want, seconds=10.0):
+    """The captured calls' tile counters once they are ``want``: a graph's objects go
+    on a thread of the driver's."""
+    end = time.monotonic() + seconds
+    while (n := ep.ep_get_test_counters(h.raw)[1]) != want and time.monotonic() < end:
+        time.sleep(0.01)
+    return n
+
+
+def test_captured_calls_give_their_counters_back():
+    """A program that captures its step again and again: every call of a graph that
+    exists holds a counter, none does when the graphs are gone, and a graph that is
+    destroyed while it runs keeps its counters until it has run."""
+    buf, h, grp = group([300, 0, 17, 640, 128, 1, 77, 256] * 4)
+    used = in_use(buf.rows, grp)
+    x, w = receive(buf.rows, 256, grp, 1), weights(32, 2048, 256, 2)
+    want, out = buf.expert_gemm(x, w, h), sentinel((buf.rows, 2048))
+    torch.cuda.synchronize()
+    for _ in range(4):      # 6000 calls in all
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(1500):
+                buf.expert_gemm(x, w, h, out=out)
+        assert ep.ep_get_test_counters(h.raw)[1] == 1500
+        out.fill_(0)
+        g.replay()
+        done(buf)
+        assert torch.equal(out[used], want[used])
+        del g
+        assert held_by_captured_calls(h, 0) == 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(1500):
+            buf.expert_gemm(x, w, h, out=out)
+    for _ in range(4):
+        g.replay()
+    ran = torch.cuda.Event()
+    ran.record()
+    del g
+    early = ep.ep_get_test_counters(h.raw)[1], ran.query()
+    done(buf)
+    assert early[1] or early[0] == 1500
+    assert held_by_captured_calls(h, 0) == 0
+
+
+def test_more_streams_than_counters():
+    """Past the counters for streams the tiles come in a fixed order, with the same bits."""
+    buf, h, grp = group([300, 0, 17, 640, 128, 1, 77, 256])
+    used = in_use(buf.rows, grp)
+    x, w = receive(buf.rows, 256, grp, 1), weights(8, 2560, 256, 2)
+    want, out = buf.expert_gemm(x, w, h), sentinel((buf.rows, 2560))
+    rt = torch.cuda.cudart()
+    for _ in range(520):
+        raw = ctypes.c_void_p()
+        assert int(rt.cudaStreamCreate(ctypes.addressof(raw))) == 0
+        out.fill_(0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw.value)):
+            buf.expert_gemm(x, w, h, out=out)
+        torch.cuda.synchronize()
+        assert torch.equal(out[used], want[used])
+        assert int(rt.cudaStreamDestroy(raw.value)) == 0
+    assert ep.ep_get_test_counters(h.raw)[0] == 512
+    done(buf)
