@@ -77,7 +77,8 @@ class Buffer:
     ``low_latency_mode=True`` gives the padded layout (E fixed buffers of
     R*num_max_dispatch_tokens_per_rank rows); False gives the packed layout
     of the normal (high-throughput) kernels.  ``max_sms`` caps the SMs the
-    dispatch / combine kernels use (0 = all)."""
+    dispatch / combine kernels use (0 = all); the experts' products take
+    SMs in pairs, 2 at least."""
 
     def __init__(self, num_ranks: int, num_max_dispatch_tokens_per_rank: int, hidden: int,
                  num_experts: int, num_topk: int, low_latency_mode: bool = True, max_sms: int = 0,

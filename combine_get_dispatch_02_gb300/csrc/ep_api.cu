@@ -689,7 +689,7 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
     p.sms = expert_sms(ctx);
     p.withhold = ctx->hooks.move_withhold_item < c.num_experts ? (int32_t)ctx->hooks.move_withhold_item : -1;
     // 2 clocks a ns (a little over the fastest clock)
-    p.wait_cycles = ctx->hooks.move_wait_ns > 0 ? 2 * ctx->hooks.move_wait_ns : 1ll << 32;
+    p.wait_cycles = ctx->hooks.move_wait_ns > 0 ? 2 * ctx->hooks.move_wait_ns : ep::kExpertWaitCycles;
     p.status = ctx->d_status;
     p.next = tile_counter(ctx, h, st);
     return p;

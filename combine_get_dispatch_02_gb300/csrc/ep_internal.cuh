@@ -202,6 +202,7 @@ int identity_blocks_per_sm(bool fp8);
 // ------------------------------------------------------------------ expert products
 // Matrix products over the rows of each expert (see expert_gemm.cu).
 enum class ExpertOp : int { kBf16 = 0, kBf16T = 1, kFp8 = 2, kGateFp8 = 3, kWgrad = 4 };
+constexpr int64_t kExpertWaitCycles = int64_t(1) << 32;  // about 2 s
 struct ExpertGemmParams {
     const void *x;          // bf16 or e4m3 [rows, k]
     const float *xs;        // [rows, k/128] (FP8)
@@ -220,7 +221,7 @@ struct ExpertGemmParams {
                                     // y written 32 bytes at a time
     int32_t sms;            // SMs to spread over
     int32_t withhold;       // test hook: expert whose rows are never loaded (-1: none)
-    int64_t wait_cycles;    // bound of each wait in SM clocks
+    int64_t wait_cycles;    // bound of each wait in SM clocks (kExpertWaitCycles)
     uint32_t *status;
     uint32_t *next;         // tile counter and count of the pairs that are done with it: both zero
                             // between launches, each launch puts them back; nullptr: none free

@@ -40,8 +40,10 @@
 //              sum would drift: 8e-6 of the result over 7168 terms, measured);
 //              stored, or added to what is there, by tensor map from shared
 //              memory, which also leaves out what lies past the matrix
-// All waits are bounded; a wait that gives up sets the status word and ends
-// its role.
+// Every wait for another role or CTA is bounded; one that gives up sets the status
+// word and ends its role.  Not bounded are the hardware's own: for the kernel
+// before this one, for tensor memory that another kernel on the SM still holds, for
+// stores under way, and for the other CTA at the start and the end.
 //
 // Measured (one GB300, rows spread evenly unless said; of the 6.78 TB/s copy and
 // the 1913 TFLOP/s bf16 peak, 1706 over seconds):

@@ -87,7 +87,6 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 // Bounded wait for the phase with this parity; false when it gave up, after
 // `cycles` of the SM's own counter (it never steps back, unlike the global
 // timer), which is read every 1024 polls.
-constexpr long long kWaitCycles = 1ll << 32;  // about 2 s
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, long long cycles) {
     if (bar_try<CLUSTER>(bar, parity)) return true;

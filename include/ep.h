@@ -81,7 +81,8 @@ typedef enum ep_status {
     EP_ERR_BAD_EXPERT = 5,   /* device: a topk_idx entry was outside [-1, E) */
     EP_ERR_CAPACITY = 6,     /* device: padded layout, an expert was offered more than R*Tmax entries */
     EP_ERR_NO_LAYOUT = 7,    /* the handle holds no layout yet, or one for other sizes */
-    EP_ERR_TIMEOUT = 8,      /* device: a bounded wait of a copy kernel gave up (about 1 s) */
+    EP_ERR_TIMEOUT = 8,      /* device: a bounded wait of a copy kernel (about 1 s) or of an expert
+                                product (about 2 s) gave up */
     EP_ERR_TIMEOUT_IN_FLIGHT = 9  /* device: as EP_ERR_TIMEOUT, and the kernel's wait for its own
                                      row loads gave up too: a bulk load may have landed in shared
                                      memory after the kernel exited, so nothing the device ran
@@ -102,7 +103,7 @@ typedef enum ep_layout {
  *   (SM count) * 2^20 entries R*T*K (about 1.6e8 on 152 SMs; larger calls
  *   return EP_ERR_UNSUPPORTED).
  * max_sms caps the SMs the dispatch and combine kernels spread over (0 = all),
- * the SM-count control of the normal kernels. */
+ * the SM-count control of the normal kernels (expert products: see there). */
 typedef struct ep_config {
     int32_t num_ranks;            /* R */
     int32_t max_tokens_per_rank;  /* Tmax (num_max_dispatch_tokens_per_rank) */
@@ -301,8 +302,11 @@ ep_status ep_expert_identity(ep_ctx *ctx, const ep_handle *handle, int32_t use_f
  * 16-byte aligned (scales 4).  Channel counts n, k and inner are multiples of 8
  * (EP_ERR_INVALID_ARG otherwise) up to 65536, where FP8 blocks run along them
  * multiples of 128 (EP_ERR_UNSUPPORTED otherwise).  A call uses the context's
- * SMs (max_sms).  Outputs must not overlap inputs.  Every wait inside the
- * kernels is bounded (EP_ERR_TIMEOUT through ep_get_device_status).
+ * SMs (max_sms); the products take them in pairs, max_sms rounded down to an even
+ * number and 2 at least.  Outputs must not overlap inputs.  Every wait of the
+ * kernels for one another's parts is bounded (about 2 s, EP_ERR_TIMEOUT through
+ * ep_get_device_status); a product also waits, without a bound, for kernels
+ * queued before it and for tensor memory that another kernel on its SMs holds.
  *
  * ep_expert_gemm: y[r] = W[e] x[r] for every row r of every expert e, products
  *   of bf16 values summed in fp32, rounded once to bf16.

@@ -152,3 +152,16 @@ def test_more_streams_than_counters():
         assert int(rt.cudaStreamDestroy(raw.value)) == 0
     assert ep.ep_get_test_counters(h.raw)[0] == 512
     done(buf)
+
+
+@pytest.mark.parametrize("sms", [1, 2, 3])
+def test_products_on_one_pair_of_sms(sms):
+    """The products take SMs in pairs, one pair at least: the same bits as on all."""
+    counts = [0, 1, 31, 300, 700, 64]
+    outs = []
+    for n in (0, sms):
+        buf, h, grp = group(counts, max_sms=n)
+        x, w = receive(buf.rows, 256, grp, 1), weights(6, 512, 256, 2)
+        outs.append((buf.expert_gemm(x, w, h)[in_use(buf.rows, grp)], buf.expert_wgrad(x, x, h)))
+        done(buf)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
