@@ -336,7 +336,7 @@ ep_status ep_expert_identity(ep_ctx *ctx, const ep_handle *handle, int32_t use_f
  *   and are added up with rounding, so sums of equal sign come out low by up to
  *   2^-21 of themselves (mean over the outputs), as a plain fp32 product is off
  *   either way.  bf16 outputs take the whole sum (8e-6 low over 7168 equal-signed
- *   terms), like the other bf16 products; their rounding is 2^-9.
+ *   terms), like the other bf16 products; their rounding is up to 2^-8.
  * ep_expert_swiglu: h = g / (1 + exp(-g)) * u of gu = [g | u] rows, in fp32,
  *   one bf16 rounding.
  *     d_gu  device bf16 [rows, 2*inner];  d_h  device bf16 [rows, inner]

@@ -25,7 +25,8 @@ def test_step_is_the_gradient_of_its_forward_pass(padded):
     """Tokens -> dispatch -> experts -> combine with routing weights (masked entries
     among them), for a loss sum(out * t): the gradients of the tokens, both weights
     and the routing weights.  The step keeps gu, h, y, dy, dh, dgu, dx and its result
-    in bf16, 2^-9 each at most: 2^-6 over all of them."""
+    in bf16.  A bf16 rounding is 1.7e-3 in the 2-norm (2^-8 at most, over all
+    mantissas): eight of them stay below 2^-6."""
     R, T, H, E, K, inner = 2, 45, 136, 6, 3, 72
     gen = torch.Generator("cuda").manual_seed(11)
     x = torch.randn(R, T, H, device="cuda", generator=gen).bfloat16()

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 from combine_get_dispatch_02_gb300 import ep
-from expert_reference import BF16, assert_close, in_use, receive, silu, weights
+from expert_reference import (BF16, assert_close, cast_blocks, cast_rows, in_use, receive, silu, weights, wide_block,
+                              wide_rows)
+from norm_bounds import bf16_bound, fp32_bound, relative
 from test_gpu_experts import _setup, check_wgrad, done, group, sentinel  # noqa: F401  (_setup: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -165,3 +167,58 @@ def test_products_on_one_pair_of_sms(sms):
         outs.append((buf.expert_gemm(x, w, h)[in_use(buf.rows, grp)], buf.expert_wgrad(x, x, h)))
         done(buf)
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# rows per expert of a long sum: a few (the FP8 products' column form), many (their row form)
+LONG = [[33, 0, 130], [300, 520]]
+
+
+@pytest.mark.parametrize("counts", LONG)
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "fp8"])
+def test_long_sums_lose_no_term(op, counts):
+    """k = 7168 in the 2-norm of each row and column of the result, where one lost
+    term is three times the bound (see norm_bounds)."""
+    n, k = 264, 7168
+    buf, h, grp = group(counts)
+    x = receive(buf.rows, k, grp, 1)
+    if op == "fp8":
+        xq, wq = cast_rows(x.float()), cast_blocks(weights(len(counts), n, k, 2))
+        y = buf.expert_gemm_fp8(xq, wq, h)
+        operands = lambda e, r: (wide_rows(xq[0][r], xq[1][r]), wide_block(wq[0][e], wq[1][e]))  # noqa: E731
+    else:
+        w = weights(len(counts), *((k, n) if op == "dgrad" else (n, k)), 2)
+        y = buf.expert_gemm(x, w, h, transpose_w=op == "dgrad")
+        operands = lambda e, r: (x[r].double(), (w[e].T if op == "dgrad" else w[e]).double())  # noqa: E731
+    done(buf)
+    for e, (b, c) in enumerate(grp):
+        if c:
+            xe, we = operands(e, slice(b, b + c))
+            assert relative(y[b:b + c], xe @ we.T) <= bf16_bound(k), e
+
+
+@pytest.mark.parametrize("rows", [7168, 7201])
+def test_long_sums_over_rows_lose_no_row(rows):
+    buf, h, grp = group([rows])
+    dy, x = receive(buf.rows, 136, grp, 1), receive(buf.rows, 264, grp, 2)
+    want = dy.double().T @ x.double()
+    dw = buf.expert_wgrad(dy, x, h)
+    dw16 = buf.expert_wgrad(dy, x, h, out=torch.empty(1, 136, 264, dtype=torch.bfloat16, device="cuda"))
+    done(buf)
+    assert relative(dw[0], want) <= fp32_bound(rows)
+    assert relative(dw16[0], want) <= bf16_bound(rows)
+
+
+@pytest.mark.parametrize("counts", LONG)
+def test_gate_over_long_sums_loses_no_term(counts):
+    """The scales of h, which are in fp32: a gate and an up sum off by k / 16 * 2^-23
+    each and a gate's slope of 1.1 at most give 2^-12; a lost term is 1.2e-2."""
+    inner, k = 256, 7168
+    buf, h, grp = group(counts)
+    xq, wq = cast_rows(receive(buf.rows, k, grp, 1).float()), cast_blocks(weights(len(counts), 2 * inner, k, 2))
+    _, hs = buf.expert_gate_fp8(xq, wq, h)
+    done(buf)
+    for e, (b, c) in enumerate(grp):
+        if c:
+            v = wide_rows(xq[0][b:b + c], xq[1][b:b + c]) @ wide_block(wq[0][e], wq[1][e]).T
+            want = (silu(v[:, :inner]) * v[:, inner:]).view(c, -1, 128).abs().amax(2) / 448
+            assert relative(hs[b:b + c], want) <= 2.0 ** -12, e
