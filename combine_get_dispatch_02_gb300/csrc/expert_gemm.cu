@@ -76,9 +76,20 @@ constexpr int kNextRing = 4;      // tile numbers on their way to the second CTA
 constexpr int kScaleGroup = 4;    // 128-channel blocks per fill of the scale buffer
 constexpr int kMaxSmem = 232448;
 // Mean rows per expert from which the e4m3 products take the row form.  Up to 128
-// rows the column form needs one tile and the weights' bytes bound it (64
-// experts x 4096 x 7168, gate: 305 us, row form 461); with 144 rows in two
-// tiles it takes 508 us, the row form 463.
+// rows the column form needs one tile and the weights' bytes bound it; past that
+// it takes two.  Of nine shapes (gate and plain product, n and k of 1024 to 7168, 16 to
+// 128 experts) with the same rows in every expert, all had the column form ahead up to
+// 128 rows (by 1.13 to 1.7 times) and the row form at 136 to 256 rows (by 1.1 to 1.3);
+// at 320 they are within 9 % (column form ahead), at 384 within 8 %, at 512 the row
+// form leads by 1.2 to 1.3.  64 experts, us, column / row form:
+//   rows                      64        128        136        256        512
+//   gate  4096 x 7168    285/428    305/437    501/438    554/445   1069/848
+//         1024 x 1024    20/31      23/32      36/32      41/32      67/53
+//   plain 7168 x 2048    151/217    162/232    261/232    300/244    586/465
+//         1992 x 2176    56/72      63/78      89/78      99/81     190/150
+// The mean is over the layout's entries and all experts: the host does not know
+// which entries are masked or which experts get none, and such a call may take the
+// slower form.
 constexpr int kRowFormRows = 136;
 constexpr int kSortExperts = 256;  // wgrad: most experts that are put in order
 constexpr int kKeepExperts = 256;  // most experts whose counts and bases are kept in shared memory
