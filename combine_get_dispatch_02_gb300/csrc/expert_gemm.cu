@@ -47,16 +47,18 @@
 //
 // Measured (one GB300, rows spread evenly unless said; of the 6.78 TB/s copy and
 // the 1913 TFLOP/s bf16 peak, 1706 over seconds):
-//   bf16   262144 rows x 2048 x 7168    4.9 ms, 1.57 PFLOP/s (power limit), 4.1 ms cold
+//   bf16   262144 rows x 2048 x 7168    5.0 ms, 1.53 PFLOP/s (power limit), 4.2 ms cold
 //          256 experts x 16 rows x 7168 x 2048   1.10 ms, 6.9 TB/s
 //   wgrad  16 x 1024 rows x 2048 x 7168   278 us, 1.73 PFLOP/s; fp32 output 356 us
-//          (0.94 GB, which the tensor cores' work only partly covers)
-//   e4m3   8192^3   485 us, 2.27 PFLOP/s (row form: reading the partial sums takes
+//          (0.94 GB, which the tensor cores' work only partly covers), added 421 us
+//   e4m3   8192^3   483 us, 2.28 PFLOP/s (row form: reading the partial sums takes
 //          about 950 cycles a block, the products 512)
-//          76 experts x 16 rows x 4096 x 7168   327 us, 6.9 TB/s
+//          76 experts x 16 rows x 4096 x 7168   325 us, 6.9 TB/s; 256 experts x 16
+//          rows x 7168 x 2048   545 us, 7.0 TB/s
 //   gate   256 experts x 128 rows x 2 * 2048 x 7168   1.17 ms, 6.7 TB/s; 32768
-//          entries drawn over 256 experts 1.59 ms (half the experts have more than
-//          128 rows and take two tiles, whose weights come through L2 twice)
+//          entries drawn over 256 experts 1.56 to 1.59 ms (half the experts have more
+//          than 128 rows and take two tiles, whose weights come through L2 twice)
+//          256 experts x 1024 rows, the same weights   6.7 ms, 2.3 PFLOP/s
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -80,8 +82,8 @@ constexpr int kMaxSmem = 232448;
 // it takes two.  Of nine shapes (gate and plain product, n and k of 1024 to 7168, 16 to
 // 128 experts) with the same rows in every expert, all had the column form ahead up to
 // 128 rows (by 1.13 to 1.7 times) and the row form at 136 to 256 rows (by 1.1 to 1.3);
-// at 320 they are within 9 % (column form ahead), at 384 within 8 %, at 512 the row
-// form leads by 1.2 to 1.3.  64 experts, us, column / row form:
+// at 320 and 384 they are within 11 %, at 512 the row form leads by 1.2 to 1.3.
+// 64 experts, us, column / row form:
 //   rows                      64        128        136        256        512
 //   gate  4096 x 7168    285/428    305/437    501/438    554/445   1069/848
 //         1024 x 1024    20/31      23/32      36/32      41/32      67/53
