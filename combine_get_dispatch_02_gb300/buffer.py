@@ -523,6 +523,51 @@ class Buffer:
         dw_gate_up = self.expert_wgrad(dgu, x, handle, out=g_gate_up, accumulate=acc)
         return self.expert_gemm(dgu, w_gate_up, handle, transpose_w=True), dw_gate_up, dw_down
 
+    def _scales(self, s: torch.Tensor, n: int, k: int, name: str) -> None:
+        if s.shape != (self.num_experts, -(-n // 128), k // 128):
+            raise ValueError(f"{name} must be [{self.num_experts}, {-(-n // 128)}, {k // 128}], got {tuple(s.shape)}")
+
+    def expert_layer(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor | None, w_gate_up, w_down,
+                     biases=None, residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+        """The whole layer of gated experts for up to EP_LAYER_MAX_TOKENS
+        tokens (a decode step) in two kernels, without dispatch and combine:
+        out[t] = residual[t] + sum_k topk_weights[t, k] (Wd h + bd), h =
+        silu(g) u, [g; u] = Wgu x[t] + bgu of expert topk_idx[t, k] (-1:
+        none).  x, residual [N, H] bf16, topk_idx int64 and topk_weights fp32
+        [N, K] (None: ones); w_gate_up [E, 2*inner, H] and w_down [E, H,
+        inner] bf16, or both pairs (codes, scales) of cast_weights; biases =
+        (bgu [E, 2*inner], bd [E, H]) bf16.  ``out`` may be ``residual``."""
+        wgu, sgu = w_gate_up if isinstance(w_gate_up, (tuple, list)) else (w_gate_up, None)
+        wd, sd = w_down if isinstance(w_down, (tuple, list)) else (w_down, None)
+        if (sgu is None) != (sd is None):
+            raise ValueError("w_gate_up and w_down must both be bf16 or both be (codes, scales)")
+        n, k = self._weights(wgu, "w_gate_up")
+        inner = n // 2
+        if k != self.hidden or n % 2 or self._weights(wd, "w_down") != (k, inner):
+            raise ValueError(f"w_gate_up must be [E, 2*inner, {self.hidden}] and w_down [E, {self.hidden}, inner], got "
+                             f"{tuple(wgu.shape)} and {tuple(wd.shape)}")
+        if sgu is not None:
+            self._scales(sgu, n, k, "w_gate_up scales")
+            self._scales(sd, k, inner, "w_down scales")
+        N = topk_idx.numel() // self.topk
+        if topk_idx.shape[-1] != self.topk or x.shape[-1] != k or x.numel() != N * k:
+            raise ValueError(f"x must be [N, {k}] and topk_idx [N, {self.topk}], got {tuple(x.shape)} and {tuple(topk_idx.shape)}")
+        if topk_weights is not None and topk_weights.numel() != N * self.topk:
+            raise ValueError(f"topk_weights must be [{N}, {self.topk}], got {tuple(topk_weights.shape)}")
+        bgu, bd = biases if biases is not None else (None, None)
+        for name, b, width in (("gate and up bias", bgu, n), ("down bias", bd, k)):
+            if b is not None and b.shape != (self.num_experts, width):
+                raise ValueError(f"{name} must be [{self.num_experts}, {width}], got {tuple(b.shape)}")
+        if residual is not None and residual.numel() != N * k:
+            raise ValueError(f"residual must be [{N}, {k}], got {tuple(residual.shape)}")
+        if out is None:
+            out = torch.empty(N, k, dtype=torch.bfloat16, device=x.device)
+        if out.numel() != N * k:
+            raise ValueError(f"out must be [{N}, {k}], got {tuple(out.shape)}")
+        ws = torch.empty(ep.ep_expert_layer_workspace(self._ctx, N, inner), dtype=torch.uint8, device=x.device)
+        ep.ep_expert_layer(self._ctx, x, topk_idx, topk_weights, N, inner, wgu, sgu, bgu, wd, sd, bd, residual, ws, out)
+        return out
+
     def device_status(self) -> int:
         """Synchronise the current stream; return and clear the device status."""
         return ep.ep_get_device_status(self._ctx)

@@ -695,6 +695,29 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
     return p;
 }
 
+// Sizes of a layer call: tokens up to the limit, channels in whole pieces of 16
+// bytes (FP8: whole blocks).
+ep_status check_layer(const ep_ctx *ctx, int32_t num_tokens, int32_t inner, bool fp8) {
+    if (num_tokens < 0) return EP_ERR_INVALID_ARG;
+    const ep_status s = check_channels(inner, fp8 ? 128 : 8);
+    if (s != EP_OK) return s;
+    if (num_tokens > ep::kLayerMaxTokens || (fp8 && ctx->cfg.hidden % 128 != 0)) return EP_ERR_UNSUPPORTED;
+    return EP_OK;
+}
+
+ep::ExpertLayerParams layer_params(const ep_ctx *ctx, int32_t num_tokens, int32_t inner) {
+    const ep_config &c = ctx->cfg;
+    ep::ExpertLayerParams p = {};
+    p.N = num_tokens;
+    p.K = c.topk;
+    p.H = c.hidden;
+    p.I = inner;
+    p.E = c.num_experts;
+    p.sms = expert_sms(ctx);
+    p.status = ctx->d_status;
+    return p;
+}
+
 ep_status enqueue_expert(ep::ExpertOp op, const ep::ExpertGemmParams &p, cudaStream_t st) {
     const cudaError_t e = ep::launch_expert_gemm(op, p, st);
     if (e != cudaSuccess) {
@@ -1532,6 +1555,51 @@ ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, vo
     p.n = n;
     p.k = k;
     if (ep::launch_cast_weights(p, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
+    return EP_OK;
+}
+
+ep_status ep_expert_layer_workspace(const ep_ctx *ctx, int32_t num_tokens, int32_t inner, uint64_t *bytes) {
+    if (ctx == nullptr || bytes == nullptr) return EP_ERR_INVALID_ARG;
+    const ep_status s = check_layer(ctx, num_tokens, inner, false);
+    if (s != EP_OK) return s;
+    *bytes = ep::expert_layer_workspace(layer_params(ctx, num_tokens, inner));
+    return EP_OK;
+}
+
+ep_status ep_expert_layer(ep_ctx *ctx, const void *d_x, const int64_t *d_topk_idx, const float *d_topk_weights,
+                          int32_t num_tokens, int32_t inner, const void *d_w_gate_up, const float *d_gate_up_scales,
+                          const void *d_b_gate_up, const void *d_w_down, const float *d_down_scales, const void *d_b_down,
+                          const void *d_residual, void *d_workspace, void *d_out, void *stream) {
+    NvtxRange nvtx("ep_expert_layer");
+    if (ctx == nullptr) return EP_ERR_INVALID_ARG;
+    if ((d_gate_up_scales == nullptr) != (d_down_scales == nullptr)) return EP_ERR_INVALID_ARG;
+    const ep_status s = check_layer(ctx, num_tokens, inner, d_gate_up_scales != nullptr);
+    if (s != EP_OK) return s;
+    if (!on_ctx_device(ctx)) return EP_ERR_INVALID_ARG;
+    if (num_tokens == 0) return EP_OK;
+    if (d_x == nullptr || d_topk_idx == nullptr || d_w_gate_up == nullptr || d_w_down == nullptr || d_workspace == nullptr ||
+        d_out == nullptr)
+        return EP_ERR_INVALID_ARG;
+    if (!aligned(d_x, 16) || !aligned(d_topk_idx, 8) || !aligned(d_topk_weights, 4) || !aligned(d_w_gate_up, 16) ||
+        !aligned(d_w_down, 16) || !aligned(d_gate_up_scales, 4) || !aligned(d_down_scales, 4) || !aligned(d_b_gate_up, 16) ||
+        !aligned(d_b_down, 16) || !aligned(d_residual, 16) || !aligned(d_workspace, 16) || !aligned(d_out, 16))
+        return EP_ERR_INVALID_ARG;
+    ep::ExpertLayerParams p = layer_params(ctx, num_tokens, inner);
+    p.x = d_x;
+    p.idx = d_topk_idx;
+    p.wts = d_topk_weights;
+    p.w_gate_up = d_w_gate_up;
+    p.s_gate_up = d_gate_up_scales;
+    p.b_gate_up = d_b_gate_up;
+    p.w_down = d_w_down;
+    p.s_down = d_down_scales;
+    p.b_down = d_b_down;
+    p.residual = d_residual;
+    p.out = d_out;
+    if (ep::launch_expert_layer(p, d_workspace, (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return EP_ERR_CUDA;
     }

@@ -249,6 +249,31 @@ struct CastWeightsParams {
 };
 cudaError_t launch_cast_weights(const CastWeightsParams &p, int sms, cudaStream_t stream);
 
+// ------------------------------------------------------------------ whole layer for a few tokens
+constexpr int kLayerMaxTokens = 128;
+struct ExpertLayerParams {
+    const void *x;             // bf16 [N, H]
+    const int64_t *idx;        // [N, K]
+    const float *wts;          // [N, K] or nullptr (all ones)
+    const void *w_gate_up;     // [E, 2 * I, H] bf16, or e4m3 when s_gate_up is given
+    const float *s_gate_up;    // [E, ceil(2 * I / 128), H / 128] or nullptr
+    const void *b_gate_up;     // bf16 [E, 2 * I] or nullptr
+    const void *w_down;        // [E, H, I]
+    const float *s_down;       // [E, ceil(H / 128), I / 128] or nullptr
+    const void *b_down;        // bf16 [E, H] or nullptr
+    const void *residual;      // bf16 [N, H] or nullptr
+    void *out;                 // bf16 [N, H]
+    // workspace, set by the launcher
+    float *y;                  // [N * K, H] experts' outputs
+    void *h;                   // [N * K][2][I] activations as the sum of two bf16 numbers
+    uint32_t *done;            // [ceil(H / 32)] units of each tile of output rows that are done
+    int32_t N, K, H, I, E;
+    int32_t sms;
+    uint32_t *status;
+};
+size_t expert_layer_workspace(const ExpertLayerParams &p);
+cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device helpers
 #ifdef __CUDACC__
 // Programmatic dependent launch: let the next kernel in the stream start, and

@@ -46,13 +46,14 @@ ENTRY_POINTS = (
     "ep_rank_send_rows", "ep_rank_dispatch_send", "ep_rank_dispatch_recv", "ep_rank_combine_send",
     "ep_rank_combine_recv", "ep_rank_runs",
     "ep_expert_gemm", "ep_expert_gemm_fp8", "ep_expert_gate_fp8", "ep_expert_wgrad", "ep_expert_swiglu",
-    "ep_expert_swiglu_backward", "ep_cast_weights",
+    "ep_expert_swiglu_backward", "ep_cast_weights", "ep_expert_layer_workspace", "ep_expert_layer",
 )
 
 TUNE_KNOBS = {0: "dispatch", 1: "combine_chunks", 2: "round_trip_chunk",
               3: "layout_form"}  # dispatch: 100 * kernel + CTAs/SM
 
 EP_CHUNK_AUTO = -1
+EP_LAYER_MAX_TOKENS = 128
 
 
 class EPError(RuntimeError):
@@ -153,6 +154,8 @@ def lib() -> ctypes.CDLL:
             "ep_expert_swiglu": (I32, [P, P, P, I32, P, P]),
             "ep_expert_swiglu_backward": (I32, [P, P, P, P, I32, P, P, P]),
             "ep_cast_weights": (I32, [P, P, I32, I32, P, P, P]),
+            "ep_expert_layer_workspace": (I32, [P, I32, I32, ctypes.POINTER(ctypes.c_uint64)]),
+            "ep_expert_layer": (I32, [P, P, P, P, I32, I32, P, P, P, P, P, P, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -533,3 +536,24 @@ def ep_cast_weights(ctx, w: torch.Tensor, n: int, k: int, q: torch.Tensor, scale
     _check(lib().ep_cast_weights(ctx, _ptr(w, torch.bfloat16, "w"), int(n), int(k),
                                  _ptr(q, torch.float8_e4m3fn, "q"), _ptr(scales, torch.float32, "scales"),
                                  _stream(stream)), "ep_cast_weights")
+
+
+def ep_expert_layer_workspace(ctx, num_tokens: int, inner: int) -> int:
+    n = ctypes.c_uint64()
+    _check(lib().ep_expert_layer_workspace(ctx, int(num_tokens), int(inner), ctypes.byref(n)), "ep_expert_layer_workspace")
+    return n.value
+
+
+def ep_expert_layer(ctx, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor | None, num_tokens: int,
+                    inner: int, w_gate_up: torch.Tensor, gate_up_scales: torch.Tensor | None, b_gate_up: torch.Tensor | None,
+                    w_down: torch.Tensor, down_scales: torch.Tensor | None, b_down: torch.Tensor | None,
+                    residual: torch.Tensor | None, workspace: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """Weights bf16, or e4m3 with scales (both or neither)."""
+    kind = torch.bfloat16 if gate_up_scales is None else torch.float8_e4m3fn
+    _check(lib().ep_expert_layer(
+        ctx, _ptr(x, torch.bfloat16, "x"), _ptr(topk_idx, torch.int64, "topk_idx"),
+        _ptr(topk_weights, torch.float32, "topk_weights"), int(num_tokens), int(inner), _ptr(w_gate_up, kind, "w_gate_up"),
+        _ptr(gate_up_scales, torch.float32, "gate_up_scales"), _ptr(b_gate_up, torch.bfloat16, "b_gate_up"),
+        _ptr(w_down, kind, "w_down"), _ptr(down_scales, torch.float32, "down_scales"),
+        _ptr(b_down, torch.bfloat16, "b_down"), _ptr(residual, torch.bfloat16, "residual"), _ptr(workspace, None, "workspace"),
+        _ptr(out, torch.bfloat16, "out"), _stream(stream)), "ep_expert_layer")

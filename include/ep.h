@@ -373,6 +373,44 @@ ep_status ep_expert_swiglu_backward(ep_ctx *ctx, const ep_handle *handle, const 
 ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, void *d_q, float *d_scales,
                           void *stream);
 
+/* The whole layer of gated experts for a few tokens (a decode step): what
+ * dispatch, the two products and combine compute, in two kernels that read the
+ * named experts' weights once and keep no receive buffer; for more than
+ * EP_LAYER_MAX_TOKENS tokens use those calls (EP_ERR_UNSUPPORTED here).
+ *   h[t,k] = silu(g) u, [g; u] = Wgu[e] x[t] + bgu[e], e = topk_idx[t,k]
+ *   out[t] = bf16(residual[t] + fma chain over k ascending of
+ *            topk_weights[t,k] * (Wd[e] h[t,k] + bd[e]))
+ * Entries with topk_idx -1 are skipped (their weights are not read); a token
+ * without any gets its residual, or zeros.  An id outside [-1, E) is skipped too
+ * and reported by ep_get_device_status (EP_ERR_BAD_EXPERT).  An expert may be
+ * named more than once by a token.  Sums are held in fp32; x is taken as it is
+ * and h as the sum of two bf16 numbers (2^-17 of it off at most), so with FP8
+ * weights, too, no token is cast to 8 bits (the dispatched path casts x and h
+ * and differs by that).  It needs no handle.
+ *     d_x               device bf16 [num_tokens, H]
+ *     d_topk_idx        device int64 [num_tokens, K]
+ *     d_topk_weights    device fp32 [num_tokens, K], NULL = all ones
+ *     d_w_gate_up       device [E, 2*inner, H], the gate's rows first, bf16; with
+ *                       d_gate_up_scales (fp32 [E, ceil(2*inner/128), H/128])
+ *                       e4m3 as from ep_cast_weights
+ *     d_w_down          device [E, H, inner] bf16, or e4m3 with d_down_scales
+ *                       (fp32 [E, ceil(H/128), inner/128]); both or neither
+ *     d_b_gate_up, d_b_down  device bf16 [E, 2*inner], [E, H], or NULL
+ *     d_residual        device bf16 [num_tokens, H] or NULL; may be d_out itself
+ *     d_workspace       device, ep_expert_layer_workspace bytes; nothing in it
+ *                       outlives the call; calls that may run side by side
+ *                       (streams, graphs) need one each
+ *     d_out             device bf16 [num_tokens, H]
+ * All pointers 16-byte aligned (d_topk_idx 8, scales and weights 4); inner a
+ * multiple of 8, with FP8 weights H and inner multiples of 128.  The result does
+ * not depend on max_sms and repeats bit for bit. */
+#define EP_LAYER_MAX_TOKENS 128
+ep_status ep_expert_layer_workspace(const ep_ctx *ctx, int32_t num_tokens, int32_t inner, uint64_t *bytes);
+ep_status ep_expert_layer(ep_ctx *ctx, const void *d_x, const int64_t *d_topk_idx, const float *d_topk_weights,
+                          int32_t num_tokens, int32_t inner, const void *d_w_gate_up, const float *d_gate_up_scales,
+                          const void *d_b_gate_up, const void *d_w_down, const float *d_down_scales,
+                          const void *d_b_down, const void *d_residual, void *d_workspace, void *d_out, void *stream);
+
 /* Split dispatch and combine: the send half returns and a later "hook" call
  * finishes the receive (the hook-based communication-computation overlap of
  * "如何突破MoE通信瓶颈：DeepEP跨节点优化技术终极指南", section 技术解析,

@@ -1,0 +1,333 @@
+"""GPU checks of the whole layer for a few tokens against its definition in 64 bits."""
+import pytest
+import torch
+
+from combine_get_dispatch_02_gb300 import Buffer
+from combine_get_dispatch_02_gb300 import build as epbuild
+from combine_get_dispatch_02_gb300 import ep
+from expert_reference import BF16, assert_close, cast_blocks, silu, sum_bound, weights, wide_block
+from norm_bounds import bf16_bound
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    epbuild.build()
+    torch.cuda.set_device(0)
+
+
+def bf(shape, seed, scale=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * scale).bfloat16()
+
+
+def route(N, E, K, seed, drop=0.0):
+    g = torch.Generator().manual_seed(seed)
+    top = torch.randn(N, E, generator=g).topk(K, dim=1)
+    idx = top.indices.clone()
+    idx[torch.rand(N, K, generator=g) < drop] = -1
+    return idx.cuda(), torch.softmax(top.values, -1).contiguous().cuda()
+
+
+class Layer:
+    """Weights, tokens and routing of one call, and its definition with error bounds.
+
+    Bounds: a product of bf16 / e4m3 values is exact in fp32 and a sum of n of them off by
+    sum_bound(n); silu's slope is at most 1.1; h is kept to 2^-17 and computed to 2^-20 of itself;
+    the K shares add 2^-23 of their magnitudes each, the result's rounding BF16 of it."""
+
+    def __init__(self, N, H, I, E, K, fp8=False, bias=False, residual=False, drop=0.0, seed=0, idx=None, max_sms=0):
+        self.N, self.H, self.I, self.E, self.K, self.fp8 = N, H, I, E, K, fp8
+        self.buf = Buffer(1, max(N, 1), H, E, K, max_sms=max_sms)
+        self.x = bf((N, H), seed + 1)
+        made, self.wts = route(N, E, K, seed, drop)
+        self.idx = made if idx is None else idx
+        self.gu, self.down = weights(E, 2 * I, H, seed + 2), weights(E, H, I, seed + 3)
+        if fp8:
+            self.gu, self.down = cast_blocks(self.gu), cast_blocks(self.down)
+        self.bias = (bf((E, 2 * I), seed + 4, 0.5), bf((E, H), seed + 5, 0.5)) if bias else None
+        self.residual = bf((N, H), seed + 6) if residual else None
+
+    def run(self, **kw):
+        out = self.buf.expert_layer(self.x, self.idx, self.wts, self.gu, self.down, biases=self.bias, residual=self.residual, **kw)
+        assert self.buf.device_status() == ep.EP_OK
+        return out
+
+    def want(self):
+        wide = lambda w, e: wide_block(w[0][e], w[1][e]) if self.fp8 else w[e].double()  # noqa: E731
+        out = torch.zeros(self.N, self.H, device="cuda", dtype=torch.float64)
+        tol, mag = torch.zeros_like(out), torch.zeros_like(out)
+        for e in range(self.E):
+            t, k = (self.idx == e).nonzero(as_tuple=True)
+            if t.numel() == 0:
+                continue
+            x, w = self.x[t].double(), wide(self.gu, e)
+            v, dv = x @ w.T, sum_bound(self.H, x.abs() @ w.abs().T)
+            if self.bias is not None:
+                v = v + self.bias[0][e].double()
+                dv = dv + 2.0 ** -23 * v.abs()
+            (g, u), (dg, du) = v.chunk(2, 1), dv.chunk(2, 1)
+            h = silu(g) * u
+            dh = 1.1 * dg * (u.abs() + du) + silu(g).abs() * du + (2.0 ** -17 + 2.0 ** -20) * h.abs()
+            w = wide(self.down, e)
+            y, dy = h @ w.T, dh @ w.abs().T + sum_bound(2 * self.I, (h.abs() + dh) @ w.abs().T)
+            if self.bias is not None:
+                y = y + self.bias[1][e].double()
+            p = self.wts[t, k].double().unsqueeze(1)
+            out.index_add_(0, t, p * y)
+            tol.index_add_(0, t, p.abs() * dy)
+            mag.index_add_(0, t, (p * y).abs())
+        if self.residual is not None:
+            out += self.residual.double()
+            mag += self.residual.double().abs()
+        tol += (self.K + 2) * 2.0 ** -23 * mag
+        return out, tol + BF16 * (out.abs() + tol)
+
+    def check(self, **kw):
+        got = self.run(**kw)
+        want, tol = self.want()
+        assert_close(got, want, tol, "layer")
+        return got
+
+
+# N, H, I, E, K: one token; tiles cut off on every side; more than 8 and 16 tokens of an expert; the most tokens
+SIZES = [(1, 8, 8, 1, 1), (1, 1024, 512, 32, 4), (3, 264, 24, 5, 2), (7, 40, 200, 9, 3), (17, 520, 136, 2, 2), (32, 1000, 328, 64, 6),
+         (128, 256, 64, 16, 8), (128, 72, 1016, 3, 1), (5, 2048, 16, 1024, 32)]
+SIZES_FP8 = [(1, 128, 128, 1, 1), (1, 1024, 512, 32, 4), (3, 256, 128, 5, 2), (17, 640, 384, 2, 2), (31, 1152, 128, 40, 6), (128, 256, 640, 16, 8)]
+
+
+@pytest.mark.parametrize("extras", [False, True])
+@pytest.mark.parametrize("N,H,I,E,K", SIZES)
+def test_layer_bf16(N, H, I, E, K, extras):
+    Layer(N, H, I, E, K, bias=extras, residual=extras, drop=0.2 if extras and N > 1 else 0.0, seed=N).check()
+
+
+@pytest.mark.parametrize("extras", [False, True])
+@pytest.mark.parametrize("N,H,I,E,K", SIZES_FP8)
+def test_layer_fp8(N, H, I, E, K, extras):
+    Layer(N, H, I, E, K, fp8=True, bias=extras, residual=extras, drop=0.2 if extras and N > 1 else 0.0, seed=N).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_sums_in_the_norm(fp8):
+    """Per row, where a lost channel of 7168 shows: the bf16 rounding and the sums' own error."""
+    layer = Layer(6, 7168, 2048, 8, 2, fp8=fp8, seed=11)
+    got, (want, _) = layer.check(), layer.want()
+    error = (got.double() - want).norm(dim=1) / want.norm(dim=1)
+    assert float(error.max()) <= bf16_bound(7168) + 2.0 ** -17
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_expert_for_all_tokens_and_every_count(fp8):
+    """1 to 40 tokens of one expert beside others, by number of masked entries."""
+    for n in (1, 2, 7, 8, 9, 15, 16, 17, 24, 33, 40):
+        idx = torch.full((40, 2), -1, dtype=torch.int64)
+        idx[:n, 0] = 3
+        idx[::3, 1] = 1
+        Layer(40, 384, 128, 4, 2, fp8=fp8, idx=idx.cuda(), seed=n).check()
+
+
+def test_same_expert_twice_in_a_token():
+    idx = torch.tensor([[2, 2, 2], [2, 0, 2], [-1, 1, 1]]).cuda()
+    Layer(3, 136, 72, 3, 3, idx=idx, bias=True).check()
+
+
+def test_tokens_without_experts_get_their_residual_or_zeros():
+    idx = torch.tensor([[-1, -1], [1, -1], [-1, -1]]).cuda()
+    layer = Layer(3, 264, 40, 4, 2, idx=idx, residual=True)
+    got = layer.check()
+    assert torch.equal(got[0::2], layer.residual[0::2])
+    layer = Layer(3, 264, 40, 4, 2, idx=torch.full((3, 2), -1).cuda(), residual=True, bias=True)
+    assert torch.equal(layer.run(), layer.residual)
+    layer.residual = None
+    out = torch.full((3, 264), 7.0, device="cuda", dtype=torch.bfloat16)
+    assert torch.equal(layer.run(out=out), torch.zeros_like(out))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_what_masked_entries_and_unnamed_experts_hold_does_not_matter(fp8):
+    layer = Layer(9, 256, 128, 6, 3, fp8=fp8, bias=True, drop=0.3, seed=5)
+    layer.idx[layer.idx == 4] = -1
+    before = layer.check()
+    layer.wts[layer.idx < 0] = float("nan")
+    for w in (layer.gu, layer.down):
+        if fp8:
+            w[0].view(torch.uint8)[4] = 0x7F
+            w[1][4] = float("inf")
+        else:
+            w[4] = float("nan")
+    for b in layer.bias:
+        b[4] = float("nan")
+    assert torch.equal(layer.run(), before)
+
+
+@pytest.mark.parametrize("byte", [0x7F, 0xFF])
+def test_nan_codes_of_fp8_weights_give_nan(byte):
+    """One code of a row: that channel of every token of the expert, and no other."""
+    layer = Layer(4, 256, 128, 2, 1, fp8=True, idx=torch.tensor([[0], [1], [1], [0]]).cuda())
+    before = layer.check()
+    layer.down[0].view(torch.uint8)[1, 77, 101] = byte
+    got = layer.run()
+    assert bool(got[1:3, 77].isnan().all())
+    got[1:3, 77] = before[1:3, 77]
+    assert torch.equal(got, before)
+    layer.gu[0].view(torch.uint8)[0, 128 + 5, 255] = byte   # an up row: the whole token
+    assert bool(layer.run()[0::3].isnan().all())
+
+
+def test_every_fp8_code():
+    """Weights of all 254 finite codes against one-hot tokens: exact but for the roundings behind them."""
+    layer = Layer(8, 256, 128, 1, 1, fp8=True, seed=3)
+    codes = torch.arange(256, dtype=torch.int64)
+    codes[(codes & 0x7F) == 0x7F] = 0
+    layer.gu[0].view(torch.uint8)[0, :] = codes.to(torch.uint8).cuda()[(torch.arange(256)[:, None] + torch.arange(256)) % 256]
+    layer.gu[1].fill_(0.02)
+    layer.x.zero_()
+    layer.x[torch.arange(8), torch.arange(8) * 37 % 256] = 1.0
+    layer.check()
+
+
+def test_infinities_and_large_values():
+    layer = Layer(2, 64, 32, 2, 1, idx=torch.tensor([[0], [1]]).cuda())
+    layer.x[0, 5] = float("inf")
+    layer.x[1] *= 1e18
+    out = layer.run()
+    assert bool(out[0].isnan().all() | out[0].isinf().any())
+    want, _ = layer.want()
+    assert bool((out[1].double() - want[1]).abs().max() <= want[1].abs().max() * 2.0 ** -7)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_results_do_not_depend_on_max_sms_and_repeat(fp8):
+    args = dict(N=21, H=512, I=256, E=12, K=3, fp8=fp8, bias=True, residual=True, seed=2)
+    first = Layer(**args).check()
+    for sms in (1, 7, 152):
+        layer = Layer(**args, max_sms=sms)
+        for _ in range(3):
+            assert torch.equal(layer.run(), first)
+
+
+def test_residual_may_be_the_output():
+    layer = Layer(13, 328, 72, 7, 2, bias=True, residual=True)
+    want = layer.check()
+    layer.residual = layer.residual.clone()
+    assert layer.run(out=layer.residual) is layer.residual
+    assert torch.equal(layer.residual, want)
+
+
+def test_bad_ids_are_reported_and_skipped():
+    layer = Layer(4, 136, 64, 5, 2)
+    clean = layer.idx.clone()
+    clean[1, 0] = clean[3, 1] = -1
+    layer.idx = clean
+    want = layer.check()
+    layer.idx = clean.clone()
+    layer.idx[1, 0], layer.idx[3, 1] = 5, -(1 << 40)
+    out = layer.buf.expert_layer(layer.x, layer.idx, layer.wts, layer.gu, layer.down)
+    assert layer.buf.device_status() == ep.EP_ERR_BAD_EXPERT
+    assert torch.equal(out, want)
+    layer.idx = clean
+    assert torch.equal(layer.run(), want)
+
+
+def test_weights_none_are_ones():
+    layer = Layer(5, 128, 64, 6, 2)
+    layer.wts.fill_(1.0)
+    want = layer.check()
+    layer.wts = None
+    assert torch.equal(layer.run(), want)
+
+
+def test_side_by_side_on_streams_and_in_graphs():
+    """Two calls of one context at once, and two captured ones replayed with other inputs."""
+    a, b = (Layer(9, 1024, 256, 16, 4, fp8=f, seed=s, bias=True) for f, s in ((False, 1), (True, 2)))
+    want = a.check(), b.check()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    b.buf = a.buf
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for layer, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                got.append(layer.buf.expert_layer(layer.x, layer.idx, layer.wts, layer.gu, layer.down, biases=layer.bias))
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graphs, outs = [], []
+    for layer in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer.buf.expert_layer(layer.x, layer.idx, layer.wts, layer.gu, layer.down, biases=layer.bias))
+        graphs.append(g)
+    fresh = Layer(9, 1024, 256, 16, 4, seed=7, bias=True)
+    for layer in (a, b):
+        layer.x.copy_(fresh.x)
+        layer.idx.copy_(fresh.idx)
+        layer.wts.copy_(fresh.wts)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for layer, out in zip((a, b), outs):
+            want, tol = layer.want()
+            assert_close(out, want, tol, "replayed")
+
+
+def test_agrees_with_dispatch_experts_combine():
+    """The bf16 path through the receive layout rounds h and y to bf16; the layer does not."""
+    layer = Layer(24, 512, 256, 8, 2, seed=4)
+    recv, _, h = layer.buf.low_latency_dispatch(layer.x.view(1, 24, 512), layer.idx.view(1, 24, 2), 24, 8, use_fp8=False)
+    y, _ = layer.buf.expert_mlp(recv, layer.gu, layer.down, h)
+    out = layer.buf.low_latency_combine(y, layer.idx.view(1, 24, 2), layer.wts, h, 8)
+    want, tol = layer.want()
+    got = layer.check()
+    # gu (twice), h and y rounded to bf16: 2-norm well within the sum of the four roundings
+    assert float((out.double() - want).norm() / want.norm()) <= 5 * BF16
+    assert float((got.double() - want).norm() / want.norm()) <= BF16
+
+
+def test_refusals_touch_nothing():
+    layer = Layer(4, 128, 64, 5, 2)
+    buf, out = layer.buf, torch.full((4, 128), 3.0, device="cuda", dtype=torch.bfloat16)
+    call = lambda **kw: buf.expert_layer(**{**dict(x=layer.x, topk_idx=layer.idx, topk_weights=layer.wts, w_gate_up=layer.gu,  # noqa: E731
+                                                   w_down=layer.down, out=out), **kw})
+    with pytest.raises(ValueError):
+        call(x=layer.x[:, :64].contiguous())
+    with pytest.raises(ValueError):
+        call(x=layer.x.float())
+    with pytest.raises(ValueError):
+        call(w_down=cast_blocks(bf((5, 128, 128), 0)))
+    with pytest.raises(ValueError):
+        call(topk_weights=layer.wts[:2])
+    with pytest.raises(ValueError):
+        call(biases=(bf((5, 64), 0), None))
+    with pytest.raises(ValueError):
+        call(residual=layer.x[:2].contiguous())
+    with pytest.raises(ValueError):
+        call(topk_idx=layer.idx.int())
+    with pytest.raises(ep.EPError) as e:
+        call(w_gate_up=bf((5, 24, 128), 0), w_down=bf((5, 128, 12), 0))
+    assert e.value.status == ep.EP_ERR_INVALID_ARG
+    big = Layer(ep.EP_LAYER_MAX_TOKENS + 1, 128, 64, 5, 2)
+    with pytest.raises(ep.EPError) as e:
+        big.run()
+    assert e.value.status == ep.EP_ERR_UNSUPPORTED
+    lib, p = ep.lib(), lambda t: t.data_ptr()  # noqa: E731
+    ws = torch.empty(ep.ep_expert_layer_workspace(buf.ctx, 4, 64), dtype=torch.uint8, device="cuda")
+    args = [buf.ctx, p(layer.x), p(layer.idx), p(layer.wts), 4, 64, p(layer.gu), None, None, p(layer.down), None, None, None, p(ws),
+            p(out), None]
+    for at, value in ((1, None), (2, None), (6, None), (9, None), (13, None), (14, None), (1, p(layer.x) + 2), (13, p(ws) + 8), (4, -1),
+                      (5, 0), (7, p(layer.wts))):
+        bad = list(args)
+        bad[at] = value
+        assert lib.ep_expert_layer(*bad) == ep.EP_ERR_INVALID_ARG, (at, value)
+    torch.cuda.synchronize()
+    assert bool((out == 3.0).all())
+    zero = list(args)
+    zero[4] = 0
+    assert lib.ep_expert_layer(*zero) == ep.EP_OK
+    assert buf.device_status() == ep.EP_OK and bool((out == 3.0).all())
