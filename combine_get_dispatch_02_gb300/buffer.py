@@ -502,26 +502,99 @@ class Buffer:
         returns y [rows, H] bf16."""
         return self.expert_gemm_fp8(self.expert_gate_fp8(x, w_gate_up, handle), w_down, handle, out=out)
 
-    def expert_mlp(self, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, handle: Handle):
+    def expert_mlp(self, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, handle: Handle, biases=None):
         """Gated experts in bf16 on the received rows x [rows, H]: w_gate_up
-        [E, 2*inner, H], w_down [E, H, inner].  Returns (y [rows, H], saved)
-        with what expert_mlp_backward needs."""
-        gu = self.expert_gemm(x, w_gate_up, handle)
-        y = self.expert_gemm(self.expert_swiglu(gu, handle), w_down, handle)
+        [E, 2*inner, H], w_down [E, H, inner]; biases = ([E, 2*inner], [E,
+        H]), bf16 or fp32.  Returns (y [rows, H], saved) with what
+        expert_mlp_backward needs."""
+        if biases is None:
+            gu = self.expert_gemm(x, w_gate_up, handle)
+            y = self.expert_gemm(self.expert_swiglu(gu, handle), w_down, handle)
+        else:
+            gu = self.expert_linear(x, w_gate_up, handle, bias=biases[0])
+            y = self.expert_linear(self.expert_swiglu(gu, handle), w_down, handle, bias=biases[1])
         return y, (x, gu)
 
     def expert_mlp_backward(self, dy: torch.Tensor, saved, w_gate_up: torch.Tensor, w_down: torch.Tensor,
-                            handle: Handle, grads=None):
+                            handle: Handle, grads=None, bias_grads=None):
         """Gradients (dx [rows, H] bf16, dw_gate_up, dw_down) of expert_mlp
         for dy [rows, H].  The weight gradients are fp32; ``grads`` = a pair
-        of fp32 tensors to add them to."""
+        of fp32 tensors to add them to.  ``bias_grads`` = a pair of fp32
+        tensors ([E, 2*inner], [E, H]) for the biases' gradients, written, or
+        added to where ``grads`` is given."""
         x, gu = saved
         dgu, h = self.expert_swiglu_backward(gu, self.expert_gemm(dy, w_down, handle, transpose_w=True), handle)
         acc = grads is not None
+        if bias_grads is not None:
+            self.expert_linear_backward(dgu, None, handle, dbias=bias_grads[0], accumulate=acc)
+            self.expert_linear_backward(dy, None, handle, dbias=bias_grads[1], accumulate=acc)
         g_gate_up, g_down = grads if acc else (None, None)
         dw_down = self.expert_wgrad(dy, h, handle, out=g_down, accumulate=acc)
         dw_gate_up = self.expert_wgrad(dgu, x, handle, out=g_gate_up, accumulate=acc)
         return self.expert_gemm(dgu, w_gate_up, handle, transpose_w=True), dw_gate_up, dw_down
+
+    def _bias(self, b: torch.Tensor | None, width: int, name: str) -> None:
+        if b is not None and b.shape != (self.num_experts, width):
+            raise ValueError(f"{name} must be [{self.num_experts}, {width}], got {tuple(b.shape)}")
+
+    def expert_linear(self, x: torch.Tensor, w: torch.Tensor, handle: Handle, bias: torch.Tensor | None = None,
+                      activation: str = "none", residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      z: torch.Tensor | None = None) -> torch.Tensor:
+        """expert_gemm with its epilogue: z[r] = W[e] x[r] + bias[e], y[r] =
+        act(z[r]) + residual[r], in fp32 with one rounding.  bias [E, n] bf16
+        or fp32; activation "none", "relu", "gelu", "gelu_tanh" or "silu";
+        residual [rows, n] bf16 (may be ``out``); ``z`` [rows, n] bf16 takes
+        what went into the activation, for expert_linear_backward."""
+        n, k = self._weights(w, "w")
+        self._rows(x, k, "x")
+        self._bias(bias, n, "bias")
+        for name, t in (("residual", residual), ("z", z)):
+            if t is not None:
+                self._rows(t, n, name)
+        if out is None:
+            out = self._new_rows(n, torch.bfloat16, x)
+        self._rows(out, n, "out")
+        ep.ep_expert_linear(self._ctx, handle.raw, x, w, n, k, bias, activation, residual, z, out)
+        return out
+
+    def expert_linear_backward(self, dy: torch.Tensor, z: torch.Tensor | None, handle: Handle, activation: str = "none",
+                               out: torch.Tensor | None = None, dbias: torch.Tensor | None = None, accumulate: bool = False):
+        """(dz [rows, n], dbias [E, n] fp32) for the gradient dy of
+        expert_linear's y: dz = dy act'(z), dbias[e] its sum over the rows of
+        e.  The other gradients are expert_gemm(dz, w, transpose_w=True) and
+        expert_wgrad(dz, x); the residual's is dy.  accumulate=True adds to
+        ``dbias``.  Without an activation z may be None, and dz is dy itself
+        unless ``out`` is given."""
+        n = dy.shape[-1]
+        self._rows(dy, n, "dy")
+        if z is not None:
+            self._rows(z, n, "z")
+        elif activation != "none":
+            raise ValueError(f"activation {activation!r} needs z")
+        if dbias is None:
+            if accumulate:
+                raise ValueError("accumulate=True needs dbias")
+            dbias = torch.empty(self.num_experts, n, dtype=torch.float32, device=dy.device)
+        self._bias(dbias, n, "dbias")
+        if out is None and activation != "none":
+            out = self._new_rows(n, torch.bfloat16, dy)
+        if out is not None:
+            self._rows(out, n, "out")
+        ep.ep_expert_linear_backward(self._ctx, handle.raw, dy, z, n, activation, accumulate, out, dbias)
+        return (dy if out is None else out), dbias
+
+    def clip_grads(self, grads, max_norm: float, out=None) -> torch.Tensor:
+        """Scale a list of fp32 / bf16 tensors by min(1, max_norm / norm), norm
+        the 2-norm of all of them together, and return the norm (fp32, on the
+        device).  In place, or into the tensors ``out``.  A norm that is not
+        finite scales nothing; max_norm=inf gives the norm alone."""
+        table = ep.grad_list(grads, out)
+        dev = torch.device("cuda", torch.cuda.current_device())
+        partials = torch.empty(ep.EP_GRAD_PARTIALS, dtype=torch.float64, device=dev)
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ep.ep_grad_norm(self._ctx, table, partials)
+        ep.ep_grad_clip(self._ctx, table, partials, max_norm, norm)
+        return norm
 
     def _scales(self, s: torch.Tensor, n: int, k: int, name: str) -> None:
         if s.shape != (self.num_experts, -(-n // 128), k // 128):
@@ -555,9 +628,8 @@ class Buffer:
         if topk_weights is not None and topk_weights.numel() != N * self.topk:
             raise ValueError(f"topk_weights must be [{N}, {self.topk}], got {tuple(topk_weights.shape)}")
         bgu, bd = biases if biases is not None else (None, None)
-        for name, b, width in (("gate and up bias", bgu, n), ("down bias", bd, k)):
-            if b is not None and b.shape != (self.num_experts, width):
-                raise ValueError(f"{name} must be [{self.num_experts}, {width}], got {tuple(b.shape)}")
+        self._bias(bgu, n, "gate and up bias")
+        self._bias(bd, k, "down bias")
         if residual is not None and residual.numel() != N * k:
             raise ValueError(f"residual must be [{N}, {k}], got {tuple(residual.shape)}")
         if out is None:

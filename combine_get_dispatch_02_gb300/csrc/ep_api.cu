@@ -695,6 +695,40 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
     return p;
 }
 
+// A list of gradients: aligned to their type, sizes that can be numbered, and, where
+// they are written, none that overlaps another (it would be scaled twice, or read
+// by one part of the GPU while another writes it).
+ep_status check_grads(const ep_grad *g, int32_t count, bool written) {
+    if (count < 0 || (count > 0 && g == nullptr)) return EP_ERR_INVALID_ARG;
+    struct Range {
+        uintptr_t from, to;
+        int32_t i;  // tensor; its own data and out may be one
+    };
+    std::vector<Range> r;
+    try {
+        r.reserve(2 * (size_t)count);
+    } catch (...) {
+        return EP_ERR_OOM;
+    }
+    int64_t total = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        if (g[i].numel < 0 || (g[i].fp32 != 0 && g[i].fp32 != 1)) return EP_ERR_INVALID_ARG;
+        if (g[i].numel == 0) continue;
+        const size_t es = g[i].fp32 ? 4 : 2;
+        if (g[i].data == nullptr || !aligned(g[i].data, es)) return EP_ERR_INVALID_ARG;
+        if (g[i].numel > (int64_t)1 << 42 || (total += g[i].numel) > (int64_t)1 << 42) return EP_ERR_UNSUPPORTED;
+        const uintptr_t a = (uintptr_t)g[i].data, o = (uintptr_t)g[i].out, bytes = (uintptr_t)g[i].numel * es;
+        if (!written) continue;
+        if (g[i].out == nullptr || !aligned(g[i].out, es)) return EP_ERR_INVALID_ARG;
+        r.push_back({a, a + bytes, i});
+        if (o != a) r.push_back({o, o + bytes, i});
+    }
+    std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
+    for (size_t i = 1; i < r.size(); ++i)
+        if (r[i].from < r[i - 1].to) return EP_ERR_INVALID_ARG;
+    return EP_OK;
+}
+
 // Sizes of a layer call: tokens up to the limit, channels in whole pieces of 16
 // bytes (FP8: whole blocks).
 ep_status check_layer(const ep_ctx *ctx, int32_t num_tokens, int32_t inner, bool fp8) {
@@ -1492,6 +1526,102 @@ ep_status ep_expert_wgrad(ep_ctx *ctx, const ep_handle *handle, const void *d_dy
     p.out_fp32 = out_fp32;
     p.accumulate = accumulate;
     return enqueue_expert(ep::ExpertOp::kWgrad, p, (cudaStream_t)stream);
+}
+
+ep_status ep_expert_linear(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const void *d_w, int32_t n, int32_t k,
+                           const void *d_bias, int32_t bias_fp32, int32_t activation, const void *d_residual, void *d_z,
+                           void *d_y, void *stream) {
+    NvtxRange nvtx("ep_expert_linear");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(n, 8);
+    if (s == EP_OK) s = check_channels(k, 8);
+    if (s != EP_OK) return s;
+    if ((bias_fp32 != 0 && bias_fp32 != 1) || activation < EP_ACT_NONE || activation > EP_ACT_SILU) return EP_ERR_INVALID_ARG;
+    if (handle->tokens_per_rank == 0) return EP_OK;
+    if (d_x == nullptr || d_w == nullptr || d_y == nullptr || d_z == d_y) return EP_ERR_INVALID_ARG;
+    if (!aligned(d_x, 16) || !aligned(d_w, 16) || !aligned(d_y, 16) || !aligned(d_bias, bias_fp32 ? 4 : 2) ||
+        !aligned(d_residual, 16) || !aligned(d_z, 16))
+        return EP_ERR_INVALID_ARG;
+    ep::ExpertGemmParams p = expert_params(ctx, handle, n, k, (cudaStream_t)stream);
+    p.x = d_x;
+    p.w = d_w;
+    p.y = d_y;
+    p.bias = d_bias;
+    p.bias_fp32 = bias_fp32;
+    p.residual = d_residual;
+    p.z = d_z;
+    p.act = (ep::Act)activation;
+    return enqueue_expert(ep::ExpertOp::kLinear, p, (cudaStream_t)stream);
+}
+
+ep_status ep_expert_linear_backward(ep_ctx *ctx, const ep_handle *handle, const void *d_dy, const void *d_z, int32_t n,
+                                    int32_t activation, int32_t accumulate, void *d_dz, float *d_dbias, void *stream) {
+    NvtxRange nvtx("ep_expert_linear_backward");
+    ep_status s = check_expert(ctx, handle);
+    if (s == EP_OK) s = check_channels(n, 8);
+    if (s != EP_OK) return s;
+    if ((accumulate != 0 && accumulate != 1) || activation < EP_ACT_NONE || activation > EP_ACT_SILU) return EP_ERR_INVALID_ARG;
+    if (d_dz == nullptr && d_dbias == nullptr) return EP_ERR_INVALID_ARG;
+    if (!aligned(d_dbias, 4)) return EP_ERR_INVALID_ARG;
+    if (handle->tokens_per_rank == 0) {
+        // no rows: the bias gradient is zero
+        if (d_dbias != nullptr && !accumulate &&
+            cudaMemsetAsync(d_dbias, 0, (size_t)ctx->cfg.num_experts * n * 4, (cudaStream_t)stream) != cudaSuccess) {
+            cudaGetLastError();
+            return EP_ERR_CUDA;
+        }
+        return EP_OK;
+    }
+    if (d_dy == nullptr || (d_z == nullptr && activation != EP_ACT_NONE)) return EP_ERR_INVALID_ARG;
+    if (!aligned(d_dy, 16) || !aligned(d_z, 16) || !aligned(d_dz, 16)) return EP_ERR_INVALID_ARG;
+    ep::LinearBackwardParams p = {};
+    p.dy = d_dy;
+    p.z = d_z;
+    p.dz = d_dz;
+    p.db = d_dbias;
+    p.base = handle->base;
+    p.count = handle->tokens_per_expert;
+    p.E = ctx->cfg.num_experts;
+    p.n = n;
+    p.live = (int64_t)ctx->cfg.num_ranks * handle->tokens_per_rank * ctx->cfg.topk;
+    p.accumulate = accumulate;
+    p.sms = expert_sms(ctx);
+    p.act = (ep::Act)activation;
+    if (ep::launch_linear_backward(p, (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
+    return EP_OK;
+}
+
+ep_status ep_grad_norm(ep_ctx *ctx, const void *grads, int32_t count, double *d_partials, void *stream) {
+    NvtxRange nvtx("ep_grad_norm");
+    if (ctx == nullptr || !on_ctx_device(ctx)) return EP_ERR_INVALID_ARG;
+    const ep_grad *g = static_cast<const ep_grad *>(grads);
+    const ep_status s = check_grads(g, count, false);
+    if (s != EP_OK) return s;
+    if (d_partials == nullptr || !aligned(d_partials, 8)) return EP_ERR_INVALID_ARG;
+    if (ep::launch_grad_norm(g, count, d_partials, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
+    return EP_OK;
+}
+
+ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const double *d_partials, const void *max_norm,
+                       float *d_norm, void *stream) {
+    NvtxRange nvtx("ep_grad_clip");
+    if (ctx == nullptr || !on_ctx_device(ctx) || max_norm == nullptr) return EP_ERR_INVALID_ARG;
+    const float limit = *static_cast<const float *>(max_norm);
+    const ep_grad *g = static_cast<const ep_grad *>(grads);
+    const ep_status s = check_grads(g, count, true);
+    if (s != EP_OK) return s;
+    if (!(limit >= 0.0f) || d_partials == nullptr || !aligned(d_partials, 8) || !aligned(d_norm, 4)) return EP_ERR_INVALID_ARG;
+    if (ep::launch_grad_clip(g, count, d_partials, limit, d_norm, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return EP_ERR_CUDA;
+    }
+    return EP_OK;
 }
 
 ep_status ep_expert_swiglu(ep_ctx *ctx, const ep_handle *handle, const void *d_gu, int32_t inner, void *d_h,

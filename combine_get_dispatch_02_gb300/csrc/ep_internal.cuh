@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+struct ep_grad;
+
 namespace ep {
 
 // Bits of the per-context device status word.
@@ -201,7 +203,8 @@ int identity_blocks_per_sm(bool fp8);
 
 // ------------------------------------------------------------------ expert products
 // Matrix products over the rows of each expert (see expert_gemm.cu).
-enum class ExpertOp : int { kBf16 = 0, kBf16T = 1, kFp8 = 2, kGateFp8 = 3, kWgrad = 4 };
+enum class ExpertOp : int { kBf16 = 0, kBf16T = 1, kFp8 = 2, kGateFp8 = 3, kWgrad = 4, kLinear = 5 };
+enum class Act : int { kNone = 0, kRelu = 1, kGelu = 2, kGeluTanh = 3, kSilu = 4 };  // ep_activation
 constexpr int64_t kExpertWaitCycles = int64_t(1) << 32;  // about 2 s
 struct ExpertGemmParams {
     const void *x;          // bf16 or e4m3 [rows, k]
@@ -217,6 +220,11 @@ struct ExpertGemmParams {
     int64_t rows;           // receive rows
     int64_t live;           // entries of the layout (an upper bound of the rows in use)
     int32_t out_fp32, accumulate;  // wgrad
+    const void *bias;       // linear: [E, n] bf16 or fp32 (bias_fp32), or nullptr
+    const void *residual;   // linear: bf16 [rows, n] or nullptr
+    void *z;                // linear: bf16 [rows, n], what goes into the activation, or nullptr
+    int32_t bias_fp32;
+    Act act;
     int32_t xs_vec, ws_vec, y_vec;  // set by the launcher: rows of xs / ws can be read 16 bytes, rows of
                                     // y written 32 bytes at a time
     int32_t sms;            // SMs to spread over
@@ -248,6 +256,28 @@ struct CastWeightsParams {
     int32_t E, n, k;
 };
 cudaError_t launch_cast_weights(const CastWeightsParams &p, int sms, cudaStream_t stream);
+
+// ------------------------------------------------------------------ backward of bias and activation
+struct LinearBackwardParams {
+    const void *dy;         // bf16 [rows, n]
+    const void *z;          // bf16 [rows, n] (kNone: may be nullptr)
+    void *dz;               // bf16 [rows, n] or nullptr
+    float *db;              // [E, n] or nullptr
+    const int64_t *base;    // [E]
+    const int32_t *count;   // [E]
+    int32_t E, n;
+    int64_t live;           // entries of the layout (an upper bound of the rows in use)
+    int32_t accumulate;
+    int32_t sms;
+    Act act;
+};
+cudaError_t launch_linear_backward(const LinearBackwardParams &p, cudaStream_t stream);
+
+// ------------------------------------------------------------------ norm and clipping of gradients
+constexpr int kGradPartials = 1024;  // EP_GRAD_PARTIALS
+cudaError_t launch_grad_norm(const ep_grad *g, int count, double *partials, int sms, cudaStream_t stream);
+cudaError_t launch_grad_clip(const ep_grad *g, int count, const double *partials, float max_norm, float *norm, int sms,
+                             cudaStream_t stream);
 
 // ------------------------------------------------------------------ whole layer for a few tokens
 constexpr int kLayerMaxTokens = 128;

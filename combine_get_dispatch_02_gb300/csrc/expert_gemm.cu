@@ -64,6 +64,7 @@
 
 #include <atomic>
 
+#include "activation.cuh"
 #include "ep_internal.cuh"
 #include "umma.cuh"
 
@@ -109,6 +110,7 @@ struct Shape {
     static constexpr bool FP8 = OP == ExpertOp::kFp8 || OP == ExpertOp::kGateFp8;
     static constexpr bool GATE = OP == ExpertOp::kGateFp8;
     static constexpr bool WG = OP == ExpertOp::kWgrad;
+    static constexpr bool LIN = OP == ExpertOp::kLinear;  // bf16 with bias, activation and residual
     static constexpr bool F32 = WG && ALT;
     static constexpr bool ROW = FP8 && ALT;
     static constexpr bool COL = FP8 && !ALT;         // two M-side operands: gate and up product, or 2 x 256 weight rows
@@ -265,6 +267,41 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf,
                      : "r"(buf + tok * 64 + c * 2));
         if (tok < tokens && c < channels) *reinterpret_cast<uint4 *>(dst + tok * ld + c) = q;
     }
+}
+
+// The same 32 tokens x 32 channels the other way: loaded like the stores above, and,
+// through the same 2 KB, added to v.
+struct Residual {
+    uint4 q[4];
+};
+__device__ __forceinline__ void load_residual(Residual &r, int lane, const __nv_bfloat16 *src, int64_t ld, int tokens, int channels) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int tok = (lane >> 2) + 8 * j, c = (lane & 3) * 8;
+        r.q[j] = make_uint4(0, 0, 0, 0);
+        if (tok < tokens && c < channels) r.q[j] = *reinterpret_cast<const uint4 *>(src + tok * ld + c);
+    }
+}
+__device__ __forceinline__ void add_residual(float (&v)[32], const Residual &r, uint32_t buf, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + ((lane >> 2) + 8 * j) * 64 + (lane & 3) * 16), "r"(r.q[j].x),
+                     "r"(r.q[j].y), "r"(r.q[j].z), "r"(r.q[j].w)
+                     : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        uint16_t h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(buf + i * 64 + lane * 2));
+        v[i] += __uint_as_float((uint32_t)h << 16);
+    }
+}
+
+template <Act ACT>
+__device__ __forceinline__ void activate32(float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = activate<ACT>(v[i]);
 }
 
 // Two pieces of 16 bytes of one row, as one 32-byte store where `whole` (the
@@ -806,12 +843,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
             } else if constexpr (S::SEG == 0) {
                 __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
                 const uint32_t buf = seg & 1;
+                [[maybe_unused]] float bias = 0.0f;
+                [[maybe_unused]] Residual res;
+                [[maybe_unused]] const __nv_bfloat16 *from = nullptr;
+                if constexpr (S::LIN) {
+                    // asked for before the products are there
+                    if (p.bias != nullptr && wc + lane < p.n) {
+                        const int64_t at = (int64_t)ti.e * p.n + wc + lane;
+                        bias = p.bias_fp32 ? static_cast<const float *>(p.bias)[at]
+                                           : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[at]);
+                    }
+                    if (p.residual != nullptr) {
+                        from = static_cast<const __nv_bfloat16 *>(p.residual) + ti.row0 * p.n + wc;
+                        load_residual(res, lane, from + (int64_t)hw * 32 * p.n, p.n, ti.valid - hw * 32, p.n - wc);
+                    }
+                }
                 ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                 if (!ok) break;
                 fence_after();
                 for (int c = hw; c < chunks; c += 2) {
                     float v[32];
                     tmem_get32(v, lanes + buf * 256 + c * 32);
+                    if constexpr (S::LIN) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += bias;
+                        if (p.z != nullptr)
+                            store_tokens(v, out, lane, static_cast<__nv_bfloat16 *>(p.z) + (ti.row0 + c * 32) * p.n + wc, p.n,
+                                         ti.valid - c * 32, p.n - wc);
+                        switch (p.act) {
+                            case Act::kRelu: activate32<Act::kRelu>(v); break;
+                            case Act::kGelu: activate32<Act::kGelu>(v); break;
+                            case Act::kGeluTanh: activate32<Act::kGeluTanh>(v); break;
+                            case Act::kSilu: activate32<Act::kSilu>(v); break;
+                            default: break;
+                        }
+                        if (p.residual != nullptr) {
+                            add_residual(v, res, out, lane);
+                            if (c + 2 < chunks)
+                                load_residual(res, lane, from + (int64_t)(c + 2) * 32 * p.n, p.n, ti.valid - (c + 2) * 32, p.n - wc);
+                        }
+                    }
                     store_tokens(v, out, lane, y + (ti.row0 + c * 32) * p.n + wc, p.n, ti.valid - c * 32, p.n - wc);
                 }
                 fence_before();
@@ -1223,6 +1294,7 @@ void allow_smem() {
 void expert_gemm_init() {
     allow_smem<ExpertOp::kBf16, false>();
     allow_smem<ExpertOp::kBf16T, false>();
+    allow_smem<ExpertOp::kLinear, false>();
     allow_smem<ExpertOp::kFp8, false>();
     allow_smem<ExpertOp::kFp8, true>();
     allow_smem<ExpertOp::kGateFp8, false>();
@@ -1236,6 +1308,7 @@ cudaError_t launch_expert_gemm(ExpertOp op, const ExpertGemmParams &p, cudaStrea
     switch (op) {
         case ExpertOp::kBf16: return launch<ExpertOp::kBf16, false>(p, stream);
         case ExpertOp::kBf16T: return launch<ExpertOp::kBf16T, false>(p, stream);
+        case ExpertOp::kLinear: return launch<ExpertOp::kLinear, false>(p, stream);
         case ExpertOp::kFp8: return row ? launch<ExpertOp::kFp8, true>(p, stream) : launch<ExpertOp::kFp8, false>(p, stream);
         case ExpertOp::kGateFp8:
             return row ? launch<ExpertOp::kGateFp8, true>(p, stream) : launch<ExpertOp::kGateFp8, false>(p, stream);

@@ -13,6 +13,7 @@
 // that the SMs end together.  Every CTA sorts the entries by expert itself.
 #include <cuda_bf16.h>
 
+#include "activation.cuh"
 #include "ep_internal.cuh"
 
 namespace ep {
@@ -45,12 +46,6 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {
 
 // Bits 7, 15, 23, 31: which bytes of w are NaN codes.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-
-// silu(g) u in fp32 from e = exp(-|g|), which does not overflow.
-__device__ __forceinline__ float swiglu(float g, float u) {
-    const float e = expf(-fabsf(g));
-    return __fdividef(g < 0.0f ? g * e : g, 1.0f + e) * u;
-}
 
 // The entries by expert, in shared memory: the D experts with entries, ascending,
 // each with its list.  The order inside a list differs between CTAs; an entry's
@@ -262,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_gate_kernel(const ExpertLay
                     }
                     // kept as the sum of two bf16 numbers, 2^-17 of the value off at most: rounded to one, h alone
                     // would put as much error into the result as its own rounding
-                    const float h = swiglu(gate, up);
+                    const float h = silu(gate) * up;
                     const __nv_bfloat16 hi = __float2bfloat16_rn(h);
                     __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.h) + (int64_t)r.list[at] * 2 * p.I + ch;
                     const float top = __bfloat162float(hi);

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 import torch
 
@@ -47,6 +48,7 @@ ENTRY_POINTS = (
     "ep_rank_combine_recv", "ep_rank_runs",
     "ep_expert_gemm", "ep_expert_gemm_fp8", "ep_expert_gate_fp8", "ep_expert_wgrad", "ep_expert_swiglu",
     "ep_expert_swiglu_backward", "ep_cast_weights", "ep_expert_layer_workspace", "ep_expert_layer",
+    "ep_expert_linear", "ep_expert_linear_backward", "ep_grad_norm", "ep_grad_clip",
 )
 
 TUNE_KNOBS = {0: "dispatch", 1: "combine_chunks", 2: "round_trip_chunk",
@@ -54,6 +56,10 @@ TUNE_KNOBS = {0: "dispatch", 1: "combine_chunks", 2: "round_trip_chunk",
 
 EP_CHUNK_AUTO = -1
 EP_LAYER_MAX_TOKENS = 128
+EP_GRAD_PARTIALS = 1024
+
+# ep_activation
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class EPError(RuntimeError):
@@ -155,6 +161,10 @@ def lib() -> ctypes.CDLL:
             "ep_expert_swiglu_backward": (I32, [P, P, P, P, I32, P, P, P]),
             "ep_cast_weights": (I32, [P, P, I32, I32, P, P, P]),
             "ep_expert_layer_workspace": (I32, [P, I32, I32, ctypes.POINTER(ctypes.c_uint64)]),
+            "ep_expert_linear": (I32, [P, P, P, P, I32, I32, P, I32, I32, P, P, P, P]),
+            "ep_expert_linear_backward": (I32, [P, P, P, P, I32, I32, I32, P, P, P]),
+            "ep_grad_norm": (I32, [P, P, I32, P, P]),
+            "ep_grad_clip": (I32, [P, P, I32, P, P, P, P]),
             "ep_expert_layer": (I32, [P, P, P, P, I32, I32, P, P, P, P, P, P, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -557,3 +567,71 @@ def ep_expert_layer(ctx, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: 
         _ptr(w_down, kind, "w_down"), _ptr(down_scales, torch.float32, "down_scales"),
         _ptr(b_down, torch.bfloat16, "b_down"), _ptr(residual, torch.bfloat16, "residual"), _ptr(workspace, None, "workspace"),
         _ptr(out, torch.bfloat16, "out"), _stream(stream)), "ep_expert_layer")
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def ep_expert_linear(ctx, handle, x: torch.Tensor, w: torch.Tensor, n: int, k: int, bias: torch.Tensor | None, activation: str,
+                     residual: torch.Tensor | None, z: torch.Tensor | None, y: torch.Tensor, stream=None) -> None:
+    """bias bf16 or fp32."""
+    if bias is not None and bias.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"bias must be torch.float32 or torch.bfloat16, got {bias.dtype}")
+    _check(lib().ep_expert_linear(
+        ctx, handle, _ptr(x, torch.bfloat16, "x"), _ptr(w, torch.bfloat16, "w"), int(n), int(k), _ptr(bias, None, "bias"),
+        int(bias is not None and bias.dtype == torch.float32), _activation(activation),
+        _ptr(residual, torch.bfloat16, "residual"), _ptr(z, torch.bfloat16, "z"), _ptr(y, torch.bfloat16, "y"),
+        _stream(stream)), "ep_expert_linear")
+
+
+def ep_expert_linear_backward(ctx, handle, dy: torch.Tensor, z: torch.Tensor | None, n: int, activation: str,
+                              accumulate: bool, dz: torch.Tensor | None, dbias: torch.Tensor | None, stream=None) -> None:
+    _check(lib().ep_expert_linear_backward(
+        ctx, handle, _ptr(dy, torch.bfloat16, "dy"), _ptr(z, torch.bfloat16, "z"), int(n), _activation(activation),
+        int(bool(accumulate)), _ptr(dz, torch.bfloat16, "dz"), _ptr(dbias, torch.float32, "dbias"), _stream(stream)),
+        "ep_expert_linear_backward")
+
+
+def grad_list(grads, out=None) -> tuple[array, int]:
+    """The host array of ep_grad for lists of tensors (``out`` None: in place)."""
+    grads = list(grads)
+    out = grads if out is None else list(out)
+    if len(out) != len(grads):
+        raise ValueError(f"out must hold {len(grads)} tensors, got {len(out)}")
+    for name, ts in (("grads", grads), ("out", out)) if out is not grads else (("grads", grads),):
+        if {t.get_device() for t in ts} - {torch._C._cuda_getDevice() if torch.cuda.is_initialized() else None}:
+            raise ValueError(f"{name} must be CUDA tensors of the current device")
+        if not all([t.is_contiguous() for t in ts]):
+            raise ValueError(f"{name} must be contiguous")
+    types = [t.dtype for t in grads]
+    if not set(types) <= {torch.float32, torch.bfloat16}:
+        raise ValueError("grads must be torch.float32 or torch.bfloat16")
+    numels = [t.numel() for t in grads]
+    if out is not grads and ([t.dtype for t in out] != types or [t.numel() for t in out] != numels):
+        raise ValueError("out must have the types and sizes of grads")
+    a = array("q", bytes(32 * len(grads)))
+    a[0::4] = array("q", [t.data_ptr() for t in grads])
+    a[1::4] = a[0::4] if out is grads else array("q", [t.data_ptr() for t in out])
+    a[2::4] = array("q", numels)
+    a[3::4] = array("q", [t is torch.float32 for t in types])
+    return a, len(grads)
+
+
+def ep_grad_norm(ctx, grads: tuple[array, int], partials: torch.Tensor, stream=None) -> None:
+    """grads from grad_list; partials fp64 [EP_GRAD_PARTIALS]."""
+    if partials.numel() != EP_GRAD_PARTIALS:
+        raise ValueError(f"partials must be [{EP_GRAD_PARTIALS}], got {tuple(partials.shape)}")
+    _check(lib().ep_grad_norm(ctx, grads[0].buffer_info()[0], grads[1], _ptr(partials, torch.float64, "partials"),
+                              _stream(stream)), "ep_grad_norm")
+
+
+def ep_grad_clip(ctx, grads: tuple[array, int], partials: torch.Tensor, max_norm: float, norm: torch.Tensor | None,
+                 stream=None) -> None:
+    if partials.numel() != EP_GRAD_PARTIALS:
+        raise ValueError(f"partials must be [{EP_GRAD_PARTIALS}], got {tuple(partials.shape)}")
+    limit = ctypes.c_float(max_norm)
+    _check(lib().ep_grad_clip(ctx, grads[0].buffer_info()[0], grads[1], _ptr(partials, torch.float64, "partials"),
+                              ctypes.addressof(limit), _ptr(norm, torch.float32, "norm"), _stream(stream)), "ep_grad_clip")

@@ -373,6 +373,77 @@ ep_status ep_expert_swiglu_backward(ep_ctx *ctx, const ep_handle *handle, const 
 ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, void *d_q, float *d_scales,
                           void *stream);
 
+/* Experts with biases and other activations: the product with its epilogue, and
+ * the epilogue's backward pass (the products' own gradients are ep_expert_gemm
+ * with transpose_w and ep_expert_wgrad, of dz).  Rows, pointers, sizes and errors
+ * as for the expert operators above.
+ *
+ * ep_expert_linear: z[r] = W[e] x[r] + bias[e], y[r] = act(z[r]) + residual[r],
+ *   summed and applied in fp32, one bf16 rounding.
+ *     d_x, d_w      device bf16 [rows, k], [E, n, k]
+ *     d_bias        device [E, n], fp32 (bias_fp32 = 1) or bf16, or NULL
+ *     activation    EP_ACT_NONE, _RELU, _GELU (z Phi(z), by the error function),
+ *                   _GELU_TANH (z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2)
+ *                   or _SILU (z / (1 + exp(-z)))
+ *     d_residual    device bf16 [rows, n] or NULL; may be d_y itself
+ *     d_z           device bf16 [rows, n] or NULL: z, for the backward pass
+ *     d_y           device bf16 [rows, n]
+ * ep_expert_linear_backward: dz[r] = dy[r] act'(z[r]) rounded to bf16, and the
+ *   bias gradient dbias[e] = sum over the rows of e of the same before the
+ *   rounding, in fp32 (RELU: the slope at 0 is 0).  The residual's gradient is dy.
+ *     d_dy    device bf16 [rows, n]
+ *     d_z     device bf16 [rows, n] as ep_expert_linear left it (EP_ACT_NONE: not
+ *             read, may be NULL)
+ *     d_dz    device bf16 [rows, n], may be d_dy itself or d_z; NULL: not wanted
+ *     d_dbias device fp32 [E, n]; accumulate = 1 adds to what it holds (an expert
+ *             without rows: zeros, or what it holds); NULL: not wanted
+ *   One of d_dz and d_dbias is given at least.  The sums have one order for one
+ *   routing and max_sms does not change it. */
+typedef enum ep_activation {
+    EP_ACT_NONE = 0,
+    EP_ACT_RELU = 1,
+    EP_ACT_GELU = 2,
+    EP_ACT_GELU_TANH = 3,
+    EP_ACT_SILU = 4
+} ep_activation;
+ep_status ep_expert_linear(ep_ctx *ctx, const ep_handle *handle, const void *d_x, const void *d_w, int32_t n, int32_t k,
+                           const void *d_bias, int32_t bias_fp32, int32_t activation, const void *d_residual, void *d_z,
+                           void *d_y, void *stream);
+ep_status ep_expert_linear_backward(ep_ctx *ctx, const ep_handle *handle, const void *d_dy, const void *d_z, int32_t n,
+                                    int32_t activation, int32_t accumulate, void *d_dz, float *d_dbias, void *stream);
+
+/* The norm of many gradients together and their clipping, as it ends a training
+ * step's backward pass:
+ *   norm = sqrt(sum over all tensors of g^2),  out = g * min(1, max_norm / norm)
+ * Squares are summed in fp64 (those of 64 bytes in fp32 first, where they cannot
+ * overflow or vanish).  An infinite or undefined norm scales nothing: the
+ * tensors keep their values and d_norm says it.
+ *
+ * ep_grad_norm: the sum of squares as EP_GRAD_PARTIALS partial sums, all of them
+ *   written.  With the experts of several processes, add these arrays up between
+ *   the two calls (an all-reduce) and each process clips by the norm of all.
+ * ep_grad_clip: the norm from the partial sums (to d_norm, unless NULL) and the
+ *   scaled tensors.  A tensor whose out is its data is written only if the norm
+ *   exceeds max_norm; any other out always is.  max_norm INFINITY: the norm alone.
+ *     grads       host array of `count` ep_grad (read during the call)
+ *     d_partials  device fp64 [EP_GRAD_PARTIALS], 8-byte aligned
+ *     max_norm    host, one float >= 0
+ *     d_norm      device fp32 [1] or NULL
+ * Tensors lie anywhere, aligned to their type; 16-byte alignment, and out aligned
+ * as data is, are faster.  For ep_grad_clip no memory may appear twice in the list
+ * (EP_ERR_INVALID_ARG) but a tensor's data as its own out.  2^42 elements in all
+ * at most (EP_ERR_UNSUPPORTED).  The sums have one order for one max_sms. */
+#define EP_GRAD_PARTIALS 1024
+typedef struct ep_grad {
+    const void *data;  /* device, fp32 or bf16 */
+    void *out;         /* device, the same type (ep_grad_norm: not used) */
+    int64_t numel;
+    int64_t fp32;      /* 1: fp32, 0: bf16 */
+} ep_grad;
+ep_status ep_grad_norm(ep_ctx *ctx, const void *grads, int32_t count, double *d_partials, void *stream);
+ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const double *d_partials, const void *max_norm,
+                       float *d_norm, void *stream);
+
 /* The whole layer of gated experts for a few tokens (a decode step): what
  * dispatch, the two products and combine compute, in two kernels that read the
  * named experts' weights once and keep no receive buffer; for more than

@@ -45,3 +45,33 @@ def test_layer_shapes(change):
                 w_down=bf(4, 64, 16))
     with pytest.raises(ValueError):
         group().expert_layer(**{**args, **change})
+
+
+def test_linear_and_gradients_without_a_context(lib):
+    assert lib.ep_expert_linear(None, None, None, None, 8, 8, None, 0, 0, None, None, None, None) == E
+    assert lib.ep_expert_linear_backward(None, None, None, None, 8, 0, 0, None, None, None) == E
+    assert lib.ep_grad_norm(None, None, 0, None, None) == E
+    assert lib.ep_grad_clip(None, None, 0, None, None, None, None) == E
+
+
+@pytest.mark.parametrize("change", [
+    dict(x=bf(16, 24)), dict(x=bf(15, 32)), dict(w=bf(3, 40, 32)), dict(bias=bf(4, 32)), dict(bias=bf(40)), dict(residual=bf(16, 32)),
+    dict(z=bf(15, 40)), dict(out=bf(16, 48))])
+def test_linear_shapes(change):
+    args = dict(x=bf(16, 32), w=bf(4, 40, 32), handle=None)
+    with pytest.raises(ValueError):
+        group().expert_linear(**{**args, **change})
+
+
+@pytest.mark.parametrize("change", [
+    dict(dy=bf(15, 40)), dict(z=bf(16, 32)), dict(z=None), dict(out=bf(16, 32)), dict(dbias=torch.zeros(4, 32)), dict(accumulate=True)])
+def test_linear_backward_shapes(change):
+    args = dict(dy=bf(16, 40), z=bf(16, 40), handle=None, activation="relu")
+    with pytest.raises(ValueError):
+        group().expert_linear_backward(**{**args, **change})
+
+
+def test_gradient_lists():
+    for grads, out in (([torch.zeros(4)], None), ([torch.zeros(4)], []), ([bf(4)], [bf(4)])):
+        with pytest.raises(ValueError):
+            group().clip_grads(grads, 1.0, out=out)
