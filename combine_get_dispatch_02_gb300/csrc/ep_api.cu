@@ -53,6 +53,9 @@ struct ep_ctx {
     cudaEvent_t ce_fork;
     cudaEvent_t ce_join[kCeStreams];
     cudaEvent_t ce_rank[ep::kRankRunsMaxRanks];  // host wire: source rank r's first leg has landed
+    // grid barriers of ep_expert_layer: two words per stream or captured call, zero between launches
+    uint32_t *d_layer_counters;
+    ep::TileCounters *layer_counters;
 };
 
 struct ep_handle {
@@ -633,10 +636,9 @@ ep_status check_channels(int32_t c, int32_t step) {
 
 int expert_sms(const ep_ctx *ctx) { return grid_cap(ctx, 1); }
 
-// The tile counter of a product on `st` (see tile_counters.h); nullptr when
-// they are all taken: the tiles are then dealt out in a fixed order.
-uint32_t *tile_counter(const ep_ctx *ctx, const ep_handle *h, cudaStream_t st) {
-    uint32_t *const first = reinterpret_cast<uint32_t *>(h->cta_hist + grid_hist_ints(ctx) + 16);
+// A pair of counters for a launch on `st` (see tile_counters.h), of those at `first`
+// that `counters` keeps the book of; nullptr when they are all taken.
+uint32_t *counter_pair(ep::TileCounters *counters, uint32_t *first, cudaStream_t st) {
     cudaStreamCaptureStatus capture;
     if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) {
         cudaGetLastError();  // the launch reports it
@@ -651,7 +653,7 @@ uint32_t *tile_counter(const ep_ctx *ctx, const ep_handle *h, cudaStream_t st) {
             cudaGetLastError();
             return nullptr;
         }
-        ep::TileCounters::Captured *const c = h->counters->take();
+        ep::TileCounters::Captured *const c = counters->take();
         if (c == nullptr) return nullptr;
         const int index = c->index;
         if (cudaUserObjectCreate(&object, c, ep::TileCounters::give_back, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
@@ -671,8 +673,14 @@ uint32_t *tile_counter(const ep_ctx *ctx, const ep_handle *h, cudaStream_t st) {
         cudaGetLastError();
         return nullptr;
     }
-    const int i = h->counters->of_stream(id);
+    const int i = counters->of_stream(id);
     return i < 0 ? nullptr : first + 2 * i;
+}
+
+// The tile counter of a product on `st`; without one the tiles are dealt out in a
+// fixed order.
+uint32_t *tile_counter(const ep_ctx *ctx, const ep_handle *h, cudaStream_t st) {
+    return counter_pair(h->counters, reinterpret_cast<uint32_t *>(h->cta_hist + grid_hist_ints(ctx) + 16), st);
 }
 
 // The parameters every expert product shares.
@@ -748,6 +756,8 @@ ep::ExpertLayerParams layer_params(const ep_ctx *ctx, int32_t num_tokens, int32_
     p.I = inner;
     p.E = c.num_experts;
     p.sms = expert_sms(ctx);
+    p.withhold = ctx->hooks.move_withhold_item < c.num_experts ? (int32_t)ctx->hooks.move_withhold_item : -1;
+    p.wait_cycles = ctx->hooks.move_wait_ns > 0 ? 2 * ctx->hooks.move_wait_ns : ep::kExpertWaitCycles;
     p.status = ctx->d_status;
     return p;
 }
@@ -839,6 +849,7 @@ ep_status ep_create(const ep_config *cfg, ep_ctx **out) {
     ep::dispatch_init();
     ep::move_init();
     ep::expert_gemm_init();
+    ep::expert_layer_init();
     if (cudaMalloc(&ctx->d_status, sizeof(uint32_t)) != cudaSuccess) {
         cudaGetLastError();
         free(ctx);
@@ -863,6 +874,19 @@ ep_status ep_create(const ep_config *cfg, ep_ctx **out) {
         ep_destroy(ctx);
         return EP_ERR_CUDA;
     }
+    const size_t counter_bytes = 2 * (ep::kStreamCounters + ep::kCapturedCounters) * sizeof(uint32_t);
+    ctx->layer_counters = ep::TileCounters::create();
+    if (ctx->layer_counters == nullptr || cudaMalloc(&ctx->d_layer_counters, counter_bytes) != cudaSuccess) {
+        cudaGetLastError();
+        ep_destroy(ctx);
+        return EP_ERR_OOM;
+    }
+    // zero before any stream's first launch
+    if (cudaMemset(ctx->d_layer_counters, 0, counter_bytes) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
+        cudaGetLastError();
+        ep_destroy(ctx);
+        return EP_ERR_CUDA;
+    }
     *out = ctx;
     return EP_OK;
 }
@@ -870,6 +894,8 @@ ep_status ep_create(const ep_config *cfg, ep_ctx **out) {
 ep_status ep_destroy(ep_ctx *ctx) {
     if (ctx == nullptr) return EP_ERR_INVALID_ARG;
     cudaFree(ctx->d_status);
+    cudaFree(ctx->d_layer_counters);
+    if (ctx->layer_counters) ctx->layer_counters->release();
     if (ctx->ce_fork) cudaEventDestroy(ctx->ce_fork);
     for (int i = 0; i < kCeStreams; ++i) {
         if (ctx->ce_stream[i]) cudaStreamDestroy(ctx->ce_stream[i]);
@@ -1729,9 +1755,11 @@ ep_status ep_expert_layer(ep_ctx *ctx, const void *d_x, const int64_t *d_topk_id
     p.b_down = d_b_down;
     p.residual = d_residual;
     p.out = d_out;
-    if (ep::launch_expert_layer(p, d_workspace, (cudaStream_t)stream) != cudaSuccess) {
+    p.barrier = counter_pair(ctx->layer_counters, ctx->d_layer_counters, (cudaStream_t)stream);
+    const cudaError_t e = ep::launch_expert_layer(p, d_workspace, (cudaStream_t)stream);
+    if (e != cudaSuccess) {
         cudaGetLastError();
-        return EP_ERR_CUDA;
+        return e == cudaErrorCooperativeLaunchTooLarge ? EP_ERR_UNSUPPORTED : EP_ERR_CUDA;
     }
     return EP_OK;
 }

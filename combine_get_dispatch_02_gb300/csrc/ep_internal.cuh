@@ -293,15 +293,24 @@ struct ExpertLayerParams {
     const void *b_down;        // bf16 [E, H] or nullptr
     const void *residual;      // bf16 [N, H] or nullptr
     void *out;                 // bf16 [N, H]
-    // workspace, set by the launcher
-    float *y;                  // [N * K, H] experts' outputs
-    void *h;                   // [N * K][2][I] activations as the sum of two bf16 numbers
-    uint32_t *done;            // [ceil(H / 32)] units of each tile of output rows that are done
+    // workspace, set by the launcher; entries in the order of the sorted list
+    void *xs;                  // [N * K][R][H] tokens as operands of the gate product (bf16 or R = 2 codes)
+    void *h;                   // [N * K][R][I] activations as operands of the down product (2 bf16 or 4 codes)
+    float *sums;               // [N * K][rows of all tiles] sums of the product at hand
+    float *pieces;             // [SMs][64][128] sums of the job that an SM does not begin
+    float *x_scale, *h_scale;  // [N * K] what a code is worth
+    uint32_t *barrier;         // grid barrier and count of the CTAs that are done with it: both zero
+                               // between launches, each launch puts them back; nullptr: none free (the
+                               // workspace's then)
     int32_t N, K, H, I, E;
     int32_t sms;
+    int32_t withhold;          // test hook: expert whose weights are never loaded (-1: none)
+    int64_t wait_cycles;       // bound of each wait in SM clocks (kExpertWaitCycles)
     uint32_t *status;
 };
-size_t expert_layer_workspace(const ExpertLayerParams &p);
+// One-time set-up with the device current (shared memory limits).
+void expert_layer_init();
+size_t expert_layer_workspace(ExpertLayerParams p);
 cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device helpers

@@ -1222,9 +1222,9 @@ EncodeTiled encode_fn() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// A row-major matrix [rows, cols] (or [planes, rows, cols]) in boxes of box_rows
-// rows by 128 bytes, swizzled.
-bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
+}  // namespace
+
+bool encode_rows(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows) {
     const EncodeTiled fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
@@ -1237,6 +1237,8 @@ bool encode(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows
     return fn(m, type, planes > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 template <ExpertOp OP, bool ALT>
 size_t smem_bytes(int E) {
@@ -1255,13 +1257,13 @@ cudaError_t launch(const ExpertGemmParams &p, cudaStream_t stream) {
     Maps maps;
     bool ok;
     if constexpr (S::WG) {
-        ok = encode(&maps.m[0], p.dy, 2, p.n, p.rows, 0, 64) && encode(&maps.m[1], p.x, 2, p.k, p.rows, 0, 64) &&
-             encode(&maps.m[5], p.y, S::F32 ? 4 : 2, p.k, p.n, p.E, 32);
+        ok = encode_rows(&maps.m[0], p.dy, 2, p.n, p.rows, 0, 64) && encode_rows(&maps.m[1], p.x, 2, p.k, p.rows, 0, 64) &&
+             encode_rows(&maps.m[5], p.y, S::F32 ? 4 : 2, p.k, p.n, p.E, 32);
     } else {
         constexpr int es = S::FP8 ? 1 : 2;
-        ok = S::A_MN ? encode(&maps.m[0], p.w, es, p.n, p.k, p.E, 64) : encode(&maps.m[0], p.w, es, p.k, p.n, p.E, 128);
-        for (int i = 0; i < 4 && ok; ++i) ok = encode(&maps.m[1 + i], p.x, es, p.k, p.rows, 0, 128 >> i);
-        if constexpr (S::ROW && !S::GATE) ok = ok && encode(&maps.m[5], p.y, 2, p.n, p.rows, 0, 32);
+        ok = S::A_MN ? encode_rows(&maps.m[0], p.w, es, p.n, p.k, p.E, 64) : encode_rows(&maps.m[0], p.w, es, p.k, p.n, p.E, 128);
+        for (int i = 0; i < 4 && ok; ++i) ok = encode_rows(&maps.m[1 + i], p.x, es, p.k, p.rows, 0, 128 >> i);
+        if constexpr (S::ROW && !S::GATE) ok = ok && encode_rows(&maps.m[5], p.y, 2, p.n, p.rows, 0, 32);
     }
     if (!ok) return cudaErrorInvalidValue;
     int pairs = p.sms / 2;

@@ -1,397 +1,892 @@
-// The whole layer of gated experts for a few tokens (a decode step), in two
-// kernels and without the receive layout between dispatch and combine:
+// The whole layer of gated experts for a few tokens (a decode step), in one
+// kernel and without the receive layout between dispatch and combine:
 //   gate   h[j] = silu(g) u, [g; u] = Wgu[e] x[t] + bgu[e]      for every entry j = (t, k), e = idx[t, k]
 //   down   y[j] = Wd[e] h[j] + bd[e]
 //          out[t] = bf16(res[t] + sum_k w[t, k] y[t, k])        k ascending, one rounding
-// Weights are bf16, or e4m3 with a scale per 128 x 128 block; the tokens are not
-// cast to 8 bits.
+// Weights are bf16, or e4m3 with a scale per 128 x 128 block.
 //
 // With few tokens the weights of the experts that are named are all that has to
-// move, each used for a handful of tokens.  The unit of work is 32 weight rows of
-// one expert (gate: 16 channels of h, their gate and up rows), over all tokens
-// of that expert, 8 at a time; a CTA takes a contiguous share of all units, so
-// that the SMs end together.  Every CTA sorts the entries by expert itself.
+// move, each used for a handful of tokens, so the kernel is one stream of weights per
+// SM that never stops: a stage is 128 weight rows x 128 bytes, the M side of the tensor
+// cores, whose N side are the tokens of one expert (16 to 64 columns).  All stages
+// of a product, in the order expert, weight rows, tokens, channels, are cut into equal
+// contiguous shares, one per SM, wherever that falls: a tile that begins in one SM's share
+// and ends in another's leaves two partial sums (fp32, in the workspace), added in
+// the order of the shares.  What needs all SMs' results is done between grid barriers
+// (cooperative launch), and the weights' loader does not wait there:
+//   entries sorted by expert (by every CTA), tokens laid out in that order
+//   -- gate product -- SwiGLU, h laid out -- down product -- sum over k
+//
+// Operands of e4m3 weights: a bf16 value has 8 significant bits, an e4m3 code 4, so x
+// times a power of two per token (the largest to 128 .. 256) is the sum of two codes,
+// the second worth 2^-4 of the first; exactly, down to 2^-13 of the largest, and to 2^-21
+// of that below.  h, which has more bits, is the sum of four (2^-17 of it).  They are columns
+// of the product, so nothing is converted on the weights' way.  The weights' scales vary
+// along the channels: a stage's sums leave tensor memory and are scaled and added in
+// fp32 registers.  bf16 weights: x as it is, h as the sum of two bf16 numbers.
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "activation.cuh"
 #include "ep_internal.cuh"
+#include "umma.cuh"
 
 namespace ep {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+using namespace umma;
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// Warps: 0 .. 3 read the sums out of tensor memory, 4 loads weights, 5 tokens, 6 issues the products; 0 .. 3
+// and 8 .. 11 do what lies between the products ("workers").
+constexpr int kWarpWeights = 4, kWarpTokens = 5, kWarpMma = 6;
+constexpr int kThreads = 12 * 32, kWorkers = 256;
+constexpr int kTile = 128;                   // weight rows of a job
+constexpr int kColumns = 64;                 // most columns of a job
+constexpr int kWeightBytes = kTile * 128, kStage = kWeightBytes + kColumns * 128;
+constexpr int kStages = 8, kSums = 4;        // stages of the ring, accumulators
+constexpr size_t kFixed = 1024 + (size_t)kStages * kStage;
+constexpr int kMaxSms = 256;
+
+// Columns of an entry (codes or numbers whose sum it is) and entries of a job.
+template <bool FP8, bool DOWN>
+struct Parts {
+    static constexpr int R = FP8 ? (DOWN ? 4 : 2) : (DOWN ? 2 : 1);
+    static constexpr int TOKENS = kColumns / R;
+};
+template <bool FP8>
+constexpr int kLine = FP8 ? 128 : 64;        // channels of a stage
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
-
-// The two e4m3 codes in bytes 2 * HALF and + 1 of w as bf16 pairs, exactly: exponent
-// and mantissa moved into place give the value times 2^-120 (subnormal codes are
-// subnormal numbers there), which the product with 2^120 undoes.  A NaN code (0x7F)
-// comes out as 480, more than any other: see nan_codes.
-template <int HALF>
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {
-    const uint32_t p = __byte_perm(w, 0, HALF ? 0x3424 : 0x1404);  // a code in the upper byte of each half
-    const uint32_t v = ((p >> 4) & 0x07F007F0u) | (p & 0x80008000u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7B807B80u));
-    return r;
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
-
-// Bits 7, 15, 23, 31: which bytes of w are NaN codes.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+// Tensor memory and products of one CTA (umma.cuh has those of a pair).
+__device__ __forceinline__ void tmem_alloc_one(uint32_t dst, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_one(uint32_t addr, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+template <bool FP8>
+__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    if constexpr (FP8)
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(accumulate)
+            : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers) : "memory"); }
 
 // The entries by expert, in shared memory: the D experts with entries, ascending,
-// each with its list.  The order inside a list differs between CTAs; an entry's
-// result does not depend on its place.
+// each with its list.
 struct Route {
-    int *first;        // [E + 1] count, then first place in list, of each expert
-    uint16_t *live;    // [min(E, M)] experts with entries
-    uint16_t *list;    // [M] entries by expert
-    uint16_t *place;   // [M] place in its expert's list, 0xFFFF: no expert
+    int *first;           // [E + 1] first place in `list` of each expert
+    uint16_t *live;       // [D] experts with entries
+    uint16_t *list;       // [M] entries (token, k) by expert: token * 32 + k
+    uint16_t *spot;       // [M] an entry's place in the list, 0xFFFF: none
+    uint16_t *before[2];  // [D + 1] jobs of a tile (gate, down) before each live expert
     int D;
 };
+size_t route_bytes(int E, int M) {
+    const int D = E < M ? E : M;
+    return (size_t)(E + 2) * 4 + (size_t)D * 2 + (size_t)M * 4 + 2 * (size_t)(D + 1) * 2 + 16;
+}
 
-size_t route_bytes(int E, int M) { return (size_t)(E + 2) * 4 + (size_t)(E < M ? E : M) * 2 + (size_t)M * 4 + 16; }
-
-__device__ __forceinline__ Route route(const ExpertLayerParams &p, uint8_t *smem) {
-    __shared__ int live_experts;
+// `scratch`: 512 bytes for each warp, and 17 KB behind them.
+template <bool FP8>
+__device__ __forceinline__ Route route(const ExpertLayerParams &p, uint8_t *at, uint32_t *scratch) {
+    constexpr int kWarps = kThreads / 32, kGateTokens = Parts<FP8, false>::TOKENS, kDownTokens = Parts<FP8, true>::TOKENS;
     Route r;
-    const int M = p.N * p.K, tid = threadIdx.x;
-    r.first = reinterpret_cast<int *>(smem);
+    const int M = p.N * p.K, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    r.first = reinterpret_cast<int *>(at);
     r.list = reinterpret_cast<uint16_t *>(r.first + p.E + 1);
-    r.place = r.list + M;
-    r.live = r.place + M;
+    r.spot = r.list + M;
+    r.live = r.spot + M;
+    r.before[0] = r.live + min(p.E, M);
+    r.before[1] = r.before[0] + min(p.E, M) + 1;
+    uint2 *const sums = reinterpret_cast<uint2 *>(scratch + kWarps * 128);       // [32] of 32 experts each
+    uint16_t *const place = reinterpret_cast<uint16_t *>(sums + 32);            // [M] in its expert's list
+    uint16_t *const owner = place + M;                                          // [M] expert, 0xFFFF: none
     for (int e = tid; e <= p.E; e += kThreads) r.first[e] = 0;
     __syncthreads();
     for (int j = tid; j < M; j += kThreads) {
         const int64_t e = p.idx[j];
         const bool ok = e >= 0 && e < p.E;
         if (!ok && e != -1 && blockIdx.x == 0) atomicOr(p.status, kStatusBadExpert);
-        r.place[j] = ok ? (uint16_t)atomicAdd(&r.first[e], 1) : 0xFFFFu;
+        owner[j] = ok ? (uint16_t)e : 0xFFFFu;
+        r.spot[j] = 0xFFFFu;
+        if (ok) place[j] = (uint16_t)atomicAdd(&r.first[e], 1);
     }
     __syncthreads();
-    if (tid < 32) {
-        // first places and the live experts, both by prefix sums over the experts
-        const int per = (p.E + 31) / 32, e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
-        int n = 0, d = 0;
-        for (int e = e0; e < e1; ++e) {
-            n += r.first[e];
-            d += r.first[e] > 0 ? 1 : 0;
-        }
-        int ns = n, ds = d;
+    // Prefix sums over the experts, 32 to a warp: entries and live experts, jobs of both products, two in
+    // a word (4096 at most).
+    const int chunks = (p.E + 31) / 32;
+    constexpr int kTurns = (32 + kWarps - 1) / kWarps;  // 32 chunks at most
+    uint2 own[kTurns], run[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int e = (warp + i * kWarps) * 32 + lane;
+        const uint32_t c = warp + i * kWarps < chunks && e < p.E ? (uint32_t)r.first[e] : 0u;
+        own[i] = make_uint2(c | (c > 0 ? 1u : 0u) << 16, (c + kGateTokens - 1) / kGateTokens | (c + kDownTokens - 1) / kDownTokens << 16);
+        run[i] = own[i];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int a = __shfl_up_sync(0xFFFFFFFFu, ns, o), b = __shfl_up_sync(0xFFFFFFFFu, ds, o);
-            if (tid >= o) ns += a, ds += b;
+            const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, run[i].x, o), y = __shfl_up_sync(0xFFFFFFFFu, run[i].y, o);
+            if (lane >= o) run[i].x += x, run[i].y += y;
         }
-        if (tid == 31) live_experts = ds, r.first[p.E] = ns;
-        ns -= n;
-        ds -= d;
-        for (int e = e0; e < e1; ++e) {
-            const int c = r.first[e];
-            r.first[e] = ns;
-            ns += c;
-            if (c > 0) r.live[ds++] = (uint16_t)e;
-        }
+        if (lane == 31 && warp + i * kWarps < 32) sums[warp + i * kWarps] = run[i];
+    }
+    __syncthreads();
+    uint2 all = sums[lane];
+    const uint2 mine = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, all.x, o), y = __shfl_up_sync(0xFFFFFFFFu, all.y, o);
+        if (lane >= o) all.x += x, all.y += y;
+    }
+    const uint2 total = make_uint2(__shfl_sync(0xFFFFFFFFu, all.x, 31), __shfl_sync(0xFFFFFFFFu, all.y, 31));
+    r.D = (int)(total.x >> 16);
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int chunk = min(warp + i * kWarps, 31), e = chunk * 32 + lane;
+        const uint32_t x = __shfl_sync(0xFFFFFFFFu, all.x - mine.x, chunk) + run[i].x - own[i].x;
+        const uint32_t y = __shfl_sync(0xFFFFFFFFu, all.y - mine.y, chunk) + run[i].y - own[i].y;
+        if (warp + i * kWarps >= chunks || e >= p.E) continue;
+        r.first[e] = (int)(x & 0xFFFFu);
+        if (own[i].x == 0) continue;
+        r.live[x >> 16] = (uint16_t)e;
+        r.before[0][x >> 16] = (uint16_t)(y & 0xFFFFu);
+        r.before[1][x >> 16] = (uint16_t)(y >> 16);
+    }
+    if (tid == 0) {
+        r.first[p.E] = (int)(total.x & 0xFFFFu);
+        r.before[0][r.D] = (uint16_t)(total.y & 0xFFFFu);
+        r.before[1][r.D] = (uint16_t)(total.y >> 16);
     }
     __syncthreads();
     for (int j = tid; j < M; j += kThreads)
-        if (r.place[j] != 0xFFFFu) r.list[r.first[p.idx[j]] + r.place[j]] = (uint16_t)j;
+        if (owner[j] != 0xFFFFu) r.list[r.first[owner[j]] + place[j]] = (uint16_t)(j / p.K * 32 + j % p.K);
     __syncthreads();
-    r.D = live_experts;
+    // The order inside a list is the atomics', and has to be the same in every CTA: ascending, up to 32
+    // entries by counting the smaller ones, else by a bit per entry.
+    uint32_t *bits = scratch + warp * 128;
+    for (int d = warp; d < r.D; d += kWarps) {
+        const int e = r.live[d], a = r.first[e], b = r.first[e + 1];
+        if (b - a <= 32) {
+            const uint32_t v = a + lane < b ? r.list[a + lane] : 0xFFFFu;
+            int rank = 0;
+            for (int i = 0; i < b - a; ++i) rank += __shfl_sync(0xFFFFFFFFu, v, i) < v ? 1 : 0;
+            if (a + lane < b) r.list[a + rank] = (uint16_t)v;
+            continue;
+        }
+        for (int i = lane; i < 128; i += 32) bits[i] = 0;
+        __syncwarp();
+        for (int i = a + lane; i < b; i += 32) {
+            const uint32_t v = r.list[i], j = (v >> 5) * p.K + (v & 31);
+            atomicOr(bits + (j >> 5), 1u << (j & 31));
+        }
+        __syncwarp();
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n += __popc(bits[lane * 4 + i]);
+        int at0 = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, at0, o);
+            if (lane >= o) at0 += v;
+        }
+        at0 += a - n;
+        for (int i = 0; i < 4; ++i)
+            for (uint32_t w = bits[lane * 4 + i]; w != 0; w &= w - 1) {
+                const uint32_t j = (lane * 4 + i) * 32 + __ffs(w) - 1;
+                r.list[at0++] = (uint16_t)(j / p.K * 32 + j % p.K);
+            }
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int i = tid; i < r.first[p.E]; i += kThreads) {
+        const uint32_t v = r.list[i];
+        r.spot[(v >> 5) * p.K + (v & 31)] = (uint16_t)i;
+    }
     return r;
 }
 
-// Products of two tiles of 16 weight rows (row(i, g): tile i, row g of 0 .. 15, as a
-// pointer) with up to 8 columns, over this warp's share of K channels.  PLANES: a
-// column is the sum of this many bf16 vectors, `plane` elements apart.
-template <bool FP8, int PLANES>
-__device__ __forceinline__ void products(float (&acc)[2][4], const uint8_t *const (&wr)[2][2], const float *const (&ws)[2][2],
-                                         const __nv_bfloat16 *col, int64_t plane, int K, int warp, int t) {
-    if constexpr (!FP8) {
-        constexpr int U = 4;
-        const int steps = (K + 31) / 32;
-        for (int s0 = warp; s0 < steps; s0 += kWarps * U) {
-            uint4 a[U][2][2], b[U][PLANES];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int c = (s0 + u * kWarps) * 32 + t * 8;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) a[u][i][q] = c < K ? ld_nc_na_v4(wr[i][q] + 2 * (int64_t)c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int q = 0; q < PLANES; ++q)
-                    b[u][q] = c < K ? __ldg(reinterpret_cast<const uint4 *>(col + q * plane + c)) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int q = 0; q < PLANES; ++q)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        mma_bf16(acc[i], a[u][i][0].x, a[u][i][1].x, a[u][i][0].y, a[u][i][1].y, b[u][q].x, b[u][q].y);
-                        mma_bf16(acc[i], a[u][i][0].z, a[u][i][1].z, a[u][i][0].w, a[u][i][1].w, b[u][q].z, b[u][q].w);
-                    }
-        }
-    } else {
-        const int blocks = K / 128;
-        uint32_t bad[2][2] = {};
-        for (int s = warp; s < blocks; s += kWarps) {
-            uint4 a[2][2][2], b[2][PLANES][2];
-            float sc[2][2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int c = s * 128 + u * 64 + t * 16;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) a[u][i][q] = ld_nc_na_v4(wr[i][q] + c);
-#pragma unroll
-                for (int q = 0; q < PLANES; ++q)
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) b[u][q][v] = __ldg(reinterpret_cast<const uint4 *>(col + q * plane + c + 8 * v));
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) sc[i][q] = __ldg(ws[i][q] + s);
-            float part[2][4] = {};
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t w0[4] = {a[u][i][0].x, a[u][i][0].y, a[u][i][0].z, a[u][i][0].w};
-                    const uint32_t w1[4] = {a[u][i][1].x, a[u][i][1].y, a[u][i][1].z, a[u][i][1].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        bad[i][0] |= nan_codes(w0[j]);
-                        bad[i][1] |= nan_codes(w1[j]);
-                        const uint32_t a0 = e4m3x2<0>(w0[j]), a1 = e4m3x2<0>(w1[j]), a2 = e4m3x2<1>(w0[j]), a3 = e4m3x2<1>(w1[j]);
-#pragma unroll
-                        for (int q = 0; q < PLANES; ++q) {
-                            const uint4 &v = b[u][q][j >> 1];
-                            mma_bf16(part[i], a0, a1, a2, a3, j & 1 ? v.z : v.x, j & 1 ? v.w : v.y);
-                        }
-                    }
-                }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[i][c] = fmaf(part[i][c], sc[i][c >> 1], acc[i][c]);
-        }
-        // a NaN code: the row's sums are NaN
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t any = bad[i][q];
-                any |= __shfl_xor_sync(0xFFFFFFFFu, any, 1);
-                any |= __shfl_xor_sync(0xFFFFFFFFu, any, 2);
-                if (any != 0) acc[i][2 * q] = acc[i][2 * q + 1] = __int_as_float(0x7FC00000);
-            }
+// The jobs of a product, in the order expert, tile of weight rows, tokens, and a CTA's share of their stages:
+// pieces of jobs, stages l0 .. l1 - 1 of each.
+template <bool FP8, bool DOWN>
+struct Walk {
+    static constexpr int TOKENS = Parts<FP8, DOWN>::TOKENS;
+    int tiles, lines, d, part, parts;  // tiles of an expert, stages of a job, live expert, its tokens' part and parts
+    int e, tile, first, count;         // the job: expert, tile, its tokens' places in the list
+    int l0, l1;
+    uint32_t left;                     // stages of the share from this piece on
+    __device__ __forceinline__ void expert(const Route &r) {
+        e = r.live[d];
+        parts = r.before[DOWN][d + 1] - r.before[DOWN][d];
     }
+    __device__ __forceinline__ void tokens(const Route &r) {
+        first = r.first[e] + part * TOKENS;
+        count = min(TOKENS, r.first[e + 1] - first);
+        l1 = min(lines, l0 + (int)min(left, 0x7FFFFFFFu));
+    }
+    // To the first piece of the stages from .. to - 1; false: there are none.
+    __device__ __forceinline__ bool start(const Route &r, int tiles_, int lines_, uint32_t from, uint32_t to) {
+        if (from == to) return false;
+        tiles = tiles_;
+        lines = lines_;
+        left = to - from;
+        const uint32_t q = from / lines;
+        l0 = (int)(from - q * lines);
+        const uint16_t *before = r.before[DOWN];
+        int lo = 0, hi = r.D - 1;  // the last d with before[d] * tiles <= q
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((uint32_t)before[mid] * tiles <= q)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        d = lo;
+        expert(r);
+        const uint32_t rest = q - (uint32_t)before[lo] * tiles;
+        tile = (int)(rest / parts);
+        part = (int)(rest - tile * parts);
+        tokens(r);
+        return true;
+    }
+    __device__ __forceinline__ bool next(const Route &r) {
+        left -= l1 - l0;
+        if (left == 0) return false;
+        l0 = 0;
+        if (++part == parts) {
+            part = 0;
+            if (++tile == tiles) {
+                tile = 0;
+                ++d;
+                expert(r);
+            }
+        }
+        tokens(r);
+        return true;
+    }
+};
+
+struct Maps {
+    CUtensorMap w[2];  // gate and up, down: [E, rows, channels] in boxes of 64 rows x 128 bytes, swizzled
+    CUtensorMap t[2];  // x, h laid out by entry: [entries * R, channels] in boxes of 16 rows x 128 bytes
+};
+
+struct Bars {
+    uint64_t full[kStages], empty[kStages], tfull[kSums], tempty[kSums];
+    uint32_t from[2][kMaxSms + 1];  // first stage of each CTA's share
+    uint32_t armed[2];              // stages loaded (weights, tokens)
+    uint32_t failed, tmem;
+    float top[kWorkers / 32];
+};
+
+// The CTA whose share stage u belongs to.  scale: CTAs per stage.
+__device__ __forceinline__ int owner_of(const uint32_t *from, int ctas, float scale, uint32_t u) {
+    int b = min((int)(__uint2float_rd(u) * scale), ctas - 1);
+    while (from[b] > u) --b;
+    while (from[b + 1] <= u) ++b;
+    return b;
 }
 
-// The 8 warps' sums of element c of tile i, lane l of the fragments.
-__device__ __forceinline__ float summed(const float (*red)[2][4][32], int i, int c, int l) {
-    float v = 0.0f;
+// The largest of the workers' values.
+__device__ __forceinline__ float workers_max(float v, float *part, int worker) {
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][i][c][l];
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    workers_sync();
+    if ((worker & 31) == 0) part[worker >> 5] = v;
+    workers_sync();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < kWorkers / 32; ++i) v = fmaxf(v, part[i]);
     return v;
 }
 
+// The power of two that brings top to 128 .. 256 (within fp32's own), and 1 over it.
+__device__ __forceinline__ float2 scale_of(float top) {
+    if (top == 0.0f) return make_float2(1.0f, 1.0f);
+    const int ex = max((int)(__float_as_uint(top) >> 23), 1) - 127;        // top = 1.. * 2^ex
+    const int k = min(7 - ex, 126);
+    return make_float2(__uint_as_float((uint32_t)(127 + k) << 23), __uint_as_float((uint32_t)(127 - k) << 23));
+}
+
+// v[8] times s as the sum of R e4m3 codes, code r worth 2^(-4 r): rows of `row` bytes from dst on.  What is not
+// finite becomes NaN.
+template <int R>
+__device__ __forceinline__ void store_codes(const float (&v)[8], float s, uint8_t *dst, int64_t row) {
+    float rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = isfinite(v[i]) ? v[i] * s : __int_as_float(0x7FC00000);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const __nv_fp8x2_storage_t q = __nv_cvt_float2_to_fp8x2(make_float2(rest[i], rest[i + 1]), __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            rest[i] = (rest[i] - f.x) * 16.0f;
+            rest[i + 1] = (rest[i + 1] - f.y) * 16.0f;
+            w[i >> 2] |= (uint32_t)q << (8 * (i & 3));
+        }
+        *reinterpret_cast<uint2 *>(dst + r * row) = make_uint2(w[0], w[1]);
+    }
+}
+
+__device__ __forceinline__ float finite_or_0(float v) { return isfinite(v) ? fabsf(v) : 0.0f; }
+
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads, 2) layer_gate_kernel(const ExpertLayerParams p) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float red[kWarps][2][4][32];
+__global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const ExpertLayerParams p) {
+    extern __shared__ uint8_t dyn[];
+    __shared__ Bars bars;
+    uint8_t *const ring = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ctas = gridDim.x, cta = blockIdx.x;
+    const uint32_t b_full = saddr(bars.full), b_empty = saddr(bars.empty), b_tfull = saddr(bars.tfull), b_tempty = saddr(bars.tempty);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            bar_init(b_full + 8 * i, 2);  // both loaders
+            bar_init(b_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < kSums; ++i) {
+            bar_init(b_tfull + 8 * i, 1);
+            bar_init(b_tempty + 8 * i, 4);
+        }
+        bar_init_fence();
+        bars.failed = bars.armed[0] = bars.armed[1] = 0;
+        for (int i = 0; i < 2; ++i) {
+            prefetch_map(&maps.w[i]);
+            prefetch_map(&maps.t[i]);
+        }
+    }
     pdl_wait();
-    pdl_launch_dependents();
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < (p.H + 31) / 32; i += gridDim.x * kThreads) p.done[i] = 0;
-    const Route r = route(p, smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int tiles = (p.I + 15) / 16;
-    const int64_t total = (int64_t)r.D * tiles;
-    const int es = FP8 ? 1 : 2, nb = (2 * p.I + 127) / 128, kb = p.H / 128;
-    const int64_t it1 = total * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t it = total * blockIdx.x / gridDim.x; it < it1; ++it) {
-        const int d = (int)(it / tiles), c0 = (int)(it - (int64_t)d * tiles) * 16, e = r.live[d];
-        const int j0 = r.first[e], j1 = r.first[e + 1];
-        // tile i: channels c0 + 8 i .. of h, their gate rows above, their up rows below
-        const uint8_t *wr[2][2];
-        const float *ws[2][2];
+    const Route r = route<FP8>(p, ring + kStages * kStage, reinterpret_cast<uint32_t *>(ring));
+    const bool worker = warp < 4 || warp >= 8;
+    const int wid = warp < 4 ? tid : tid - 128;  // of a worker
+    // tiles of an expert's weights, stages of a job, rows of the tiles
+    const int tiles[2] = {(p.I + kTile / 2 - 1) / (kTile / 2), (p.H + kTile - 1) / kTile};
+    const int lines[2] = {(p.H + kLine<FP8> - 1) / kLine<FP8>, (p.I + kLine<FP8> - 1) / kLine<FP8>};
+    uint32_t total[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int row = q * p.I + min(c0 + 8 * i, p.I - 8) + g;
-                wr[i][q] = static_cast<const uint8_t *>(p.w_gate_up) + ((int64_t)e * 2 * p.I + row) * p.H * es;
-                ws[i][q] = FP8 ? p.s_gate_up + ((int64_t)e * nb + row / 128) * kb : nullptr;
-            }
-        for (int j = j0; j < j1; j += 8) {
-            float acc[2][4] = {};
-            const int token = r.list[min(j + g, j1 - 1)] / p.K;
-            products<FP8, 1>(acc, wr, ws, static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)token * p.H, 0, p.H, warp, t);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) red[warp][i][c][lane] = acc[i][c];
-            __syncthreads();
-            if (tid < 128) {
-                const int i = tid >> 6, c = tid >> 5 & 1, l = tid & 31;
-                const int at = j + 2 * (l & 3) + c, ch = c0 + 8 * i + (l >> 2);
-                if (at < j1 && ch < p.I) {
-                    float gate = summed(red, i, c, l), up = summed(red, i, c + 2, l);
-                    if (p.b_gate_up != nullptr) {
-                        const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.b_gate_up) + (int64_t)e * 2 * p.I;
-                        gate += __bfloat162float(b[ch]);
-                        up += __bfloat162float(b[p.I + ch]);
+    for (int d = 0; d < 2; ++d) {
+        total[d] = (uint32_t)tiles[d] * r.before[d][r.D] * lines[d];
+        for (int b = tid; b <= ctas; b += kThreads) bars.from[d][b] = (uint32_t)((uint64_t)total[d] * b / ctas);
+    }
+    if (warp == kWarpMma && r.D > 0) tmem_alloc_one(saddr(&bars.tmem), kSums * kColumns);
+    fence_async_shared();  // the scratch lies where the stages land
+    fence_before();
+    __syncthreads();
+    fence_after();
+    // A wait that has given up ends its warp's waits; one thread may know of it alone (`met`), so that every
+    // wait of a warp is one of all its lanes.
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        bool there = ok;
+        if (there) there = bar_wait(bar, parity, p.wait_cycles);
+        return __all_sync(0xFFFFFFFFu, there);
+    };
+    // All CTAs' workers have come to the i-th meeting; by one thread.
+    auto met = [&](uint32_t i) {
+        const long long t0 = clock64();
+        uint32_t v;
+        do {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p.barrier) : "memory");
+            if (v >= i * ctas) return true;
+        } while (clock64() - t0 < p.wait_cycles);
+        return false;
+    };
+
+    if (r.D > 0 && warp == kWarpWeights) {
+        uint32_t n = 0;
+        auto product = [&](auto down) {
+            constexpr bool DOWN = decltype(down)::value;
+            Walk<FP8, DOWN> w;
+            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
+            do {
+                if (w.e == p.withhold) ok = false;  // test hook
+                const int row0 = w.tile * (DOWN ? kTile : kTile / 2), row1 = DOWN ? row0 + kTile / 2 : p.I + row0;
+                for (int l = w.l0; l < w.l1 && ok; ++l) {
+                    const uint32_t slot = n % kStages;
+                    ok = wait(b_empty + 8 * slot, (n / kStages & 1) ^ 1);
+                    if (!ok) break;
+                    ++n;
+                    if (elect()) {
+                        const uint32_t bar = b_full + 8 * slot, at = saddr(ring + slot * kStage);
+                        bar_expect(bar, kWeightBytes);
+                        load_box(at, &maps.w[DOWN], l * kLine<FP8>, row0, w.e, bar);
+                        load_box(at + kWeightBytes / 2, &maps.w[DOWN], l * kLine<FP8>, row1, w.e, bar);
                     }
-                    // kept as the sum of two bf16 numbers, 2^-17 of the value off at most: rounded to one, h alone
-                    // would put as much error into the result as its own rounding
-                    const float h = silu(gate) * up;
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.h) + (int64_t)r.list[at] * 2 * p.I + ch;
-                    const float top = __bfloat162float(hi);
-                    to[0] = hi;
-                    to[p.I] = __float2bfloat16_rn(isfinite(top) ? h - top : 0.0f);
+                    __syncwarp();
+                }
+            } while (ok && w.next(r));
+        };
+        product(std::false_type{});
+        product(std::true_type{});
+        if (lane == 0) bars.armed[0] = n;
+    } else if (r.D > 0 && warp == kWarpTokens) {
+        uint32_t n = 0;
+        auto product = [&](auto down) {
+            constexpr bool DOWN = decltype(down)::value;
+            constexpr int R = Parts<FP8, DOWN>::R;
+            Walk<FP8, DOWN> w;
+            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
+            // x is laid out before the first meeting, h before the third
+            if (lane == 0) ok = met(DOWN ? 3 : 1);
+            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0);
+            asm volatile("fence.proxy.async;" ::: "memory");
+            __syncwarp();
+            if (!ok) return;
+            do {
+                const int boxes = (w.count * R + 15) / 16;
+                for (int l = w.l0; l < w.l1 && ok; ++l) {
+                    const uint32_t slot = n % kStages;
+                    ok = wait(b_empty + 8 * slot, (n / kStages & 1) ^ 1);
+                    if (!ok) break;
+                    ++n;
+                    if (elect()) {
+                        const uint32_t bar = b_full + 8 * slot, at = saddr(ring + slot * kStage) + kWeightBytes;
+                        bar_expect(bar, boxes * 2048);
+                        for (int i = 0; i < boxes; ++i) load_box(at + i * 2048, &maps.t[DOWN], l * kLine<FP8>, w.first * R + i * 16, bar);
+                    }
+                    __syncwarp();
+                }
+            } while (ok && w.next(r));
+        };
+        product(std::false_type{});
+        product(std::true_type{});
+        if (lane == 0) bars.armed[1] = n;
+    } else if (r.D > 0 && warp == kWarpMma) {
+        uint32_t n = 0, seg = 0;
+        auto product = [&](auto down) {
+            constexpr bool DOWN = decltype(down)::value;
+            constexpr int R = Parts<FP8, DOWN>::R;
+            Walk<FP8, DOWN> w;
+            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
+            do {
+                // fp32 accumulator, both operands bf16 or both e4m3, 128 x columns
+                const uint32_t columns = (w.count * R + 15) & ~15;
+                const uint32_t id = (1u << 4) | (FP8 ? 0u : (1u << 7 | 1u << 10)) | (columns >> 3) << 17 | (kTile >> 4) << 24;
+                for (int l = w.l0; l < w.l1 && ok; ++l) {
+                    const uint32_t slot = n % kStages, buf = seg % kSums;
+                    const bool begins = FP8 || l == w.l0, ends = FP8 || l == w.l1 - 1;
+                    ok = wait(b_full + 8 * slot, n / kStages & 1);
+                    if (ok && begins) ok = wait(b_tempty + 8 * buf, (seg / kSums & 1) ^ 1);
+                    if (!ok) break;
+                    fence_after();
+                    ++n;
+                    if (elect()) {
+                        const uint32_t a = saddr(ring + slot * kStage), b = a + kWeightBytes;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_one<FP8>(bars.tmem + buf * kColumns, desc(a + j * 32, 16), desc(b + j * 32, 16), id, !begins || j != 0);
+                        commit_one(b_empty + 8 * slot);
+                        if (ends) commit_one(b_tfull + 8 * buf);
+                    }
+                    __syncwarp();
+                    if (ends) ++seg;
+                }
+            } while (ok && w.next(r));
+        };
+        product(std::false_type{});
+        product(std::true_type{});
+        // all products have been computed before tensor memory is given back
+        for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+            if (!__all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * (i % kStages), i / kStages & 1, p.wait_cycles))) ok = false;
+    } else if (worker) {
+        uint32_t seg = 0;
+        const float scales[2] = {(float)ctas / (float)total[0], (float)ctas / (float)total[1]};
+        // Comes to the i-th meeting: what this CTA's workers wrote can be read behind it, by copies too.  Not
+        // before all have come to the one before: a CTA without a share would be counted for a slow one.
+        auto come = [&](uint32_t i) {
+            asm volatile("fence.proxy.async;" ::: "memory");
+            workers_sync();
+            if (wid == 0) {
+                if (i > 1 && !met(i - 1)) ok = false;
+                __threadfence();
+                atomicAdd(p.barrier, 1u);
+            }
+        };
+        auto meet = [&](uint32_t i) {
+            come(i);
+            if (wid == 0) {
+                if (ok && !met(i)) ok = false;
+                __threadfence();
+            }
+            workers_sync();
+        };
+        // Where the sums of entry `spot` for a tile are: in its row of p.sums, and in the pieces that other CTAs
+        // than the one where the job begins had of it.
+        struct Where {
+            int d, part, at, parts;  // live expert, part of its tokens, place in the part, parts
+        };
+        auto where = [&](int down, int spot) {
+            int lo = 0, hi = r.D - 1;  // the last live expert that begins at or before the entry
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (r.first[r.live[mid]] <= spot)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int tokens = down ? Parts<FP8, true>::TOKENS : Parts<FP8, false>::TOKENS;
+            const int within = spot - r.first[r.live[lo]];
+            return Where{lo, within / tokens, within % tokens, r.before[down][lo + 1] - r.before[down][lo]};
+        };
+        auto pieces = [&](int down, const Where &w, int tile) {
+            const uint32_t u = ((uint32_t)r.before[down][w.d] * tiles[down] + tile * w.parts + w.part) * lines[down];
+            const int first = owner_of(bars.from[down], ctas, scales[down], u);
+            int last = first;
+            while (bars.from[down][last + 1] < u + lines[down]) ++last;
+            return make_int2(first, last);
+        };
+        // Sums out of tensor memory: lane = weight row.
+        auto product = [&](auto down) {
+            constexpr bool DOWN = decltype(down)::value;
+            constexpr int R = Parts<FP8, DOWN>::R, TOKENS = Parts<FP8, DOWN>::TOKENS;
+            Walk<FP8, DOWN> w;
+            if (warp >= 4 || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
+            const uint32_t lanes = bars.tmem + ((uint32_t)(warp * 32) << 16);
+            const int kb = lines[DOWN], nb = ((DOWN ? p.H : 2 * p.I) + 127) / 128;
+            do {
+                const int columns = w.count * R;
+                float acc[FP8 ? TOKENS : 1];
+                float ws = 0.0f;
+                // from tensor memory, 16 columns at a time: f(entry, sum of its columns)
+                auto columns_of = [&](uint32_t buf, auto &&f) {
+                    ok = wait(b_tfull + 8 * buf, seg / kSums & 1);
+                    fence_after();
+#pragma unroll
+                    for (int q = 0; q < kColumns / 16; ++q) {
+                        if (q * 16 >= columns) break;
+                        uint32_t v[16];
+                        tmem_get16(v, lanes + buf * kColumns + q * 16);
+                        if ((q + 1) * 16 >= columns) {
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(b_tempty + 8 * buf);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16 / R; ++i) {
+                            float s = __uint_as_float(v[i * R + R - 1]);
+#pragma unroll
+                            for (int k = R - 2; k >= 0; --k) s = fmaf(s, FP8 ? 0.0625f : 1.0f, __uint_as_float(v[i * R + k]));
+                            f(q * (16 / R) + i, s);
+                        }
+                    }
+                    ++seg;
+                };
+                float *const to = w.l0 == 0 ? p.sums + (int64_t)w.first * (tiles[DOWN] * kTile) + w.tile * kTile + warp * 32 + lane
+                                            : p.pieces + (int64_t)cta * kColumns * kTile + warp * 32 + lane;
+                const int64_t ld = w.l0 == 0 ? tiles[DOWN] * kTile : kTile;
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int i = 0; i < TOKENS; ++i) acc[i] = 0.0f;
+                    // the scales of 32 stages, one per lane; gate: the first two warps have gate rows, the others up rows
+                    const int row = DOWN ? w.tile * kTile : w.tile * (kTile / 2) + (warp >> 1) * p.I;
+                    const float *sc = (DOWN ? p.s_down : p.s_gate_up) + ((int64_t)w.e * nb + row / 128) * kb;
+                    for (int l = w.l0; l < w.l1; ++l) {
+                        if ((l - w.l0 & 31) == 0) ws = l + lane < w.l1 ? __ldg(sc + l + lane) : 0.0f;
+                        const float f = __shfl_sync(0xFFFFFFFFu, ws, l - w.l0 & 31);
+                        columns_of(seg % kSums, [&](int i, float s) { acc[i] = fmaf(s, f, acc[i]); });
+                    }
+#pragma unroll
+                    for (int i = 0; i < TOKENS; ++i)
+                        if (i < w.count) __stcg(to + i * ld, acc[i]);
+                } else {
+                    columns_of(seg % kSums, [&](int i, float s) {
+                        if (i < w.count) __stcg(to + i * ld, s);
+                    });
+                }
+            } while (w.next(r));
+        };
+        // x of every entry, in the order of the list
+        if (r.D > 0) {
+            const int entries = r.first[p.E];
+            for (int i = cta; i < entries; i += ctas) {
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)(r.list[i] >> 5) * p.H;
+                if constexpr (!FP8) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.xs) + (int64_t)i * p.H);
+                    for (int c = wid; c < p.H / 8; c += kWorkers) dst[c] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+                } else {
+                    auto get = [&](float (&v)[8], int c) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
+                    };
+                    float v[8], top = 0.0f;
+                    for (int c = wid; c < p.H / 8; c += kWorkers) {
+                        get(v, c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) top = fmaxf(top, finite_or_0(v[k]));
+                    }
+                    const float2 s = scale_of(workers_max(top, bars.top, wid));
+                    for (int c = wid; c < p.H / 8; c += kWorkers) {
+                        get(v, c);
+                        store_codes<2>(v, s.x, static_cast<uint8_t *>(p.xs) + (int64_t)i * 2 * p.H + c * 8, p.H);
+                    }
+                    if (wid == 0) p.x_scale[i] = s.y;
                 }
             }
+            come(1);
+            product(std::false_type{});
+            meet(2);
+            // h of every entry
+            const int rows = tiles[0] * kTile;
+            for (int i = cta; i < entries; i += ctas) {
+                const Where w = where(0, i);
+                const int e = r.live[w.d];
+                const float xs = FP8 ? __ldcg(p.x_scale + i) : 1.0f;
+                auto get = [&](float (&h)[8], int c) {
+                    const int tile = c / 8, at = tile * kTile + (c & 7) * 8;  // 8 channels: c
+                    const int2 who = pieces(0, w, tile);
+                    float g[8], u[8];
+                    auto add = [&](const float *src, bool set) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float4 a = __ldcg(reinterpret_cast<const float4 *>(src) + k);
+                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + kTile / 2) + k);
+                            const float x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                g[4 * k + m] = set ? x[m] : g[4 * k + m] + x[m];
+                                u[4 * k + m] = set ? y[m] : u[4 * k + m] + y[m];
+                            }
+                        }
+                    };
+                    add(p.sums + (int64_t)i * rows + at, true);
+                    for (int b = who.x + 1; b <= who.y; ++b)
+                        if (bars.from[0][b] < bars.from[0][b + 1])  // a CTA without a share left nothing
+                            add(p.pieces + ((int64_t)b * kColumns + w.at) * kTile + (c & 7) * 8, false);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float gate = g[k] * xs, up = u[k] * xs;
+                        if (p.b_gate_up != nullptr) {
+                            const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.b_gate_up) + (int64_t)e * 2 * p.I + c * 8 + k;
+                            gate += __bfloat162float(b[0]);
+                            up += __bfloat162float(b[p.I]);
+                        }
+                        h[k] = silu(gate) * up;
+                    }
+                };
+                float h[8];
+                if constexpr (!FP8) {
+                    for (int c = wid; c < p.I / 8; c += kWorkers) {
+                        get(h, c);
+                        // the sum of two bf16 numbers, 2^-17 of the value off at most: rounded to one, h alone would
+                        // put as much error into the result as its own rounding
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 a = __floats2bfloat162_rn(h[2 * k], h[2 * k + 1]);
+                            const float2 f = __bfloat1622float2(a);
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(isfinite(f.x) ? h[2 * k] - f.x : 0.0f,
+                                                                           isfinite(f.y) ? h[2 * k + 1] - f.y : 0.0f);
+                            hi[k] = *reinterpret_cast<const uint32_t *>(&a);
+                            lo[k] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.h) + (int64_t)i * 2 * p.I + c * 8;
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(dst + p.I) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                } else {
+                    float top = 0.0f;
+                    for (int c = wid; c < p.I / 8; c += kWorkers) {
+                        get(h, c);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) top = fmaxf(top, finite_or_0(h[k]));
+                    }
+                    const float2 s = scale_of(workers_max(top, bars.top, wid));
+                    for (int c = wid; c < p.I / 8; c += kWorkers) {
+                        if (p.I > kWorkers * 8) get(h, c);  // else it is still there
+                        store_codes<4>(h, s.x, static_cast<uint8_t *>(p.h) + (int64_t)i * 4 * p.I + c * 8, p.I);
+                    }
+                    if (wid == 0) p.h_scale[i] = s.y;
+                }
+            }
+            come(3);
+            product(std::true_type{});
+            meet(4);
+        }
+        // out: a warp takes a token and the 128 channels of a tile, lane k looks entry k up
+        for (int it = cta * (kWorkers / 32) + (wid >> 5); it < p.N * tiles[1]; it += ctas * (kWorkers / 32)) {
+            const int t = it / tiles[1], tile = it - t * tiles[1], c = tile * kTile + lane * 4;
+            int spot = -1, at = 0, e = 0;
+            int2 who = make_int2(0, 0);
+            float weight = 0.0f, hs = 1.0f;
+            if (lane < p.K) {
+                const uint32_t v = r.spot[t * p.K + lane];
+                if (v != 0xFFFFu) {
+                    spot = (int)v;
+                    const Where w = where(1, spot);
+                    at = w.at;
+                    e = r.live[w.d];
+                    who = pieces(1, w, tile);
+                    weight = p.wts != nullptr ? __ldg(p.wts + t * p.K + lane) : 1.0f;
+                    if (FP8) hs = __ldcg(p.h_scale + spot);
+                }
+            }
+            float v[4] = {};
+            for (int k = 0; k < p.K; ++k) {
+                const int s = __shfl_sync(0xFFFFFFFFu, spot, k);
+                const int a = __shfl_sync(0xFFFFFFFFu, at, k), ex = __shfl_sync(0xFFFFFFFFu, e, k);
+                const int b0 = __shfl_sync(0xFFFFFFFFu, who.x, k), b1 = __shfl_sync(0xFFFFFFFFu, who.y, k);
+                const float w = __shfl_sync(0xFFFFFFFFu, weight, k), f = __shfl_sync(0xFFFFFFFFu, hs, k);
+                if (s < 0 || c >= p.H) continue;
+                float4 y = __ldcg(reinterpret_cast<const float4 *>(p.sums + (int64_t)s * (tiles[1] * kTile) + c));
+                for (int b = b0 + 1; b <= b1; ++b) {
+                    if (bars.from[1][b] == bars.from[1][b + 1]) continue;  // a CTA without a share left nothing
+                    const float4 q = __ldcg(reinterpret_cast<const float4 *>(p.pieces + ((int64_t)b * kColumns + a) * kTile + lane * 4));
+                    y = make_float4(y.x + q.x, y.y + q.y, y.z + q.z, y.w + q.w);
+                }
+                float z[4] = {y.x * f, y.y * f, y.z * f, y.w * f};
+                if (p.b_down != nullptr) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.b_down) + (int64_t)ex * p.H + c);
+                    z[0] += bf16_lo(q.x);
+                    z[1] += bf16_hi(q.x);
+                    z[2] += bf16_lo(q.y);
+                    z[3] += bf16_hi(q.y);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = fmaf(w, z[i], v[i]);
+            }
+            if (c >= p.H) continue;
+            const int64_t o = (int64_t)t * p.H + c;
+            if (p.residual != nullptr) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.residual) + o);
+                v[0] += bf16_lo(q.x);
+                v[1] += bf16_hi(q.x);
+                v[2] += bf16_lo(q.y);
+                v[3] += bf16_hi(q.y);
+            }
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + o) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         }
     }
-}
-
-// out[t, rows] from every entry's y, k ascending.
-__device__ __forceinline__ void combine_rows(const ExpertLayerParams &p, const Route &r, int row0) {
-    const int row = row0 + (threadIdx.x & 15) * 2;
-    if (row >= p.H) return;
-    for (int t = threadIdx.x >> 4; t < p.N; t += kThreads / 16) {
-        float a = 0.0f, b = 0.0f;
-        for (int k = 0; k < p.K; ++k) {
-            const int j = t * p.K + k;
-            if (r.place[j] == 0xFFFFu) continue;
-            const float w = p.wts != nullptr ? __ldg(p.wts + j) : 1.0f;
-            const float2 y = __ldcg(reinterpret_cast<const float2 *>(p.y + (int64_t)j * p.H + row));
-            a = fmaf(w, y.x, a);
-            b = fmaf(w, y.y, b);
+    if (!ok) {
+        bars.failed = 1;
+        atomicOr(p.status, kStatusTimeout);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (r.D == 0) return;
+    if (warp == kWarpMma) tmem_free_one(bars.tmem, kSums * kColumns);
+    if (tid == 0) {
+        if (bars.failed) {
+            // loads in flight land before the shared memory is given up: where only one loader came, the
+            // other's arrival is made up for
+            const uint32_t n0 = min(bars.armed[0], bars.armed[1]), n1 = max(bars.armed[0], bars.armed[1]);
+            for (uint32_t n = n0; n < n1; ++n) bar_arrive(b_full + 8 * (n % kStages));
+            for (uint32_t n = n1 > kStages ? n1 - kStages : 0; n < n1; ++n)
+                if (!bar_wait(b_full + 8 * (n % kStages), n / kStages & 1, p.wait_cycles)) atomicOr(p.status, kStatusInFlight);
         }
-        const int64_t at = (int64_t)t * p.H + row;
-        if (p.residual != nullptr) {
-            const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.residual) + at));
-            a += bf16_lo(v);
-            b += bf16_hi(v);
+        // the last CTA puts the barrier back: all arrivals are in, on a failure too
+        if (atomicAdd(p.barrier + 1, 1u) == gridDim.x - 1) {
+            p.barrier[0] = 0;
+            p.barrier[1] = 0;
         }
-        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = __floats2bfloat162_rn(a, b);
     }
 }
 
 template <bool FP8>
-__global__ void __launch_bounds__(kThreads, 2) layer_down_kernel(const ExpertLayerParams p) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float red[kWarps][2][4][32];
-    __shared__ int last;
-    const Route r = route(p, smem);
-    pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int tiles = (p.H + 31) / 32;
-    if (r.D == 0) {
-        for (int i = blockIdx.x; i < tiles; i += gridDim.x) combine_rows(p, r, i * 32);
-        return;
-    }
-    const int64_t total = (int64_t)r.D * tiles;
-    const int es = FP8 ? 1 : 2, nb = (p.H + 127) / 128, kb = p.I / 128;
-    const int64_t it0 = total * blockIdx.x / gridDim.x, it1 = total * (blockIdx.x + 1) / gridDim.x;
-    int mine = 0;  // units of this tile done here
-    for (int64_t it = it0; it < it1; ++it) {
-        const int tile = (int)(it / r.D), d = (int)(it - (int64_t)tile * r.D), e = r.live[d];
-        const int j0 = r.first[e], j1 = r.first[e + 1], row0 = tile * 32;
-        const uint8_t *wr[2][2];
-        const float *ws[2][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int row = min(row0 + 16 * i + 8 * q, p.H - 8) + g;
-                wr[i][q] = static_cast<const uint8_t *>(p.w_down) + ((int64_t)e * p.H + row) * p.I * es;
-                ws[i][q] = FP8 ? p.s_down + ((int64_t)e * nb + row / 128) * kb : nullptr;
-            }
-        for (int j = j0; j < j1; j += 8) {
-            float acc[2][4] = {};
-            const int entry = r.list[min(j + g, j1 - 1)];
-            products<FP8, 2>(acc, wr, ws, static_cast<const __nv_bfloat16 *>(p.h) + (int64_t)entry * 2 * p.I, p.I, p.I, warp, t);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) red[warp][i][c][lane] = acc[i][c];
-            __syncthreads();
-            const int i = tid >> 7, c = tid >> 5 & 3, l = tid & 31;
-            const int at = j + 2 * (l & 3) + (c & 1), row = row0 + 16 * i + 8 * (c >> 1) + (l >> 2);
-            if (at < j1 && row < p.H) {
-                float y = summed(red, i, c, l);
-                if (p.b_down != nullptr) y += __bfloat162float(static_cast<const __nv_bfloat16 *>(p.b_down)[(int64_t)e * p.H + row]);
-                __stcg(p.y + (int64_t)r.list[at] * p.H + row, y);
-            }
-        }
-        ++mine;
-        if (d == r.D - 1 || it == it1 - 1) {
-            // whoever completes the tile's experts adds them up
-            bool whole = mine == r.D;
-            if (!whole) {
-                __threadfence();
-                __syncthreads();
-                if (tid == 0) last = atomicAdd(p.done + tile, (uint32_t)mine) + mine == (uint32_t)r.D;
-                __syncthreads();
-                whole = last;
-                __threadfence();
-            } else {
-                __syncthreads();
-            }
-            if (whole) combine_rows(p, r, row0);
-            mine = 0;
-        }
-    }
+cudaError_t launch(const Maps &maps, const ExpertLayerParams &p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.sms, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kFixed + route_bytes(p.E, p.N * p.K);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident: the grid barriers end
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, expert_layer_kernel<FP8>, maps, p);
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const ExpertLayerParams &p, size_t smem, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * p.sms, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+template <bool FP8>
+void allow_smem() {
+    // failing here means failing at the launch, which reports it
+    if (cudaFuncSetAttribute(expert_layer_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kFixed + route_bytes(1024, kLayerMaxTokens * 32))) != cudaSuccess)
+        cudaGetLastError();
+}
+
+// The workspace's parts, each on a 256-byte boundary: sets their addresses from `base` on, returns the size.
+size_t lay_out(ExpertLayerParams &p, uint8_t *base) {
+    const size_t M = (size_t)p.N * p.K;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t *const q = base + at;
+        at += (bytes + 255) / 256 * 256;
+        return q;
+    };
+    const size_t gate = (size_t)((p.I + kTile / 2 - 1) / (kTile / 2)) * kTile, down = (size_t)((p.H + kTile - 1) / kTile) * kTile;
+    p.xs = take(M * p.H * 2);
+    p.h = take(M * p.I * 4);
+    p.sums = reinterpret_cast<float *>(take(M * (gate > down ? gate : down) * 4));
+    p.pieces = reinterpret_cast<float *>(take((size_t)p.sms * kColumns * kTile * 4));
+    p.x_scale = reinterpret_cast<float *>(take(M * 4));
+    p.h_scale = reinterpret_cast<float *>(take(M * 4));
+    uint32_t *const barrier = reinterpret_cast<uint32_t *>(take(8));
+    if (p.barrier == nullptr) p.barrier = barrier;
+    return at;
 }
 
 }  // namespace
 
-size_t expert_layer_workspace(const ExpertLayerParams &p) {
-    const size_t M = (size_t)p.N * p.K;
-    return M * p.H * 4 + M * p.I * 4 + (size_t)((p.H + 31) / 32) * 4;
+void expert_layer_init() {
+    allow_smem<false>();
+    allow_smem<true>();
 }
 
+size_t expert_layer_workspace(ExpertLayerParams p) { return lay_out(p, nullptr); }
+
 cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream_t stream) {
-    const size_t M = (size_t)p.N * p.K, smem = route_bytes(p.E, (int)M);
-    p.y = static_cast<float *>(workspace);
-    p.h = p.y + M * p.H;
-    p.done = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.h) + M * p.I * 4);
-    const bool fp8 = p.s_gate_up != nullptr;
-    cudaError_t e = fp8 ? launch(layer_gate_kernel<true>, p, smem, stream) : launch(layer_gate_kernel<false>, p, smem, stream);
-    if (e == cudaSuccess) e = fp8 ? launch(layer_down_kernel<true>, p, smem, stream) : launch(layer_down_kernel<false>, p, smem, stream);
-    return e;
+    const bool fp8 = p.s_gate_up != nullptr, own = p.barrier != nullptr;
+    if (p.sms > kMaxSms) p.sms = kMaxSms;
+    lay_out(p, static_cast<uint8_t *>(workspace));
+    if (!own) {
+        // no counter of the context's left: the workspace's, cleared by a call of its own
+        const cudaError_t e = cudaMemsetAsync(p.barrier, 0, 8, stream);
+        if (e != cudaSuccess) return e;
+    }
+    const int es = fp8 ? 1 : 2;
+    const int64_t M = (int64_t)p.N * p.K;
+    Maps maps;
+    if (!encode_rows(&maps.w[0], p.w_gate_up, es, p.H, 2 * (int64_t)p.I, p.E, kTile / 2) ||
+        !encode_rows(&maps.w[1], p.w_down, es, p.I, p.H, p.E, kTile / 2) ||
+        !encode_rows(&maps.t[0], p.xs, es, p.H, M * (fp8 ? 2 : 1), 0, 16) || !encode_rows(&maps.t[1], p.h, es, p.I, M * (fp8 ? 4 : 2), 0, 16))
+        return cudaErrorInvalidValue;
+    return fp8 ? launch<true>(maps, p, stream) : launch<false>(maps, p, stream);
 }
 
 }  // namespace ep

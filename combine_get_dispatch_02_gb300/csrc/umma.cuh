@@ -8,6 +8,11 @@
 #include <stdint.h>
 
 namespace ep {
+
+// A row-major matrix [rows, cols] (planes > 0: [planes, rows, cols]) of elements of es bytes
+// as a tensor map with boxes of box_rows rows by 128 bytes, swizzled (expert_gemm.cu).
+bool encode_rows(CUtensorMap *m, const void *base, int es, int64_t cols, int64_t rows, int64_t planes, int box_rows);
+
 namespace umma {
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }

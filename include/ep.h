@@ -473,8 +473,9 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
  *                       (streams, graphs) need one each
  *     d_out             device bf16 [num_tokens, H]
  * All pointers 16-byte aligned (d_topk_idx 8, scales and weights 4); inner a
- * multiple of 8, with FP8 weights H and inner multiples of 128.  The result does
- * not depend on max_sms and repeats bit for bit. */
+ * multiple of 8, with FP8 weights H and inner multiples of 128.  The same call
+ * repeats bit for bit; the order in which its sums are taken follows from the SMs
+ * (max_sms) and from which experts are named. */
 #define EP_LAYER_MAX_TOKENS 128
 ep_status ep_expert_layer_workspace(const ep_ctx *ctx, int32_t num_tokens, int32_t inner, uint64_t *bytes);
 ep_status ep_expert_layer(ep_ctx *ctx, const void *d_x, const int64_t *d_topk_idx, const float *d_topk_weights,

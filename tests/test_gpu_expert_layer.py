@@ -1,4 +1,6 @@
 """GPU checks of the whole layer for a few tokens against its definition in 64 bits."""
+import ctypes
+
 import pytest
 import torch
 
@@ -201,11 +203,12 @@ def test_infinities_and_large_values():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-def test_results_do_not_depend_on_max_sms_and_repeat(fp8):
-    args = dict(N=21, H=512, I=256, E=12, K=3, fp8=fp8, bias=True, residual=True, seed=2)
-    first = Layer(**args).check()
-    for sms in (1, 7, 152):
-        layer = Layer(**args, max_sms=sms)
+def test_every_number_of_sms_and_repeated_calls(fp8):
+    """The sums are cut into as many shares as there are SMs: within the bounds for each number, and the same bits
+    every time for one."""
+    for sms in (0, 1, 7, 64, 151, 152):
+        layer = Layer(N=21, H=512, I=256, E=12, K=3, fp8=fp8, bias=True, residual=True, seed=2, max_sms=sms)
+        first = layer.check()
         for _ in range(3):
             assert torch.equal(layer.run(), first)
 
@@ -331,3 +334,55 @@ def test_refusals_touch_nothing():
     zero[4] = 0
     assert lib.ep_expert_layer(*zero) == ep.EP_OK
     assert buf.device_status() == ep.EP_OK and bool((out == 3.0).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_lists_cut_into_jobs_agree_between_the_sms(fp8):
+    """128 tokens of one expert, few tiles, many SMs: the jobs of one list run on different SMs."""
+    for seed in range(4):
+        layer = Layer(128, 256, 128, 3, 2, fp8=fp8, seed=seed, bias=True)
+        first = layer.check()
+        for _ in range(5):
+            assert torch.equal(layer.run(), first)
+
+
+def test_the_same_expert_for_every_entry():
+    """4096 entries of one expert, 32 of each token."""
+    Layer(128, 64, 16, 32, 32, idx=torch.ones(128, 32, dtype=torch.int64).cuda()).check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_wait_that_runs_out_is_reported_and_leaves_nothing_behind(fp8):
+    """An expert whose weights never come, 1 ms waits: the status says so; the next call is right again."""
+    layer = Layer(12, 1024, 512, 8, 2, fp8=fp8, seed=1)
+    want = layer.check()
+    for _ in range(2):
+        ep.ep_set_test_hooks(layer.buf.ctx, move_withhold_item=int(layer.idx[3, 1]), move_wait_ns=1_000_000)
+        layer.buf.expert_layer(layer.x, layer.idx, layer.wts, layer.gu, layer.down)
+        assert layer.buf.device_status() == ep.EP_ERR_TIMEOUT
+        ep.ep_set_test_hooks(layer.buf.ctx)
+        for _ in range(3):
+            assert torch.equal(layer.run(), want)
+
+
+def test_more_streams_than_there_are_counters():
+    """From the 513th stream on a barrier counter comes from the workspace."""
+    layer = Layer(2, 64, 16, 4, 2)
+    want = layer.check()
+    raw = lambda s: ep.ep_expert_layer(layer.buf.ctx, layer.x, layer.idx, layer.wts, 2, 16, layer.gu, None, None, layer.down, None,  # noqa: E731
+                                       None, None, ws, out, stream=s)
+    rt = ctypes.CDLL("libcudart.so")
+    made = []
+    for i in range(530):
+        h = ctypes.c_void_p()
+        assert rt.cudaStreamCreate(ctypes.byref(h)) == 0
+        made.append(h)
+        ws = torch.empty(ep.ep_expert_layer_workspace(layer.buf.ctx, 2, 16), dtype=torch.uint8, device="cuda")
+        out = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        raw(torch.cuda.ExternalStream(h.value))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
+    for h in made:
+        assert rt.cudaStreamDestroy(h) == 0
+    assert layer.buf.device_status() == ep.EP_OK
