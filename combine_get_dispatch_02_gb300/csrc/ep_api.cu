@@ -1612,6 +1612,8 @@ ep_status ep_expert_linear_backward(ep_ctx *ctx, const ep_handle *handle, const 
     p.live = (int64_t)ctx->cfg.num_ranks * handle->tokens_per_rank * ctx->cfg.topk;
     p.accumulate = accumulate;
     p.sms = expert_sms(ctx);
+    p.all_sms = ctx->num_sms;
+    p.status = ctx->d_status;
     p.act = (ep::Act)activation;
     if (ep::launch_linear_backward(p, (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();

@@ -268,7 +268,9 @@ struct LinearBackwardParams {
     int32_t E, n;
     int64_t live;           // entries of the layout (an upper bound of the rows in use)
     int32_t accumulate;
-    int32_t sms;
+    int32_t ctas;           // set by the launcher: CTAs that share an expert's rows
+    int32_t sms, all_sms;   // to spread over; the device's
+    uint32_t *status;
     Act act;
 };
 cudaError_t launch_linear_backward(const LinearBackwardParams &p, cudaStream_t stream);
