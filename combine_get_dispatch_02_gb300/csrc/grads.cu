@@ -30,6 +30,7 @@ struct Table {
     int64_t n[CAP];            // elements; ~n for fp32
     int32_t first[CAP + 1];    // first piece of each tensor
     int32_t count;
+    int32_t in_place;          // every tensor is its own out
 };
 
 struct Piece {
@@ -92,15 +93,10 @@ __device__ __forceinline__ uint4 load_vec(const Piece &p, int64_t i, int ve) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[kThreads / 32];
+// Over a warp, in every lane.
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) v += part[i];
     return v;
 }
 
@@ -145,22 +141,55 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
             sum += wide;
         }
     }
-    sum = block_sum(sum);
-    if (threadIdx.x == 0) partials[blockIdx.x] = add ? partials[blockIdx.x] + sum : sum;
+    // by one warp: an fp64 instruction of a warp takes 16 cycles, and with all of them at it 12 small tensors
+    // took 8 us here and 12 below
+    __shared__ double part[kThreads];
+    part[threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        sum = part[threadIdx.x];
+#pragma unroll
+        for (int i = 1; i < kThreads / 32; ++i) sum += part[threadIdx.x + 32 * i];
+        sum = warp_sum(sum);
+        if (threadIdx.x == 0) partials[blockIdx.x] = add ? partials[blockIdx.x] + sum : sum;
+    }
     if (!add && blockIdx.x == 0)
         for (int i = gridDim.x + threadIdx.x; i < kGradPartials; i += kThreads) partials[i] = 0.0;
+}
+
+// The root of a sum of squares in fp32: the sum brought to 1 .. 4 by an even power of two, which fp32 takes
+// with 24 bits; infinite past fp32's range.
+__device__ __forceinline__ float root(double sum) {
+    const long long bits = __double_as_longlong(sum);
+    const int ex = (int)(bits >> 52) - 1023;
+    if (ex == 1024 || ex < -1022) return sum == 0.0 ? 0.0f : ex == 1024 ? (float)sum : 0.0f;  // infinite, NaN; subnormal
+    const int half = ex >> 1;
+    const float m = (float)__longlong_as_double((bits & 0xFFFFFFFFFFFFFll) | (long long)(1023 + (ex & 1)) << 52);
+    return ldexpf(__fsqrt_rn(m), half);
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_constant__ Table<CAP> tab, const double *partials,
                                                              float max_norm, float *norm_out) {
     pdl_wait();
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < kGradPartials; i += kThreads) sum += partials[i];
-    const double norm = sqrt(block_sum(sum));
-    if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-    // an infinite or undefined norm scales nothing
-    const float f = isfinite(norm) && norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.0f;
+    __shared__ double part[kGradPartials];
+    __shared__ float factor;
+#pragma unroll
+    for (int i = 0; i < kGradPartials / kThreads; ++i) part[threadIdx.x + i * kThreads] = partials[threadIdx.x + i * kThreads];
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        double sum = part[threadIdx.x];
+        for (int i = 1; i < kGradPartials / 32; ++i) sum += part[threadIdx.x + 32 * i];
+        const float norm = root(warp_sum(sum));
+        if (threadIdx.x == 0) {
+            if (norm_out != nullptr && blockIdx.x == 0) *norm_out = norm;
+            // an infinite or undefined norm scales nothing
+            factor = isfinite(norm) && norm > max_norm ? __fdiv_rn(max_norm, norm) : 1.0f;
+        }
+    }
+    __syncthreads();
+    const float f = factor;
+    if (f == 1.0f && tab.in_place) return;
     const int total = tab.first[tab.count];
     const int c0 = (int)((int64_t)total * blockIdx.x / gridDim.x), c1 = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
     int t = c0 < c1 ? tensor_of(tab, c1 - 1) : 0;
@@ -206,11 +235,13 @@ template <int CAP>
 int fill(Table<CAP> &tab, const ep_grad *g, int count) {
     int pieces = 0;
     tab.count = count;
+    tab.in_place = 1;
     for (int i = 0; i < count; ++i) {
         const int es = g[i].fp32 ? 4 : 2;
         const int64_t lead = ((uintptr_t)g[i].data & 15) / es;
         tab.src[i] = static_cast<const uint8_t *>(g[i].data);
         tab.dst[i] = static_cast<uint8_t *>(g[i].out);
+        if (g[i].out != g[i].data) tab.in_place = 0;
         tab.n[i] = g[i].fp32 ? ~g[i].numel : g[i].numel;
         tab.first[i] = pieces;
         if (g[i].numel > 0) pieces += (int)((g[i].numel + lead + kPiece / es - 1) / (kPiece / es));
@@ -240,22 +271,26 @@ int grid_of(int pieces, int sms) {
     return grid < 1 ? 1 : grid;
 }
 
-// Calls f(table, pieces, index) for the tensors in groups that a table holds.
-template <typename F>
-cudaError_t in_groups(const ep_grad *g, int count, F &&f) {
-    constexpr int kSmall = 64, kLarge = 1024;
-    if (count <= kSmall) {
-        Table<kSmall> tab;
-        const int pieces = fill(tab, g, count);
-        return f(tab, pieces, 0);
-    }
-    for (int i = 0, k = 0; i < count; i += kLarge, ++k) {
-        Table<kLarge> tab;
-        const int pieces = fill(tab, g + i, count - i < kLarge ? count - i : kLarge);
+template <int CAP, typename F>
+cudaError_t in_groups_of(const ep_grad *g, int count, F &&f) {
+    for (int i = 0, k = 0; i < count || k == 0; i += CAP, ++k) {
+        Table<CAP> tab;
+        const int pieces = fill(tab, g + i, count - i < CAP ? count - i : CAP);
         const cudaError_t e = f(tab, pieces, k);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+// Calls f(table, pieces, index) for the tensors in groups that a table holds: the smallest table that holds
+// all, because a launch copies it whole (300 tensors, in place: 28 us for the clipping that has nothing to do
+// with a table of 1024).
+template <typename F>
+cudaError_t in_groups(const ep_grad *g, int count, F &&f) {
+    if (count <= 32) return in_groups_of<32>(g, count, f);
+    if (count <= 128) return in_groups_of<128>(g, count, f);
+    if (count <= 384) return in_groups_of<384>(g, count, f);
+    return in_groups_of<1024>(g, count, f);
 }
 
 }  // namespace

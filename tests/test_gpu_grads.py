@@ -89,7 +89,7 @@ def test_clip_to_other_tensors(buf, types, offsets, limit):
     assert all(torch.equal(a, b) for a, b in zip(grads, kept))
 
 
-@pytest.mark.parametrize("count", [64, 65, 1024, 1025, 2500])
+@pytest.mark.parametrize("count", [32, 33, 128, 129, 384, 385, 1024, 1025, 2500])
 def test_many_tensors(buf, count):
     """One table, a larger one, several."""
     flat = torch.full((count * 70,), 0.0, device="cuda", dtype=B16).normal_(generator=torch.Generator("cuda").manual_seed(count))
