@@ -296,11 +296,10 @@ struct ExpertLayerParams {
     const void *residual;      // bf16 [N, H] or nullptr
     void *out;                 // bf16 [N, H]
     // workspace, set by the launcher; entries in the order of the sorted list
-    void *xs;                  // [N * K][R][H] tokens as operands of the gate product (bf16 or R = 2 codes)
     void *h;                   // [N * K][R][I] activations as operands of the down product (2 bf16 or 4 codes)
     float *sums;               // [N * K][rows of all tiles] sums of the product at hand
     float *pieces;             // [SMs][64][128] sums of the job that an SM does not begin
-    float *x_scale, *h_scale;  // [N * K] what a code is worth
+    float *h_scale;            // [N * K][I / 128] what a code is worth
     uint32_t *barrier;         // grid barrier and count of the CTAs that are done with it: both zero
                                // between launches, each launch puts them back; nullptr: none free (the
                                // workspace's then)

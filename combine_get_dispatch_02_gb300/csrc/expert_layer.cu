@@ -14,16 +14,16 @@
 // and ends in another's leaves two partial sums (fp32, in the workspace), added in
 // the order of the shares.  What needs all SMs' results is done between grid barriers
 // (cooperative launch), and the weights' loader does not wait there:
-//   entries sorted by expert (by every CTA), tokens laid out in that order
-//   -- gate product -- SwiGLU, h laid out -- down product -- sum over k
+//   entries sorted by expert (by every CTA) -- gate product -- SwiGLU, h laid out --
+//   down product -- sum over k
 //
 // Operands of e4m3 weights: a bf16 value has 8 significant bits, an e4m3 code 4, so x
-// times a power of two per token (the largest to 128 .. 256) is the sum of two codes,
+// times a power of two per 128 channels (the largest to 128 .. 256) is the sum of two codes,
 // the second worth 2^-4 of the first; exactly, down to 2^-13 of the largest, and to 2^-21
 // of that below.  h, which has more bits, is the sum of four (2^-17 of it).  They are columns
-// of the product, so nothing is converted on the weights' way.  The weights' scales vary
-// along the channels: a stage's sums leave tensor memory and are scaled and added in
-// fp32 registers.  bf16 weights: x as it is, h as the sum of two bf16 numbers.
+// of the product, so nothing is converted on the weights' way.  The scales vary along the
+// channels: a stage's sums leave tensor memory and are scaled and added in fp32
+// registers.  bf16 weights: x as it is, h as the sum of two bf16 numbers.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -39,16 +39,19 @@ namespace {
 
 using namespace umma;
 
-// Warps: 0 .. 3 read the sums out of tensor memory, 4 loads weights, 5 tokens, 6 issues the products; 0 .. 3
-// and 8 .. 11 do what lies between the products ("workers").
-constexpr int kWarpWeights = 4, kWarpTokens = 5, kWarpMma = 6;
-constexpr int kThreads = 12 * 32, kWorkers = 256;
+// Warps: 0 .. 3 read the sums out of tensor memory, 4 loads weights, 6 issues the products, 8 .. 15 bring the
+// tokens, a stage each in turn; 0 .. 3 and 8 .. 15 do what lies between the products ("workers").  Warp 7 goes through
+// the latter's code once at the start, for nothing: the weights have washed the code out of L2, and the first
+// run of 100 instructions takes 1300 cycles (one token, top-8 of 256, 7168 x 2048, FP8: _US_).
+constexpr int kWarpWeights = 4, kWarpMma = 6, kWarpSpare = 7, kWarpTokens = 8, kTokenWarps = 8;
+constexpr int kThreads = 16 * 32, kWorkers = 12 * 32;
 constexpr int kTile = 128;                   // weight rows of a job
 constexpr int kColumns = 64;                 // most columns of a job
 constexpr int kWeightBytes = kTile * 128, kStage = kWeightBytes + kColumns * 128;
 constexpr int kStages = 8, kSums = 4;        // stages of the ring, accumulators
+constexpr int kScales = 16;                  // stages whose tokens' scales are kept: the readers are up to kSums behind
+                                             // the products, which are kStages behind the loaders
 constexpr size_t kFixed = 1024 + (size_t)kStages * kStage;
-constexpr int kMaxSms = 256;
 
 // Columns of an entry (codes or numbers whose sum it is) and entries of a job.
 template <bool FP8, bool DOWN>
@@ -295,37 +298,25 @@ struct Walk {
 
 struct Maps {
     CUtensorMap w[2];  // gate and up, down: [E, rows, channels] in boxes of 64 rows x 128 bytes, swizzled
-    CUtensorMap t[2];  // x, h laid out by entry: [entries * R, channels] in boxes of 16 rows x 128 bytes
+    CUtensorMap h;     // h laid out by entry: [entries * R, channels] in boxes of 16 rows x 128 bytes
 };
 
 struct Bars {
     uint64_t full[kStages], empty[kStages], tfull[kSums], tempty[kSums];
-    uint32_t from[2][kMaxSms + 1];  // first stage of each CTA's share
-    uint32_t armed[2];              // stages loaded (weights, tokens)
+    uint32_t armed[1 + kTokenWarps];  // stages loaded (weights; by each token warp of its own)
     uint32_t failed, tmem;
-    float top[kWorkers / 32];
+    float scale[kScales][kColumns / 2];  // what a code of an entry is worth
 };
 
-// The CTA whose share stage u belongs to.  scale: CTAs per stage.
-__device__ __forceinline__ int owner_of(const uint32_t *from, int ctas, float scale, uint32_t u) {
-    int b = min((int)(__uint2float_rd(u) * scale), ctas - 1);
-    while (from[b] > u) --b;
-    while (from[b + 1] <= u) ++b;
-    return b;
-}
-
-// The largest of the workers' values.
-__device__ __forceinline__ float workers_max(float v, float *part, int worker) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    workers_sync();
-    if ((worker & 31) == 0) part[worker >> 5] = v;
-    workers_sync();
-    v = part[0];
-#pragma unroll
-    for (int i = 1; i < kWorkers / 32; ++i) v = fmaxf(v, part[i]);
-    return v;
-}
+// The stages of a product in equal shares: CTA b has those from from(b) on, the first `more` CTAs one more.
+struct Shares {
+    uint32_t each, more;
+    __device__ __forceinline__ uint32_t from(uint32_t b) const { return each * b + min(b, more); }
+    __device__ __forceinline__ int owner(uint32_t u) const {
+        const uint32_t first = more * (each + 1);
+        return (int)(u < first ? u / (each + 1) : more + (u - first) / each);
+    }
+};
 
 // The power of two that brings top to 128 .. 256 (within fp32's own), and 1 over it.
 __device__ __forceinline__ float2 scale_of(float top) {
@@ -335,30 +326,41 @@ __device__ __forceinline__ float2 scale_of(float top) {
     return make_float2(__uint_as_float((uint32_t)(127 + k) << 23), __uint_as_float((uint32_t)(127 - k) << 23));
 }
 
-// v[8] times s as the sum of R e4m3 codes, code r worth 2^(-4 r): rows of `row` bytes from dst on.  What is not
-// finite becomes NaN.
-template <int R>
-__device__ __forceinline__ void store_codes(const float (&v)[8], float s, uint8_t *dst, int64_t row) {
-    float rest[8];
+// v times s as the sum of R e4m3 codes, code r worth 2^(-4 r): four bytes at a time to store(r, j, .).  What is
+// not finite becomes NaN.
+template <int R, int N, typename F>
+__device__ __forceinline__ void codes(float (&v)[N], float s, F &&store) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rest[i] = isfinite(v[i]) ? v[i] * s : __int_as_float(0x7FC00000);
+    for (int i = 0; i < N; ++i) v[i] = isfinite(v[i]) ? v[i] * s : __int_as_float(0x7FC00000);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        uint32_t w[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const __nv_fp8x2_storage_t q = __nv_cvt_float2_to_fp8x2(make_float2(rest[i], rest[i + 1]), __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            rest[i] = (rest[i] - f.x) * 16.0f;
-            rest[i + 1] = (rest[i + 1] - f.y) * 16.0f;
-            w[i >> 2] |= (uint32_t)q << (8 * (i & 3));
+        for (int j = 0; j < N; j += 4) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int i = j; i < j + 4; i += 2) {
+                const __nv_fp8x2_storage_t q = __nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3);
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                v[i] = (v[i] - f.x) * 16.0f;
+                v[i + 1] = (v[i + 1] - f.y) * 16.0f;
+                w |= (uint32_t)q << (8 * (i - j));
+            }
+            store(r, j / 4, w);
         }
-        *reinterpret_cast<uint2 *>(dst + r * row) = make_uint2(w[0], w[1]);
     }
 }
 
-__device__ __forceinline__ float finite_or_0(float v) { return isfinite(v) ? fabsf(v) : 0.0f; }
+// The scale of a block of 128 channels, N to a lane.
+template <int N>
+__device__ __forceinline__ float2 block_scale(const float (&v)[N]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, isfinite(v[i]) ? fabsf(v[i]) : 0.0f);
+#pragma unroll
+    for (int o = 64 / N; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    return scale_of(top);
+}
 
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const ExpertLayerParams p) {
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
     const uint32_t b_full = saddr(bars.full), b_empty = saddr(bars.empty), b_tfull = saddr(bars.tfull), b_tempty = saddr(bars.tempty);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            bar_init(b_full + 8 * i, 2);  // both loaders
+            bar_init(b_full + 8 * i, 2);  // the weights' loader and a token warp
             bar_init(b_empty + 8 * i, 1);
         }
         for (int i = 0; i < kSums; ++i) {
@@ -378,12 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
             bar_init(b_tempty + 8 * i, 4);
         }
         bar_init_fence();
-        bars.failed = bars.armed[0] = bars.armed[1] = 0;
-        for (int i = 0; i < 2; ++i) {
-            prefetch_map(&maps.w[i]);
-            prefetch_map(&maps.t[i]);
-        }
+        bars.failed = 0;
+        for (int i = 0; i <= kTokenWarps; ++i) bars.armed[i] = 0;
+        prefetch_map(&maps.w[0]);
+        prefetch_map(&maps.w[1]);
+        prefetch_map(&maps.h);
     }
+    if (warp == kWarpMma) tmem_alloc_one(saddr(&bars.tmem), kSums * kColumns);
     pdl_wait();
     const Route r = route<FP8>(p, ring + kStages * kStage, reinterpret_cast<uint32_t *>(ring));
     const bool worker = warp < 4 || warp >= 8;
@@ -391,13 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
     // tiles of an expert's weights, stages of a job, rows of the tiles
     const int tiles[2] = {(p.I + kTile / 2 - 1) / (kTile / 2), (p.H + kTile - 1) / kTile};
     const int lines[2] = {(p.H + kLine<FP8> - 1) / kLine<FP8>, (p.I + kLine<FP8> - 1) / kLine<FP8>};
-    uint32_t total[2];
+    Shares shares[2];
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
-        total[d] = (uint32_t)tiles[d] * r.before[d][r.D] * lines[d];
-        for (int b = tid; b <= ctas; b += kThreads) bars.from[d][b] = (uint32_t)((uint64_t)total[d] * b / ctas);
+        const uint32_t total = (uint32_t)tiles[d] * r.before[d][r.D] * lines[d];
+        shares[d].each = total / ctas;
+        shares[d].more = total - shares[d].each * ctas;
     }
-    if (warp == kWarpMma && r.D > 0) tmem_alloc_one(saddr(&bars.tmem), kSums * kColumns);
     fence_async_shared();  // the scratch lies where the stages land
     fence_before();
     __syncthreads();
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         auto product = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
             Walk<FP8, DOWN> w;
-            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
+            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
             do {
                 if (w.e == p.withhold) ok = false;  // test hook
                 const int row0 = w.tile * (DOWN ? kTile : kTile / 2), row1 = DOWN ? row0 + kTile / 2 : p.I + row0;
@@ -448,45 +451,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         product(std::false_type{});
         product(std::true_type{});
         if (lane == 0) bars.armed[0] = n;
-    } else if (r.D > 0 && warp == kWarpTokens) {
-        uint32_t n = 0;
-        auto product = [&](auto down) {
-            constexpr bool DOWN = decltype(down)::value;
-            constexpr int R = Parts<FP8, DOWN>::R;
-            Walk<FP8, DOWN> w;
-            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
-            // x is laid out before the first meeting, h before the third
-            if (lane == 0) ok = met(DOWN ? 3 : 1);
-            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0);
-            asm volatile("fence.proxy.async;" ::: "memory");
-            __syncwarp();
-            if (!ok) return;
-            do {
-                const int boxes = (w.count * R + 15) / 16;
-                for (int l = w.l0; l < w.l1 && ok; ++l) {
-                    const uint32_t slot = n % kStages;
-                    ok = wait(b_empty + 8 * slot, (n / kStages & 1) ^ 1);
-                    if (!ok) break;
-                    ++n;
-                    if (elect()) {
-                        const uint32_t bar = b_full + 8 * slot, at = saddr(ring + slot * kStage) + kWeightBytes;
-                        bar_expect(bar, boxes * 2048);
-                        for (int i = 0; i < boxes; ++i) load_box(at + i * 2048, &maps.t[DOWN], l * kLine<FP8>, w.first * R + i * 16, bar);
-                    }
-                    __syncwarp();
-                }
-            } while (ok && w.next(r));
-        };
-        product(std::false_type{});
-        product(std::true_type{});
-        if (lane == 0) bars.armed[1] = n;
     } else if (r.D > 0 && warp == kWarpMma) {
         uint32_t n = 0, seg = 0;
         auto product = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
             constexpr int R = Parts<FP8, DOWN>::R;
             Walk<FP8, DOWN> w;
-            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
+            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
             do {
                 // fp32 accumulator, both operands bf16 or both e4m3, 128 x columns
                 const uint32_t columns = (w.count * R + 15) & ~15;
@@ -517,16 +488,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         // all products have been computed before tensor memory is given back
         for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
             if (!__all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * (i % kStages), i / kStages & 1, p.wait_cycles))) ok = false;
-    } else if (worker) {
-        uint32_t seg = 0;
-        const float scales[2] = {(float)ctas / (float)total[0], (float)ctas / (float)total[1]};
-        // Comes to the i-th meeting: what this CTA's workers wrote can be read behind it, by copies too.  Not
-        // before all have come to the one before: a CTA without a share would be counted for a slow one.
+    } else if (worker || (r.D > 0 && warp == kWarpSpare)) {
+        const bool spare = warp == kWarpSpare;
+        uint32_t seg = 0, stages = 0, brought = 0;  // accumulators read; stages gone by and brought (token warps)
+        // Comes to the i-th meeting: what this CTA's workers wrote can be read behind it.  Not before all have
+        // come to the one before (to the third: behind the second this CTA does not wait): a CTA without a share
+        // would be counted for a slow one.
         auto come = [&](uint32_t i) {
-            asm volatile("fence.proxy.async;" ::: "memory");
             workers_sync();
             if (wid == 0) {
-                if (i > 1 && !met(i - 1)) ok = false;
+                if (i == 3 && !met(2)) ok = false;
                 __threadfence();
                 atomicAdd(p.barrier, 1u);
             }
@@ -559,17 +530,112 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         };
         auto pieces = [&](int down, const Where &w, int tile) {
             const uint32_t u = ((uint32_t)r.before[down][w.d] * tiles[down] + tile * w.parts + w.part) * lines[down];
-            const int first = owner_of(bars.from[down], ctas, scales[down], u);
-            int last = first;
-            while (bars.from[down][last + 1] < u + lines[down]) ++last;
-            return make_int2(first, last);
+            return make_int2(shares[down].owner(u), shares[down].owner(u + lines[down] - 1));
+        };
+        // Tokens of every fourth stage, rows of 128 bytes, swizzled as the weights are.  Gate: x, by this warp; down:
+        // h, by tensor map, once all have laid theirs out.
+        auto bring = [&](auto down) {
+            constexpr bool DOWN = decltype(down)::value;
+            constexpr int R = Parts<FP8, DOWN>::R;
+            Walk<FP8, DOWN> w;
+            if (!w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
+            if constexpr (DOWN) {
+                if (lane == 0 && !met(2)) ok = false;
+                asm volatile("fence.proxy.async;" ::: "memory");
+                ok = __all_sync(0xFFFFFFFFu, ok);
+            }
+            do {
+                for (int l = w.l0; l < w.l1; ++l, ++stages) {
+                    if (stages % kTokenWarps != warp - kWarpTokens) continue;
+                    const uint32_t slot = stages % kStages, bar = b_full + 8 * slot, at = saddr(ring + slot * kStage) + kWeightBytes;
+                    if constexpr (DOWN) {
+                        float s = 0.0f;
+                        if (FP8 && lane < w.count) s = __ldcg(p.h_scale + (int64_t)(w.first + lane) * lines[1] + l);
+                        ok = wait(b_empty + 8 * slot, (stages / kStages & 1) ^ 1);
+                        if (!ok) return;
+                        if (elect()) {
+                            // expected now, arrived for below
+                            const int boxes = (w.count * R + 15) / 16;
+                            asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(boxes * 2048) : "memory");
+                            for (int i = 0; i < boxes; ++i) load_box(at + i * 2048, &maps.h, l * kLine<FP8>, w.first * R + i * 16, bar);
+                        }
+                        __syncwarp();
+                        if (FP8 && lane < w.count) bars.scale[stages % kScales][lane] = s;
+                    } else if constexpr (FP8) {
+                        // four entries at a time, 16 channels to a lane
+                        struct Two {
+                            uint4 a, b;
+                        };
+                        auto get = [&](int i) {
+                            const uint4 *src = reinterpret_cast<const uint4 *>(
+                                static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)(r.list[w.first + min(i, w.count - 1)] >> 5) * p.H + l * 128 +
+                                (lane & 7) * 16);
+                            return Two{__ldg(src), __ldg(src + 1)};
+                        };
+                        Two next = get(lane >> 3);
+                        ok = wait(b_empty + 8 * slot, (stages / kStages & 1) ^ 1);
+                        if (!ok) return;
+                        for (int i0 = 0; i0 < w.count; i0 += 4) {
+                            const Two q = next;
+                            const int i = i0 + (lane >> 3);
+                            if (i0 + 4 < w.count) next = get(i + 4);
+                            const uint32_t q8[8] = {q.a.x, q.a.y, q.a.z, q.a.w, q.b.x, q.b.y, q.b.z, q.b.w};
+                            float v[16];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[2 * k] = bf16_lo(q8[k]), v[2 * k + 1] = bf16_hi(q8[k]);
+                            const float2 s = block_scale(v);
+                            uint32_t c[2][4];
+                            codes<2>(v, s.x, [&](int k, int j, uint32_t x) { c[k][j] = x; });
+                            if (i < w.count) {
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const int row = i * 2 + k;
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + row * 128 + (((lane & 7) ^ (row & 7)) << 4)),
+                                                 "r"(c[k][0]), "r"(c[k][1]), "r"(c[k][2]), "r"(c[k][3])
+                                                 : "memory");
+                                }
+                                if ((lane & 7) == 0) bars.scale[stages % kScales][i] = s.y;
+                            }
+                        }
+                    } else {
+                        // four entries at a time, 8 channels to a lane; past the last channel zeros (the weights are
+                        // zeros there, but times what was in the ring that may be NaN)
+                        const int c = l * 64 + (lane & 7) * 8;
+                        auto get = [&](int i) {
+                            uint4 q = make_uint4(0, 0, 0, 0);
+                            if (i < w.count && c < p.H)
+                                q = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) +
+                                                                          (int64_t)(r.list[w.first + i] >> 5) * p.H + c));
+                            return q;
+                        };
+                        uint4 next = get(lane >> 3);
+                        ok = wait(b_empty + 8 * slot, (stages / kStages & 1) ^ 1);
+                        if (!ok) return;
+                        for (int i = lane >> 3; i < ((w.count + 3) & ~3); i += 4) {
+                            const uint4 q = next;
+                            if (i + 4 < w.count) next = get(i + 4);
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 128 + (((lane & 7) ^ (i & 7)) << 4)),
+                                         "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                                         : "memory");
+                        }
+                    }
+                    if constexpr (!DOWN) fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar);
+                    ++brought;
+                }
+            } while (w.next(r));
         };
         // Sums out of tensor memory: lane = weight row.
         auto product = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
             constexpr int R = Parts<FP8, DOWN>::R, TOKENS = Parts<FP8, DOWN>::TOKENS;
+            if (warp >= kWarpTokens) {
+                if (ok) bring(down);
+                return;
+            }
             Walk<FP8, DOWN> w;
-            if (warp >= 4 || !w.start(r, tiles[DOWN], lines[DOWN], bars.from[DOWN][cta], bars.from[DOWN][cta + 1])) return;
+            if (!w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
             const uint32_t lanes = bars.tmem + ((uint32_t)(warp * 32) << 16);
             const int kb = lines[DOWN], nb = ((DOWN ? p.H : 2 * p.I) + 127) / 128;
             do {
@@ -612,7 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                     for (int l = w.l0; l < w.l1; ++l) {
                         if ((l - w.l0 & 31) == 0) ws = l + lane < w.l1 ? __ldg(sc + l + lane) : 0.0f;
                         const float f = __shfl_sync(0xFFFFFFFFu, ws, l - w.l0 & 31);
-                        columns_of(seg % kSums, [&](int i, float s) { acc[i] = fmaf(s, f, acc[i]); });
+                        const float *xs = bars.scale[seg % kScales];  // a stage an accumulator
+                        columns_of(seg % kSums, [&](int i, float s) { acc[i] = fmaf(s, f * xs[i], acc[i]); });
                     }
 #pragma unroll
                     for (int i = 0; i < TOKENS; ++i)
@@ -624,170 +691,186 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 }
             } while (w.next(r));
         };
-        // x of every entry, in the order of the list
         if (r.D > 0) {
             const int entries = r.first[p.E];
-            for (int i = cta; i < entries; i += ctas) {
-                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)(r.list[i] >> 5) * p.H;
-                if constexpr (!FP8) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.xs) + (int64_t)i * p.H);
-                    for (int c = wid; c < p.H / 8; c += kWorkers) dst[c] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                } else {
-                    auto get = [&](float (&v)[8], int c) {
-                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[2 * k] = bf16_lo(w[k]), v[2 * k + 1] = bf16_hi(w[k]);
-                    };
-                    float v[8], top = 0.0f;
-                    for (int c = wid; c < p.H / 8; c += kWorkers) {
-                        get(v, c);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) top = fmaxf(top, finite_or_0(v[k]));
-                    }
-                    const float2 s = scale_of(workers_max(top, bars.top, wid));
-                    for (int c = wid; c < p.H / 8; c += kWorkers) {
-                        get(v, c);
-                        store_codes<2>(v, s.x, static_cast<uint8_t *>(p.xs) + (int64_t)i * 2 * p.H + c * 8, p.H);
-                    }
-                    if (wid == 0) p.x_scale[i] = s.y;
-                }
-            }
-            come(1);
-            product(std::false_type{});
-            meet(2);
-            // h of every entry
-            const int rows = tiles[0] * kTile;
-            for (int i = cta; i < entries; i += ctas) {
+            // h: a warp takes 128 channels of an entry, 4 to a lane.  What does not hang on the sums is looked up before
+            // they are there (the first item's; few tokens have no more).
+            const int rows = tiles[0] * kTile, blocks = (p.I + 127) / 128, warps = ctas * (kWorkers / 32);
+            struct Item {
+                const float *own, *piece;  // sums: of the CTA where the job begins, of the first one behind it
+                int others;                // CTAs behind it
+                uint2 gate, up;            // biases
+            };
+            auto look = [&](int it) {
+                Item q = {nullptr, nullptr, 0, make_uint2(0, 0), make_uint2(0, 0)};
+                const int i = it / blocks, c = (it - i * blocks) * 128 + lane * 4;
+                if (it >= entries * blocks || c >= p.I) return q;
                 const Where w = where(0, i);
-                const int e = r.live[w.d];
-                const float xs = FP8 ? __ldcg(p.x_scale + i) : 1.0f;
-                auto get = [&](float (&h)[8], int c) {
-                    const int tile = c / 8, at = tile * kTile + (c & 7) * 8;  // 8 channels: c
-                    const int2 who = pieces(0, w, tile);
-                    float g[8], u[8];
-                    auto add = [&](const float *src, bool set) {
+                const int tile = c / (kTile / 2), at = c % (kTile / 2);
+                const int2 who = pieces(0, w, tile);
+                q.own = p.sums + (int64_t)i * rows + tile * kTile + at;
+                q.piece = p.pieces + ((int64_t)(who.x + 1) * kColumns + w.at) * kTile + at;
+                q.others = who.y - who.x;
+                if (p.b_gate_up != nullptr) {
+                    const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.b_gate_up) + (int64_t)r.live[w.d] * 2 * p.I + c;
+                    q.gate = __ldg(reinterpret_cast<const uint2 *>(b));
+                    q.up = __ldg(reinterpret_cast<const uint2 *>(b + p.I));
+                }
+                return q;
+            };
+            const int it0 = spare ? 0 : cta * (kWorkers / 32) + (wid >> 5);
+            if (!spare) product(std::false_type{});
+            Item item = look(it0);
+            if (!spare) meet(1);
+            for (int it = it0; it < entries * blocks; it += warps) {
+                if (it != it0) item = look(it);
+                const int i = it / blocks, c = (it - i * blocks) * 128 + lane * 4;
+                float h[4] = {};
+                if (c < p.I) {
+                    float4 g = __ldcg(reinterpret_cast<const float4 *>(item.own));
+                    float4 u = __ldcg(reinterpret_cast<const float4 *>(item.own + kTile / 2));
+                    for (int b0 = 0; b0 < item.others; b0 += 4) {
+                        float4 x[4], y[4];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float4 a = __ldcg(reinterpret_cast<const float4 *>(src) + k);
-                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(src + kTile / 2) + k);
-                            const float x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                g[4 * k + m] = set ? x[m] : g[4 * k + m] + x[m];
-                                u[4 * k + m] = set ? y[m] : u[4 * k + m] + y[m];
-                            }
+                        for (int b = 0; b < 4; ++b) {
+                            const float *q = item.piece + (int64_t)min(b0 + b, item.others - 1) * kColumns * kTile;
+                            x[b] = __ldcg(reinterpret_cast<const float4 *>(q));
+                            y[b] = __ldcg(reinterpret_cast<const float4 *>(q + kTile / 2));
                         }
-                    };
-                    add(p.sums + (int64_t)i * rows + at, true);
-                    for (int b = who.x + 1; b <= who.y; ++b)
-                        if (bars.from[0][b] < bars.from[0][b + 1])  // a CTA without a share left nothing
-                            add(p.pieces + ((int64_t)b * kColumns + w.at) * kTile + (c & 7) * 8, false);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float gate = g[k] * xs, up = u[k] * xs;
-                        if (p.b_gate_up != nullptr) {
-                            const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.b_gate_up) + (int64_t)e * 2 * p.I + c * 8 + k;
-                            gate += __bfloat162float(b[0]);
-                            up += __bfloat162float(b[p.I]);
+                        for (int b = 0; b < 4; ++b) {
+                            if (b0 + b >= item.others) break;
+                            g = make_float4(g.x + x[b].x, g.y + x[b].y, g.z + x[b].z, g.w + x[b].w);
+                            u = make_float4(u.x + y[b].x, u.y + y[b].y, u.z + y[b].z, u.w + y[b].w);
                         }
-                        h[k] = silu(gate) * up;
                     }
-                };
-                float h[8];
-                if constexpr (!FP8) {
-                    for (int c = wid; c < p.I / 8; c += kWorkers) {
-                        get(h, c);
-                        // the sum of two bf16 numbers, 2^-17 of the value off at most: rounded to one, h alone would
-                        // put as much error into the result as its own rounding
-                        uint32_t hi[4], lo[4];
+                    const float g4[4] = {g.x + bf16_lo(item.gate.x), g.y + bf16_hi(item.gate.x), g.z + bf16_lo(item.gate.y),
+                                         g.w + bf16_hi(item.gate.y)};
+                    const float u4[4] = {u.x + bf16_lo(item.up.x), u.y + bf16_hi(item.up.x), u.z + bf16_lo(item.up.y),
+                                         u.w + bf16_hi(item.up.y)};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 a = __floats2bfloat162_rn(h[2 * k], h[2 * k + 1]);
-                            const float2 f = __bfloat1622float2(a);
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(isfinite(f.x) ? h[2 * k] - f.x : 0.0f,
-                                                                           isfinite(f.y) ? h[2 * k + 1] - f.y : 0.0f);
-                            hi[k] = *reinterpret_cast<const uint32_t *>(&a);
-                            lo[k] = *reinterpret_cast<const uint32_t *>(&b);
-                        }
-                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.h) + (int64_t)i * 2 * p.I + c * 8;
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(dst + p.I) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                } else {
-                    float top = 0.0f;
-                    for (int c = wid; c < p.I / 8; c += kWorkers) {
-                        get(h, c);
+                    for (int k = 0; k < 4; ++k) h[k] = silu(g4[k]) * u4[k];
+                }
+                if (spare) {
+                    asm volatile("" ::"f"(h[0]), "f"(h[1]), "f"(h[2]), "f"(h[3]));
+                    break;
+                }
+                if constexpr (FP8) {
+                    const float2 s = block_scale(h);
+                    uint8_t *const dst = static_cast<uint8_t *>(p.h) + (int64_t)i * 4 * p.I + c;
+                    codes<4>(h, s.x, [&](int q, int, uint32_t w) { *reinterpret_cast<uint32_t *>(dst + (int64_t)q * p.I) = w; });
+                    if (lane == 0) p.h_scale[it] = s.y;
+                } else if (c < p.I) {
+                    // the sum of two bf16 numbers, 2^-17 of the value off at most: rounded to one, h alone would put
+                    // as much error into the result as its own rounding
+                    uint32_t hi[2], lo[2];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) top = fmaxf(top, finite_or_0(h[k]));
+                    for (int k = 0; k < 2; ++k) {
+                        const __nv_bfloat162 a = __floats2bfloat162_rn(h[2 * k], h[2 * k + 1]);
+                        const float2 f = __bfloat1622float2(a);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(isfinite(f.x) ? h[2 * k] - f.x : 0.0f,
+                                                                       isfinite(f.y) ? h[2 * k + 1] - f.y : 0.0f);
+                        hi[k] = *reinterpret_cast<const uint32_t *>(&a);
+                        lo[k] = *reinterpret_cast<const uint32_t *>(&b);
                     }
-                    const float2 s = scale_of(workers_max(top, bars.top, wid));
-                    for (int c = wid; c < p.I / 8; c += kWorkers) {
-                        if (p.I > kWorkers * 8) get(h, c);  // else it is still there
-                        store_codes<4>(h, s.x, static_cast<uint8_t *>(p.h) + (int64_t)i * 4 * p.I + c * 8, p.I);
-                    }
-                    if (wid == 0) p.h_scale[i] = s.y;
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.h) + (int64_t)i * 2 * p.I + c;
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(dst + p.I) = make_uint2(lo[0], lo[1]);
                 }
             }
-            come(3);
-            product(std::true_type{});
-            meet(4);
+            if (!spare) {
+                asm volatile("fence.proxy.async;" ::: "memory");  // h is read by copies
+                come(2);
+                product(std::true_type{});
+            }
         }
-        // out: a warp takes a token and the 128 channels of a tile, lane k looks entry k up
-        for (int it = cta * (kWorkers / 32) + (wid >> 5); it < p.N * tiles[1]; it += ctas * (kWorkers / 32)) {
+        // out: a warp takes a token and the 128 channels of a tile; lane k looks entry k up, again before the sums
+        // are there
+        struct Item {
+            int spot, at, e, b0, others;  // entry (-1: none), place in its job's tokens, expert, CTAs that have sums
+            float weight;
+            uint2 residual;               // of the lane's channels
+        };
+        auto look = [&](int it) {
+            Item q = {-1, 0, 0, 0, 0, 0.0f, make_uint2(0, 0)};
+            if (it >= p.N * tiles[1]) return q;
             const int t = it / tiles[1], tile = it - t * tiles[1], c = tile * kTile + lane * 4;
-            int spot = -1, at = 0, e = 0;
-            int2 who = make_int2(0, 0);
-            float weight = 0.0f, hs = 1.0f;
-            if (lane < p.K) {
-                const uint32_t v = r.spot[t * p.K + lane];
-                if (v != 0xFFFFu) {
-                    spot = (int)v;
-                    const Where w = where(1, spot);
-                    at = w.at;
-                    e = r.live[w.d];
-                    who = pieces(1, w, tile);
-                    weight = p.wts != nullptr ? __ldg(p.wts + t * p.K + lane) : 1.0f;
-                    if (FP8) hs = __ldcg(p.h_scale + spot);
-                }
-            }
+            if (p.residual != nullptr && c < p.H)
+                q.residual = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.residual) + (int64_t)t * p.H + c);
+            const uint32_t v = lane < p.K ? r.spot[t * p.K + lane] : 0xFFFFu;
+            if (v == 0xFFFFu) return q;
+            q.weight = p.wts != nullptr ? __ldg(p.wts + t * p.K + lane) : 1.0f;
+            const Where w = where(1, (int)v);
+            const int2 who = pieces(1, w, tile);
+            q.spot = (int)v;
+            q.at = w.at;
+            q.e = r.live[w.d];
+            q.b0 = who.x;
+            q.others = who.y - who.x;
+            return q;
+        };
+        const int it0 = spare ? 0 : cta * (kWorkers / 32) + (wid >> 5);
+        Item item = look(it0);
+        if (r.D > 0 && !spare) meet(3);
+        for (int it = it0; it < p.N * tiles[1]; it += ctas * (kWorkers / 32)) {
+            if (it != it0) item = look(it);
+            const int t = it / tiles[1], c = (it - t * tiles[1]) * kTile + lane * 4;
+            const bool in = c < p.H;
             float v[4] = {};
-            for (int k = 0; k < p.K; ++k) {
-                const int s = __shfl_sync(0xFFFFFFFFu, spot, k);
-                const int a = __shfl_sync(0xFFFFFFFFu, at, k), ex = __shfl_sync(0xFFFFFFFFu, e, k);
-                const int b0 = __shfl_sync(0xFFFFFFFFu, who.x, k), b1 = __shfl_sync(0xFFFFFFFFu, who.y, k);
-                const float w = __shfl_sync(0xFFFFFFFFu, weight, k), f = __shfl_sync(0xFFFFFFFFu, hs, k);
-                if (s < 0 || c >= p.H) continue;
-                float4 y = __ldcg(reinterpret_cast<const float4 *>(p.sums + (int64_t)s * (tiles[1] * kTile) + c));
-                for (int b = b0 + 1; b <= b1; ++b) {
-                    if (bars.from[1][b] == bars.from[1][b + 1]) continue;  // a CTA without a share left nothing
-                    const float4 q = __ldcg(reinterpret_cast<const float4 *>(p.pieces + ((int64_t)b * kColumns + a) * kTile + lane * 4));
-                    y = make_float4(y.x + q.x, y.y + q.y, y.z + q.z, y.w + q.w);
-                }
-                float z[4] = {y.x * f, y.y * f, y.z * f, y.w * f};
-                if (p.b_down != nullptr) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.b_down) + (int64_t)ex * p.H + c);
-                    z[0] += bf16_lo(q.x);
-                    z[1] += bf16_hi(q.x);
-                    z[2] += bf16_lo(q.y);
-                    z[3] += bf16_hi(q.y);
+            constexpr int U = 4;  // entries whose loads are in flight together
+            for (int k0 = 0; k0 < p.K; k0 += U) {
+                float4 y[U], z[U];
+                uint2 bias[U];
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int k = k0 + j, s = __shfl_sync(0xFFFFFFFFu, item.spot, k), e = __shfl_sync(0xFFFFFFFFu, item.e, k);
+                    const int b0 = __shfl_sync(0xFFFFFFFFu, item.b0, k), at = __shfl_sync(0xFFFFFFFFu, item.at, k);
+                    const int others = __shfl_sync(0xFFFFFFFFu, item.others, k);
+                    const bool there = k < p.K && s >= 0 && in;
+                    y[j] = z[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    bias[j] = make_uint2(0, 0);
+                    if (there) y[j] = __ldcg(reinterpret_cast<const float4 *>(p.sums + (int64_t)s * (tiles[1] * kTile) + c));
+                    const float *piece = p.pieces + ((int64_t)(b0 + 1) * kColumns + at) * kTile + lane * 4;
+                    if (there && others > 0) z[j] = __ldcg(reinterpret_cast<const float4 *>(piece));
+                    if (there && p.b_down != nullptr)
+                        bias[j] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.b_down) + (int64_t)e * p.H + c));
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = fmaf(w, z[i], v[i]);
+                for (int j = 0; j < U; ++j) {
+                    const int k = k0 + j, s = __shfl_sync(0xFFFFFFFFu, item.spot, k), at = __shfl_sync(0xFFFFFFFFu, item.at, k);
+                    const int b0 = __shfl_sync(0xFFFFFFFFu, item.b0, k), others = __shfl_sync(0xFFFFFFFFu, item.others, k);
+                    const float w = __shfl_sync(0xFFFFFFFFu, item.weight, k);
+                    if (k >= p.K || s < 0) continue;
+                    y[j] = make_float4(y[j].x + z[j].x, y[j].y + z[j].y, y[j].z + z[j].z, y[j].w + z[j].w);
+                    for (int b = 2; b <= others; b += 4) {
+                        float4 q[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            q[i] = __ldcg(reinterpret_cast<const float4 *>(p.pieces +
+                                                                           ((int64_t)(b0 + min(b + i, others)) * kColumns + at) * kTile + lane * 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (b + i > others) break;
+                            y[j] = make_float4(y[j].x + q[i].x, y[j].y + q[i].y, y[j].z + q[i].z, y[j].w + q[i].w);
+                        }
+                    }
+                    v[0] = fmaf(w, y[j].x + bf16_lo(bias[j].x), v[0]);
+                    v[1] = fmaf(w, y[j].y + bf16_hi(bias[j].x), v[1]);
+                    v[2] = fmaf(w, y[j].z + bf16_lo(bias[j].y), v[2]);
+                    v[3] = fmaf(w, y[j].w + bf16_hi(bias[j].y), v[3]);
+                }
             }
-            if (c >= p.H) continue;
-            const int64_t o = (int64_t)t * p.H + c;
-            if (p.residual != nullptr) {
-                const uint2 q = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.residual) + o);
-                v[0] += bf16_lo(q.x);
-                v[1] += bf16_hi(q.x);
-                v[2] += bf16_lo(q.y);
-                v[3] += bf16_hi(q.y);
+            if (spare) {
+                asm volatile("" ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+                break;
             }
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + o) =
+            if (!in) continue;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0] + bf16_lo(item.residual.x), v[1] + bf16_hi(item.residual.x));
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(v[2] + bf16_lo(item.residual.y), v[3] + bf16_hi(item.residual.y));
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + (int64_t)t * p.H + c) =
                 make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
         }
+        if (warp >= kWarpTokens && lane == 0) bars.armed[1 + warp - kWarpTokens] = brought;
     }
     if (!ok) {
         bars.failed = 1;
@@ -796,16 +879,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
     fence_before();
     __syncthreads();
     fence_after();
-    if (r.D == 0) return;
     if (warp == kWarpMma) tmem_free_one(bars.tmem, kSums * kColumns);
+    if (r.D == 0) return;
     if (tid == 0) {
         if (bars.failed) {
-            // loads in flight land before the shared memory is given up: where only one loader came, the
-            // other's arrival is made up for
-            const uint32_t n0 = min(bars.armed[0], bars.armed[1]), n1 = max(bars.armed[0], bars.armed[1]);
-            for (uint32_t n = n0; n < n1; ++n) bar_arrive(b_full + 8 * (n % kStages));
-            for (uint32_t n = n1 > kStages ? n1 - kStages : 0; n < n1; ++n)
+            // loads in flight land before the shared memory is given up: where only one side came, the other's
+            // arrival is made up for
+            uint32_t last = bars.armed[0];
+            for (int i = 0; i < kTokenWarps; ++i)
+                if (bars.armed[1 + i] > 0) last = max(last, (bars.armed[1 + i] - 1) * kTokenWarps + i + 1);
+            for (uint32_t n = last > kStages ? last - kStages : 0; n < last; ++n) {
+                const bool weights = n < bars.armed[0], tokens = n / kTokenWarps < bars.armed[1 + n % kTokenWarps];
+                if (!weights && !tokens) continue;
+                if (weights != tokens) bar_arrive(b_full + 8 * (n % kStages));
                 if (!bar_wait(b_full + 8 * (n % kStages), n / kStages & 1, p.wait_cycles)) atomicOr(p.status, kStatusInFlight);
+            }
         }
         // the last CTA puts the barrier back: all arrivals are in, on a failure too
         if (atomicAdd(p.barrier + 1, 1u) == gridDim.x - 1) {
@@ -850,12 +938,10 @@ size_t lay_out(ExpertLayerParams &p, uint8_t *base) {
         return q;
     };
     const size_t gate = (size_t)((p.I + kTile / 2 - 1) / (kTile / 2)) * kTile, down = (size_t)((p.H + kTile - 1) / kTile) * kTile;
-    p.xs = take(M * p.H * 2);
     p.h = take(M * p.I * 4);
     p.sums = reinterpret_cast<float *>(take(M * (gate > down ? gate : down) * 4));
     p.pieces = reinterpret_cast<float *>(take((size_t)p.sms * kColumns * kTile * 4));
-    p.x_scale = reinterpret_cast<float *>(take(M * 4));
-    p.h_scale = reinterpret_cast<float *>(take(M * 4));
+    p.h_scale = reinterpret_cast<float *>(take(M * ((p.I + 127) / 128) * 4));
     uint32_t *const barrier = reinterpret_cast<uint32_t *>(take(8));
     if (p.barrier == nullptr) p.barrier = barrier;
     return at;
@@ -872,7 +958,6 @@ size_t expert_layer_workspace(ExpertLayerParams p) { return lay_out(p, nullptr);
 
 cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream_t stream) {
     const bool fp8 = p.s_gate_up != nullptr, own = p.barrier != nullptr;
-    if (p.sms > kMaxSms) p.sms = kMaxSms;
     lay_out(p, static_cast<uint8_t *>(workspace));
     if (!own) {
         // no counter of the context's left: the workspace's, cleared by a call of its own
@@ -884,7 +969,7 @@ cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream
     Maps maps;
     if (!encode_rows(&maps.w[0], p.w_gate_up, es, p.H, 2 * (int64_t)p.I, p.E, kTile / 2) ||
         !encode_rows(&maps.w[1], p.w_down, es, p.I, p.H, p.E, kTile / 2) ||
-        !encode_rows(&maps.t[0], p.xs, es, p.H, M * (fp8 ? 2 : 1), 0, 16) || !encode_rows(&maps.t[1], p.h, es, p.I, M * (fp8 ? 4 : 2), 0, 16))
+        !encode_rows(&maps.h, p.h, es, p.I, M * (fp8 ? 4 : 2), 0, 16))
         return cudaErrorInvalidValue;
     return fp8 ? launch<true>(maps, p, stream) : launch<false>(maps, p, stream);
 }
