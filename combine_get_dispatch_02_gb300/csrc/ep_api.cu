@@ -1757,7 +1757,7 @@ ep_status ep_expert_layer(ep_ctx *ctx, const void *d_x, const int64_t *d_topk_id
     p.b_down = d_b_down;
     p.residual = d_residual;
     p.out = d_out;
-    p.barrier = counter_pair(ctx->layer_counters, ctx->d_layer_counters, (cudaStream_t)stream);
+    if (!ep::expert_layer_small(p)) p.barrier = counter_pair(ctx->layer_counters, ctx->d_layer_counters, (cudaStream_t)stream);
     const cudaError_t e = ep::launch_expert_layer(p, d_workspace, (cudaStream_t)stream);
     if (e != cudaSuccess) {
         cudaGetLastError();

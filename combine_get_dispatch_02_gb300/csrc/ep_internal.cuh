@@ -295,11 +295,12 @@ struct ExpertLayerParams {
     const void *b_down;        // bf16 [E, H] or nullptr
     const void *residual;      // bf16 [N, H] or nullptr
     void *out;                 // bf16 [N, H]
-    // workspace, set by the launcher; entries in the order of the sorted list
+    // workspace, set by the launcher; entries in the order of the sorted list (small form: as they come)
     void *h;                   // [N * K][R][I] activations as operands of the down product (2 bf16 or 4 codes)
-    float *sums;               // [N * K][rows of all tiles] sums of the product at hand
+    float *sums;               // [N * K][rows of all tiles] sums of the product at hand (small form: [N * K, H] outputs)
     float *pieces;             // [SMs][64][128] sums of the job that an SM does not begin
     float *h_scale;            // [N * K][I / 128] what a code is worth
+    uint32_t *done;            // small form: [ceil(H / 32)] units of each tile of output rows that are done
     uint32_t *barrier;         // grid barrier and count of the CTAs that are done with it: both zero
                                // between launches, each launch puts them back; nullptr: none free (the
                                // workspace's then)
@@ -311,8 +312,12 @@ struct ExpertLayerParams {
 };
 // One-time set-up with the device current (shared memory limits).
 void expert_layer_init();
+// The form that expert_layer_small chooses; the workspace does for both.
 size_t expert_layer_workspace(ExpertLayerParams p);
 cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream_t stream);
+bool expert_layer_small(const ExpertLayerParams &p);
+size_t expert_layer_small_workspace(const ExpertLayerParams &p);
+cudaError_t launch_expert_layer_small(ExpertLayerParams p, void *workspace, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device helpers
 #ifdef __CUDACC__

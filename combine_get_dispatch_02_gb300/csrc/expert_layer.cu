@@ -17,6 +17,12 @@
 //   entries sorted by expert (by every CTA) -- gate product -- SwiGLU, h laid out --
 //   down product -- sum over k
 //
+// Measured (one GB300), bytes of the named experts' weights over the time: 128 tokens, top-8 of 256, 7168 x 2048,
+// FP8 1.81 ms, 6.1 TB/s; 32 tokens, top-6 of 64, 4096 x 1024, bf16 252 us, 6.0 TB/s; one token, top-8 of 256, 7168 x
+// 2048, FP8 74 us, 4.8 TB/s: HBM bounds the products, which leave 10 us before the first stage, at the meetings (2
+// us each, of which the ring covers 3 together) and behind the last.  Products on mma.sync with the codes
+// converted on the way took 92 us and 2.4 ms there.
+//
 // Operands of e4m3 weights: a bf16 value has 8 significant bits, an e4m3 code 4, so x
 // times a power of two per 128 channels (the largest to 128 .. 256) is the sum of two codes,
 // the second worth 2^-4 of the first; exactly, down to 2^-13 of the largest, and to 2^-21
@@ -42,7 +48,8 @@ using namespace umma;
 // Warps: 0 .. 3 read the sums out of tensor memory, 4 loads weights, 6 issues the products, 8 .. 15 bring the
 // tokens, a stage each in turn; 0 .. 3 and 8 .. 15 do what lies between the products ("workers").  Warp 7 goes through
 // the latter's code once at the start, for nothing: the weights have washed the code out of L2, and the first
-// run of 100 instructions takes 1300 cycles (one token, top-8 of 256, 7168 x 2048, FP8: _US_).
+// run of 100 instructions takes 1300 cycles (one token, top-8 of 256, 7168 x 2048, FP8: 82 instead
+// of 76 us).
 constexpr int kWarpWeights = 4, kWarpMma = 6, kWarpSpare = 7, kWarpTokens = 8, kTokenWarps = 8;
 constexpr int kThreads = 16 * 32, kWorkers = 12 * 32;
 constexpr int kTile = 128;                   // weight rows of a job
@@ -236,33 +243,36 @@ __device__ __forceinline__ Route route(const ExpertLayerParams &p, uint8_t *at, 
     return r;
 }
 
-// The jobs of a product, in the order expert, tile of weight rows, tokens, and a CTA's share of their stages:
-// pieces of jobs, stages l0 .. l1 - 1 of each.
-template <bool FP8, bool DOWN>
+// The jobs of a product (0: gate, 1: down), in the order expert, tile of weight rows, tokens, and a CTA's share of
+// their stages: pieces of jobs, stages l0 .. l1 - 1 of each.  (One code for both products: the second time it is
+// there, see kWarpSpare.)
+template <bool FP8>
 struct Walk {
-    static constexpr int TOKENS = Parts<FP8, DOWN>::TOKENS;
+    const uint16_t *before;
+    int tokens;                        // most of a job
     int tiles, lines, d, part, parts;  // tiles of an expert, stages of a job, live expert, its tokens' part and parts
     int e, tile, first, count;         // the job: expert, tile, its tokens' places in the list
     int l0, l1;
     uint32_t left;                     // stages of the share from this piece on
     __device__ __forceinline__ void expert(const Route &r) {
         e = r.live[d];
-        parts = r.before[DOWN][d + 1] - r.before[DOWN][d];
+        parts = before[d + 1] - before[d];
     }
-    __device__ __forceinline__ void tokens(const Route &r) {
-        first = r.first[e] + part * TOKENS;
-        count = min(TOKENS, r.first[e + 1] - first);
+    __device__ __forceinline__ void job(const Route &r) {
+        first = r.first[e] + part * tokens;
+        count = min(tokens, r.first[e + 1] - first);
         l1 = min(lines, l0 + (int)min(left, 0x7FFFFFFFu));
     }
     // To the first piece of the stages from .. to - 1; false: there are none.
-    __device__ __forceinline__ bool start(const Route &r, int tiles_, int lines_, uint32_t from, uint32_t to) {
+    __device__ __forceinline__ bool start(const Route &r, int down, int tiles_, int lines_, uint32_t from, uint32_t to) {
         if (from == to) return false;
+        before = down ? r.before[1] : r.before[0];
+        tokens = down ? Parts<FP8, true>::TOKENS : Parts<FP8, false>::TOKENS;
         tiles = tiles_;
         lines = lines_;
         left = to - from;
         const uint32_t q = from / lines;
         l0 = (int)(from - q * lines);
-        const uint16_t *before = r.before[DOWN];
         int lo = 0, hi = r.D - 1;  // the last d with before[d] * tiles <= q
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -276,7 +286,7 @@ struct Walk {
         const uint32_t rest = q - (uint32_t)before[lo] * tiles;
         tile = (int)(rest / parts);
         part = (int)(rest - tile * parts);
-        tokens(r);
+        job(r);
         return true;
     }
     __device__ __forceinline__ bool next(const Route &r) {
@@ -291,7 +301,7 @@ struct Walk {
                 expert(r);
             }
         }
-        tokens(r);
+        job(r);
         return true;
     }
 };
@@ -424,15 +434,22 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         return false;
     };
 
+    // this CTA's share of a product
+    auto begin = [&](Walk<FP8> &w, int down) {
+        return w.start(r, down, down ? tiles[1] : tiles[0], down ? lines[1] : lines[0], (down ? shares[1] : shares[0]).from(cta),
+                       (down ? shares[1] : shares[0]).from(cta + 1));
+    };
+
     if (r.D > 0 && warp == kWarpWeights) {
         uint32_t n = 0;
-        auto product = [&](auto down) {
-            constexpr bool DOWN = decltype(down)::value;
-            Walk<FP8, DOWN> w;
-            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
+#pragma unroll 1
+        for (int down = 0; down < 2; ++down) {
+            Walk<FP8> w;
+            if (!ok || !begin(w, down)) continue;
+            const CUtensorMap *const map = &maps.w[down];
             do {
                 if (w.e == p.withhold) ok = false;  // test hook
-                const int row0 = w.tile * (DOWN ? kTile : kTile / 2), row1 = DOWN ? row0 + kTile / 2 : p.I + row0;
+                const int row0 = w.tile * (down ? kTile : kTile / 2), row1 = row0 + (down ? kTile / 2 : p.I);
                 for (int l = w.l0; l < w.l1 && ok; ++l) {
                     const uint32_t slot = n % kStages;
                     ok = wait(b_empty + 8 * slot, (n / kStages & 1) ^ 1);
@@ -441,23 +458,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                     if (elect()) {
                         const uint32_t bar = b_full + 8 * slot, at = saddr(ring + slot * kStage);
                         bar_expect(bar, kWeightBytes);
-                        load_box(at, &maps.w[DOWN], l * kLine<FP8>, row0, w.e, bar);
-                        load_box(at + kWeightBytes / 2, &maps.w[DOWN], l * kLine<FP8>, row1, w.e, bar);
+                        load_box(at, map, l * kLine<FP8>, row0, w.e, bar);
+                        load_box(at + kWeightBytes / 2, map, l * kLine<FP8>, row1, w.e, bar);
                     }
                     __syncwarp();
                 }
             } while (ok && w.next(r));
-        };
-        product(std::false_type{});
-        product(std::true_type{});
+        }
         if (lane == 0) bars.armed[0] = n;
     } else if (r.D > 0 && warp == kWarpMma) {
         uint32_t n = 0, seg = 0;
-        auto product = [&](auto down) {
-            constexpr bool DOWN = decltype(down)::value;
-            constexpr int R = Parts<FP8, DOWN>::R;
-            Walk<FP8, DOWN> w;
-            if (!ok || !w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
+#pragma unroll 1
+        for (int down = 0; down < 2; ++down) {
+            const int R = down ? Parts<FP8, true>::R : Parts<FP8, false>::R;
+            Walk<FP8> w;
+            if (!ok || !begin(w, down)) continue;
             do {
                 // fp32 accumulator, both operands bf16 or both e4m3, 128 x columns
                 const uint32_t columns = (w.count * R + 15) & ~15;
@@ -482,9 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                     if (ends) ++seg;
                 }
             } while (ok && w.next(r));
-        };
-        product(std::false_type{});
-        product(std::true_type{});
+        }
         // all products have been computed before tensor memory is given back
         for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
             if (!__all_sync(0xFFFFFFFFu, bar_wait(b_empty + 8 * (i % kStages), i / kStages & 1, p.wait_cycles))) ok = false;
@@ -498,16 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
             workers_sync();
             if (wid == 0) {
                 if (i == 3 && !met(2)) ok = false;
-                __threadfence();
-                atomicAdd(p.barrier, 1u);
+                asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.barrier) : "memory");
             }
         };
         auto meet = [&](uint32_t i) {
             come(i);
-            if (wid == 0) {
-                if (ok && !met(i)) ok = false;
-                __threadfence();
-            }
+            if (wid == 0 && ok && !met(i)) ok = false;
             workers_sync();
         };
         // Where the sums of entry `spot` for a tile are: in its row of p.sums, and in the pieces that other CTAs
@@ -526,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
             }
             const int tokens = down ? Parts<FP8, true>::TOKENS : Parts<FP8, false>::TOKENS;
             const int within = spot - r.first[r.live[lo]];
-            return Where{lo, within / tokens, within % tokens, r.before[down][lo + 1] - r.before[down][lo]};
+            return Where{lo, within / tokens, within % tokens, (down ? r.before[1] : r.before[0])[lo + 1] - (down ? r.before[1] : r.before[0])[lo]};
         };
         auto pieces = [&](int down, const Where &w, int tile) {
             const uint32_t u = ((uint32_t)r.before[down][w.d] * tiles[down] + tile * w.parts + w.part) * lines[down];
@@ -537,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         auto bring = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
             constexpr int R = Parts<FP8, DOWN>::R;
-            Walk<FP8, DOWN> w;
-            if (!w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
+            Walk<FP8> w;
+            if (!begin(w, DOWN)) return;
             if constexpr (DOWN) {
                 if (lane == 0 && !met(2)) ok = false;
                 asm volatile("fence.proxy.async;" ::: "memory");
@@ -634,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 if (ok) bring(down);
                 return;
             }
-            Walk<FP8, DOWN> w;
-            if (!w.start(r, tiles[DOWN], lines[DOWN], shares[DOWN].from(cta), shares[DOWN].from(cta + 1))) return;
+            Walk<FP8> w;
+            if (!begin(w, DOWN)) return;
             const uint32_t lanes = bars.tmem + ((uint32_t)(warp * 32) << 16);
             const int kb = lines[DOWN], nb = ((DOWN ? p.H : 2 * p.I) + 127) / 128;
             do {
@@ -920,6 +929,15 @@ cudaError_t launch(const Maps &maps, const ExpertLayerParams &p, cudaStream_t st
     return cudaLaunchKernelEx(&cfg, expert_layer_kernel<FP8>, maps, p);
 }
 
+// Most bytes of weights (of as many experts as there are entries) of the small form, for up to 4 entries per
+// expert on average: past 8 it reads the weights again, where the large form has columns left.  Us, small /
+// large form, captured, the weights from HBM:
+//   bf16  13 MB 11.6/18.6   25 MB 15.1/20.2   75 MB 25.7/27.9   83 MB 26.9/27.7   130 MB 36.5/35.7   151 MB 38.2/39.2
+//         8 entries per expert: 104 MB 41/35   32: 25 MB 34/27
+//   e4m3  38 MB 23.7/23.0   41 MB 23.2/22.9   50 MB 23.0/24.1   73 MB 32.7/29.0
+//         8 entries per expert: 8 MB 20.6/19.4   12: 32 MB 40/25
+constexpr double kSmallBytes[2] = {96e6, 32e6};  // bf16, e4m3
+
 template <bool FP8>
 void allow_smem() {
     // failing here means failing at the launch, which reports it
@@ -954,9 +972,19 @@ void expert_layer_init() {
     allow_smem<true>();
 }
 
-size_t expert_layer_workspace(ExpertLayerParams p) { return lay_out(p, nullptr); }
+size_t expert_layer_workspace(ExpertLayerParams p) {
+    const size_t large = lay_out(p, nullptr), small = expert_layer_small_workspace(p);
+    return large > small ? large : small;
+}
+
+bool expert_layer_small(const ExpertLayerParams &p) {
+    const double entries = (double)p.N * p.K, experts = entries < p.E ? entries : p.E;
+    const double bytes = 3.0 * experts * p.H * p.I * (p.s_gate_up != nullptr ? 1 : 2);
+    return entries <= 4.0 * p.E && bytes <= kSmallBytes[p.s_gate_up != nullptr];
+}
 
 cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream_t stream) {
+    if (expert_layer_small(p)) return launch_expert_layer_small(p, workspace, stream);
     const bool fp8 = p.s_gate_up != nullptr, own = p.barrier != nullptr;
     lay_out(p, static_cast<uint8_t *>(workspace));
     if (!own) {

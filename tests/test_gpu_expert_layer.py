@@ -45,7 +45,7 @@ class Layer:
         self.N, self.H, self.I, self.E, self.K, self.fp8 = N, H, I, E, K, fp8
         self.buf = Buffer(1, max(N, 1), H, E, K, max_sms=max_sms)
         self.x = bf((N, H), seed + 1)
-        made, self.wts = route(N, E, K, seed, drop)
+        made, self.wts = route(N, max(E, K), K, seed, drop)     # with idx given, K may be more than E
         self.idx = made if idx is None else idx
         self.gu, self.down = weights(E, 2 * I, H, seed + 2), weights(E, H, I, seed + 3)
         if fp8:
@@ -95,10 +95,18 @@ class Layer:
         return got
 
 
+# Two forms: the small one up to 96 MB of bf16 or 32 MB of e4m3 weights (of as many experts as there are entries)
+# and 4 entries per expert, the large one past either.
 # N, H, I, E, K: one token; tiles cut off on every side; more than 8 and 16 tokens of an expert; the most tokens
 SIZES = [(1, 8, 8, 1, 1), (1, 1024, 512, 32, 4), (3, 264, 24, 5, 2), (7, 40, 200, 9, 3), (17, 520, 136, 2, 2), (32, 1000, 328, 64, 6),
          (128, 256, 64, 16, 8), (128, 72, 1016, 3, 1), (5, 2048, 16, 1024, 32)]
 SIZES_FP8 = [(1, 128, 128, 1, 1), (1, 1024, 512, 32, 4), (3, 256, 128, 5, 2), (17, 640, 384, 2, 2), (31, 1152, 128, 40, 6), (128, 256, 640, 16, 8)]
+
+
+# the large form: many tokens of few experts, odd channels; weights past the small form's
+SIZES += [(5, 8, 8, 1, 1), (40, 264, 24, 5, 2), (33, 40, 200, 4, 3), (21, 1000, 328, 3, 1), (70, 2048, 16, 8, 8), (1, 4096, 2048, 16, 8),
+          (3, 2824, 1416, 40, 6), (65, 200, 264, 2, 1), (128, 136, 72, 2, 2)]
+SIZES_FP8 += [(5, 128, 128, 1, 1), (33, 1152, 256, 4, 3), (1, 7168, 2048, 8, 8), (5, 2176, 1920, 20, 4), (100, 384, 640, 3, 2)]
 
 
 @pytest.mark.parametrize("extras", [False, True])
@@ -130,28 +138,37 @@ def test_one_expert_for_all_tokens_and_every_count(fp8):
         idx[:n, 0] = 3
         idx[::3, 1] = 1
         Layer(40, 384, 128, 4, 2, fp8=fp8, idx=idx.cuda(), seed=n).check()
+        Layer(40, 384, 128, 20, 2, fp8=fp8, idx=idx.cuda(), seed=n).check()     # the small form
 
 
-def test_same_expert_twice_in_a_token():
-    idx = torch.tensor([[2, 2, 2], [2, 0, 2], [-1, 1, 1]]).cuda()
-    Layer(3, 136, 72, 3, 3, idx=idx, bias=True).check()
+@pytest.mark.parametrize("tokens", [3, 6])      # 3 and 6 entries per expert: the small and the large form
+def test_same_expert_twice_in_a_token(tokens):
+    idx = torch.tensor([[2, 2, 2], [2, 0, 2], [-1, 1, 1]]).repeat(tokens // 3, 1).cuda()
+    Layer(tokens, 136, 72, 3, 3, idx=idx, bias=True).check()
 
 
-def test_tokens_without_experts_get_their_residual_or_zeros():
-    idx = torch.tensor([[-1, -1], [1, -1], [-1, -1]]).cuda()
-    layer = Layer(3, 264, 40, 4, 2, idx=idx, residual=True)
+@pytest.mark.parametrize("E", [4, 1])           # the small and the large form
+def test_tokens_without_experts_get_their_residual_or_zeros(E):
+    idx = torch.tensor([[-1, -1], [E - 1, -1], [-1, -1]]).cuda()
+    buf = dict(N=3, H=264, I=40, E=E, K=2) if E > 1 else dict(N=3, H=264, I=40, E=1, K=1)
+    idx = idx[:, :buf["K"]].contiguous()
+    if E == 1:
+        idx = idx.repeat(3, 1)
+        buf["N"] = 9
+    layer = Layer(**buf, idx=idx, residual=True)
     got = layer.check()
-    assert torch.equal(got[0::2], layer.residual[0::2])
-    layer = Layer(3, 264, 40, 4, 2, idx=torch.full((3, 2), -1).cuda(), residual=True, bias=True)
+    assert torch.equal(got[0::3], layer.residual[0::3]) and torch.equal(got[2::3], layer.residual[2::3])
+    layer = Layer(**buf, idx=torch.full_like(idx, -1), residual=True, bias=True)
     assert torch.equal(layer.run(), layer.residual)
     layer.residual = None
-    out = torch.full((3, 264), 7.0, device="cuda", dtype=torch.bfloat16)
+    out = torch.full((buf["N"], 264), 7.0, device="cuda", dtype=torch.bfloat16)
     assert torch.equal(layer.run(out=out), torch.zeros_like(out))
 
 
+@pytest.mark.parametrize("tokens", [7, 19])     # the small and the large form
 @pytest.mark.parametrize("fp8", [False, True])
-def test_what_masked_entries_and_unnamed_experts_hold_does_not_matter(fp8):
-    layer = Layer(9, 256, 128, 6, 3, fp8=fp8, bias=True, drop=0.3, seed=5)
+def test_what_masked_entries_and_unnamed_experts_hold_does_not_matter(fp8, tokens):
+    layer = Layer(tokens, 256, 128, 6, 3, fp8=fp8, bias=True, drop=0.3, seed=5)
     layer.idx[layer.idx == 4] = -1
     before = layer.check()
     layer.wts[layer.idx < 0] = float("nan")
@@ -166,23 +183,27 @@ def test_what_masked_entries_and_unnamed_experts_hold_does_not_matter(fp8):
     assert torch.equal(layer.run(), before)
 
 
+@pytest.mark.parametrize("copies", [1, 4])      # the small and the large form
 @pytest.mark.parametrize("byte", [0x7F, 0xFF])
-def test_nan_codes_of_fp8_weights_give_nan(byte):
+def test_nan_codes_of_fp8_weights_give_nan(byte, copies):
     """One code of a row: that channel of every token of the expert, and no other."""
-    layer = Layer(4, 256, 128, 2, 1, fp8=True, idx=torch.tensor([[0], [1], [1], [0]]).cuda())
+    idx = torch.tensor([[0], [1], [1], [0]]).repeat(copies, 1).cuda()
+    layer = Layer(4 * copies, 256, 128, 2, 1, fp8=True, idx=idx)
+    second = idx[:, 0] == 1
     before = layer.check()
     layer.down[0].view(torch.uint8)[1, 77, 101] = byte
     got = layer.run()
-    assert bool(got[1:3, 77].isnan().all())
-    got[1:3, 77] = before[1:3, 77]
+    assert bool(got[second, 77].isnan().all())
+    got[second, 77] = before[second, 77]
     assert torch.equal(got, before)
     layer.gu[0].view(torch.uint8)[0, 128 + 5, 255] = byte   # an up row: the whole token
-    assert bool(layer.run()[0::3].isnan().all())
+    assert bool(layer.run()[~second].isnan().all())
 
 
-def test_every_fp8_code():
+@pytest.mark.parametrize("E", [1, 2])           # the large and the small form
+def test_every_fp8_code(E):
     """Weights of all 254 finite codes against one-hot tokens: exact but for the roundings behind them."""
-    layer = Layer(8, 256, 128, 1, 1, fp8=True, seed=3)
+    layer = Layer(8, 256, 128, E, 1, fp8=True, seed=3, idx=torch.zeros(8, 1, dtype=torch.int64).cuda())
     codes = torch.arange(256, dtype=torch.int64)
     codes[(codes & 0x7F) == 0x7F] = 0
     layer.gu[0].view(torch.uint8)[0, :] = codes.to(torch.uint8).cuda()[(torch.arange(256)[:, None] + torch.arange(256)) % 256]
@@ -193,36 +214,43 @@ def test_every_fp8_code():
 
 
 def test_infinities_and_large_values():
-    layer = Layer(2, 64, 32, 2, 1, idx=torch.tensor([[0], [1]]).cuda())
-    layer.x[0, 5] = float("inf")
-    layer.x[1] *= 1e18
-    out = layer.run()
-    assert bool(out[0].isnan().all() | out[0].isinf().any())
-    want, _ = layer.want()
-    assert bool((out[1].double() - want[1]).abs().max() <= want[1].abs().max() * 2.0 ** -7)
+    """A token of infinities and a huge one, beside others that stay as they are, in both forms and types."""
+    for copies in (1, 5):
+        for fp8 in (False, True):
+            layer = Layer(3 * copies, 128, 128, 3, 1, fp8=fp8, idx=torch.tensor([[0], [1], [1]]).repeat(copies, 1).cuda())
+            before = layer.check()
+            layer.x[0, 5] = float("inf")
+            layer.x[1] *= 1e18
+            out = layer.run()
+            assert not bool(out[0].isfinite().all())
+            want, _ = layer.want()
+            assert bool((out[1].double() - want[1]).abs().max() <= want[1].abs().max() * 2.0 ** -7)
+            assert torch.equal(out[2:], before[2:])
 
 
 @pytest.mark.parametrize("fp8", [False, True])
 def test_every_number_of_sms_and_repeated_calls(fp8):
     """The sums are cut into as many shares as there are SMs: within the bounds for each number, and the same bits
     every time for one."""
-    for sms in (0, 1, 7, 64, 151, 152):
-        layer = Layer(N=21, H=512, I=256, E=12, K=3, fp8=fp8, bias=True, residual=True, seed=2, max_sms=sms)
+    for sms, N in [(s, n) for s in (0, 1, 7, 64, 151, 152) for n in (15, 21)]:    # the small and the large form
+        layer = Layer(N=N, H=512, I=256, E=12, K=3, fp8=fp8, bias=True, residual=True, seed=2, max_sms=sms)
         first = layer.check()
         for _ in range(3):
             assert torch.equal(layer.run(), first)
 
 
-def test_residual_may_be_the_output():
-    layer = Layer(13, 328, 72, 7, 2, bias=True, residual=True)
+@pytest.mark.parametrize("N", [13, 15])         # the small and the large form
+def test_residual_may_be_the_output(N):
+    layer = Layer(N, 328, 72, 7, 2, bias=True, residual=True)
     want = layer.check()
     layer.residual = layer.residual.clone()
     assert layer.run(out=layer.residual) is layer.residual
     assert torch.equal(layer.residual, want)
 
 
-def test_bad_ids_are_reported_and_skipped():
-    layer = Layer(4, 136, 64, 5, 2)
+@pytest.mark.parametrize("N", [4, 11])          # the small and the large form
+def test_bad_ids_are_reported_and_skipped(N):
+    layer = Layer(N, 136, 64, 5, 2)
     clean = layer.idx.clone()
     clean[1, 0] = clean[3, 1] = -1
     layer.idx = clean
@@ -236,17 +264,19 @@ def test_bad_ids_are_reported_and_skipped():
     assert torch.equal(layer.run(), want)
 
 
-def test_weights_none_are_ones():
-    layer = Layer(5, 128, 64, 6, 2)
+@pytest.mark.parametrize("N", [5, 13])          # the small and the large form
+def test_weights_none_are_ones(N):
+    layer = Layer(N, 128, 64, 6, 2)
     layer.wts.fill_(1.0)
     want = layer.check()
     layer.wts = None
     assert torch.equal(layer.run(), want)
 
 
-def test_side_by_side_on_streams_and_in_graphs():
+@pytest.mark.parametrize("N", [9, 21])          # the small and the large form
+def test_side_by_side_on_streams_and_in_graphs(N):
     """Two calls of one context at once, and two captured ones replayed with other inputs."""
-    a, b = (Layer(9, 1024, 256, 16, 4, fp8=f, seed=s, bias=True) for f, s in ((False, 1), (True, 2)))
+    a, b = (Layer(N, 1024, 256, 16, 4, fp8=f, seed=s, bias=True) for f, s in ((False, 1), (True, 2)))
     want = a.check(), b.check()
     streams = torch.cuda.Stream(), torch.cuda.Stream()
     b.buf = a.buf
@@ -264,7 +294,7 @@ def test_side_by_side_on_streams_and_in_graphs():
         with torch.cuda.graph(g):
             outs.append(layer.buf.expert_layer(layer.x, layer.idx, layer.wts, layer.gu, layer.down, biases=layer.bias))
         graphs.append(g)
-    fresh = Layer(9, 1024, 256, 16, 4, seed=7, bias=True)
+    fresh = Layer(N, 1024, 256, 16, 4, seed=7, bias=True)
     for layer in (a, b):
         layer.x.copy_(fresh.x)
         layer.idx.copy_(fresh.idx)
@@ -353,8 +383,9 @@ def test_the_same_expert_for_every_entry():
 
 @pytest.mark.parametrize("fp8", [False, True])
 def test_a_wait_that_runs_out_is_reported_and_leaves_nothing_behind(fp8):
-    """An expert whose weights never come, 1 ms waits: the status says so; the next call is right again."""
-    layer = Layer(12, 1024, 512, 8, 2, fp8=fp8, seed=1)
+    """The large form, an expert whose weights never come, 1 ms waits: the status says so; the next call is right
+    again."""
+    layer = Layer(24, 1024, 512, 8, 2, fp8=fp8, seed=1)
     want = layer.check()
     for _ in range(2):
         ep.ep_set_test_hooks(layer.buf.ctx, move_withhold_item=int(layer.idx[3, 1]), move_wait_ns=1_000_000)
@@ -366,8 +397,8 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_nothing_behind(fp8):
 
 
 def test_more_streams_than_there_are_counters():
-    """From the 513th stream on a barrier counter comes from the workspace."""
-    layer = Layer(2, 64, 16, 4, 2)
+    """The large form: from the 513th stream on a barrier counter comes from the workspace."""
+    layer = Layer(2, 64, 16, 2, 5, idx=torch.tensor([[0, 1, 0, 1, 1], [1, 1, 0, 0, 0]]).cuda())
     want = layer.check()
     raw = lambda s: ep.ep_expert_layer(layer.buf.ctx, layer.x, layer.idx, layer.wts, 2, 16, layer.gu, None, None, layer.down, None,  # noqa: E731
                                        None, None, ws, out, stream=s)
