@@ -274,7 +274,7 @@ def _own(s):
         return y if s["z"] is None else (y, s["z"])
     if s["op"] == "linear_bwd":
         return buf.expert_linear_backward(s["dy"], s["z"], s["handle"], activation=s["act"], out=s["dz"], dbias=s["db"])
-    norm = buf.clip_grads(s["grads"], s["max_norm"], out=s["out"])
+    norm = buf.clip_grads(s["grads"], s["max_norm"], out=None if s["to"] is s["flat"] else s["out"])
     return norm, s["to"]
 
 
