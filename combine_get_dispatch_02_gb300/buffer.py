@@ -96,6 +96,7 @@ class Buffer:
         self.rows = ep.ep_recv_rows(self.cfg)
         self.num_hook_sms = num_hook_sms   # SMs of the receive hooks' copy kernels (0: max_sms / all)
         self._send = {}                    # send / staging buffers of the split calls, made on first use
+        self._layer_bytes = {}             # workspace bytes of expert_layer by (tokens, inner)
 
     def __del__(self):
         ctx = getattr(self, "_ctx", None)
@@ -603,13 +604,14 @@ class Buffer:
     def expert_layer(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor | None, w_gate_up, w_down,
                      biases=None, residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
         """The whole layer of gated experts for up to EP_LAYER_MAX_TOKENS
-        tokens (a decode step) in two kernels, without dispatch and combine:
+        tokens (a decode step) in one or two kernels, without dispatch and combine:
         out[t] = residual[t] + sum_k topk_weights[t, k] (Wd h + bd), h =
         silu(g) u, [g; u] = Wgu x[t] + bgu of expert topk_idx[t, k] (-1:
         none).  x, residual [N, H] bf16, topk_idx int64 and topk_weights fp32
         [N, K] (None: ones); w_gate_up [E, 2*inner, H] and w_down [E, H,
         inner] bf16, or both pairs (codes, scales) of cast_weights; biases =
-        (bgu [E, 2*inner], bd [E, H]) bf16.  ``out`` may be ``residual``."""
+        (bgu [E, 2*inner], bd [E, H]) bf16.  ``out`` may be ``x`` or
+        ``residual``, and ``residual`` may be ``x``."""
         wgu, sgu = w_gate_up if isinstance(w_gate_up, (tuple, list)) else (w_gate_up, None)
         wd, sd = w_down if isinstance(w_down, (tuple, list)) else (w_down, None)
         if (sgu is None) != (sd is None):
@@ -636,7 +638,10 @@ class Buffer:
             out = torch.empty(N, k, dtype=torch.bfloat16, device=x.device)
         if out.numel() != N * k:
             raise ValueError(f"out must be [{N}, {k}], got {tuple(out.shape)}")
-        ws = torch.empty(ep.ep_expert_layer_workspace(self._ctx, N, inner), dtype=torch.uint8, device=x.device)
+        size = self._layer_bytes.get((N, inner))
+        if size is None:
+            size = self._layer_bytes[N, inner] = ep.ep_expert_layer_workspace(self._ctx, N, inner)
+        ws = torch.empty(size, dtype=torch.uint8, device=x.device)
         ep.ep_expert_layer(self._ctx, x, topk_idx, topk_weights, N, inner, wgu, sgu, bgu, wd, sd, bd, residual, ws, out)
         return out
 

@@ -416,8 +416,8 @@ ep_status ep_expert_linear_backward(ep_ctx *ctx, const ep_handle *handle, const 
  * step's backward pass:
  *   norm = sqrt(sum over all tensors of g^2),  out = g * min(1, max_norm / norm)
  * Squares are summed in fp64 (those of 64 bytes in fp32 first, where they cannot
- * overflow or vanish).  An infinite or undefined norm scales nothing: the
- * tensors keep their values and d_norm says it.
+ * overflow or vanish).  An infinite norm (fp32's: past 3.4e38) or an undefined one scales
+ * nothing: the tensors keep their values and d_norm says it.
  *
  * ep_grad_norm: the sum of squares as EP_GRAD_PARTIALS partial sums, all of them
  *   written.  With the experts of several processes, add these arrays up between
@@ -445,8 +445,9 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
                        float *d_norm, void *stream);
 
 /* The whole layer of gated experts for a few tokens (a decode step): what
- * dispatch, the two products and combine compute, in two kernels that read the
- * named experts' weights once and keep no receive buffer; for more than
+ * dispatch, the two products and combine compute, in one kernel (two where the
+ * weights are few) that reads the named experts' weights once and keeps no receive
+ * buffer; for more than
  * EP_LAYER_MAX_TOKENS tokens use those calls (EP_ERR_UNSUPPORTED here).
  *   h[t,k] = silu(g) u, [g; u] = Wgu[e] x[t] + bgu[e], e = topk_idx[t,k]
  *   out[t] = bf16(residual[t] + fma chain over k ascending of
@@ -454,10 +455,14 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
  * Entries with topk_idx -1 are skipped (their weights are not read); a token
  * without any gets its residual, or zeros.  An id outside [-1, E) is skipped too
  * and reported by ep_get_device_status (EP_ERR_BAD_EXPERT).  An expert may be
- * named more than once by a token.  Sums are held in fp32; x is taken as it is
- * and h as the sum of two bf16 numbers (2^-17 of it off at most), so with FP8
- * weights, too, no token is cast to 8 bits (the dispatched path casts x and h
- * and differs by that).  It needs no handle.
+ * named more than once by a token.  Sums are held in fp32.  x is taken as it is (with
+ * FP8 weights as the sum of two e4m3 codes per 128 channels, which is x down to 2^-13
+ * of the block's largest and off by 2^-21 of that at most below), h as the sum of two
+ * bf16 numbers or four codes, 2^-17 of it off at most; the dispatched FP8 path casts x
+ * and h to one code each and differs by that.  A channel of x that is infinite or NaN
+ * makes its token's result NaN or infinite.  It needs no handle.  The grid's CTAs meet
+ * with bounded waits (about 2 s, EP_ERR_TIMEOUT through ep_get_device_status); the call
+ * starts when all SMs that it takes (max_sms) are free.
  *     d_x               device bf16 [num_tokens, H]
  *     d_topk_idx        device int64 [num_tokens, K]
  *     d_topk_weights    device fp32 [num_tokens, K], NULL = all ones
@@ -467,11 +472,11 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
  *     d_w_down          device [E, H, inner] bf16, or e4m3 with d_down_scales
  *                       (fp32 [E, ceil(H/128), inner/128]); both or neither
  *     d_b_gate_up, d_b_down  device bf16 [E, 2*inner], [E, H], or NULL
- *     d_residual        device bf16 [num_tokens, H] or NULL; may be d_out itself
+ *     d_residual        device bf16 [num_tokens, H] or NULL; may be d_x
  *     d_workspace       device, ep_expert_layer_workspace bytes; nothing in it
  *                       outlives the call; calls that may run side by side
  *                       (streams, graphs) need one each
- *     d_out             device bf16 [num_tokens, H]
+ *     d_out             device bf16 [num_tokens, H]; may be d_x or d_residual itself
  * All pointers 16-byte aligned (d_topk_idx 8, scales and weights 4); inner a
  * multiple of 8, with FP8 weights H and inner multiples of 128.  The same call
  * repeats bit for bit; the order in which its sums are taken follows from the SMs

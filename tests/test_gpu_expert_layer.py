@@ -248,6 +248,42 @@ def test_residual_may_be_the_output(N):
     assert torch.equal(layer.residual, want)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("N", [13, 40])         # the small and the large form
+def test_in_place_on_the_residual_stream(N, fp8):
+    """x + layer(x) written to x."""
+    layer = Layer(N, 512, 256, 8, 2, fp8=fp8, bias=True)
+    layer.residual = layer.x
+    want = layer.check()
+    for _ in range(5):
+        x = layer.x.clone()
+        got = layer.buf.expert_layer(x, layer.idx, layer.wts, layer.gu, layer.down, biases=layer.bias, residual=x, out=x)
+        assert got is x and layer.buf.device_status() == ep.EP_OK and torch.equal(x, want)
+
+
+def test_long_sums_of_equal_sign():
+    """x = 1 and positive weights, 7168 channels: the tensor cores drop what falls off when they add (16 at a time,
+    2^-23 of the sum each at most), and nothing else is lost: both products, both forms (1 and 3 experts' weights)."""
+    for E in (1, 12):
+        layer = Layer(5, 7168, 64, E, 1, idx=torch.zeros(5, 1, dtype=torch.int64).cuda())
+        layer.x.fill_(1.0)
+        layer.gu.abs_()
+        layer.down.abs_()
+        got, (want, _) = layer.run(), layer.want()
+        error = (got.double() - want).norm() / want.norm()
+        assert float(error) <= 2.0 ** -8 + 2 * (7168 / 16 + 64 / 16) * 2.0 ** -23
+
+
+def test_a_wide_range_of_values_in_a_token():
+    """FP8 weights: channels over seven decades beside each other in blocks of 128 (two codes hold 2^-13 of a block's
+    largest exactly, and 2^-21 of it below)."""
+    for N in (4, 40):
+        layer = Layer(N, 512, 256, 8, 2, fp8=True, seed=9)
+        g = torch.Generator("cuda").manual_seed(1)
+        layer.x *= 10.0 ** (torch.rand(layer.x.shape, generator=g, device="cuda") * 7.0 - 3.5)
+        layer.check()
+
+
 @pytest.mark.parametrize("N", [4, 11])          # the small and the large form
 def test_bad_ids_are_reported_and_skipped(N):
     layer = Layer(N, 136, 64, 5, 2)
