@@ -53,19 +53,28 @@ using namespace umma;
 constexpr int kWarpWeights = 4, kWarpMma = 6, kWarpSpare = 7, kWarpTokens = 8, kTokenWarps = 8;
 constexpr int kThreads = 16 * 32, kWorkers = 12 * 32;
 constexpr int kTile = 128;                   // weight rows of a job
-constexpr int kColumns = 64;                 // most columns of a job
-constexpr int kWeightBytes = kTile * 128, kStage = kWeightBytes + kColumns * 128;
-constexpr int kStages = 8, kSums = 4;        // stages of the ring, accumulators
-constexpr int kScales = 16;                  // stages whose tokens' scales are kept: the readers are up to kSums behind
-                                             // the products, which are kStages behind the loaders
-constexpr size_t kFixed = 1024 + (size_t)kStages * kStage;
+constexpr int kMostColumns = 64;             // most columns of a job
+constexpr int kWeightBytes = kTile * 128;
+constexpr int kSums = 4;                     // accumulators
+constexpr int kScales = 32;                  // stages whose tokens' scales are kept: the loaders are up to kStages ahead
+                                             // of the products, and those kSums + 1 ahead of the readers
 
-// Columns of an entry (codes or numbers whose sum it is) and entries of a job.
+// Columns of an entry (codes or numbers whose sum it is).
 template <bool FP8, bool DOWN>
-struct Parts {
-    static constexpr int R = FP8 ? (DOWN ? 4 : 2) : (DOWN ? 2 : 1);
-    static constexpr int TOKENS = kColumns / R;
+constexpr int kParts = FP8 ? (DOWN ? 4 : 2) : (DOWN ? 2 : 1);
+
+// C: most columns of a job.  16 where no expert has more than 4 tokens of e4m3 (8 of bf16): what the ring does not
+// hold of tokens it holds of weights, and is further ahead when the SMs meet.
+template <bool FP8, int C>
+struct Shape {
+    static constexpr int STAGE = kWeightBytes + C * 128;
+    static constexpr int STAGES = C == 16 ? 12 : 8;
+    static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE;
+    static_assert(STAGES + kSums + 1 <= kScales, "scales are overwritten before they are read");
 };
+// Entries of a job.
+template <bool FP8, bool DOWN, int C>
+constexpr int kTokens = C / kParts<FP8, DOWN>;
 template <bool FP8>
 constexpr int kLine = FP8 ? 128 : 64;        // channels of a stage
 
@@ -125,9 +134,9 @@ size_t route_bytes(int E, int M) {
 }
 
 // `scratch`: 512 bytes for each warp, and 17 KB behind them.
-template <bool FP8>
+template <bool FP8, int C>
 __device__ __forceinline__ Route route(const ExpertLayerParams &p, uint8_t *at, uint32_t *scratch) {
-    constexpr int kWarps = kThreads / 32, kGateTokens = Parts<FP8, false>::TOKENS, kDownTokens = Parts<FP8, true>::TOKENS;
+    constexpr int kWarps = kThreads / 32, kGateTokens = kTokens<FP8, false, C>, kDownTokens = kTokens<FP8, true, C>;
     Route r;
     const int M = p.N * p.K, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     r.first = reinterpret_cast<int *>(at);
@@ -246,7 +255,7 @@ __device__ __forceinline__ Route route(const ExpertLayerParams &p, uint8_t *at, 
 // The jobs of a product (0: gate, 1: down), in the order expert, tile of weight rows, tokens, and a CTA's share of
 // their stages: pieces of jobs, stages l0 .. l1 - 1 of each.  (One code for both products: the second time it is
 // there, see kWarpSpare.)
-template <bool FP8>
+template <bool FP8, int C>
 struct Walk {
     const uint16_t *before;
     int tokens;                        // most of a job
@@ -267,7 +276,7 @@ struct Walk {
     __device__ __forceinline__ bool start(const Route &r, int down, int tiles_, int lines_, uint32_t from, uint32_t to) {
         if (from == to) return false;
         before = down ? r.before[1] : r.before[0];
-        tokens = down ? Parts<FP8, true>::TOKENS : Parts<FP8, false>::TOKENS;
+        tokens = down ? kTokens<FP8, true, C> : kTokens<FP8, false, C>;
         tiles = tiles_;
         lines = lines_;
         left = to - from;
@@ -311,11 +320,12 @@ struct Maps {
     CUtensorMap h;     // h laid out by entry: [entries * R, channels] in boxes of 16 rows x 128 bytes
 };
 
+template <int C>
 struct Bars {
-    uint64_t full[kStages], empty[kStages], tfull[kSums], tempty[kSums];
+    uint64_t full[12], empty[12], tfull[kSums], tempty[kSums];
     uint32_t armed[1 + kTokenWarps];  // stages loaded (weights; by each token warp of its own)
     uint32_t failed, tmem;
-    float scale[kScales][kColumns / 2];  // what a code of an entry is worth
+    float scale[kScales][C / 2];  // what a code of an entry is worth
 };
 
 // The stages of a product in equal shares: CTA b has those from from(b) on, the first `more` CTAs one more.
@@ -372,10 +382,11 @@ __device__ __forceinline__ float2 block_scale(const float (&v)[N]) {
     return scale_of(top);
 }
 
-template <bool FP8>
+template <bool FP8, int C>
 __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const ExpertLayerParams p) {
+    constexpr int kStages = Shape<FP8, C>::STAGES, kStage = Shape<FP8, C>::STAGE;
     extern __shared__ uint8_t dyn[];
-    __shared__ Bars bars;
+    __shared__ Bars<C> bars;
     uint8_t *const ring = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ctas = gridDim.x, cta = blockIdx.x;
@@ -396,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         prefetch_map(&maps.w[1]);
         prefetch_map(&maps.h);
     }
-    if (warp == kWarpMma) tmem_alloc_one(saddr(&bars.tmem), kSums * kColumns);
+    if (warp == kWarpMma) tmem_alloc_one(saddr(&bars.tmem), kSums * C);
     pdl_wait();
-    const Route r = route<FP8>(p, ring + kStages * kStage, reinterpret_cast<uint32_t *>(ring));
+    const Route r = route<FP8, C>(p, ring + kStages * kStage, reinterpret_cast<uint32_t *>(ring));
     const bool worker = warp < 4 || warp >= 8;
     const int wid = warp < 4 ? tid : tid - 128;  // of a worker
     // tiles of an expert's weights, stages of a job, rows of the tiles
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
     };
 
     // this CTA's share of a product
-    auto begin = [&](Walk<FP8> &w, int down) {
+    auto begin = [&](Walk<FP8, C> &w, int down) {
         return w.start(r, down, down ? tiles[1] : tiles[0], down ? lines[1] : lines[0], (down ? shares[1] : shares[0]).from(cta),
                        (down ? shares[1] : shares[0]).from(cta + 1));
     };
@@ -444,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         uint32_t n = 0;
 #pragma unroll 1
         for (int down = 0; down < 2; ++down) {
-            Walk<FP8> w;
+            Walk<FP8, C> w;
             if (!ok || !begin(w, down)) continue;
             const CUtensorMap *const map = &maps.w[down];
             do {
@@ -470,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         uint32_t n = 0, seg = 0;
 #pragma unroll 1
         for (int down = 0; down < 2; ++down) {
-            const int R = down ? Parts<FP8, true>::R : Parts<FP8, false>::R;
-            Walk<FP8> w;
+            const int R = down ? kParts<FP8, true> : kParts<FP8, false>;
+            Walk<FP8, C> w;
             if (!ok || !begin(w, down)) continue;
             do {
                 // fp32 accumulator, both operands bf16 or both e4m3, 128 x columns
@@ -489,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                         const uint32_t a = saddr(ring + slot * kStage), b = a + kWeightBytes;
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            mma_one<FP8>(bars.tmem + buf * kColumns, desc(a + j * 32, 16), desc(b + j * 32, 16), id, !begins || j != 0);
+                            mma_one<FP8>(bars.tmem + buf * C, desc(a + j * 32, 16), desc(b + j * 32, 16), id, !begins || j != 0);
                         commit_one(b_empty + 8 * slot);
                         if (ends) commit_one(b_tfull + 8 * buf);
                     }
@@ -533,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 else
                     hi = mid - 1;
             }
-            const int tokens = down ? Parts<FP8, true>::TOKENS : Parts<FP8, false>::TOKENS;
+            const int tokens = down ? kTokens<FP8, true, C> : kTokens<FP8, false, C>;
             const int within = spot - r.first[r.live[lo]];
             return Where{lo, within / tokens, within % tokens, (down ? r.before[1] : r.before[0])[lo + 1] - (down ? r.before[1] : r.before[0])[lo]};
         };
@@ -545,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         // h, by tensor map, once all have laid theirs out.
         auto bring = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
-            constexpr int R = Parts<FP8, DOWN>::R;
-            Walk<FP8> w;
+            constexpr int R = kParts<FP8, DOWN>;
+            Walk<FP8, C> w;
             if (!begin(w, DOWN)) return;
             if constexpr (DOWN) {
                 if (lane == 0 && !met(2)) ok = false;
@@ -638,12 +649,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         // Sums out of tensor memory: lane = weight row.
         auto product = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
-            constexpr int R = Parts<FP8, DOWN>::R, TOKENS = Parts<FP8, DOWN>::TOKENS;
+            constexpr int R = kParts<FP8, DOWN>, TOKENS = kTokens<FP8, DOWN, C>;
             if (warp >= kWarpTokens) {
                 if (ok) bring(down);
                 return;
             }
-            Walk<FP8> w;
+            Walk<FP8, C> w;
             if (!begin(w, DOWN)) return;
             const uint32_t lanes = bars.tmem + ((uint32_t)(warp * 32) << 16);
             const int kb = lines[DOWN], nb = ((DOWN ? p.H : 2 * p.I) + 127) / 128;
@@ -656,10 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                     ok = wait(b_tfull + 8 * buf, seg / kSums & 1);
                     fence_after();
 #pragma unroll
-                    for (int q = 0; q < kColumns / 16; ++q) {
+                    for (int q = 0; q < C / 16; ++q) {
                         if (q * 16 >= columns) break;
                         uint32_t v[16];
-                        tmem_get16(v, lanes + buf * kColumns + q * 16);
+                        tmem_get16(v, lanes + buf * C + q * 16);
                         if ((q + 1) * 16 >= columns) {
                             fence_before();
                             __syncwarp();
@@ -676,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                     ++seg;
                 };
                 float *const to = w.l0 == 0 ? p.sums + (int64_t)w.first * (tiles[DOWN] * kTile) + w.tile * kTile + warp * 32 + lane
-                                            : p.pieces + (int64_t)cta * kColumns * kTile + warp * 32 + lane;
+                                            : p.pieces + (int64_t)cta * C * kTile + warp * 32 + lane;
                 const int64_t ld = w.l0 == 0 ? tiles[DOWN] * kTile : kTile;
                 if constexpr (FP8) {
 #pragma unroll
@@ -718,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 const int tile = c / (kTile / 2), at = c % (kTile / 2);
                 const int2 who = pieces(0, w, tile);
                 q.own = p.sums + (int64_t)i * rows + tile * kTile + at;
-                q.piece = p.pieces + ((int64_t)(who.x + 1) * kColumns + w.at) * kTile + at;
+                q.piece = p.pieces + ((int64_t)(who.x + 1) * C + w.at) * kTile + at;
                 q.others = who.y - who.x;
                 if (p.b_gate_up != nullptr) {
                     const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(p.b_gate_up) + (int64_t)r.live[w.d] * 2 * p.I + c;
@@ -742,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                         float4 x[4], y[4];
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            const float *q = item.piece + (int64_t)min(b0 + b, item.others - 1) * kColumns * kTile;
+                            const float *q = item.piece + (int64_t)min(b0 + b, item.others - 1) * C * kTile;
                             x[b] = __ldcg(reinterpret_cast<const float4 *>(q));
                             y[b] = __ldcg(reinterpret_cast<const float4 *>(q + kTile / 2));
                         }
@@ -839,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                     y[j] = z[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     bias[j] = make_uint2(0, 0);
                     if (there) y[j] = __ldcg(reinterpret_cast<const float4 *>(p.sums + (int64_t)s * (tiles[1] * kTile) + c));
-                    const float *piece = p.pieces + ((int64_t)(b0 + 1) * kColumns + at) * kTile + lane * 4;
+                    const float *piece = p.pieces + ((int64_t)(b0 + 1) * C + at) * kTile + lane * 4;
                     if (there && others > 0) z[j] = __ldcg(reinterpret_cast<const float4 *>(piece));
                     if (there && p.b_down != nullptr)
                         bias[j] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.b_down) + (int64_t)e * p.H + c));
@@ -856,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             q[i] = __ldcg(reinterpret_cast<const float4 *>(p.pieces +
-                                                                           ((int64_t)(b0 + min(b + i, others)) * kColumns + at) * kTile + lane * 4));
+                                                                           ((int64_t)(b0 + min(b + i, others)) * C + at) * kTile + lane * 4));
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             if (b + i > others) break;
@@ -888,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kWarpMma) tmem_free_one(bars.tmem, kSums * kColumns);
+    if (warp == kWarpMma) tmem_free_one(bars.tmem, kSums * C);
     if (r.D == 0) return;
     if (tid == 0) {
         if (bars.failed) {
@@ -912,12 +923,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
     }
 }
 
-template <bool FP8>
+template <bool FP8, int C>
 cudaError_t launch(const Maps &maps, const ExpertLayerParams &p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.sms, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kFixed + route_bytes(p.E, p.N * p.K);
+    cfg.dynamicSmemBytes = Shape<FP8, C>::fixed + route_bytes(p.E, p.N * p.K);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;  // every CTA resident: the grid barriers end
@@ -926,7 +937,7 @@ cudaError_t launch(const Maps &maps, const ExpertLayerParams &p, cudaStream_t st
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, expert_layer_kernel<FP8>, maps, p);
+    return cudaLaunchKernelEx(&cfg, expert_layer_kernel<FP8, C>, maps, p);
 }
 
 // Most bytes of weights (of as many experts as there are entries) of the small form, for up to 4 entries per
@@ -938,11 +949,16 @@ cudaError_t launch(const Maps &maps, const ExpertLayerParams &p, cudaStream_t st
 //         8 entries per expert: 8 MB 20.6/19.4   12: 32 MB 40/25
 constexpr double kSmallBytes[2] = {96e6, 32e6};  // bf16, e4m3
 
+// Most tokens of a call whose jobs have 16 columns at most.
 template <bool FP8>
+constexpr int kFewTokens = kTokens<FP8, true, 16>;
+
+template <bool FP8, int C>
 void allow_smem() {
     // failing here means failing at the launch, which reports it
-    if (cudaFuncSetAttribute(expert_layer_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(kFixed + route_bytes(1024, kLayerMaxTokens * 32))) != cudaSuccess)
+    const int tokens = C == 16 ? kFewTokens<FP8> : kLayerMaxTokens;
+    if (cudaFuncSetAttribute(expert_layer_kernel<FP8, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(Shape<FP8, C>::fixed + route_bytes(1024, tokens * 32))) != cudaSuccess)
         cudaGetLastError();
 }
 
@@ -958,7 +974,7 @@ size_t lay_out(ExpertLayerParams &p, uint8_t *base) {
     const size_t gate = (size_t)((p.I + kTile / 2 - 1) / (kTile / 2)) * kTile, down = (size_t)((p.H + kTile - 1) / kTile) * kTile;
     p.h = take(M * p.I * 4);
     p.sums = reinterpret_cast<float *>(take(M * (gate > down ? gate : down) * 4));
-    p.pieces = reinterpret_cast<float *>(take((size_t)p.sms * kColumns * kTile * 4));
+    p.pieces = reinterpret_cast<float *>(take((size_t)p.sms * kMostColumns * kTile * 4));
     p.h_scale = reinterpret_cast<float *>(take(M * ((p.I + 127) / 128) * 4));
     uint32_t *const barrier = reinterpret_cast<uint32_t *>(take(8));
     if (p.barrier == nullptr) p.barrier = barrier;
@@ -968,8 +984,10 @@ size_t lay_out(ExpertLayerParams &p, uint8_t *base) {
 }  // namespace
 
 void expert_layer_init() {
-    allow_smem<false>();
-    allow_smem<true>();
+    allow_smem<false, 16>();
+    allow_smem<false, 64>();
+    allow_smem<true, 16>();
+    allow_smem<true, 64>();
 }
 
 size_t expert_layer_workspace(ExpertLayerParams p) {
@@ -999,7 +1017,8 @@ cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream
         !encode_rows(&maps.w[1], p.w_down, es, p.I, p.H, p.E, kTile / 2) ||
         !encode_rows(&maps.h, p.h, es, p.I, M * (fp8 ? 4 : 2), 0, 16))
         return cudaErrorInvalidValue;
-    return fp8 ? launch<true>(maps, p, stream) : launch<false>(maps, p, stream);
+    if (fp8) return p.N <= kFewTokens<true> ? launch<true, 16>(maps, p, stream) : launch<true, 64>(maps, p, stream);
+    return p.N <= kFewTokens<false> ? launch<false, 16>(maps, p, stream) : launch<false, 64>(maps, p, stream);
 }
 
 }  // namespace ep

@@ -105,8 +105,8 @@ SIZES_FP8 = [(1, 128, 128, 1, 1), (1, 1024, 512, 32, 4), (3, 256, 128, 5, 2), (1
 
 # the large form: many tokens of few experts, odd channels; weights past the small form's
 SIZES += [(5, 8, 8, 1, 1), (40, 264, 24, 5, 2), (33, 40, 200, 4, 3), (21, 1000, 328, 3, 1), (70, 2048, 16, 8, 8), (1, 4096, 2048, 16, 8),
-          (3, 2824, 1416, 40, 6), (65, 200, 264, 2, 1), (128, 136, 72, 2, 2)]
-SIZES_FP8 += [(5, 128, 128, 1, 1), (33, 1152, 256, 4, 3), (1, 7168, 2048, 8, 8), (5, 2176, 1920, 20, 4), (100, 384, 640, 3, 2)]
+          (3, 2824, 1416, 40, 6), (65, 200, 264, 2, 1), (128, 136, 72, 2, 2), (8, 72, 1016, 1, 1), (9, 72, 1016, 1, 1), (8, 1024, 512, 1024, 32)]
+SIZES_FP8 += [(4, 128, 384, 1, 1), (5, 128, 128, 1, 1), (4, 1024, 512, 1024, 32), (33, 1152, 256, 4, 3), (1, 7168, 2048, 8, 8), (5, 2176, 1920, 20, 4), (100, 384, 640, 3, 2)]
 
 
 @pytest.mark.parametrize("extras", [False, True])
