@@ -1645,7 +1645,7 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
     const ep_status s = check_grads(g, count, true);
     if (s != EP_OK) return s;
     if (!(limit >= 0.0f) || d_partials == nullptr || !aligned(d_partials, 8) || !aligned(d_norm, 4)) return EP_ERR_INVALID_ARG;
-    if (ep::launch_grad_clip(g, count, d_partials, limit, d_norm, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
+    if (ep::launch_grad_clip(g, count, d_partials, limit, d_norm, expert_sms(ctx), ctx->num_sms, (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return EP_ERR_CUDA;
     }

@@ -278,7 +278,7 @@ cudaError_t launch_linear_backward(const LinearBackwardParams &p, cudaStream_t s
 // ------------------------------------------------------------------ norm and clipping of gradients
 constexpr int kGradPartials = 1024;  // EP_GRAD_PARTIALS
 cudaError_t launch_grad_norm(const ep_grad *g, int count, double *partials, int sms, cudaStream_t stream);
-cudaError_t launch_grad_clip(const ep_grad *g, int count, const double *partials, float max_norm, float *norm, int sms,
+cudaError_t launch_grad_clip(const ep_grad *g, int count, const double *partials, float max_norm, float *norm, int sms, int all_sms,
                              cudaStream_t stream);
 
 // ------------------------------------------------------------------ whole layer for a few tokens

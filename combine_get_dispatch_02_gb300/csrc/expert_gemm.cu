@@ -2,6 +2,7 @@
 // expert, whose row groups are the receive rows base[e] .. base[e] + count[e]
 // of a layout (counts and bases are read on the device, never on the host).
 //   y[r]  = W[e] x[r]                        (bf16, or W stored transposed)
+//   y[r]  = act(z[r]) + res[r], z[r] = W[e] x[r] + b[e]   (linear: bf16, all in fp32 with one rounding)
 //   y[r]  = sum_b xs[r,b] ws[e,.,b] (Wq[e] xq[r])_b   (e4m3, 128-channel blocks b)
 //   h[r]  = cast(silu(g) * u), (g, u) = the two halves of the e4m3 product
 //   dW[e] = sum_r dy[r] x[r]^T
@@ -33,7 +34,8 @@
 // the tiles.  The accumulators are double buffered (2 x 256 columns).  A segment
 // of products shares an accumulator:
 //   bf16       the whole sum over k (the next tile's products run while this
-//              tile is written out)
+//              tile is written out; linear: and while bias, activation and residual,
+//              whose rows are asked for a step ahead, are done in the fp32 registers)
 //   e4m3       one block of 128 channels
 //   wgrad      the whole sum over rows; fp32 output: 256 rows, added up in
 //              registers (the tensor cores truncate when they add, and a long
@@ -49,6 +51,8 @@
 // the 1913 TFLOP/s bf16 peak, 1706 over seconds):
 //   bf16   262144 rows x 2048 x 7168    5.0 ms, 1.53 PFLOP/s (power limit), 4.2 ms cold
 //          256 experts x 16 rows x 7168 x 2048   1.10 ms, 6.9 TB/s
+//   linear 262144 rows x 2048 x 7168, bias, SiLU, z kept   5.2 ms, 1.48 PFLOP/s (power limit), 4.5 ms
+//          cold; 512 tokens, top-8 of 256, 7168 x 2048, bias and residual   1.10 ms, 7.0 TB/s
 //   wgrad  16 x 1024 rows x 2048 x 7168   278 us, 1.73 PFLOP/s; fp32 output 356 us
 //          (0.94 GB, which the tensor cores' work only partly covers), added 421 us
 //   e4m3   8192^3   483 us, 2.28 PFLOP/s (row form: reading the partial sums takes

@@ -18,8 +18,8 @@
 //   down product -- sum over k
 //
 // Measured (one GB300), bytes of the named experts' weights over the time: 128 tokens, top-8 of 256, 7168 x 2048,
-// FP8 1.81 ms, 6.1 TB/s; 32 tokens, top-6 of 64, 4096 x 1024, bf16 252 us, 6.0 TB/s; one token, top-8 of 256, 7168 x
-// 2048, FP8 74 us, 4.8 TB/s: HBM bounds the products, which leave 10 us before the first stage, at the meetings (2
+// FP8 1.81 ms, 6.1 TB/s; 32 tokens, top-6 of 64, 4096 x 1024, bf16 243 us, 6.2 TB/s; one token, top-8 of 256, 7168 x
+// 2048, FP8 72 us, 4.9 TB/s: HBM bounds the products, which leave 10 us before the first stage, at the meetings (2
 // us each, of which the ring covers 3 together) and behind the last.  Products on mma.sync with the codes
 // converted on the way took 92 us and 2.4 ms there.
 //
@@ -56,7 +56,7 @@ constexpr int kTile = 128;                   // weight rows of a job
 constexpr int kMostColumns = 64;             // most columns of a job
 constexpr int kWeightBytes = kTile * 128;
 constexpr int kSums = 4;                     // accumulators
-constexpr int kScales = 32;                  // stages whose tokens' scales are kept: the loaders are up to kStages ahead
+constexpr int kScales = 32;                  // stages whose tokens' scales are kept: the loaders are up to STAGES ahead
                                              // of the products, and those kSums + 1 ahead of the readers
 
 // Columns of an entry (codes or numbers whose sum it is).
@@ -949,7 +949,8 @@ cudaError_t launch(const Maps &maps, const ExpertLayerParams &p, cudaStream_t st
 //         8 entries per expert: 8 MB 20.6/19.4   12: 32 MB 40/25
 constexpr double kSmallBytes[2] = {96e6, 32e6};  // bf16, e4m3
 
-// Most tokens of a call whose jobs have 16 columns at most.
+// Most tokens of a call whose jobs have 16 columns at most (one token, top-8 of 256, 7168 x 2048, FP8: 72 us with
+// 12 stages, 74 with the 8 of the other form).
 template <bool FP8>
 constexpr int kFewTokens = kTokens<FP8, true, 16>;
 

@@ -214,6 +214,26 @@ def test_max_sms(buf):
         assert abs(float(small.clip_grads(grads, math.inf)) - want) <= NORM * want
 
 
+def test_many_short_ctas_and_few_long_ones_clip_alike(buf):
+    # 150 MB into other tensors: more CTAs than fit at a time, and with 7 SMs a few that go through all
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    grads = [torch.randn(n, device="cuda", generator=gen).to(t) for n, t in ((30_000_001, torch.float32), (77, B16), (15_000_003, B16))]
+    want = norm_of(grads)
+    partials = torch.empty(ep.EP_GRAD_PARTIALS, dtype=torch.float64, device="cuda")
+    ep.ep_grad_norm(buf.ctx, ep.grad_list(grads), partials)
+    outs = []
+    for b in (buf, Buffer(1, 1, 128, 1, 1, max_sms=7)):
+        out, norm = [torch.full_like(g, math.nan) for g in grads], torch.zeros(1, device="cuda")
+        ep.ep_grad_clip(b.ctx, ep.grad_list(grads, out), partials, 0.25 * want, norm)
+        assert abs(float(norm) - want) <= NORM * want
+        outs.append(out)
+    for g, a, b in zip(grads, *outs):
+        assert torch.equal(a, b)
+        # the factor's own errors as above, and the rounding of the result
+        rel = NORM + 2.0 ** -22 + torch.finfo(g.dtype).eps / 2
+        assert_close(a, g.double() * 0.25, rel * g.double().abs() * 0.25 * 1.01, "scaled")
+
+
 def test_refusals(buf):
     a, b = torch.ones(100, device="cuda"), torch.ones(100, device="cuda", dtype=B16)
     for grads, out in (([a.cpu()], None), ([a.view(10, 10).T], None), ([a.half()], None), ([a, b], [a]), ([a], [b]), ([a], [a[:50]])):
