@@ -302,10 +302,16 @@ __device__ __forceinline__ void add_residual(float (&v)[32], const Residual &r, 
     }
 }
 
+// Of the tokens that are there, 8 at a time: with few, most of the time is fetching the code (4 tokens, top-4 of 32,
+// 1024 x 1024, GELU: 10.8 us for all 32, 9.0).
 template <Act ACT>
-__device__ __forceinline__ void activate32(float (&v)[32]) {
+__device__ __forceinline__ void activate32(float (&v)[32], int tokens) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate<ACT>(v[i]);
+    for (int i = 0; i < 32; i += 8) {
+        if (i >= tokens) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i + j] = activate<ACT>(v[i + j]);
+    }
 }
 
 // Two pieces of 16 bytes of one row, as one 32-byte store where `whole` (the
@@ -875,10 +881,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                             store_tokens(v, out, lane, static_cast<__nv_bfloat16 *>(p.z) + (ti.row0 + c * 32) * p.n + wc, p.n,
                                          ti.valid - c * 32, p.n - wc);
                         switch (p.act) {
-                            case Act::kRelu: activate32<Act::kRelu>(v); break;
-                            case Act::kGelu: activate32<Act::kGelu>(v); break;
-                            case Act::kGeluTanh: activate32<Act::kGeluTanh>(v); break;
-                            case Act::kSilu: activate32<Act::kSilu>(v); break;
+                            case Act::kRelu: activate32<Act::kRelu>(v, ti.valid - c * 32); break;
+                            case Act::kGelu: activate32<Act::kGelu>(v, ti.valid - c * 32); break;
+                            case Act::kGeluTanh: activate32<Act::kGeluTanh>(v, ti.valid - c * 32); break;
+                            case Act::kSilu: activate32<Act::kSilu>(v, ti.valid - c * 32); break;
                             default: break;
                         }
                         if (p.residual != nullptr) {
