@@ -506,7 +506,7 @@ class Buffer:
     def expert_mlp(self, x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, handle: Handle, biases=None):
         """Gated experts in bf16 on the received rows x [rows, H]: w_gate_up
         [E, 2*inner, H], w_down [E, H, inner]; biases = ([E, 2*inner], [E,
-        H]), bf16 or fp32.  Returns (y [rows, H], saved) with what
+        H]), bf16 or fp32, or None for either.  Returns (y [rows, H], saved) with what
         expert_mlp_backward needs."""
         if biases is None:
             gu = self.expert_gemm(x, w_gate_up, handle)
@@ -522,13 +522,13 @@ class Buffer:
         for dy [rows, H].  The weight gradients are fp32; ``grads`` = a pair
         of fp32 tensors to add them to.  ``bias_grads`` = a pair of fp32
         tensors ([E, 2*inner], [E, H]) for the biases' gradients, written, or
-        added to where ``grads`` is given."""
+        added to where ``grads`` is given; either may be None, as in ``biases``."""
         x, gu = saved
         dgu, h = self.expert_swiglu_backward(gu, self.expert_gemm(dy, w_down, handle, transpose_w=True), handle)
         acc = grads is not None
-        if bias_grads is not None:
-            self.expert_linear_backward(dgu, None, handle, dbias=bias_grads[0], accumulate=acc)
-            self.expert_linear_backward(dy, None, handle, dbias=bias_grads[1], accumulate=acc)
+        for d, to in zip((dgu, dy), bias_grads or ()):
+            if to is not None:
+                self.expert_linear_backward(d, None, handle, dbias=to, accumulate=acc)
         g_gate_up, g_down = grads if acc else (None, None)
         dw_down = self.expert_wgrad(dy, h, handle, out=g_down, accumulate=acc)
         dw_gate_up = self.expert_wgrad(dgu, x, handle, out=g_gate_up, accumulate=acc)

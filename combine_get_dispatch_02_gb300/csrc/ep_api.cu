@@ -1565,6 +1565,7 @@ ep_status ep_expert_linear(ep_ctx *ctx, const ep_handle *handle, const void *d_x
     if ((bias_fp32 != 0 && bias_fp32 != 1) || activation < EP_ACT_NONE || activation > EP_ACT_SILU) return EP_ERR_INVALID_ARG;
     if (handle->tokens_per_rank == 0) return EP_OK;
     if (d_x == nullptr || d_w == nullptr || d_y == nullptr || d_z == d_y) return EP_ERR_INVALID_ARG;
+    if (d_x == d_y || d_x == d_z) return EP_ERR_INVALID_ARG;  // other tiles still read the row
     if (!aligned(d_x, 16) || !aligned(d_w, 16) || !aligned(d_y, 16) || !aligned(d_bias, bias_fp32 ? 4 : 2) ||
         !aligned(d_residual, 16) || !aligned(d_z, 16))
         return EP_ERR_INVALID_ARG;

@@ -387,7 +387,8 @@ ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, vo
  *                   or _SILU (z / (1 + exp(-z)))
  *     d_residual    device bf16 [rows, n] or NULL; may be d_y itself
  *     d_z           device bf16 [rows, n] or NULL: z, for the backward pass
- *     d_y           device bf16 [rows, n]
+ *     d_y           device bf16 [rows, n]; neither it nor d_z may be d_x, nor one the
+ *                   other (EP_ERR_INVALID_ARG)
  * ep_expert_linear_backward: dz[r] = dy[r] act'(z[r]) rounded to bf16, and the
  *   bias gradient dbias[e] = sum over the rows of e of the same before the
  *   rounding, in fp32 (RELU: the slope at 0 is 0).  The residual's gradient is dy.

@@ -109,6 +109,11 @@ SIZES += [(5, 8, 8, 1, 1), (40, 264, 24, 5, 2), (33, 40, 200, 4, 3), (21, 1000, 
 SIZES_FP8 += [(4, 128, 384, 1, 1), (5, 128, 128, 1, 1), (4, 1024, 512, 1024, 32), (33, 1152, 256, 4, 3), (1, 7168, 2048, 8, 8), (5, 2176, 1920, 20, 4), (100, 384, 640, 3, 2)]
 
 
+# the most tokens, experts and entries of a token at a time
+SIZES += [(128, 512, 264, 1024, 32)]
+SIZES_FP8 += [(128, 512, 256, 1024, 32)]
+
+
 @pytest.mark.parametrize("extras", [False, True])
 @pytest.mark.parametrize("N,H,I,E,K", SIZES)
 def test_layer_bf16(N, H, I, E, K, extras):

@@ -387,3 +387,37 @@ def test_empty_calls():
     assert bool((out == -777.0).all()) and bool((db == 5.0).all())
     buf.expert_linear_backward(z, z, h, activation="relu", out=out, dbias=db)
     assert bool((out == -777.0).all()) and bool((db == 0.0).all()) and buf.device_status() == ep.EP_OK
+
+
+def test_the_input_is_no_output():
+    buf, h, grp = group([3, 5])
+    x, w, out = receive(buf.rows, 40, grp, 1), weights(2, 40, 40, 2), sentinel((buf.rows, 40))
+    kept = x.clone()
+    for kw in ({"out": x}, {"out": out, "z": x}):
+        with pytest.raises(ep.EPError) as e:
+            buf.expert_linear(x, w, h, activation="relu", **kw)
+        assert e.value.status == ep.EP_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.equal(x.view(torch.int16), kept.view(torch.int16)) and bool((out == -777.0).all())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_a_bias_in_one_of_the_two_products(accumulate):
+    """The other one's is left out, forward and backward: the same bits as with zeros for it."""
+    buf, h, grp = group([9, 0, 40, 17])
+    H, I = 64, 48
+    x, dy = receive(buf.rows, H, grp, 1), receive(buf.rows, H, grp, 2)
+    w13, w2 = weights(4, 2 * I, H, 3), weights(4, H, I, 4)
+    used = in_use(buf.rows, grp)
+    for at, n in ((0, 2 * I), (1, H)):
+        b, zeros = bias_of(4, n, 5, torch.bfloat16), torch.zeros(4, (H, 2 * I)[at], device="cuda")
+        some, both = ((b, None), (b, zeros)) if at == 0 else ((None, b), (zeros, b))
+        y, saved = buf.expert_mlp(x, w13, w2, h, biases=some)
+        y0, saved0 = buf.expert_mlp(x, w13, w2, h, biases=both)
+        assert torch.equal(y[used], y0[used])
+        grads = tuple(torch.zeros(t.shape, device="cuda") for t in (w13, w2)) if accumulate else None
+        db, db0 = torch.zeros(4, n, device="cuda"), [torch.zeros(4, c, device="cuda") for c in (2 * I, H)]
+        dx, *_ = buf.expert_mlp_backward(dy, saved, w13, w2, h, grads=grads, bias_grads=(db, None) if at == 0 else (None, db))
+        dx0, *_ = buf.expert_mlp_backward(dy, saved0, w13, w2, h, grads=grads, bias_grads=db0)
+        assert torch.equal(dx[used], dx0[used]) and torch.equal(db, db0[at])
+    assert buf.device_status() == ep.EP_OK
