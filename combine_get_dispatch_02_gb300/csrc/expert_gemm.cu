@@ -303,14 +303,18 @@ __device__ __forceinline__ void add_residual(float (&v)[32], const Residual &r, 
 }
 
 // Of the tokens that are there, 8 at a time: with few, most of the time is fetching the code (4 tokens, top-4 of 32,
-// 1024 x 1024, GELU: 10.8 us for all 32, 9.0).
+// 1024 x 1024, GELU by erfcf: 10.8 us for all 32, 9.0).
 template <Act ACT>
 __device__ __forceinline__ void activate32(float (&v)[32], int tokens) {
 #pragma unroll
     for (int i = 0; i < 32; i += 8) {
         if (i >= tokens) break;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i + j] = activate<ACT>(v[i + j]);
+        for (int j = 0; j < 8; j += 2) {
+            const uint64_t y = activate2<ACT>(two(v[i + j], v[i + j + 1]));
+            v[i + j] = lo2(y);
+            v[i + j + 1] = hi2(y);
+        }
     }
 }
 
