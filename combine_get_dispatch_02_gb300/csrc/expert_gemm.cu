@@ -27,7 +27,7 @@
 // with its token tiles fastest and drawn in that order, so pairs that run at the
 // same time share its weights in L2.
 //
-// Warps of a CTA: READ (8, e4m3 row form 16) that read the accumulators out of
+// Warps of a CTA: READ (8, e4m3 row form and linear 16) that read the accumulators out of
 // tensor memory, then one that loads (tensor maps, 128-byte swizzle), one that
 // issues the products (in the pair's first CTA), one that brings the e4m3
 // scales or clears the rows past the end of an expert (wgrad), one that draws
@@ -120,18 +120,22 @@ struct Shape {
     static constexpr bool COL = FP8 && !ALT;         // two M-side operands: gate and up product, or 2 x 256 weight rows
     static constexpr bool A_MN = OP == ExpertOp::kBf16T || WG;
     static constexpr bool B_MN = WG;
-    static constexpr int READ = ROW ? 16 : 8;       // warps that read the accumulators
+    // Warps that read the accumulators: 16 where there is work to do on them (linear, 32768 rows x 2048, SiLU and z
+    // kept: k = 256 76 us, with 8 warps 92; k = 1024 107 and 111; k = 4096 332 and 333; 131072 rows x 4096 x 1024, GELU,
+    // z and residual 1.01 ms and 1.13)
+    static constexpr bool MANY = ROW || LIN;
+    static constexpr int READ = MANY ? 16 : 8;
     static constexpr int THREADS = (READ + 4) * 32;
-    // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72 (row form: 640 x 96, split
+    // registers per thread: 384 x 168 at launch, split 256 x 216 + 128 x 72 (row form, linear: 640 x 96, split
     // 512 x 104 + 128 x 64)
-    static constexpr int REGS_READ = ROW ? 104 : 216, REGS_REST = ROW ? 64 : 72;
+    static constexpr int REGS_READ = MANY ? 104 : 216, REGS_REST = MANY ? 64 : 72;
     static constexpr int TOKENS = COL ? 128 : 256;            // most rows of a tile
     // weight rows (gate: channels of h) of a pair's tile
     static constexpr int WROWS = COL && !GATE ? 512 : GATE && ROW ? 128 : 256;
     static constexpr int A_BYTES = COL ? 32768 : 16384;       // per CTA and stage
     static constexpr int B_BYTES = ROW ? 16384 : TOKENS / 2 * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : WG ? 4096 : 2048;  // per reading warp
+    static constexpr int OUT_BYTES = ROW ? (GATE ? 0 : 4096) : COL ? 512 : WG ? 4096 : LIN ? 1024 : 2048;  // per reading warp
     static constexpr int STAGES = ROW && !GATE ? 4 : COL ? 5 : 6;
     static constexpr int SCALES = FP8 ? 2 * kScaleGroup * 256 * 4 : 0;
     static constexpr int AMAX = GATE ? 2 * 4 * 128 * 4 + (COL ? READ * 64 * 4 : 0) : 0;
@@ -243,14 +247,15 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 
 // Write 32 tokens x 32 channels of a warp (lane = channel, v[i] = token i) as
 // bf16 rows: neighbouring lanes swap halves so that each holds channel pairs,
-// the pairs go through 2 KB of shared memory (64 bytes per token, free of bank
-// conflicts), and 4 lanes store the 64 bytes of a token.
-__device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf, int lane, __nv_bfloat16 *dst, int64_t ld,
+// the pairs go through shared memory (64 bytes per token, free of bank conflicts), and
+// 4 lanes store the 64 bytes of a token.
+template <int T>
+__device__ __forceinline__ void store_tokens(const float (&v)[T], uint32_t buf, int lane, __nv_bfloat16 *dst, int64_t ld,
                                              int tokens, int channels) {
     const bool odd = lane & 1;
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < T / 4; ++j) {
         const uint32_t a = bf16x2(v[4 * j], v[4 * j + 2]), b = bf16x2(v[4 * j + 1], v[4 * j + 3]);
         const uint32_t keep = odd ? b : a;
         const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 1);
@@ -263,7 +268,7 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf,
     }
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < T / 8; ++j) {
         const int tok = (lane >> 2) + 8 * j, c = (lane & 3) * 8;
         uint4 q;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -273,29 +278,32 @@ __device__ __forceinline__ void store_tokens(const float (&v)[32], uint32_t buf,
     }
 }
 
-// The same 32 tokens x 32 channels the other way: loaded like the stores above, and,
-// through the same 2 KB, added to v.
+// linear: a step of a reading warp is 16 tokens x 32 channels.
+constexpr int kStep = 16;
+
+// A step's tokens the other way: loaded like the stores above, and, through the same
+// 1 KB, added to v.
 struct Residual {
-    uint4 q[4];
+    uint4 q[kStep / 8];
 };
 __device__ __forceinline__ void load_residual(Residual &r, int lane, const __nv_bfloat16 *src, int64_t ld, int tokens, int channels) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kStep / 8; ++j) {
         const int tok = (lane >> 2) + 8 * j, c = (lane & 3) * 8;
         r.q[j] = make_uint4(0, 0, 0, 0);
         if (tok < tokens && c < channels) r.q[j] = *reinterpret_cast<const uint4 *>(src + tok * ld + c);
     }
 }
-__device__ __forceinline__ void add_residual(float (&v)[32], const Residual &r, uint32_t buf, int lane) {
+__device__ __forceinline__ void add_residual(float (&v)[kStep], const Residual &r, uint32_t buf, int lane) {
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kStep / 8; ++j)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + ((lane >> 2) + 8 * j) * 64 + (lane & 3) * 16), "r"(r.q[j].x),
                      "r"(r.q[j].y), "r"(r.q[j].z), "r"(r.q[j].w)
                      : "memory");
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < kStep; ++i) {
         uint16_t h;
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(buf + i * 64 + lane * 2));
         v[i] += __uint_as_float((uint32_t)h << 16);
@@ -305,9 +313,9 @@ __device__ __forceinline__ void add_residual(float (&v)[32], const Residual &r, 
 // Of the tokens that are there, 8 at a time: with few, most of the time is fetching the code (4 tokens, top-4 of 32,
 // 1024 x 1024, GELU by erfcf: 10.8 us for all 32, 9.0).
 template <Act ACT>
-__device__ __forceinline__ void activate32(float (&v)[32], int tokens) {
+__device__ __forceinline__ void activate(float (&v)[kStep], int tokens) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
+    for (int i = 0; i < kStep; i += 8) {
         if (i >= tokens) break;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -854,49 +862,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shape<OP, ALT>::THRE
                     fill_box(line, out, lane);
                     if (lane == 0) tma_store_3d(&maps.m[5], out, ti.c0 + col, wc, ti.e);
                 }
+            } else if constexpr (S::LIN) {
+                const uint32_t buf = seg & 1;
+                // asked for before the products are there: the bias of the lane's channel, the residual's first step
+                // (the others into L2)
+                float bias = 0.0f;
+                Residual res;
+                const int64_t at = ti.row0 * p.n + wc;
+                const __nv_bfloat16 *const from = static_cast<const __nv_bfloat16 *>(p.residual) + at;
+                if (p.bias != nullptr && wc + lane < p.n) {
+                    const int64_t c = (int64_t)ti.e * p.n + wc + lane;
+                    bias = p.bias_fp32 ? static_cast<const float *>(p.bias)[c] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[c]);
+                }
+                if (p.residual != nullptr) {
+                    load_residual(res, lane, from + (int64_t)hw * kStep * p.n, p.n, ti.valid - hw * kStep, p.n - wc);
+                    for (int i = lane; i < 3 * kStep; i += 32) {
+                        const int t = (hw + 4 + i / kStep * 4) * kStep + i % kStep;
+                        if (t < ti.valid && wc < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + (int64_t)t * p.n));
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
+                if (!ok) break;
+                fence_after();
+                for (int c = hw; c * kStep < ti.valid; c += 4) {
+                    const int tokens = ti.valid - c * kStep;
+                    uint32_t raw[kStep];
+                    float v[kStep];
+                    tmem_get16(raw, lanes + buf * 256 + c * kStep);
+#pragma unroll
+                    for (int i = 0; i < kStep; ++i) v[i] = __uint_as_float(raw[i]) + bias;
+                    if (p.z != nullptr)
+                        store_tokens(v, out, lane, static_cast<__nv_bfloat16 *>(p.z) + at + (int64_t)c * kStep * p.n, p.n, tokens, p.n - wc);
+                    switch (p.act) {
+                        case Act::kRelu: activate<Act::kRelu>(v, tokens); break;
+                        case Act::kGelu: activate<Act::kGelu>(v, tokens); break;
+                        case Act::kGeluTanh: activate<Act::kGeluTanh>(v, tokens); break;
+                        case Act::kSilu: activate<Act::kSilu>(v, tokens); break;
+                        default: break;
+                    }
+                    if (p.residual != nullptr) {
+                        add_residual(v, res, out, lane);
+                        load_residual(res, lane, from + (int64_t)(c + 4) * kStep * p.n, p.n, tokens - 4 * kStep, p.n - wc);
+                    }
+                    store_tokens(v, out, lane, static_cast<__nv_bfloat16 *>(p.y) + at + (int64_t)c * kStep * p.n, p.n, tokens, p.n - wc);
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_remote(tempty0 + 8 * buf);
+                ++seg;
             } else if constexpr (S::SEG == 0) {
                 __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y);
                 const uint32_t buf = seg & 1;
-                [[maybe_unused]] float bias = 0.0f;
-                [[maybe_unused]] Residual res;
-                [[maybe_unused]] const __nv_bfloat16 *from = nullptr;
-                if constexpr (S::LIN) {
-                    // asked for before the products are there
-                    if (p.bias != nullptr && wc + lane < p.n) {
-                        const int64_t at = (int64_t)ti.e * p.n + wc + lane;
-                        bias = p.bias_fp32 ? static_cast<const float *>(p.bias)[at]
-                                           : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.bias)[at]);
-                    }
-                    if (p.residual != nullptr) {
-                        from = static_cast<const __nv_bfloat16 *>(p.residual) + ti.row0 * p.n + wc;
-                        load_residual(res, lane, from + (int64_t)hw * 32 * p.n, p.n, ti.valid - hw * 32, p.n - wc);
-                    }
-                }
                 ok = __all_sync(0xFFFFFFFFu, wait(b_tfull + 8 * buf, (seg >> 1) & 1));
                 if (!ok) break;
                 fence_after();
                 for (int c = hw; c < chunks; c += 2) {
                     float v[32];
                     tmem_get32(v, lanes + buf * 256 + c * 32);
-                    if constexpr (S::LIN) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += bias;
-                        if (p.z != nullptr)
-                            store_tokens(v, out, lane, static_cast<__nv_bfloat16 *>(p.z) + (ti.row0 + c * 32) * p.n + wc, p.n,
-                                         ti.valid - c * 32, p.n - wc);
-                        switch (p.act) {
-                            case Act::kRelu: activate32<Act::kRelu>(v, ti.valid - c * 32); break;
-                            case Act::kGelu: activate32<Act::kGelu>(v, ti.valid - c * 32); break;
-                            case Act::kGeluTanh: activate32<Act::kGeluTanh>(v, ti.valid - c * 32); break;
-                            case Act::kSilu: activate32<Act::kSilu>(v, ti.valid - c * 32); break;
-                            default: break;
-                        }
-                        if (p.residual != nullptr) {
-                            add_residual(v, res, out, lane);
-                            if (c + 2 < chunks)
-                                load_residual(res, lane, from + (int64_t)(c + 2) * 32 * p.n, p.n, ti.valid - (c + 2) * 32, p.n - wc);
-                        }
-                    }
                     store_tokens(v, out, lane, y + (ti.row0 + c * 32) * p.n + wc, p.n, ti.valid - c * 32, p.n - wc);
                 }
                 fence_before();
