@@ -51,7 +51,7 @@
 // the 1913 TFLOP/s bf16 peak, 1706 over seconds):
 //   bf16   262144 rows x 2048 x 7168    5.0 ms, 1.53 PFLOP/s (power limit), 4.2 ms cold
 //          256 experts x 16 rows x 7168 x 2048   1.10 ms, 6.9 TB/s
-//   linear 262144 rows x 2048 x 7168, bias, SiLU, z kept   5.2 ms, 1.48 PFLOP/s (power limit), 4.5 ms
+//   linear 262144 rows x 2048 x 7168, bias, SiLU, z kept   5.2 ms, 1.48 PFLOP/s (power limit), 4.3 ms
 //          cold; 512 tokens, top-8 of 256, 7168 x 2048, bias and residual   1.10 ms, 7.0 TB/s
 //   wgrad  16 x 1024 rows x 2048 x 7168   278 us, 1.73 PFLOP/s; fp32 output 356 us
 //          (0.94 GB, which the tensor cores' work only partly covers), added 421 us
