@@ -300,12 +300,15 @@ struct ExpertLayerParams {
     float *sums;               // [N * K][rows of all tiles] sums of the product at hand (small form: [N * K, H] outputs)
     float *pieces;             // [SMs][64][128] sums of the job that an SM does not begin
     float *h_scale;            // [N * K][I / 128] what a code is worth
+    void *xq;                  // [N * K][2][H] tokens by entry as codes (e4m3 weights, more than a few tokens)
+    float *x_scale;            // [N * K][H / 128]
     uint32_t *done;            // small form: [ceil(H / 32)] units of each tile of output rows that are done
     uint32_t *barrier;         // grid barrier and count of the CTAs that are done with it: both zero
                                // between launches, each launch puts them back; nullptr: none free (the
                                // workspace's then)
     int32_t N, K, H, I, E;
     int32_t sms;
+    bool laid;                 // xq is used
     int32_t withhold;          // test hook: expert whose weights are never loaded (-1: none)
     int64_t wait_cycles;       // bound of each wait in SM clocks (kExpertWaitCycles)
     uint32_t *status;

@@ -69,6 +69,7 @@ template <bool FP8, int C>
 struct Shape {
     static constexpr int STAGE = kWeightBytes + C * 128;
     static constexpr int STAGES = C == 16 ? 12 : 8;
+    static constexpr bool LAID = FP8 && C != 16;  // has the form that lays the tokens out (p.laid)
     static constexpr size_t fixed = 1024 + (size_t)STAGES * STAGE;
     static_assert(STAGES + kSums + 1 <= kScales, "scales are overwritten before they are read");
 };
@@ -318,6 +319,7 @@ struct Walk {
 struct Maps {
     CUtensorMap w[2];  // gate and up, down: [E, rows, channels] in boxes of 64 rows x 128 bytes, swizzled
     CUtensorMap h;     // h laid out by entry: [entries * R, channels] in boxes of 16 rows x 128 bytes
+    CUtensorMap x;     // tokens laid out by entry, the same
 };
 
 template <int C>
@@ -385,6 +387,8 @@ __device__ __forceinline__ float2 block_scale(const float (&v)[N]) {
 template <bool FP8, int C>
 __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_constant__ Maps maps, const ExpertLayerParams p) {
     constexpr int kStages = Shape<FP8, C>::STAGES, kStage = Shape<FP8, C>::STAGE;
+    const bool laid = Shape<FP8, C>::LAID && p.laid;
+    const int at_gate = laid ? 2 : 1, at_h = at_gate + 1, at_down = at_gate + 2;  // meetings: gate done, h laid out, down done
     extern __shared__ uint8_t dyn[];
     __shared__ Bars<C> bars;
     uint8_t *const ring = reinterpret_cast<uint8_t *>(((uintptr_t)dyn + 1023) & ~(uintptr_t)1023);
@@ -406,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         prefetch_map(&maps.w[0]);
         prefetch_map(&maps.w[1]);
         prefetch_map(&maps.h);
+        if (laid) prefetch_map(&maps.x);
     }
     if (warp == kWarpMma) tmem_alloc_one(saddr(&bars.tmem), kSums * C);
     pdl_wait();
@@ -516,12 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         const bool spare = warp == kWarpSpare;
         uint32_t seg = 0, stages = 0, brought = 0;  // accumulators read; stages gone by and brought (token warps)
         // Comes to the i-th meeting: what this CTA's workers wrote can be read behind it.  Not before all have
-        // come to the one before (to the third: behind the second this CTA does not wait): a CTA without a share
-        // would be counted for a slow one.
+        // come to the one before, for which this CTA has not waited where only its tokens do: a CTA without a
+        // share would be counted for a slow one.
         auto come = [&](uint32_t i) {
             workers_sync();
             if (wid == 0) {
-                if (i == 3 && !met(2)) ok = false;
+                if ((i == at_down || (laid && i == at_gate)) && !met(i - 1)) ok = false;
                 asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.barrier) : "memory");
             }
         };
@@ -552,15 +557,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
             const uint32_t u = ((uint32_t)r.before[down][w.d] * tiles[down] + tile * w.parts + w.part) * lines[down];
             return make_int2(shares[down].owner(u), shares[down].owner(u + lines[down] - 1));
         };
-        // Tokens of every fourth stage, rows of 128 bytes, swizzled as the weights are.  Gate: x, by this warp; down:
-        // h, by tensor map, once all have laid theirs out.
+        // Tokens of every eighth stage, rows of 128 bytes, swizzled as the weights are.  Gate: x, by this warp; down (and
+        // gate, laid): by tensor map, once all have laid theirs out.
         auto bring = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
             constexpr int R = kParts<FP8, DOWN>;
             Walk<FP8, C> w;
             if (!begin(w, DOWN)) return;
-            if constexpr (DOWN) {
-                if (lane == 0 && !met(2)) ok = false;
+            if (DOWN || laid) {
+                if (lane == 0 && !met(DOWN ? at_h : 1)) ok = false;
                 asm volatile("fence.proxy.async;" ::: "memory");
                 ok = __all_sync(0xFFFFFFFFu, ok);
             }
@@ -568,16 +573,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 for (int l = w.l0; l < w.l1; ++l, ++stages) {
                     if (stages % kTokenWarps != warp - kWarpTokens) continue;
                     const uint32_t slot = stages % kStages, bar = b_full + 8 * slot, at = saddr(ring + slot * kStage) + kWeightBytes;
-                    if constexpr (DOWN) {
+                    if (DOWN || laid) {
+                        const CUtensorMap *const map = DOWN ? &maps.h : &maps.x;
                         float s = 0.0f;
-                        if (FP8 && lane < w.count) s = __ldcg(p.h_scale + (int64_t)(w.first + lane) * lines[1] + l);
+                        if (FP8 && lane < w.count) s = __ldcg((DOWN ? p.h_scale : p.x_scale) + (int64_t)(w.first + lane) * lines[DOWN] + l);
                         ok = wait(b_empty + 8 * slot, (stages / kStages & 1) ^ 1);
                         if (!ok) return;
                         if (elect()) {
                             // expected now, arrived for below
                             const int boxes = (w.count * R + 15) / 16;
                             asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(boxes * 2048) : "memory");
-                            for (int i = 0; i < boxes; ++i) load_box(at + i * 2048, &maps.h, l * kLine<FP8>, w.first * R + i * 16, bar);
+                            for (int i = 0; i < boxes; ++i) load_box(at + i * 2048, map, l * kLine<FP8>, w.first * R + i * 16, bar);
                         }
                         __syncwarp();
                         if (FP8 && lane < w.count) bars.scale[stages % kScales][lane] = s;
@@ -628,18 +634,28 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                                                                           (int64_t)(r.list[w.first + i] >> 5) * p.H + c));
                             return q;
                         };
-                        uint4 next = get(lane >> 3);
+                        constexpr int U = C == 16 ? 2 : 8;  // loads in flight (128 tokens, top-2 of 8, 4096 x 4096: 1 227 us, 8 176)
+                        uint4 next[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) next[u] = get(u * 4 + (lane >> 3));
                         ok = wait(b_empty + 8 * slot, (stages / kStages & 1) ^ 1);
                         if (!ok) return;
-                        for (int i = lane >> 3; i < ((w.count + 3) & ~3); i += 4) {
-                            const uint4 q = next;
-                            if (i + 4 < w.count) next = get(i + 4);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 128 + (((lane & 7) ^ (i & 7)) << 4)),
-                                         "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
-                                         : "memory");
+                        const int rows = (w.count + 3) & ~3;
+#pragma unroll 1
+                        for (int i0 = lane >> 3; i0 < rows; i0 += 4 * U) {
+#pragma unroll
+                            for (int u = 0; u < U; ++u) {
+                                const int i = i0 + u * 4;
+                                if (i >= rows) break;
+                                const uint4 q = next[u];
+                                next[u] = get(i + 4 * U);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + i * 128 + (((lane & 7) ^ (i & 7)) << 4)),
+                                             "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                                             : "memory");
+                            }
                         }
                     }
-                    if constexpr (!DOWN) fence_async_shared();
+                    if (!DOWN && !laid) fence_async_shared();
                     __syncwarp();
                     if (lane == 0) bar_arrive(bar);
                     ++brought;
@@ -739,9 +755,32 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 return q;
             };
             const int it0 = spare ? 0 : cta * (kWorkers / 32) + (wid >> 5);
+            if (laid) {
+                // a warp takes 128 channels of a token, 4 to a lane, for all its entries
+                for (int it = it0; it < p.N * lines[0] && !spare; it += warps) {
+                    const int t = it / lines[0], l = it - t * lines[0];
+                    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)t * p.H + l * 128) + lane);
+                    float v[4] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+                    const float2 s = block_scale(v);
+                    uint32_t c[2];
+                    codes<2>(v, s.x, [&](int k, int, uint32_t w) { c[k] = w; });
+                    for (int k = 0; k < p.K; ++k) {
+                        const uint32_t i = r.spot[t * p.K + k];
+                        if (i == 0xFFFFu) continue;
+                        uint8_t *const dst = static_cast<uint8_t *>(p.xq) + (int64_t)i * 2 * p.H + l * 128 + lane * 4;
+                        *reinterpret_cast<uint32_t *>(dst) = c[0];
+                        *reinterpret_cast<uint32_t *>(dst + p.H) = c[1];
+                        if (lane == 0) p.x_scale[(int64_t)i * lines[0] + l] = s.y;
+                    }
+                }
+                if (!spare) {
+                    asm volatile("fence.proxy.async;" ::: "memory");  // read by copies
+                    come(1);
+                }
+            }
             if (!spare) product(std::false_type{});
             Item item = look(it0);
-            if (!spare) meet(1);
+            if (!spare) meet(at_gate);
             for (int it = it0; it < entries * blocks; it += warps) {
                 if (it != it0) item = look(it);
                 const int i = it / blocks, c = (it - i * blocks) * 128 + lane * 4;
@@ -800,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
             }
             if (!spare) {
                 asm volatile("fence.proxy.async;" ::: "memory");  // h is read by copies
-                come(2);
+                come(at_h);
                 product(std::true_type{});
             }
         }
@@ -831,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
         };
         const int it0 = spare ? 0 : cta * (kWorkers / 32) + (wid >> 5);
         Item item = look(it0);
-        if (r.D > 0 && !spare) meet(3);
+        if (r.D > 0 && !spare) meet(at_down);
         for (int it = it0; it < p.N * tiles[1]; it += ctas * (kWorkers / 32)) {
             if (it != it0) item = look(it);
             const int t = it / tiles[1], c = (it - t * tiles[1]) * kTile + lane * 4;
@@ -963,6 +1002,14 @@ void allow_smem() {
         cudaGetLastError();
 }
 
+// e4m3: from this many times on that an SM turns 128 channels of an entry into codes for a stage of the gate
+// product, all SMs lay the tokens out as codes once, before, and meet once more.  Us, each tile its own / laid out
+// (times; tokens, top-k of experts, channels):
+//   65 (46, 2 of 7, 1152 x 768) 22.4/24.9   161 (8, 6 of 64, 4096 x 1024) 92/94   471 (5, 8 of 32, 7168 x 2048) 168.6/170.9
+//   1160 (105, 8 of 14, 896 x 1920) 79.0/72.1   1725 (64, 2 of 8, 4096 x 4096) 114/103   3018 (32, 8 of 256, 7168 x 2048)
+//   1096/1084   3449 (128, 2 of 8, 4096 x 4096) 198/161   12072 (128, 8 of 32, 7168 x 2048) 620/490
+constexpr double kLaidStages = 800;
+
 // The workspace's parts, each on a 256-byte boundary: sets their addresses from `base` on, returns the size.
 size_t lay_out(ExpertLayerParams &p, uint8_t *base) {
     const size_t M = (size_t)p.N * p.K;
@@ -977,6 +1024,8 @@ size_t lay_out(ExpertLayerParams &p, uint8_t *base) {
     p.sums = reinterpret_cast<float *>(take(M * (gate > down ? gate : down) * 4));
     p.pieces = reinterpret_cast<float *>(take((size_t)p.sms * kMostColumns * kTile * 4));
     p.h_scale = reinterpret_cast<float *>(take(M * ((p.I + 127) / 128) * 4));
+    p.xq = take(M * p.H * 2);
+    p.x_scale = reinterpret_cast<float *>(take(M * ((p.H + 127) / 128) * 4));
     uint32_t *const barrier = reinterpret_cast<uint32_t *>(take(8));
     if (p.barrier == nullptr) p.barrier = barrier;
     return at;
@@ -1016,8 +1065,9 @@ cudaError_t launch_expert_layer(ExpertLayerParams p, void *workspace, cudaStream
     Maps maps;
     if (!encode_rows(&maps.w[0], p.w_gate_up, es, p.H, 2 * (int64_t)p.I, p.E, kTile / 2) ||
         !encode_rows(&maps.w[1], p.w_down, es, p.I, p.H, p.E, kTile / 2) ||
-        !encode_rows(&maps.h, p.h, es, p.I, M * (fp8 ? 4 : 2), 0, 16))
+        !encode_rows(&maps.h, p.h, es, p.I, M * (fp8 ? 4 : 2), 0, 16) || !encode_rows(&maps.x, p.xq, es, p.H, M * (fp8 ? 2 : 1), 0, 16))
         return cudaErrorInvalidValue;
+    p.laid = (double)M * ((p.I + kTile / 2 - 1) / (kTile / 2)) * (p.H / 128) >= kLaidStages * p.sms;
     if (fp8) return p.N <= kFewTokens<true> ? launch<true, 16>(maps, p, stream) : launch<true, 64>(maps, p, stream);
     return p.N <= kFewTokens<false> ? launch<false, 16>(maps, p, stream) : launch<false, 64>(maps, p, stream);
 }

@@ -458,3 +458,70 @@ def test_more_streams_than_there_are_counters():
     for h in made:
         assert rt.cudaStreamDestroy(h) == 0
     assert layer.buf.device_status() == ep.EP_OK
+
+
+# e4m3, many entries for the SMs: tokens are laid out as codes before the products
+LAID = [(128, 1920, 1024, 8, 8, 0), (67, 1664, 1920, 5, 5, 0), (60, 1152, 640, 4, 3, 16), (128, 256, 640, 16, 8, 7), (9, 1152, 640, 2, 2, 1)]
+
+
+@pytest.mark.parametrize("N,H,I,E,K,sms", LAID)
+@pytest.mark.parametrize("extras", [False, True])
+def test_tokens_laid_out_as_codes(N, H, I, E, K, sms, extras):
+    layer = Layer(N, H, I, E, K, fp8=True, bias=extras, residual=extras, drop=0.2 if extras else 0.0, max_sms=sms, seed=3)
+    first = layer.check()
+    for _ in range(3):
+        assert torch.equal(layer.run(), first)
+
+
+def test_laid_out_tokens_do_not_touch_each_other():
+    """Tokens of NaN, infinities, zeros and the largest and smallest numbers change their own rows only."""
+    layer = Layer(60, 1152, 640, 4, 3, fp8=True, max_sms=16, seed=5)
+    first = layer.check()
+    layer.x = layer.x.clone()
+    layer.x[3, 5], layer.x[17, 200], layer.x[41] = float("inf"), float("nan"), 0.0
+    layer.x[50] *= 2.0 ** 100
+    layer.x[51] *= 2.0 ** -100
+    got = layer.run()
+    others = torch.ones(60, dtype=torch.bool, device="cuda")
+    others[[3, 17, 41, 50, 51]] = False
+    assert torch.equal(got[others], first[others])
+    assert not bool(got[3].isfinite().any()) and bool(got[17].isnan().all()) and bool((got[41] == 0).all())
+
+
+def test_laid_out_tokens_on_streams_and_in_graphs():
+    layer = Layer(60, 1152, 640, 4, 3, fp8=True, bias=True, max_sms=16, seed=6)
+    want = layer.check()
+    call = lambda: layer.buf.expert_layer(layer.x, layer.idx, layer.wts, layer.gu, layer.down, biases=layer.bias)  # noqa: E731
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, call()))
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for _ in range(5):
+        outs = []
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i < 2:
+                    graphs[i][0].replay()
+                    outs.append(graphs[i][1])
+                else:
+                    outs.append(call())
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+        for _, o in graphs:
+            o.zero_()
+    assert layer.buf.device_status() == ep.EP_OK
+
+
+def test_a_wait_that_runs_out_with_tokens_laid_out():
+    layer = Layer(60, 1152, 640, 4, 3, fp8=True, max_sms=16, seed=7)
+    want = layer.check()
+    for _ in range(2):
+        ep.ep_set_test_hooks(layer.buf.ctx, move_withhold_item=int(layer.idx[3, 1]), move_wait_ns=1_000_000)
+        layer.buf.expert_layer(layer.x, layer.idx, layer.wts, layer.gu, layer.down)
+        assert layer.buf.device_status() == ep.EP_ERR_TIMEOUT
+        ep.ep_set_test_hooks(layer.buf.ctx)
+        for _ in range(3):
+            assert torch.equal(layer.run(), want)
