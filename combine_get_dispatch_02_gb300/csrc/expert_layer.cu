@@ -14,11 +14,11 @@
 // and ends in another's leaves two partial sums (fp32, in the workspace), added in
 // the order of the shares.  What needs all SMs' results is done between grid barriers
 // (cooperative launch), and the weights' loader does not wait there:
-//   entries sorted by expert (by every CTA) -- gate product -- SwiGLU, h laid out --
-//   down product -- sum over k
+//   entries sorted by expert (by every CTA) -- (tokens laid out as codes: kLaidStages) -- gate product -- SwiGLU, h
+//   laid out -- down product -- sum over k
 //
 // Measured (one GB300), bytes of the named experts' weights over the time: 128 tokens, top-8 of 256, 7168 x 2048,
-// FP8 1.81 ms, 6.1 TB/s; 32 tokens, top-6 of 64, 4096 x 1024, bf16 243 us, 6.2 TB/s; one token, top-8 of 256, 7168 x
+// FP8 1.8 ms, 6.2 TB/s; 32 tokens, top-6 of 64, 4096 x 1024, bf16 243 us, 6.2 TB/s; one token, top-8 of 256, 7168 x
 // 2048, FP8 72 us, 4.9 TB/s: HBM bounds the products, which leave 10 us before the first stage, at the meetings (2
 // us each, of which the ring covers 3 together) and behind the last.  Products on mma.sync with the codes
 // converted on the way took 92 us and 2.4 ms there.
