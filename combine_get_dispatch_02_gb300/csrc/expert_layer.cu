@@ -954,8 +954,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 if (!bar_wait(b_full + 8 * (n % kStages), n / kStages & 1, p.wait_cycles)) atomicOr(p.status, kStatusInFlight);
             }
         }
-        // the last CTA puts the barrier back: all arrivals are in, on a failure too
+        // The last CTA puts the barrier back, behind all arrivals: one that came to its last meeting has seen them
+        // all there; a CTA whose waits have given up has not, so its own are done before it is counted, and where
+        // it is the last, it has those of the CTAs counted before it.
+        if (bars.failed) __threadfence();
         if (atomicAdd(p.barrier + 1, 1u) == gridDim.x - 1) {
+            if (bars.failed) __threadfence();
             p.barrier[0] = 0;
             p.barrier[1] = 0;
         }
