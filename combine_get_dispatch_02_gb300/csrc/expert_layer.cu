@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
             return make_int2(shares[down].owner(u), shares[down].owner(u + lines[down] - 1));
         };
         // Tokens of every eighth stage, rows of 128 bytes, swizzled as the weights are.  Gate: x, by this warp; down (and
-        // gate, laid): by tensor map, once all have laid theirs out.
+        // gate, laid): by tensor map, once all have laid theirs out.  (x not by read-only loads: `out` may be x.)
         auto bring = [&](auto down) {
             constexpr bool DOWN = decltype(down)::value;
             constexpr int R = kParts<FP8, DOWN>;
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                             const uint4 *src = reinterpret_cast<const uint4 *>(
                                 static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)(r.list[w.first + min(i, w.count - 1)] >> 5) * p.H + l * 128 +
                                 (lane & 7) * 16);
-                            return Two{__ldg(src), __ldg(src + 1)};
+                            return Two{src[0], src[1]};
                         };
                         Two next = get(lane >> 3);
                         ok = wait(b_empty + 8 * slot, (stages / kStages & 1) ^ 1);
@@ -630,8 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                         auto get = [&](int i) {
                             uint4 q = make_uint4(0, 0, 0, 0);
                             if (i < w.count && c < p.H)
-                                q = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) +
-                                                                          (int64_t)(r.list[w.first + i] >> 5) * p.H + c));
+                                q = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.x) +
+                                                                     (int64_t)(r.list[w.first + i] >> 5) * p.H + c);
                             return q;
                         };
                         constexpr int U = C == 16 ? 2 : 8;  // loads in flight (128 tokens, top-2 of 8, 4096 x 4096: 1 227 us, 8 176)
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_layer_kernel(const __grid_
                 // a warp takes 128 channels of a token, 4 to a lane, for all its entries
                 for (int it = it0; it < p.N * lines[0] && !spare; it += warps) {
                     const int t = it / lines[0], l = it - t * lines[0];
-                    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)t * p.H + l * 128) + lane);
+                    const uint2 q = reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.x) + (int64_t)t * p.H + l * 128)[lane];
                     float v[4] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
                     const float2 s = block_scale(v);
                     uint32_t c[2];

@@ -275,7 +275,8 @@ __device__ __forceinline__ void combine_rows(const ExpertLayerParams &p, const R
         }
         const int64_t at = (int64_t)t * p.H + row;
         if (p.residual != nullptr) {
-            const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.residual) + at));
+            // (not a read-only load: `out` may be the residual)
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.residual) + at);
             a += bf16_lo(v);
             b += bf16_hi(v);
         }

@@ -58,3 +58,24 @@ def test_the_barrier_is_put_back_behind_all_arrivals(fp8):
     finally:
         for s in made:
             assert rt.cudaStreamDestroy(ctypes.c_void_p(s.cuda_stream)) == 0
+
+
+# N, H, I, E, K, fp8, SMs: the small form, the large one with 16 and with 64 columns a job, tokens laid out
+FORMS = [(9, 264, 72, 8, 2, False, 0), (9, 256, 128, 8, 2, True, 0), (3, 2824, 1416, 40, 6, False, 0), (3, 2176, 1920, 20, 4, True, 0),
+         (40, 264, 72, 8, 2, False, 0), (33, 1152, 256, 4, 3, True, 0), (60, 1152, 640, 4, 3, True, 16)]
+
+
+@pytest.mark.parametrize("N,H,I,E,K,fp8,sms", FORMS)
+@pytest.mark.parametrize("shared", ["x", "residual", "both"])
+def test_the_output_may_be_what_is_read(N, H, I, E, K, fp8, sms, shared):
+    """In each form, over and over: the output is x, the residual, or both of them."""
+    layer = Layer(N, H, I, E, K, fp8=fp8, bias=True, residual=True, drop=0.1, seed=4, max_sms=sms)
+    if shared == "both":
+        layer.residual = layer.x
+    want = layer.check()
+    for _ in range(10):
+        x = layer.x.clone()
+        residual = x if shared == "both" else layer.residual.clone()
+        out = residual if shared == "residual" else x
+        got = layer.buf.expert_layer(x, layer.idx, layer.wts, layer.gu, layer.down, biases=layer.bias, residual=residual, out=out)
+        assert got is out and layer.buf.device_status() == ep.EP_OK and torch.equal(out, want)
