@@ -78,7 +78,9 @@ class Buffer:
     R*num_max_dispatch_tokens_per_rank rows); False gives the packed layout
     of the normal (high-throughput) kernels.  ``max_sms`` caps the SMs the
     dispatch / combine kernels use (0 = all); the experts' products take
-    SMs in pairs, 2 at least."""
+    SMs in pairs, 2 at least.  Calls enqueue on the current stream.  One thread
+    at a time calls a Buffer, and it lives as long as graphs that captured its
+    calls are replayed."""
 
     def __init__(self, num_ranks: int, num_max_dispatch_tokens_per_rank: int, hidden: int,
                  num_experts: int, num_topk: int, low_latency_mode: bool = True, max_sms: int = 0,

@@ -1,11 +1,13 @@
-// Who holds which tile counter of a handle's expert products (host side).  Two
-// launches that may run side by side must not draw from one counter.  A stream's
+// Who holds which counter (host side): the tile counters of a handle's expert
+// products, the grid barriers of a context's layer calls.  Two launches that may run
+// side by side must not share one.  A stream's
 // launches follow each other, so each stream has one, found by the stream's id
 // (ids are not used again, and nothing says when a stream is gone: these are not
 // given back).  A captured call has one of its own, because its graph can run
 // beside anything; it comes back when the graph, and whatever was instantiated from
 // it, is gone and has run.  Graphs are destroyed on any thread and may outlive the
-// handle: the book is kept until the last holder lets go.
+// handle or context: the book is kept until the last holder lets go.  Calls may come from
+// several threads at a time (each with its own handle): the book is locked.
 #pragma once
 
 #include <stdint.h>
@@ -29,13 +31,17 @@ class TileCounters {
 
     static TileCounters *create() { return new (std::nothrow) TileCounters(); }
 
-    // The counter of a stream, -1 when all are taken.  Callers of one handle do not overlap.
+    // The counter of a stream, -1 when all are taken.
     int of_stream(unsigned long long id) {
-        for (int i = 0; i < streams_; ++i)
-            if (stream_[i] == id) return i;
-        if (streams_ == kStreamCounters) return -1;
-        stream_[streams_] = id;
-        return streams_++;
+        lock();
+        int i = 0;
+        while (i < streams_ && stream_[i] != id) ++i;
+        if (i == kStreamCounters)
+            i = -1;
+        else if (i == streams_)
+            stream_[streams_++] = id;
+        unlock();
+        return i;
     }
     // A counter for a captured call, to be given back with `give_back`; nullptr when all are taken.
     Captured *take() {
@@ -70,7 +76,12 @@ class TileCounters {
     void release() {
         if (holders_.fetch_sub(1, std::memory_order_acq_rel) == 1) delete this;
     }
-    int streams() const { return streams_; }
+    int streams() {
+        lock();
+        const int n = streams_;
+        unlock();
+        return n;
+    }
     int captured() {
         lock();
         const int n = fresh_ - back_;

@@ -157,8 +157,9 @@ ep_status ep_recv_bytes(const ep_config *cfg, int32_t use_fp8,
                         uint64_t *payload_bytes, uint64_t *scale_bytes);
 
 /* Create a context on the current device: validates cfg, allocates the
- * 4-byte device status word and reads the device's SM count.  *out is NULL on
- * error. */
+ * 4-byte device status word and 32 KB of barriers (ep_expert_layer) and reads the
+ * device's SM count.  *out is NULL on error.  Calls that a graph has captured use
+ * the context's memory: no replay after ep_destroy. */
 ep_status ep_create(const ep_config *cfg, ep_ctx **out);
 ep_status ep_destroy(ep_ctx *ctx);
 
