@@ -11,6 +11,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <vector>
 
 #include <cuda_runtime.h>
@@ -86,6 +87,23 @@ struct ep_handle {
 namespace {
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Memory of a call; an input with `itself` may also be the output (the same address and size): each of its numbers
+// has been read when it is written.
+struct Range {
+    const void *at;
+    uint64_t bytes;
+    bool itself = false;
+};
+bool overlaps(const Range &out, std::initializer_list<Range> in) {
+    const uintptr_t a = (uintptr_t)out.at;
+    for (const Range &r : in) {
+        const uintptr_t b = (uintptr_t)r.at;
+        if (a == 0 || b == 0 || a >= b + r.bytes || b >= a + out.bytes) continue;
+        if (!(r.itself && a == b && out.bytes == r.bytes)) return true;
+    }
+    return false;
+}
 
 // A new layout in the handle: the rank transport's send rows and runs no
 // longer belong to it.  A copy of old run sizes into h_runs may still be
@@ -705,16 +723,15 @@ ep::ExpertGemmParams expert_params(const ep_ctx *ctx, const ep_handle *h, int32_
 
 // A list of gradients: aligned to their type, sizes that can be numbered, and, where
 // they are written, none that overlaps another (it would be scaled twice, or read
-// by one part of the GPU while another writes it).
-ep_status check_grads(const ep_grad *g, int32_t count, bool written) {
+// by one part of the GPU while another writes it) nor the partial sums or the norm.
+ep_status check_grads(const ep_grad *g, int32_t count, bool written, const double *partials, const float *norm) {
     if (count < 0 || (count > 0 && g == nullptr)) return EP_ERR_INVALID_ARG;
-    struct Range {
+    struct Taken {
         uintptr_t from, to;
-        int32_t i;  // tensor; its own data and out may be one
     };
-    std::vector<Range> r;
+    std::vector<Taken> r;
     try {
-        r.reserve(2 * (size_t)count);
+        r.reserve(2 * (size_t)count + 2);
     } catch (...) {
         return EP_ERR_OOM;
     }
@@ -726,12 +743,17 @@ ep_status check_grads(const ep_grad *g, int32_t count, bool written) {
         if (g[i].data == nullptr || !aligned(g[i].data, es)) return EP_ERR_INVALID_ARG;
         if (g[i].numel > (int64_t)1 << 42 || (total += g[i].numel) > (int64_t)1 << 42) return EP_ERR_UNSUPPORTED;
         const uintptr_t a = (uintptr_t)g[i].data, o = (uintptr_t)g[i].out, bytes = (uintptr_t)g[i].numel * es;
-        if (!written) continue;
+        if (!written) {
+            if (overlaps({partials, EP_GRAD_PARTIALS * sizeof(double)}, {{g[i].data, bytes}})) return EP_ERR_INVALID_ARG;
+            continue;
+        }
         if (g[i].out == nullptr || !aligned(g[i].out, es)) return EP_ERR_INVALID_ARG;
-        r.push_back({a, a + bytes, i});
-        if (o != a) r.push_back({o, o + bytes, i});
+        r.push_back({a, a + bytes});
+        if (o != a) r.push_back({o, o + bytes});  // its own data and out may be one
     }
-    std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
+    if (written && partials != nullptr) r.push_back({(uintptr_t)partials, (uintptr_t)(partials + EP_GRAD_PARTIALS)});
+    if (written && norm != nullptr) r.push_back({(uintptr_t)norm, (uintptr_t)(norm + 1)});
+    std::sort(r.begin(), r.end(), [](const Taken &a, const Taken &b) { return a.from < b.from; });
     for (size_t i = 1; i < r.size(); ++i)
         if (r[i].from < r[i - 1].to) return EP_ERR_INVALID_ARG;
     return EP_OK;
@@ -1564,10 +1586,15 @@ ep_status ep_expert_linear(ep_ctx *ctx, const ep_handle *handle, const void *d_x
     if (s != EP_OK) return s;
     if ((bias_fp32 != 0 && bias_fp32 != 1) || activation < EP_ACT_NONE || activation > EP_ACT_SILU) return EP_ERR_INVALID_ARG;
     if (handle->tokens_per_rank == 0) return EP_OK;
-    if (d_x == nullptr || d_w == nullptr || d_y == nullptr || d_z == d_y) return EP_ERR_INVALID_ARG;
-    if (d_x == d_y || d_x == d_z) return EP_ERR_INVALID_ARG;  // other tiles still read the row
+    if (d_x == nullptr || d_w == nullptr || d_y == nullptr) return EP_ERR_INVALID_ARG;
     if (!aligned(d_x, 16) || !aligned(d_w, 16) || !aligned(d_y, 16) || !aligned(d_bias, bias_fp32 ? 4 : 2) ||
         !aligned(d_residual, 16) || !aligned(d_z, 16))
+        return EP_ERR_INVALID_ARG;
+    // other tiles still read a row's x and the weights while its y and z are written
+    const uint64_t rows = ctx->rows, E = ctx->cfg.num_experts, own = rows * n * 2;
+    const Range x = {d_x, rows * k * 2}, w = {d_w, E * n * k * 2}, b = {d_bias, E * n * (bias_fp32 ? 4 : 2)};
+    if (overlaps({d_y, own}, {x, w, b, {d_residual, own, true}, {d_z, own}}) ||
+        overlaps({d_z, own}, {x, w, b, {d_residual, own, true}}))
         return EP_ERR_INVALID_ARG;
     ep::ExpertGemmParams p = expert_params(ctx, handle, n, k, (cudaStream_t)stream);
     p.x = d_x;
@@ -1601,6 +1628,11 @@ ep_status ep_expert_linear_backward(ep_ctx *ctx, const ep_handle *handle, const 
     }
     if (d_dy == nullptr || (d_z == nullptr && activation != EP_ACT_NONE)) return EP_ERR_INVALID_ARG;
     if (!aligned(d_dy, 16) || !aligned(d_z, 16) || !aligned(d_dz, 16)) return EP_ERR_INVALID_ARG;
+    const uint64_t own = (uint64_t)ctx->rows * n * 2;
+    const void *const z_read = activation != EP_ACT_NONE ? d_z : nullptr;
+    if (overlaps({d_dz, own}, {{d_dy, own, true}, {z_read, own, true}}) ||
+        overlaps({d_dbias, (uint64_t)ctx->cfg.num_experts * n * 4}, {{d_dy, own}, {z_read, own}, {d_dz, own}}))
+        return EP_ERR_INVALID_ARG;
     ep::LinearBackwardParams p = {};
     p.dy = d_dy;
     p.z = d_z;
@@ -1627,7 +1659,7 @@ ep_status ep_grad_norm(ep_ctx *ctx, const void *grads, int32_t count, double *d_
     NvtxRange nvtx("ep_grad_norm");
     if (ctx == nullptr || !on_ctx_device(ctx)) return EP_ERR_INVALID_ARG;
     const ep_grad *g = static_cast<const ep_grad *>(grads);
-    const ep_status s = check_grads(g, count, false);
+    const ep_status s = check_grads(g, count, false, d_partials, nullptr);
     if (s != EP_OK) return s;
     if (d_partials == nullptr || !aligned(d_partials, 8)) return EP_ERR_INVALID_ARG;
     if (ep::launch_grad_norm(g, count, d_partials, expert_sms(ctx), (cudaStream_t)stream) != cudaSuccess) {
@@ -1643,7 +1675,7 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
     if (ctx == nullptr || !on_ctx_device(ctx) || max_norm == nullptr) return EP_ERR_INVALID_ARG;
     const float limit = *static_cast<const float *>(max_norm);
     const ep_grad *g = static_cast<const ep_grad *>(grads);
-    const ep_status s = check_grads(g, count, true);
+    const ep_status s = check_grads(g, count, true, d_partials, d_norm);
     if (s != EP_OK) return s;
     if (!(limit >= 0.0f) || d_partials == nullptr || !aligned(d_partials, 8) || !aligned(d_norm, 4)) return EP_ERR_INVALID_ARG;
     if (ep::launch_grad_clip(g, count, d_partials, limit, d_norm, expert_sms(ctx), ctx->num_sms, (cudaStream_t)stream) != cudaSuccess) {
@@ -1758,6 +1790,16 @@ ep_status ep_expert_layer(ep_ctx *ctx, const void *d_x, const int64_t *d_topk_id
     p.b_down = d_b_down;
     p.residual = d_residual;
     p.out = d_out;
+    const bool fp8 = d_gate_up_scales != nullptr;
+    const uint64_t N = p.N, K = p.K, H = p.H, I = p.I, E = p.E, tokens = N * H * 2, weight = fp8 ? 1 : 2;
+    const uint64_t workspace = ep::expert_layer_workspace(p);
+    const Range idx = {d_topk_idx, N * K * 8}, wts = {d_topk_weights, N * K * 4};
+    const Range wgu = {d_w_gate_up, E * 2 * I * H * weight}, sgu = {d_gate_up_scales, E * ((2 * I + 127) / 128) * (H / 128) * 4};
+    const Range wd = {d_w_down, E * H * I * weight}, sd = {d_down_scales, E * ((H + 127) / 128) * (I / 128) * 4};
+    const Range bgu = {d_b_gate_up, E * 2 * I * 2}, bd = {d_b_down, E * H * 2};
+    if (overlaps({d_out, tokens}, {{d_x, tokens, true}, {d_residual, tokens, true}, idx, wts, wgu, sgu, wd, sd, bgu, bd}) ||
+        overlaps({d_workspace, workspace}, {{d_x, tokens}, {d_residual, tokens}, {d_out, tokens}, idx, wts, wgu, sgu, wd, sd, bgu, bd}))
+        return EP_ERR_INVALID_ARG;
     if (!ep::expert_layer_small(p)) p.barrier = counter_pair(ctx->layer_counters, ctx->d_layer_counters, (cudaStream_t)stream);
     const cudaError_t e = ep::launch_expert_layer(p, d_workspace, (cudaStream_t)stream);
     if (e != cudaSuccess) {

@@ -388,8 +388,8 @@ ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, vo
  *                   or _SILU (z / (1 + exp(-z)))
  *     d_residual    device bf16 [rows, n] or NULL; may be d_y itself
  *     d_z           device bf16 [rows, n] or NULL: z, for the backward pass
- *     d_y           device bf16 [rows, n]; neither it nor d_z may be d_x, nor one the
- *                   other (EP_ERR_INVALID_ARG)
+ *     d_y           device bf16 [rows, n]; neither it nor d_z may overlap an input but
+ *                   the residual as a whole, nor one the other (EP_ERR_INVALID_ARG)
  * ep_expert_linear_backward: dz[r] = dy[r] act'(z[r]) rounded to bf16, and the
  *   bias gradient dbias[e] = sum over the rows of e of the same before the
  *   rounding, in fp32 (RELU: the slope at 0 is 0).  The residual's gradient is dy.
@@ -399,6 +399,7 @@ ep_status ep_cast_weights(ep_ctx *ctx, const void *d_w, int32_t n, int32_t k, vo
  *     d_dz    device bf16 [rows, n], may be d_dy itself or d_z; NULL: not wanted
  *     d_dbias device fp32 [E, n]; accumulate = 1 adds to what it holds (an expert
  *             without rows: zeros, or what it holds); NULL: not wanted
+ *   Other overlaps of outputs with inputs or each other are EP_ERR_INVALID_ARG.
  *   One of d_dz and d_dbias is given at least.  The sums have one order for one
  *   routing and max_sms does not change it. */
 typedef enum ep_activation {
@@ -433,7 +434,8 @@ ep_status ep_expert_linear_backward(ep_ctx *ctx, const ep_handle *handle, const 
  *     d_norm      device fp32 [1] or NULL
  * Tensors lie anywhere, aligned to their type; 16-byte alignment, and out aligned
  * as data is, are faster.  For ep_grad_clip no memory may appear twice in the list
- * (EP_ERR_INVALID_ARG) but a tensor's data as its own out.  2^42 elements in all
+ * (EP_ERR_INVALID_ARG) but a tensor's data as its own out, and for both calls
+ * d_partials and d_norm lie outside the tensors.  2^42 elements in all
  * at most (EP_ERR_UNSUPPORTED).  The sums have one order for one max_sms. */
 #define EP_GRAD_PARTIALS 1024
 typedef struct ep_grad {
@@ -479,6 +481,8 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
  *                       outlives the call; calls that may run side by side
  *                       (streams, graphs) need one each
  *     d_out             device bf16 [num_tokens, H]; may be d_x or d_residual itself
+ * Other overlaps of d_out or d_workspace with what the call reads, or with each
+ * other, are EP_ERR_INVALID_ARG.
  * All pointers 16-byte aligned (d_topk_idx 8, scales and weights 4); inner a
  * multiple of 8, with FP8 weights H and inner multiples of 128.  The same call
  * repeats bit for bit; the order in which its sums are taken follows from the SMs
