@@ -67,6 +67,9 @@ __device__ __forceinline__ float relu(float v) {
     return r;
 }
 
+// ReLU's slope, 0 at 0; a NaN stays one.
+__device__ __forceinline__ float step(float v) { return v > 0.0f ? 1.0f : v <= 0.0f ? 0.0f : v; }
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The activations of a pair.
@@ -103,7 +106,7 @@ __device__ __forceinline__ uint64_t activate2(uint64_t v) {
 template <Act ACT>
 __device__ __forceinline__ uint64_t slope2(float a, float b) {
     using namespace umma;
-    if constexpr (ACT == Act::kRelu) return two(a > 0.0f ? 1.0f : 0.0f, b > 0.0f ? 1.0f : 0.0f);
+    if constexpr (ACT == Act::kRelu) return two(step(a), step(b));
     if constexpr (ACT == Act::kGelu) {
         const uint64_t v = two(a, b), t = rcp2(fma2(two(fabsf(a), fabsf(b)), both(0.3275911f * 0.70710678118654752f), both(1.0f)));
         const uint64_t e = exp2_2(mul2(mul2(v, v), both(-0.5f * kLog2e)));  // exp(-v^2 / 2)
