@@ -161,17 +161,6 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
         for (int i = gridDim.x + threadIdx.x; i < kGradPartials; i += kThreads) partials[i] = 0.0;
 }
 
-// The root of a sum of squares in fp32: the sum brought to 1 .. 4 by an even power of two, which fp32 takes
-// with 24 bits; infinite past fp32's range.
-__device__ __forceinline__ float root(double sum) {
-    const long long bits = __double_as_longlong(sum);
-    const int ex = (int)(bits >> 52) - 1023;
-    if (ex == 1024 || ex < -1022) return sum == 0.0 ? 0.0f : ex == 1024 ? (float)sum : 0.0f;  // infinite, NaN; subnormal
-    const int half = ex >> 1;
-    const float m = (float)__longlong_as_double((bits & 0xFFFFFFFFFFFFFll) | (long long)(1023 + (ex & 1)) << 52);
-    return ldexpf(__fsqrt_rn(m), half);
-}
-
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_constant__ Table<CAP> tab, const double *partials,
                                                              float max_norm, float *norm_out) {
@@ -184,11 +173,14 @@ __global__ void __launch_bounds__(kThreads) grad_clip_kernel(const __grid_consta
     if (threadIdx.x < 32) {
         double sum = part[threadIdx.x];
         for (int i = 1; i < kGradPartials / 32; ++i) sum += part[threadIdx.x + 32 * i];
-        const float norm = root(warp_sum(sum));
+        sum = warp_sum(sum);
         if (threadIdx.x == 0) {
+            // the root and the quotient in fp64, each rounded once; a norm past fp32's range or an undefined one
+            // scales nothing
+            const double wide = sqrt(sum);
+            const float norm = (float)wide;
             if (norm_out != nullptr && blockIdx.x == 0) *norm_out = norm;
-            // an infinite or undefined norm scales nothing
-            factor = isfinite(norm) && norm > max_norm ? __fdiv_rn(max_norm, norm) : 1.0f;
+            factor = isfinite(norm) && wide > (double)max_norm ? (float)((double)max_norm / wide) : 1.0f;
         }
     }
     __syncthreads();
