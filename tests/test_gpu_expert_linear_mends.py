@@ -5,7 +5,7 @@ import torch
 from combine_get_dispatch_02_gb300 import build as epbuild
 from combine_get_dispatch_02_gb300 import ep
 from expert_reference import in_use, receive
-from test_gpu_expert_linear import ACTS, group
+from test_gpu_expert_linear import ACTS, group, slope64
 
 pytestmark = pytest.mark.gpu
 
@@ -36,4 +36,23 @@ def test_a_nan_in_z_is_not_hidden(act):
         hit[r, c], hit_db[e, c] = True, True
     assert bool(dz2[hit].isnan().all()) and bool(db2[hit_db].isnan().all())
     assert torch.equal(dz2[used][~hit[used]], dz[used][~hit[used]]) and torch.equal(db2[~hit_db], db[~hit_db])
+    assert buf.device_status() == ep.EP_OK
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_slopes_of_bias_gradients_are_good_to_32_bits(act):
+    """dy = 1 and one row: the bias gradient is the slope as it is added up, before dz's rounding.
+
+    The slopes (1.13 at most) come out of at most eight roundings and approximations of numbers of that size or
+    less, each off by 2^-24 at most where it is a rounding and 2^-23 or 2^-22 of itself where it is the fast reciprocal or
+    exponential (whose factor is half or less): spread evenly, 2^-24 / sqrt(3) and as much for those, of which numbers
+    below 1/2 make a half or less, so in the root of the mean square sqrt(8) * 2^-24 / sqrt(3) * 0.6 = 2^-24, and
+    6 * 2^-24 at most for any."""
+    buf, h, _ = group([1])
+    g = torch.Generator("cuda").manual_seed(3)
+    for scale in (1.0, 3.0):
+        z = (torch.randn(1, 65536, generator=g, device="cuda") * scale).bfloat16()
+        _, db = buf.expert_linear_backward(torch.ones_like(z), z, h, activation=act)
+        error = db[0].double() - slope64(z[0].double(), act)
+        assert float(error.square().mean().sqrt()) <= 2.0 ** -24 and float(error.abs().max()) <= 6 * 2.0 ** -24
     assert buf.device_status() == ep.EP_OK
