@@ -5,8 +5,8 @@
 // Of the epilogue's results 8 bits are kept, and the instructions bound products of few
 // channels and the backward pass: all are written in the instructions that take two numbers
 // at a time and take the fast exponential, which is off by 1.2 |v| ulp (2^-16 of an activation
-// at most before it vanishes).  32768 rows x 2048 x 1024, GELU / SiLU: 96 / 94
-// us, with erfcf and expf 180 / 111 (without activation 92).  The slopes are 1.13 at
+// at most before it vanishes).  32768 rows x 2048 x 1024, GELU / SiLU: 102 /
+// 100 us, with erfcf and expf 180 / 111 (without activation 94).  The slopes are 1.13 at
 // most and bias gradients add them up unrounded, so they are kept to fp32's last bits, which they can be because where
 // they matter their exponential's argument is small.  Off by 4e-8 in the root of the mean square over z of N(0, 1) and
 // 1.8e-7 at most (the formulas in fp32 3e-8 and 2.4e-7); 262144 rows x 2048, tanh GELU 463 us, with erfcf and expf 669.

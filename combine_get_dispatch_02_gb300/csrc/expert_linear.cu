@@ -9,7 +9,7 @@
 // cluster barrier's release waits for dz's stores, 598 instead of 504 us below.)
 //
 // Measured (one GB300): 262144 rows over 256 experts x 2048 channels, none / ReLU / GELU /
-// tanh GELU / SiLU 303 / 449 / 463 / 469 / 451 us (copying the bytes takes 316 / 474):
+// tanh GELU / SiLU 315 / 450 / 477 / 463 / 450 us (copying the bytes takes 316 / 474):
 // HBM bounds it, with two numbers to an instruction and four CTAs to an SM (three: 504 us
 // with tanh GELU).  27 K rows over 52 experts drawn by a Zipf law x 1416, GELU: 49 us (copying
 // them takes 34): the end, when only the CTAs of the expert with a fifth of the rows are left.

@@ -6,14 +6,14 @@
 // that start on 16-byte addresses, numbered through; their table travels in the
 // kernel's parameters.
 //
-// Sums: the squares of a thread's 64 bytes in fp32, everything above in fp64.  Where the
+// Sums: the squares of a thread's 64 bytes in fp32, everything above in fp64, root and quotient too.  Where the
 // largest of them could overflow or vanish when squared they are taken again in
 // fp64 (which for all of them would bound the kernel: one fp64 operation for every
 // 4 bytes is more than the device has).
 //
 // Measured (one GB300): 671M elements in fp32 and bf16, 2.7 GB: norm 389 us (6.90 TB/s, HBM), clipping into
-// other tensors 784 us (6.85 TB/s, HBM); 12 tensors of up to 1024 bf16 both together 13 us (two launches and
-// fp64's latencies; the caller's host takes longer); 300 tensors of 0.4 GB, nothing to clip, 85 us.
+// other tensors 786 us (6.83 TB/s, HBM), in place 858 us; 12 tensors of up to 1024 bf16 both together 13 us (two
+// launches and fp64's latencies; the caller's host takes longer); 300 tensors of 0.48 GB, nothing to clip, 85 us.
 #include <cuda_bf16.h>
 
 #include "ep.h"
@@ -301,9 +301,9 @@ cudaError_t launch_grad_norm(const ep_grad *g, int count, double *partials, int 
 cudaError_t launch_grad_clip(const ep_grad *g, int count, const double *partials, float max_norm, float *norm, int sms,
                              int all_sms, cudaStream_t stream) {
     return in_groups(g, count, [&](const auto &tab, int pieces, int k) {
-        // Out of place short CTAs of 8 pieces take the stores at the copy rate (671M elements, 2.7 GB: 784 us, with
+        // Out of place short CTAs of 8 pieces take the stores at the copy rate (671M elements, 2.7 GB: 786 us, with
         // the resident CTAs each on a long way 854); in place, where there is mostly nothing to do, they would
-        // only all add up the partial sums (61 instead of 8 us).
+        // only all add up the partial sums (61 instead of 8 us; where there is something to do 858 us).
         int grid = grid_of(pieces, sms);
         if (!tab.in_place && sms == all_sms && grid < pieces / 8) grid = pieces / 8;
         return launch(grad_clip_kernel<(int)(sizeof(tab.src) / sizeof(tab.src[0]))>, grid, stream, tab, partials, max_norm,

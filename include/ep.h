@@ -450,9 +450,11 @@ ep_status ep_grad_clip(ep_ctx *ctx, const void *grads, int32_t count, const doub
 
 /* The whole layer of gated experts for a few tokens (a decode step): what
  * dispatch, the two products and combine compute, in one kernel (two where the
- * weights are few) that reads the named experts' weights once and keeps no receive
+ * weights are few) that streams the named experts' weights and keeps no receive
  * buffer; for more than EP_LAYER_MAX_TOKENS tokens use those calls (EP_ERR_UNSUPPORTED
- * here).  With FP8 weights and more than about 12 entries to an expert those are faster.
+ * here).  A pass over an expert's weights serves 8 of its entries in the two kernels; in
+ * the one 64 (gate and up) and 32 (down) with bf16 weights, 32 and 16 with FP8, up to
+ * 8 and 4 tokens 16 and 8, 8 and 4; further passes come from L2 where it holds the weights.  With FP8 weights and more than about 12 entries to an expert those are faster.
  *   h[t,k] = silu(g) u, [g; u] = Wgu[e] x[t] + bgu[e], e = topk_idx[t,k]
  *   out[t] = bf16(residual[t] + fma chain over k ascending of
  *            topk_weights[t,k] * (Wd[e] h[t,k] + bd[e]))
