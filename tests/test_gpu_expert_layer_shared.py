@@ -1,4 +1,4 @@
-"""GPU checks of the whole layer's corners: what a wait that runs out leaves behind, what may share memory."""
+"""GPU checks of the whole layer: what a wait that runs out leaves behind, and which tensors may share memory."""
 import ctypes
 
 import pytest
